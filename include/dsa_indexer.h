@@ -378,6 +378,130 @@ dsa_status dsa_sparse_mla_workspace_size(const dsa_sparse_mla_args* args, size_t
 dsa_status dsa_sparse_mla(const dsa_sparse_mla_args* args, dsa_stream_t stream);
 
 /*
+ * A serving step for a batch whose requests begin with the same prompt: page plan, latent
+ * cache append, shared-prefix attention.  They share the paged layout of the calls above
+ * (block_tables, slot_mapping, cache_c / cache_r of dsa_sparse_mla), so the indexer and
+ * dsa_sparse_mla run on the same tables and caches.
+ */
+
+/*
+ * dsa_page_plan -- block tables, slot mapping, positions and query offsets of a step, from
+ * the request lengths, in one launch.  Request b holds seq_lens[b] tokens after the step,
+ * the last q_lens[b] of them new.  With c = seq_lens[b] - q_lens[b], P = page_size, row b
+ * of block_tables holds before the call
+ *     held(b) = max(ceil(c / P), num_prefix_pages)         pages
+ * and after it have(b) = max(ceil(seq_lens[b] / P), num_prefix_pages):
+ *     entry j < num_prefix_pages     prefix_pages[j]            (written in every row)
+ *     entry j < held(b)              as it was
+ *     entry j < have(b)              free_pages[first(b) + j - held(b)]
+ *     the rest                       -1
+ * first(b) = the new pages of requests 0 .. b-1: free pages are handed out in request order
+ * from the front of free_pages, and used[0] = the new pages of all requests.  A request of
+ * seq_lens[b] = 0 gets a row of -1 and takes nothing.
+ *   cu_q_lens [B + 1]        0, q_lens[0], q_lens[0] + q_lens[1], ...
+ *   positions [total_q]      of each new token in its sequence: seq_lens[b] - q_lens[b] + i
+ *   slot_mapping [total_q]   page * P + row of that position (int64)
+ * total_q is the outputs' length: at least the sum of q_lens; entries past the sum (a step
+ * padded to a captured graph's size) are -1 in both.
+ * Only whole pages of a shared prompt can be shared: a request writes its own pages, so a
+ * partly filled last prompt page is each request's own.
+ * Recorded in the device status word (DSA_ERR_DEVICE_CHECK), never out of bounds: a
+ * free list that is too short (its entries and slots become -1; used[0] is still what the
+ * step needs), a page id < 0, a length that is negative, exceeds the table, or q_lens[b] >
+ * seq_lens[b] (taken as the nearest allowed value), and more new tokens than total_q (dropped).
+ * All arrays are 4-byte aligned device memory (slot_mapping 8-byte); prefix_pages may be
+ * NULL when num_prefix_pages is 0, free_pages when num_free is 0, slot_mapping and positions
+ * when total_q is 0.
+ */
+typedef struct {
+  int B, total_q, page_size, max_pages_per_seq, num_prefix_pages, num_free;
+  const int32_t* q_lens;
+  const int32_t* seq_lens;
+  const int32_t* prefix_pages;
+  const int32_t* free_pages;
+  int32_t* block_tables;
+  int32_t* cu_q_lens;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int32_t* used;
+} dsa_page_plan_args;
+dsa_status dsa_page_plan(const dsa_page_plan_args* args, dsa_stream_t stream);
+
+/*
+ * dsa_mla_cache_append -- this step's latent rows into the paged cache that dsa_sparse_mla
+ * and dsa_prefix_mla read:
+ *     cache_c[slot] = bf16( norm_weight * c / sqrt(mean(c^2) + norm_eps) )   (c itself without norm_weight)
+ *     cache_r[slot] = bf16( RoPE(r) )                                        (r itself without rope_cos)
+ * in fp32, rounded once.  c_kv [n, 512] and k_rope [n, 64] are bf16 rows c_stride / r_stride
+ * elements apart, so both may be views of one projection output [n, 576].  norm_weight [512]
+ * fp32.  rope_cos, rope_sin [rope_rows, 32] fp32; token t uses row positions[t] (row t when
+ * positions is NULL); pairs (i, i + 32), or (2i, 2i + 1) when rope_interleaved, turn as in
+ * dsa_indexer_prepare.  slot_mapping [n] int64, negative: the token is skipped.  A slot past
+ * the cache, or a position outside the tables, skips the token and is reported through
+ * dsa_check_device_status.  Two tokens with one slot leave either's values there.
+ * Pointers 16-byte aligned (slot_mapping 8, positions 4), strides multiples of 8 elements.
+ */
+typedef struct {
+  int n, kv_rank, rope_dim, page_size, num_pages, rope_interleaved, rope_rows;
+  float norm_eps;
+  const void* c_kv;
+  const void* k_rope;
+  int64_t c_stride, r_stride;
+  const int64_t* slot_mapping;
+  const float* norm_weight;
+  const float* rope_cos;
+  const float* rope_sin;
+  const int32_t* positions;
+  void* cache_c;
+  void* cache_r;
+} dsa_mla_cache_append_args;
+dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_stream_t stream);
+
+/*
+ * dsa_prefix_mla -- absorbed multi-head latent attention for a batch whose sequences share
+ * their first prefix_len tokens; the shared keys are scored for the queries of all requests
+ * together.  Query row i of sequence b sits at position p = seq_lens[b] - q_len(b) + i and
+ * sees the positions s <= p:
+ *     logit = scale * (q_nope[t, h] . c_kv[s] + q_rope[t, h] . k_rope[s])
+ *     out[t, h, :] = sum_s softmax_s(logit) * c_kv[s]     (bf16, latent space)
+ *     lse[t, h]    = ln sum_s exp(logit)                  (fp32; optional)
+ * where position s lies at page prefix_pages[s / page_size] when s < prefix_len and at page
+ * block_tables[b, s / page_size] otherwise, row s % page_size of cache_c / cache_r.
+ * prefix_len may end inside a page (that page of the request's own table then starts with
+ * rows nobody reads) and may be 0; a sequence may be shorter than it.  A query that sees
+ * nothing (p < 0) and the rows t >= cu_q_lens[B] (padding) give zeros and lse = -inf.
+ *   q_nope [total_q, H, 512] bf16 and q_rope [total_q, H, 64] bf16 with the given element
+ *   strides (multiples of 8; the last dimension dense); cache_c, cache_r as in dsa_sparse_mla;
+ *   block_tables [B, max_pages_per_seq]; out [total_q, H, 512] bf16 dense; lse [total_q, H].
+ * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0.
+ * Cache rows that no query sees may hold anything, NaN included; rows of positions below
+ * seq_lens[b] must be finite.  A page outside the cache, or a position past the table, is
+ * skipped and reported through dsa_check_device_status.  Probabilities enter P.V rounded to
+ * bf16; statistics and sums are fp32.  Results do not depend on the run (no atomics on data).
+ * workspace: dsa_prefix_mla_workspace_size bytes, 16-byte aligned like the other pointers.
+ */
+typedef struct {
+  int B, total_q, H, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq;
+  int prefix_len, num_prefix_pages;
+  float scale;
+  const void* q_nope;
+  const void* q_rope;
+  int64_t qn_stride_t, qn_stride_h, qr_stride_t, qr_stride_h;
+  const void* cache_c;
+  const void* cache_r;
+  const int32_t* prefix_pages;
+  const int32_t* block_tables;
+  const int32_t* cu_q_lens;
+  const int32_t* seq_lens;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} dsa_prefix_mla_args;
+dsa_status dsa_prefix_mla_workspace_size(const dsa_prefix_mla_args* args, size_t* bytes);
+dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* args, dsa_stream_t stream);
+
+/*
  * dsa_indexer_static -- dsa_indexer for callers that cannot allocate device memory.
  * The pages have no counterpart of this entry point; it exists for library users.
  *

@@ -88,6 +88,36 @@ class dsa_indexer_prepare_args(ctypes.Structure):
     ]
 
 
+class dsa_page_plan_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("total_q", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int), ("num_prefix_pages", ctypes.c_int), ("num_free", ctypes.c_int),
+                ("q_lens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("cu_q_lens", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("used", ctypes.c_void_p)]
+
+
+class dsa_mla_cache_append_args(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("kv_rank", ctypes.c_int), ("rope_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("rope_interleaved", ctypes.c_int),
+                ("rope_rows", ctypes.c_int), ("norm_eps", ctypes.c_float), ("c_kv", ctypes.c_void_p),
+                ("k_rope", ctypes.c_void_p), ("c_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("slot_mapping", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("rope_cos", ctypes.c_void_p),
+                ("rope_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("cache_c", ctypes.c_void_p),
+                ("cache_r", ctypes.c_void_p)]
+
+
+class dsa_prefix_mla_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("total_q", ctypes.c_int), ("H", ctypes.c_int), ("kv_rank", ctypes.c_int),
+                ("rope_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int), ("prefix_len", ctypes.c_int), ("num_prefix_pages", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_nope", ctypes.c_void_p), ("q_rope", ctypes.c_void_p),
+                ("qn_stride_t", ctypes.c_int64), ("qn_stride_h", ctypes.c_int64), ("qr_stride_t", ctypes.c_int64),
+                ("qr_stride_h", ctypes.c_int64), ("cache_c", ctypes.c_void_p), ("cache_r", ctypes.c_void_p),
+                ("prefix_pages", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("cu_q_lens", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _LIB = None
 
 
@@ -141,6 +171,14 @@ def lib():
         L.dsa_sparse_mla_workspace_size.argtypes = [ctypes.POINTER(dsa_sparse_mla_args), ctypes.POINTER(S)]
         L.dsa_sparse_mla.restype = I
         L.dsa_sparse_mla.argtypes = [ctypes.POINTER(dsa_sparse_mla_args), P]
+        L.dsa_page_plan.restype = I
+        L.dsa_page_plan.argtypes = [ctypes.POINTER(dsa_page_plan_args), P]
+        L.dsa_mla_cache_append.restype = I
+        L.dsa_mla_cache_append.argtypes = [ctypes.POINTER(dsa_mla_cache_append_args), P]
+        L.dsa_prefix_mla_workspace_size.restype = I
+        L.dsa_prefix_mla_workspace_size.argtypes = [ctypes.POINTER(dsa_prefix_mla_args), ctypes.POINTER(S)]
+        L.dsa_prefix_mla.restype = I
+        L.dsa_prefix_mla.argtypes = [ctypes.POINTER(dsa_prefix_mla_args), P]
         L.dsa_test_arm_score_timeout.restype = I
         L.dsa_test_arm_score_timeout.argtypes = [ctypes.c_ulonglong]
         _LIB = L
@@ -643,6 +681,153 @@ def dsa_sparse_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
                                    scale=scale, out=out, workspace=workspace)
     _check(lib().dsa_sparse_mla(ctypes.byref(a), _stream_ptr(stream)), "dsa_sparse_mla")
     return keep[8]
+
+
+# ---- a batch that shares its prompt: page plan, latent cache append, attention --------------
+
+def _record(tensors, stream) -> None:
+    """Memory of these tensors must not be reused ahead of `stream`'s kernels (torch's
+    allocator only knows the stream a tensor was allocated on)."""
+    if stream is not None:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+
+
+def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor, free_pages: torch.Tensor,
+                  *, page_size: int, total_q: int, prefix_pages: Optional[torch.Tensor] = None, cu_q_lens=None,
+                  slot_mapping=None, positions=None, used=None, stream=None):
+    """Block tables, slots, positions and query offsets of a step from the request lengths.
+
+    Request b holds seq_lens[b] tokens after the step, the last q_lens[b] of them new.
+    block_tables [B, max_pages] is updated in place: the shared prompt's whole pages
+    (prefix_pages) in front, the pages a request already holds kept, new ones from the front
+    of free_pages in request order, -1 behind.  total_q: the outputs' length, at least the
+    sum of q_lens (the rest is -1).  Returns (cu_q_lens [B + 1] int32, slot_mapping [total_q]
+    int64, positions [total_q] int32, used [1] int32: the free pages taken)."""
+    _expect([(q_lens, "q_lens", (None,))])
+    B = q_lens.shape[0]
+    _expect([(seq_lens, "seq_lens", (B,)), (block_tables, "block_tables", (B, None)),
+             (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
+    dev = block_tables.device
+    if cu_q_lens is None:
+        cu_q_lens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(total_q, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(total_q, dtype=torch.int32, device=dev)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=dev)
+    _expect([(cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
+             (positions, "positions", (total_q,)), (used, "used", (1,))])
+    i32 = torch.int32
+    a = dsa_page_plan_args(
+        B, int(total_q), int(page_size), block_tables.shape[1], 0 if prefix_pages is None else prefix_pages.shape[0],
+        free_pages.shape[0], _dev(q_lens, "q_lens", i32), _dev(seq_lens, "seq_lens", i32),
+        _dev(prefix_pages, "prefix_pages", i32), _dev(free_pages, "free_pages", i32),
+        _dev(block_tables, "block_tables", i32), _dev(cu_q_lens, "cu_q_lens", i32),
+        _dev(slot_mapping, "slot_mapping", torch.int64), _dev(positions, "positions", i32), _dev(used, "used", i32))
+    _check(lib().dsa_page_plan(ctypes.byref(a), _stream_ptr(stream)), "dsa_page_plan")
+    _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
+            stream)
+    return cu_q_lens, slot_mapping, positions, used
+
+
+def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16) -> int:
+    """Device pointer of a tensor whose last dimension is dense; the others may have any
+    strides that are multiples of 16 bytes."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return t.data_ptr()
+
+
+def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor, cache_c: torch.Tensor,
+                         cache_r: torch.Tensor, *, norm_weight: Optional[torch.Tensor] = None,
+                         norm_eps: float = 1e-6, rope_cos: Optional[torch.Tensor] = None,
+                         rope_sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                         rope_interleaved: bool = False, stream=None) -> None:
+    """This step's latent rows into the paged cache, in place: c_kv [n, 512] (root-mean-square
+    norm times norm_weight [512] fp32, when given) into cache_c [num_pages, page_size, 512]
+    and k_rope [n, 64] (turned by row positions[t] of rope_cos / rope_sin [rows, 32] fp32,
+    when given; row t without positions) into cache_r [num_pages, page_size, 64], at the slots
+    slot_mapping [n] (int64, page * page_size + row; negative = skip).  c_kv and k_rope may be
+    views of one [n, 576] projection output."""
+    _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (cache_c, "cache_c", (None, None, None))])
+    n, R = c_kv.shape
+    rd = k_rope.shape[1]
+    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
+    _expect([(k_rope, "k_rope", (n, rd)), (slot_mapping, "slot_mapping", (n,)),
+             (cache_c, "cache_c", (num_pages, page_size, R)), (cache_r, "cache_r", (num_pages, page_size, rd)),
+             (norm_weight, "norm_weight", (R,)), (rope_cos, "rope_cos", (None, rd // 2)),
+             (positions, "positions", (n,))])
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    rows = 0 if rope_cos is None else rope_cos.shape[0]
+    _expect([(rope_sin, "rope_sin", (rows, rd // 2))])
+    f32 = torch.float32
+    a = dsa_mla_cache_append_args(
+        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, float(norm_eps), _rows(c_kv, "c_kv"),
+        _rows(k_rope, "k_rope"), c_kv.stride(0), k_rope.stride(0), _dev(slot_mapping, "slot_mapping", torch.int64),
+        _dev(norm_weight, "norm_weight", f32), _dev(rope_cos, "rope_cos", f32), _dev(rope_sin, "rope_sin", f32),
+        _dev(positions, "positions", torch.int32), _dev(cache_c, "cache_c", torch.bfloat16),
+        _dev(cache_r, "cache_r", torch.bfloat16))
+    _check(lib().dsa_mla_cache_append(ctypes.byref(a), _stream_ptr(stream)), "dsa_mla_cache_append")
+    _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
+
+
+def make_prefix_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages=None, *,
+                         prefix_len: int, scale: float, out=None, lse=None, workspace=None):
+    """dsa_prefix_mla_args for these tensors (every shape checked); returns (args, kept
+    tensors, (out, lse)).  out, lse and the workspace are allocated when not given."""
+    _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
+             (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,))])
+    total_q, H, R = q_nope.shape
+    rd = q_rope.shape[2]
+    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
+    B = seq_lens.shape[0]
+    _expect([(q_rope, "q_rope", (total_q, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
+             (cache_r, "cache_r", (num_pages, page_size, rd)), (cu_q_lens, "cu_q_lens", (B + 1,)),
+             (block_tables, "block_tables", (B, None)), (prefix_pages, "prefix_pages", (None,))])
+    dev = q_nope.device
+    if out is None:
+        out = torch.empty((total_q, H, R), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+    _expect([(out, "out", (total_q, H, R)), (lse, "lse", (total_q, H))])
+    i32, bf16 = torch.int32, torch.bfloat16
+    a = dsa_prefix_mla_args(
+        B, total_q, H, R, rd, page_size, num_pages, block_tables.shape[1], int(prefix_len),
+        0 if prefix_pages is None else prefix_pages.shape[0], float(scale), _rows(q_nope, "q_nope"),
+        _rows(q_rope, "q_rope"), q_nope.stride(0), q_nope.stride(1), q_rope.stride(0), q_rope.stride(1),
+        _dev(cache_c, "cache_c", bf16), _dev(cache_r, "cache_r", bf16), _dev(prefix_pages, "prefix_pages", i32),
+        _dev(block_tables, "block_tables", i32), _dev(cu_q_lens, "cu_q_lens", i32), _dev(seq_lens, "seq_lens", i32),
+        _dev(out, "out", bf16), _dev(lse, "lse", torch.float32))
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check(lib().dsa_prefix_mla_workspace_size(ctypes.byref(a), ctypes.byref(n)), "dsa_prefix_mla_workspace_size")
+        workspace = torch.empty(max(n.value, 16), dtype=torch.uint8, device=dev)
+    a.workspace = _dev(workspace, "workspace")
+    a.workspace_bytes = workspace.numel() * workspace.element_size()
+    return a, (q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
+               workspace), (out, lse)
+
+
+def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages=None, *,
+                   prefix_len: int, scale: float, out=None, lse=None, workspace=None, stream=None):
+    """Latent attention of a batch whose sequences share their first prefix_len tokens (their
+    pages in prefix_pages; the rest through block_tables): (out [total_q, H, 512] bf16,
+    lse [total_q, H] fp32, the natural logarithm of the sum of exponentials).  q_nope and
+    q_rope may be views of one [total_q, H, 576] tensor."""
+    a, keep, res = make_prefix_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens,
+                                        prefix_pages, prefix_len=prefix_len, scale=scale, out=out, lse=lse,
+                                        workspace=workspace)
+    _check(lib().dsa_prefix_mla(ctypes.byref(a), _stream_ptr(stream)), "dsa_prefix_mla")
+    _record(keep, stream)
+    return res
 
 
 def dsa_test_arm_score_timeout(limit_ns: int) -> None:
