@@ -5,22 +5,26 @@
 //
 // Three launches.
 //
-// plan (one CTA): the (query, head) rows are cut into tiles of up to 64 rows, and every tile's
-// keys into blocks of 64.  A request of 64 rows or more fills tiles of its own, which walk the
-// prefix and then the request's keys.  Smaller requests (few heads, one query) share: tiles
-// packed across requests walk the prefix, further tiles, one request each, walk its own keys,
-// and the two are joined.  The blocks of all tiles stand in one line, cut into equal parts,
-// one per SM: a part may start and end inside a tile, so one long prefix fills every SM.
+// plan (one CTA): the (query, head) rows are cut into tiles of up to 128 rows, and every tile's
+// keys into blocks of 128.  A request of many rows fills tiles of its own, which walk the prefix
+// and then the request's keys.  Small requests (few heads, one query) share: tiles packed across
+// requests walk the prefix, further tiles, one request each, walk its own keys, and the two are
+// joined.  The blocks of all tiles stand in one line, cut into equal parts, one per pair of SMs:
+// a part may start and end inside a tile, so one long prefix fills every SM.
 //
-// attend (one CTA per SM): for each piece of a tile in its part
-//   warp 4      keys: one TMA box per page piece and 128-byte column, one lane a box, into a ring
-//               of two tiles of 64 keys (9 columns of 64 bf16, 128-byte swizzle);
-//   warps 5..7  the piece's query rows (16-byte cp.async, any strides);
-//   warp 8      TMEM; lane 0 issues  S [rows x 64 keys] = Q . K^T  (M = 128 lanes, 64 used) and
-//               O^T [512 x rows] += V^T . P^T (4 x M = 128, the key tile read MN-major), the next
-//               block's S ahead of this block's P . V;
-//   warps 0..3  softmax with a reference maximum that moves only when a block's maximum passes it
-//               by 8 (a factor 256), P as bf16, rescaling of O^T, and the piece's result.
+// attend (a cluster of two CTAs on two SMs per part, each holding 64 rows of a tile): the 512
+// latent sums of 64 rows fill half a TMEM, and the pair's 2-SM MMAs (M = 128) run at the full
+// rate of both, which one SM's MMAs on 64 rows cannot.  For each block of a piece of a tile:
+//   S [128 rows x 128 keys] = Q . K^T       each CTA stages its rows of Q and 64 of the keys
+//   O [128 rows x 512]     += P . V         each CTA stages its rows of P and, of all 128 keys,
+//                                           its half of the latent columns (MN-major)
+//   warp 4      keys of S (9 columns of 64 bf16, in three groups with barriers of their own);
+//   warp 5      keys of P . V (2 x 2 columns); both by TMA, one lane per page piece and column;
+//   warps 6, 7  the piece's query rows (16-byte cp.async, any strides);
+//   warp 8      TMEM; lane 0 of the even CTA issues the MMAs, whichever product has its inputs;
+//   warps 0..3  softmax.  A thread holds one row and one half: 64 of the block's keys, 256 of the
+//               row's latent sums (the row's halves meet in shared memory).  The reference maximum
+//               moves only when a block's maximum passes it by 8 (a factor 256).
 // A tile done in one piece is normalised and written; the others leave (O, m, l) in fp32.
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
@@ -40,15 +44,15 @@ namespace dsa {
 namespace {
 
 constexpr int kRank = 512, kRope = 64, kAtoms = 9;        // 576 = 9 columns of 64 bf16
-constexpr int kRows = 64;                                 // rows per tile
-constexpr int kKeys = 64;                                 // keys per block
-constexpr int kThreads = 288;                             // warps 0-3 softmax, 4 keys, 5-7 queries, 8 MMA
-constexpr uint32_t kAtomBytes = 64 * 128;                 // one column of 64 rows or keys
-constexpr uint32_t kTileBytes = kAtoms * kAtomBytes;      // 73728
-constexpr uint32_t kOffQ = 0, kOffTile = kTileBytes, kOffP = kOffTile + 2 * kTileBytes;
-constexpr uint32_t kOffMisc = kOffP + kRows * 128;        // P: 64 rows x 64 keys bf16
-constexpr size_t kSmem = kOffMisc + 1024;
-constexpr uint32_t kOCol0 = 2 * kKeys;                    // O^T behind the two S buffers
+constexpr int kRows = 128;                                // rows per tile, 64 in each CTA of a pair
+constexpr int kKeys = 128;                                // keys per block
+constexpr int kThreads = 288;                             // warps 0-3 softmax, 4 K, 5 V, 6-7 queries, 8 MMA
+constexpr uint32_t kAtomBytes = 64 * 128;                 // a column of 64 rows or keys
+constexpr uint32_t kKGroup = 3 * kAtomBytes, kVGroup = 2 * 128 * 128;
+constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtoms * kAtomBytes;
+constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
+constexpr size_t kSmem = kOffMisc + 2560;
+constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Tile {
@@ -62,7 +66,7 @@ struct Tile {
 struct Args {
   int B, total_q, H, page_size, num_pages, max_pages, prefix_len, num_prefix_pages;
   int packed;              // small requests: prefix tiles packed across requests
-  int max_tiles, G;        // tiles there is room for; CTAs (parts)
+  int max_tiles, G;        // tiles there is room for; CTA pairs
   int past_row;            // a row coordinate past the cache: copies from there are zeros
   float scale_log2;        // scale * log2(e)
   const __nv_bfloat16 *qn, *qr;
@@ -77,8 +81,15 @@ struct Args {
   unsigned* status;
 };
 
+// Barriers of a CTA.  L: the even CTA's, waited for by the issuer; the others are waited for in
+// each CTA and completed by the issuer's commits in both.
 struct Bars {
-  uint64_t qfull, qempty, tfull[2], tempty[2], sfull[2], sempty[2], pfull, ofree, done;
+  uint64_t qfull, qempty;        // L: 2 query warps of each CTA
+  uint64_t kfull[3], kempty[3];  // L: each CTA's copies
+  uint64_t vfull[2], vempty[2];  // L
+  uint64_t vown[2];              // this CTA's copies of a block with rows to clear
+  uint64_t sfull[2], sempty[2];  // sempty L: 4 softmax warps of each CTA
+  uint64_t pfull, ofree, done;   // pfull, done L
 };
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
   if (bad) atomicOr(a.status, kStatusUncovered);
 }
 
-// The line of U blocks in G = min(CTAs, U) parts, none of them empty: part c is
+// The line of U blocks in G = min(CTA pairs, U) parts, none of them empty: part c is
 // [c U / G, (c + 1) U / G).
 __device__ __forceinline__ int parts(const Args& a, long long U) {
   return static_cast<int>(min(static_cast<long long>(a.G), U));
@@ -241,40 +252,103 @@ __device__ __forceinline__ int find_tile(const long long* u0, int n, long long u
 }
 
 // ------------------------------------------------------------------ attend
-__global__ void __launch_bounds__(kThreads, 1) prefix_mla_kernel(const __grid_constant__ CUtensorMap tmap_c,
-                                                                  const __grid_constant__ CUtensorMap tmap_r,
-                                                                  const Args a) {
+// The part's pieces: tile i, its blocks [k0, k1).  Every role walks the same list.
+struct Piece {
+  int i, k0, k1;
+  long long u;   // first block of the piece in the line
+};
+__device__ __forceinline__ bool next_piece(const Args& a, Piece& p, long long u, long long u_hi, Tile& t) {
+  if (u >= u_hi) return false;
+  long long b0 = __ldcg(a.u0 + p.i), b1 = __ldcg(a.u0 + p.i + 1);
+  while (b1 <= u) {  // tiles without blocks, and the one just done
+    ++p.i;
+    b0 = b1;
+    b1 = __ldcg(a.u0 + p.i + 1);
+  }
+  p.u = u;
+  p.k0 = static_cast<int>(u - b0);
+  p.k1 = static_cast<int>(min(b1, u_hi) - b0);
+  const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
+  t.row0 = w.x;
+  t.nrows = w.y;
+  t.b = w.z;
+  t.n_pre = w.w;
+  t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
+  return true;
+}
+
+// Block k of a tile: its first position, and the positions [lo, hi) of it that the tile sees.
+struct Block {
+  int s0, lo, hi;
+  bool pre;
+};
+__device__ __forceinline__ Block block_at(const Args& a, const Tile& t, int k) {
+  Block b;
+  b.pre = k < t.n_pre;
+  b.s0 = (b.pre ? k : k - t.n_pre + a.prefix_len / kKeys) * kKeys;
+  b.lo = b.pre ? 0 : a.prefix_len;
+  b.hi = b.pre ? min(t.limit, a.prefix_len) : t.limit;
+  return b;
+}
+// Cache row of position s (a multiple of the box) of a block, for a copy of `box` rows from
+// there: past_row (zeros) when the tile sees none of them, or the page is not there (*bad).
+__device__ __forceinline__ int cache_row(const Args& a, const Tile& t, const Block& b, int s, int box, bool* bad) {
+  if (s >= b.hi || s + box <= b.lo) return a.past_row;
+  const int j = s / a.page_size;
+  int pg = -1;
+  if (b.pre) {
+    if (j < a.num_prefix_pages) pg = __ldg(a.prefix_pages + j);
+  } else if (j < a.max_pages) {
+    pg = __ldg(a.block_tables + static_cast<long long>(t.b) * a.max_pages + j);
+  }
+  if (pg < 0 || pg >= a.num_pages) {
+    *bad = true;
+    return a.past_row;
+  }
+  return pg * a.page_size + (s & (a.page_size - 1));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_mla_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r,
+                      const Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in both CTAs, so both return together
   if ((ptx::smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(a.status, kStatusSmemAlign);
     return;
   }
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffMisc);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc + 128);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 132);
-  volatile int* first_tile = reinterpret_cast<volatile int*>(smem + kOffMisc + 136);
-  volatile unsigned* kmask = reinterpret_cast<volatile unsigned*>(smem + kOffMisc + 144);  // [2] 16-key pieces there
-  float* corr = reinterpret_cast<float*>(smem + kOffMisc + 256);                          // [64]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 260);
+  volatile int* first_tile = reinterpret_cast<volatile int*>(smem + kOffMisc + 264);
+  float* xmax = reinterpret_cast<float*>(smem + kOffMisc + 512);   // [2][2][64] by block parity, half, row
+  float* xsum = reinterpret_cast<float*>(smem + kOffMisc + 1536);  // [2][64]
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(&bars->qfull, 96);
+    ptx::mbar_init(&bars->qfull, 4);
     ptx::mbar_init(&bars->qempty, 1);
-    for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&bars->tfull[s], 1);
-      ptx::mbar_init(&bars->tempty[s], 1);
-      ptx::mbar_init(&bars->sfull[s], 1);
-      ptx::mbar_init(&bars->sempty[s], 2);   // the two row warps
+    for (int g = 0; g < 3; ++g) {
+      ptx::mbar_init(&bars->kfull[g], 2);
+      ptx::mbar_init(&bars->kempty[g], 1);
     }
-    ptx::mbar_init(&bars->pfull, 4);
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(&bars->vfull[g], 2);
+      ptx::mbar_init(&bars->vempty[g], 1);
+      ptx::mbar_init(&bars->vown[g], 1);
+      ptx::mbar_init(&bars->sfull[g], 1);
+      ptx::mbar_init(&bars->sempty[g], 8);
+    }
+    ptx::mbar_init(&bars->pfull, 8);
     ptx::mbar_init(&bars->ofree, 1);
     ptx::mbar_init(&bars->done, 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 8) {
-    ptx::tmem_alloc(tmem_holder, 512);
-    ptx::tmem_relinquish();
+    ptx::tmem_alloc_pair(tmem_holder, 512);
+    ptx::tmem_relinquish_pair();
   }
   if (warp == 4 && lane == 0) {
     ptx::prefetch_tmap(&tmap_c);
@@ -284,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mla_kernel(const __grid_co
   ptx::grid_dep_launch();
   const int n_tiles = __ldcg(a.head);
   const long long U = __ldcg(a.u0 + n_tiles);
-  const int c = blockIdx.x, G = parts(a, U);
+  const int c = blockIdx.x >> 1, G = parts(a, U);
   const long long u_lo = c < G ? part_begin(U, G, c) : 0, u_hi = c < G ? part_begin(U, G, c + 1) : 0;
   if (warp == 0 && u_lo < u_hi) {
     const int i = find_tile(a.u0, n_tiles, u_lo);
@@ -292,96 +366,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mla_kernel(const __grid_co
   }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int i_first = u_lo < u_hi ? *first_tile : 0;
-  const int kO = a.prefix_len / kKeys;
-
-  // The part's pieces: tile i, its blocks [k0, k1).  Every role walks the same list.
-  struct Piece {
-    int i, k0, k1;
-    long long u;   // first block of the piece in the line
-  };
-  auto next_piece = [&](Piece& p, long long u, Tile& t) -> bool {
-    if (u >= u_hi) return false;
-    long long b0 = __ldcg(a.u0 + p.i), b1 = __ldcg(a.u0 + p.i + 1);
-    while (b1 <= u) {  // tiles without blocks, and the one just done
-      ++p.i;
-      b0 = b1;
-      b1 = __ldcg(a.u0 + p.i + 1);
-    }
-    p.u = u;
-    p.k0 = static_cast<int>(u - b0);
-    p.k1 = static_cast<int>(min(b1, u_hi) - b0);
-    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
-    t.row0 = w.x;
-    t.nrows = w.y;
-    t.b = w.z;
-    t.n_pre = w.w;
-    t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
-    return true;
-  };
+  const int box = min(a.page_size, 64);  // rows of one copy
+  const int box_log2 = 31 - __clz(box);
+  Piece p{i_first, 0, 0, 0};
+  Tile t;
 
   if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
       const uint32_t sbase = ptx::smem_u32(smem);
-      const uint32_t id1 = ptx::idesc_f32acc(128, kKeys, true);        // S: 128 lanes (64 rows) x 64 keys
+      const uint32_t id1 = ptx::idesc_f32acc(128, kKeys, true);
+      const uint32_t id2 = ptx::idesc_f32acc_bf16_bmn(128, 256);
+      const uint64_t q0 = ptx::sw128_kmajor_desc(sbase + kOffQ), k0 = ptx::sw128_kmajor_desc(sbase + kOffK);
+      const uint64_t p0 = ptx::sw128_kmajor_desc(sbase + kOffP);
+      const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + kOffV, 128 * 128);
       bool ok = true;
-      uint32_t n1 = 0, n2 = 0;  // blocks whose S / P . V was issued, over all pieces
+      uint32_t n1 = 0, n2 = 0, g1 = 0, g2 = 0;  // blocks (and groups of the next) issued, over all pieces
       uint32_t seg = 0;
-      Piece p{i_first, 0, 0, 0};
-      Tile t;
-      uint64_t t0 = ptx::globaltimer();
-      for (long long u = u_lo; ok && next_piece(p, u, t); u = p.u + (p.k1 - p.k0), ++seg) {
-        const uint32_t id2 = ptx::idesc_f32acc_bf16_amn(128, (t.nrows + 15) / 16 * 16);  // O^T: 128 latent x rows
-        if (!ptx::mbar_wait(&bars->qfull, seg & 1, abort, a.status, kStatusTimeout)) {
+      for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
+        if (!ptx::mbar_wait_cluster(&bars->qfull, seg & 1, abort, a.status, kStatusTimeout)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t s_begin = n1, s_end = n1 + (p.k1 - p.k0);
-        // Issue whichever product has its inputs first: the next block's S or this block's P . V.
-        t0 = ptx::globaltimer();
+        uint64_t t0 = ptx::globaltimer();
         for (uint32_t spin = 0; ok && n2 < s_end; ++spin) {
           bool progress = false;
-          if (n1 < s_end && n1 <= n2 + 1 && ptx::mbar_try_wait(&bars->tfull[n1 & 1], (n1 >> 1) & 1) &&
-              ptx::mbar_try_wait(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1)) {
+          if (n2 < n1 && (g2 > 0 || ptx::mbar_test_wait_cluster(&bars->pfull, n2 & 1)) &&
+              ptx::mbar_test_wait_cluster(&bars->vfull[g2], n2 & 1)) {
             ptx::tc_fence_after();
-            const int tb = n1 & 1;
-            const uint32_t d = tmem_base + tb * kKeys;
-            const uint64_t ad0 = ptx::sw128_kmajor_desc(sbase + kOffQ);
-            const uint64_t bd0 = ptx::sw128_kmajor_desc(sbase + kOffTile + tb * kTileBytes);
+            const uint64_t v = v0 + g2 * (kVGroup >> 4);
+            const uint32_t d = tmem_base + kOCol0 + g2 * 128;
 #pragma unroll
-            for (int j = 0; j < kAtoms * 4; ++j) {
-              const uint64_t off = ((j >> 2) * kAtomBytes + (j & 3) * 32) >> 4;
-              ptx::mma_bf16(d, ad0 + off, bd0 + off, id1, j > 0 ? 1u : 0u);
+            for (int s = 0; s < 8; ++s)  // 16 keys per MMA: two 8-key groups of 1024 bytes
+              ptx::mma_bf16_pair(d, p0 + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4), v + ((s * 2048) >> 4), id2,
+                                 (n2 > s_begin || s > 0) ? 1u : 0u);
+            ptx::mma_commit_pair(&bars->vempty[g2], 3);
+            if (++g2 == 2) {
+              ptx::mma_commit_pair(&bars->ofree, 3);
+              g2 = 0;
+              ++n2;
             }
-            ptx::mma_commit(&bars->sfull[tb]);
-            if (n1 + 1 == s_end) ptx::mma_commit(&bars->qempty);
-            ++n1;
             progress = true;
           }
-          if (n2 < n1 && ptx::mbar_try_wait(&bars->pfull, n2 & 1)) {
+          if (n1 < s_end && n1 <= n2 + 1 &&
+              (g1 > 0 || ptx::mbar_test_wait_cluster(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1)) &&
+              ptx::mbar_test_wait_cluster(&bars->kfull[g1], n1 & 1)) {
             ptx::tc_fence_after();
-            const int tb = n2 & 1;
-            const uint64_t ad0 = ptx::sw128_mnmajor_desc(sbase + kOffTile + tb * kTileBytes, kAtomBytes);
-            const uint64_t bd0 = ptx::sw128_kmajor_desc(sbase + kOffP);
+            const uint32_t d = tmem_base + (n1 & 1) * 64;
+            const uint64_t go = g1 * (kKGroup >> 4);
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {  // latent 128 cc .. + 127: columns 2 cc and 2 cc + 1
-#pragma unroll
-              for (int s = 0; s < 4; ++s)     // 16 keys per MMA: two 8-key groups of 1024 bytes
-                ptx::mma_bf16(tmem_base + kOCol0 + cc * kRows, ad0 + ((2 * cc * kAtomBytes + s * 2048) >> 4),
-                              bd0 + 2 * s, id2, (n2 > s_begin || s > 0) ? 1u : 0u);
+            for (int s = 0; s < 12; ++s) {  // 16 values of K per MMA, four in a column
+              const uint64_t off = go + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4);
+              ptx::mma_bf16_pair(d, q0 + off, k0 + off, id1, (g1 > 0 || s > 0) ? 1u : 0u);
             }
-            ptx::mma_commit(&bars->tempty[tb]);
-            ptx::mma_commit(&bars->ofree);
-            ++n2;
+            ptx::mma_commit_pair(&bars->kempty[g1], 3);
+            if (++g1 == 3) {
+              ptx::mma_commit_pair(&bars->sfull[n1 & 1], 3);
+              g1 = 0;
+              if (++n1 == s_end) ptx::mma_commit_pair(&bars->qempty, 3);
+            }
             progress = true;
           }
           if (progress) {
             t0 = ptx::globaltimer();
-          } else if ((spin & 15u) == 15u) {
+          } else if ((spin & 63u) == 63u) {
             if (*abort) ok = false;
             else if (ptx::globaltimer() - t0 > 2000000000ull) {
               *abort = 1;
@@ -391,83 +445,119 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mla_kernel(const __grid_co
           }
         }
       }
-      ptx::mma_commit(&bars->done);
-      ptx::mbar_wait_drain(&bars->done, 0, a.status, kStatusTimeout, 200000000ull);
+      ptx::mma_commit_pair(&bars->done, 1);
+      ptx::mbar_wait_cluster_drain(&bars->done, 0, a.status, kStatusTimeout, 200000000ull);
     }
     __syncwarp();
   } else if (warp == 4) {
-    // ------------------------------------------------------------ keys
-    const int box = min(a.page_size, kKeys), per = kKeys / box;  // boxes per column
+    // ------------------------------------------------------------ keys of S: this CTA's 64 of a block
+    const int per = 64 / box;
     uint32_t n = 0;
     bool ok = true;
-    Piece p{i_first, 0, 0, 0};
-    Tile t;
-    uint32_t issued = 0;
-    for (long long u = u_lo; ok && next_piece(p, u, t); u = p.u + (p.k1 - p.k0)) {
-      const int32_t* own = a.block_tables + static_cast<long long>(max(t.b, 0)) * a.max_pages;
-      for (int k = p.k0; k < p.k1; ++k, ++n) {
-        const bool pre = k < t.n_pre;
-        const int s0 = (pre ? k : k - t.n_pre + kO) * kKeys;  // first position of the block
-        // lane j < per: the page of keys [s0 + j box, + box)
-        const int lo = pre ? 0 : a.prefix_len, hi = pre ? min(t.limit, a.prefix_len) : t.limit;
-        const int sj = s0 + (lane & (per - 1)) * box;
-        const int pj = sj / a.page_size;
-        const bool want = sj < hi && sj + box > lo;  // some row of the tile may see a key here
-        int pg = -1;
-        if (want) pg = pre ? (pj < a.num_prefix_pages ? __ldg(a.prefix_pages + pj) : -1)
-                           : (pj < a.max_pages ? __ldg(own + pj) : -1);
-        const bool there = want && pg >= 0 && pg < a.num_pages;
-        if (want && !there) atomicOr(a.status, kStatusBadPage);
-        // a page that is not there: a row past the cache, which the copy fills with zeros
-        const int row = there ? pg * a.page_size + (sj & (a.page_size - 1)) : a.past_row;
-        const unsigned m = __ballot_sync(0xffffffffu, there) & ((1u << per) - 1u);
-        const int st = n & 1;
-        int good = 1;
-        if (lane == 0) good = ptx::mbar_wait(&bars->tempty[st], ((n >> 1) & 1) ^ 1, abort, a.status, kStatusTimeout);
-        good = __shfl_sync(0xffffffffu, good, 0);
-        if (!good) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          kmask[st] = m;
-          ptx::mbar_arrive_expect_tx(&bars->tfull[st], kTileBytes);
-        }
-        __syncwarp();
-        uint8_t* tile = smem + kOffTile + st * kTileBytes;
-        for (int e0 = 0; e0 < kAtoms * per; e0 += 32) {
-          const int e = e0 + lane;
-          const int j = e & (per - 1), at = e / per;
-          const int r = __shfl_sync(0xffffffffu, row, j);
-          if (at < kAtoms) {
-            uint8_t* dst = tile + at * kAtomBytes + j * box * 128;
-            if (at < 8) ptx::tma_load_2d(dst, &tmap_c, &bars->tfull[st], at * 64, r);
-            else ptx::tma_load_2d(dst, &tmap_r, &bars->tfull[st], 0, r);
+    for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
+        const Block b = block_at(a, t, k);
+        bool bad = false;
+        const int row = cache_row(a, t, b, b.s0 + rank * 64 + (lane & (per - 1)) * box, box, &bad);
+        if (bad) atomicOr(a.status, kStatusBadPage);
+        const int at = lane / per, j = lane & (per - 1);  // column of the group, box of the column
+        for (int g = 0; g < 3; ++g) {
+          int good = 1;
+          if (lane == 0)
+            good = ptx::mbar_wait_cluster(&bars->kempty[g], (n & 1) ^ 1, abort, a.status, kStatusTimeout);
+          good = __shfl_sync(0xffffffffu, good, 0);
+          if (!good) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
+          if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
+          __syncwarp();
+          if (at < 3) {
+            uint8_t* dst = smem + kOffK + (3 * g + at) * kAtomBytes + j * box * 128;
+            if (3 * g + at < 8) ptx::tma_load_2d_pair(dst, &tmap_c, full, (3 * g + at) * 64, row);
+            else ptx::tma_load_2d_pair(dst, &tmap_r, full, 0, row);
           }
         }
-        ++issued;
       }
     }
-    // every copy lands before the CTA can exit, whatever happened
-    if (lane == 0) {
-      for (uint32_t q = issued > 2 ? issued - 2 : 0; q < issued; ++q)
-        ptx::mbar_wait_drain(&bars->tfull[q & 1], (q >> 1) & 1, a.status, kStatusTimeout, 200000000ull);
-    }
+    // every copy lands before the pair can exit, whatever happened
+    if (rank == 0 && lane == 0 && n > 0 && !ok)
+      for (int g = 0; g < 3; ++g)
+        ptx::mbar_wait_cluster_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
     __syncwarp();
-  } else if (warp > 4) {
-    // ------------------------------------------------------------ queries (96 threads)
-    const int gt = threadIdx.x - 160;
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ keys of P . V: 256 latent columns of all 128
+    const int per = 128 / box;
+    uint32_t n = 0, cleared = 0;
+    bool ok = true;
+    for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
+        const Block b = block_at(a, t, k);
+        bool bad = false;
+        const int row = cache_row(a, t, b, b.s0 + (lane & (per - 1)) * box, box, &bad);
+        const int at = lane / per, j = lane & (per - 1);
+        // rows that no row of this tile sees may hold anything: their weights are 0, and the
+        // values are cleared so that the products are
+        const bool clear = b.s0 < b.lo || b.s0 + kKeys > b.hi;
+        for (int g = 0; g < 2; ++g) {
+          int good = 1;
+          if (lane == 0)
+            good = ptx::mbar_wait_cluster(&bars->vempty[g], (n & 1) ^ 1, abort, a.status, kStatusTimeout);
+          good = __shfl_sync(0xffffffffu, good, 0);
+          if (!good) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
+          uint8_t* base = smem + kOffV + g * kVGroup;
+          if (lane == 0) {
+            if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
+            else ptx::mbar_arrive_expect_tx_cluster(full, kVGroup);
+          }
+          __syncwarp();
+          if (at < 2) {
+            uint8_t* dst = base + at * (128 * 128) + j * box * 128;
+            const int x = rank * 256 + (2 * g + at) * 64;
+            if (clear) ptx::tma_load_2d(dst, &tmap_c, &bars->vown[g], x, row);
+            else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
+          }
+          if (clear) {
+            good = ptx::mbar_wait_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout, 2000000000ull);
+            if (!__all_sync(0xffffffffu, good != 0)) {
+              ok = false;
+              break;
+            }
+            for (int e = lane; e < 2 * 128 * 8; e += 32) {  // column, row, 16-byte chunk
+              const int key = (e >> 3) & 127;
+              if (b.s0 + key < b.lo || b.s0 + key >= b.hi)
+                *reinterpret_cast<uint4*>(base + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(full);
+          }
+        }
+        if (clear) ++cleared;
+      }
+    }
+    if (rank == 0 && lane == 0 && n > 0 && !ok)
+      for (int g = 0; g < 2; ++g)
+        ptx::mbar_wait_cluster_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
+    __syncwarp();
+  } else if (warp > 5) {
+    // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
+    const int gt = threadIdx.x - 192;
+    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
     uint32_t seg = 0;
-    Piece p{i_first, 0, 0, 0};
-    Tile t;
-    for (long long u = u_lo; next_piece(p, u, t); u = p.u + (p.k1 - p.k0), ++seg) {
-      const bool good = ptx::mbar_wait(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
-      if (!good) break;
-      for (int e = gt; e < kRows * 72; e += 96) {
+    for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
+      const bool good = ptx::mbar_wait_cluster(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
+      if (!__all_sync(0xffffffffu, good)) break;
+      for (int e = gt; e < 64 * 72; e += 64) {
         const int r = e / 72, ch = e - r * 72;
         const int at = ch >> 3, c16 = ch & 7;
-        const bool live = r < t.nrows;
-        const int row = t.row0 + (live ? r : 0);
+        const bool live = rank * 64 + r < t.nrows;
+        const int row = t.row0 + (live ? rank * 64 + r : 0);
         const int tq = row / a.H, h = row - tq * a.H;
         const __nv_bfloat16* src = at < 8 ? a.qn + tq * a.qn_t + h * a.qn_h + at * 64 + c16 * 8
                                           : a.qr + tq * a.qr_t + h * a.qr_h + c16 * 8;
@@ -475,193 +565,180 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mla_kernel(const __grid_co
       }
       cp_async_wait_all();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&bars->qfull);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(full);
     }
   } else {
     // ------------------------------------------------------------ softmax, rescale, output (warps 0..3)
-    const int h = threadIdx.x;                  // row of the tile (warps 0, 1) / latent lane within a chunk
+    const int row = (warp & 1) * 32 + lane, half = warp >> 1;  // TMEM lane = 64 half + row
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const bool row_lane = warp < 2;
+    const uint32_t pair_bar = 2 + (warp & 1);                  // warps w and w + 2: the halves of the same rows
+    const int per = 64 / box;
+    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->pfull), 0);
+    const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&bars->sempty[0]), 0);
     bool ok = true;
     uint32_t n = 0;
-    Piece p{i_first, 0, 0, 0};
-    Tile t;
-    for (long long u = u_lo; next_piece(p, u, t); u = p.u + (p.k1 - p.k0)) {
-      float m = -INFINITY, l = 0.f;
-      int lim = 0;  // keys this row sees
-      if (row_lane && h < t.nrows) {
-        const int tq = (t.row0 + h) / a.H;
+    for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+      float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this half's sum
+      int lim = 0;                   // keys this row sees
+      const int trow = rank * 64 + row;
+      if (trow < t.nrows) {
+        const int tq = (t.row0 + trow) / a.H;
         bool bad = false;
         lim = min(sees(a, t.b >= 0 ? t.b : request_of(a, tq), tq, &bad), t.limit);
       }
-      const int nr32 = (t.nrows + 31) / 32 * 32;
-      if (threadIdx.x < 64) corr[threadIdx.x] = 1.f;
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const int tb = n & 1;
-        const bool pre = k < t.n_pre;
-        const int s0 = (pre ? k : k - t.n_pre + kO) * kKeys;
-        const int klo = pre ? 0 : a.prefix_len, khi = pre ? min(t.limit, a.prefix_len) : t.limit;
-        float cr = 1.f;
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
-                                                            kStatusTimeout)) != 0;
-        // the copies have landed (S was computed from them); the wait orders kmask as well
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->tfull[tb], (n >> 1) & 1, abort, a.status,
-                                                            kStatusTimeout)) != 0;
-        if (ok && (s0 < klo || s0 + kKeys > khi)) {
-          // rows of the key tile that no row of this tile sees may hold anything: their weights
-          // are 0, and the values become 0 so that the product is
-          for (int e = threadIdx.x; e < kKeys * 64; e += 128) {
-            const int key = e >> 6, ch = e & 63;
-            if (s0 + key < klo || s0 + key >= khi)
-              *reinterpret_cast<uint4*>(smem + kOffTile + tb * kTileBytes + (ch >> 3) * kAtomBytes + key * 128 +
-                                        ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          ptx::fence_proxy_async_smem();
-        }
-        if (row_lane) {
-          if (ok) {
-            ptx::tc_fence_after();
-            uint32_t x0[32], x1[32];
-            ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * kKeys, x0);
-            ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * kKeys + 32, x1);
-            ptx::tmem_ld_wait_regs(x0);
-            ptx::tmem_ld_wait_regs(x1);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->sempty[tb]);
-            float x[64];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = __uint_as_float(x0[i]) * a.scale_log2;
-              x[32 + i] = __uint_as_float(x1[i]) * a.scale_log2;
-            }
-            const int box = min(a.page_size, kKeys), per = kKeys / box;
-            const unsigned km = kmask[tb];
-            const int end = min(khi, lim);
-            if (s0 < klo || s0 + kKeys > end || km != (1u << per) - 1u) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                const int s = s0 + i;
-                const bool v = s >= klo && s < end && ((km >> (i / box)) & 1u);
-                x[i] = v ? x[i] : -INFINITY;
-              }
-            }
-            float mb = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) mb = fmaxf(mb, x[i]);
-            // The reference maximum moves only when the block's maximum exceeds it by more
-            // than 8 (a factor 256 in probability): p stays below 256 and the output, which
-            // divides by the sum taken against the same reference, is unchanged.
-            float mn = m;
-            if (m == -INFINITY) mn = mb;
-            else if (mb > m + 8.f) mn = mb;
-            cr = (m == -INFINITY || mn == m) ? 1.f : exp2f(m - mn);
-            float ls = 0.f;
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float p0 = mn == -INFINITY ? 0.f : exp2f(x[2 * i] - mn);
-              const float p1 = mn == -INFINITY ? 0.f : exp2f(x[2 * i + 1] - mn);
-              ls += p0 + p1;
-              const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&pb);
-            }
-            l = l * cr + ls;
-            m = mn;
-            // P is free once the previous block's P . V has completed
-            if (n > 0)
-              ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
-                                                          kStatusTimeout)) != 0;
-            if (ok) {
-              uint8_t* prow = smem + kOffP + h * 128;
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4*>(prow + ((q ^ (h & 7)) << 4)) =
-                    make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-              corr[h] = cr;
-            }
-            ptx::fence_proxy_async_smem();
-          }
-        } else if (n > 0 && ok) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status, kStatusTimeout)) != 0;
-        }
-        // P and the correction factors are written; does any row need its output rescaled?
-        uint32_t any;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.f32 q, %1, 0f3F800000;\n\t"
-                     "bar.red.or.pred p, 2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(any) : "f"(cr) : "memory");
-        if (any && k > p.k0 && ok && !*abort) {
+        const Block b = block_at(a, t, k);
+        const int s0 = b.s0 + half * 64;  // this thread's 64 keys
+        bool bad = false;
+        const int crow = cache_row(a, t, b, s0 + (lane & (per - 1)) * box, box, &bad);
+        const unsigned there = __ballot_sync(0xffffffffu, crow != a.past_row);
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
+                                                                    kStatusTimeout)) != 0;
+        float x[64];
+        float mb = -INFINITY;
+        if (ok) {
           ptx::tc_fence_after();
-          for (int cc = 0; cc < 4; ++cc) {
-            const uint32_t col = tmem_base + lane_addr + kOCol0 + cc * kRows;
-            for (int h0 = 0; h0 < nr32; h0 += 32) {
+          uint32_t x0[32], x1[32];
+          ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * 64, x0);
+          ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * 64 + 32, x1);
+          ptx::tmem_ld_wait_regs(x0);
+          ptx::tmem_ld_wait_regs(x1);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(empty0 + tb * 8);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] = __uint_as_float(x0[i]);
+            x[32 + i] = __uint_as_float(x1[i]);
+          }
+          const int end = min(b.hi, lim);
+          const unsigned all = (1u << per) - 1u;
+          if (s0 < b.lo || s0 + 64 > end || (there & all) != all) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const int s = s0 + i;
+              const bool v = s >= b.lo && s < end && ((there >> (i >> box_log2)) & 1u);
+              x[i] = v ? x[i] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 64; ++i) mb = fmaxf(mb, x[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = -INFINITY;
+        }
+        // the row's block maximum over both halves
+        float* xm = xmax + tb * 128;
+        xm[half * 64 + row] = mb;
+        ptx::named_bar_sync(pair_bar, 64);
+        mb = fmaxf(mb, xm[(half ^ 1) * 64 + row]) * a.scale_log2;
+        // The reference maximum moves only when the block's maximum exceeds it by more than 8
+        // (a factor 256 in probability): p stays below 256 and the output, which divides by
+        // the sum taken against the same reference, is unchanged.
+        float mn = m;
+        if (m == -INFINITY || mb > m + 8.f) mn = mb;
+        const float cr = (m == -INFINITY || mn == m) ? 1.f : ptx::ex2(m - mn);
+        const float off = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every x is -inf, p = 0
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float p0 = ptx::ex2(fmaf(x[2 * i], a.scale_log2, -off));
+          const float p1 = ptx::ex2(fmaf(x[2 * i + 1], a.scale_log2, -off));
+          ls[(2 * i) & 3] += p0;
+          ls[(2 * i + 1) & 3] += p1;
+          const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+          pk[i] = *reinterpret_cast<const uint32_t*>(&pb);
+        }
+        l = l * cr + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+        m = mn;
+        // P and O are free once the previous block's P . V has completed
+        if (n > 0 && ok)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->ofree, (n - 1) & 1, abort, a.status,
+                                                              kStatusTimeout)) != 0;
+        if (ok) {
+          // row of P: this half's 64 keys = 8 chunks of 16 bytes, swizzled by the row
+          uint8_t* prow = smem + kOffP + half * kAtomBytes + row * 128;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(prow + ((q ^ (row & 7)) << 4)) =
+                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          ptx::fence_proxy_async_smem();
+          if (k > p.k0 && __any_sync(0xffffffffu, cr != 1.f)) {
+            ptx::tc_fence_after();
+            for (int q = 0; q < 8; ++q) {
               uint32_t r[32];
-              ptx::tmem_ld_32x32b_x32(col + h0, r);
+              ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
               ptx::tmem_ld_wait_regs(r);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr[h0 + i]);
-              ptx::tmem_st_32x32b_x32(col + h0, r);
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * cr);
+              ptx::tmem_st_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
             }
+            ptx::tmem_st_wait();
           }
-          ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
-        if (any) ptx::named_bar_sync(2, 128);  // corr is read by everyone before the next block rewrites it
-        if (lane == 0) ptx::mbar_arrive(&bars->pfull);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(full);
       }
       // the piece's result
       const bool at_start = p.k0 == 0;
       const bool whole = at_start && p.u + (p.k1 - p.k0) == __ldcg(a.u0 + p.i + 1);
       const bool direct = whole && !a.packed;
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
-                                                          kStatusTimeout)) != 0;
-      ptx::named_bar_sync(2, 128);  // corr was read for the last time
-      const long long slot = piece_slot(a.G, c, p.i, at_start, whole) * kRows;
-      if (row_lane && h < t.nrows) {
-        corr[h] = l > 0.f ? 1.f / l : 0.f;
-        if (direct) {
-          if (a.lse) a.lse[t.row0 + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        } else {
-          *reinterpret_cast<float2*>(a.part_ml + (slot + h) * 2) = make_float2(m, l);
-        }
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->ofree, (n - 1) & 1, abort, a.status,
+                                                                  kStatusTimeout)) != 0;
+      xsum[half * 64 + row] = l;
+      ptx::named_bar_sync(pair_bar, 64);
+      l += xsum[(half ^ 1) * 64 + row];
+      ptx::named_bar_sync(pair_bar, 64);  // read before the next piece writes them
+      const bool live = trow < t.nrows && ok;
+      const long long prow = piece_slot(a.G, c, p.i, at_start, whole) * kRows + trow;
+      if (live && half == 0) {
+        if (!direct) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m, l);
+        else if (a.lse) a.lse[t.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
-      ptx::named_bar_sync(2, 128);
-      if (ok) {
-        ptx::tc_fence_after();
-        for (int cc = 0; cc < 4; ++cc) {
-          const int lat = cc * 128 + warp * 32 + lane;
-          for (int h0 = 0; h0 < nr32; h0 += 32) {
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + cc * kRows + h0, r);
-            ptx::tmem_ld_wait_regs(r);
-            if (direct) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      ptx::tc_fence_after();
+      for (int q = 0; q < 8; ++q) {
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
+        ptx::tmem_ld_wait_regs(r);
+        const int lat = half * 256 + q * 32;
+        if (live && direct) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (t.row0 + trow) * static_cast<long long>(kRank) + lat);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (h0 + i < t.nrows)
-                  a.out[(t.row0 + h0 + i) * static_cast<long long>(kRank) + lat] =
-                      __float2bfloat16_rn(__uint_as_float(r[i]) * corr[h0 + i]);
-            } else {
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (h0 + i < t.nrows) a.part_o[(slot + h0 + i) * kRank + lat] = __uint_as_float(r[i]);
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]) * inv,
+                                                             __uint_as_float(r[8 * i + 2 * j + 1]) * inv);
+              w[j] = *reinterpret_cast<const uint32_t*>(&v);
             }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * kRank + lat);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
         }
-        ptx::tc_fence_before();
       }
-      ptx::named_bar_sync(2, 128);  // corr and O^T are read before the next piece writes them
+      ptx::tc_fence_before();
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();  // no CTA leaves while its peer may still touch its memory, barriers or TMEM
   if (warp == 8) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, 512);
+    ptx::tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
 // ------------------------------------------------------------------ join
-// A CTA takes rows_per rows of a group of 64 (a packed prefix tile, or a tile); a thread four
+// A CTA takes rows_per rows of a group of 128 (a packed prefix tile, or a tile); a thread four
 // latent values.
 __global__ void __launch_bounds__(128) prefix_mla_join_kernel(const Args a, int rows_per) {
   ptx::grid_dep_wait();
@@ -752,13 +829,30 @@ bool key_map(CUtensorMap* m, const void* base, long long rows, int cols, int box
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
+// CTA pairs that run at once (one per two SMs, less where a cluster does not fit), per device.
+int pair_count() {
   int dev = 0;
   static int cached[64] = {};
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 76;
   if (cached[dev] == 0) {
     int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(prefix_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, prefix_mla_kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 76;
+    }
     cached[dev] = n;
   }
   return cached[dev];
@@ -787,11 +881,11 @@ struct Layout {
 Layout layout(const dsa_prefix_mla_args* a) {
   Layout p{};
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  // Requests of few rows share prefix tiles: with H a multiple of 64, or 256 rows a request on
+  // Requests of few rows share prefix tiles: with H a multiple of 128, or 512 rows a request on
   // average, a request's own tiles are (nearly) full and the join would be extra traffic.
-  p.packed = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 && rows < 256LL * a->B ? 1 : 0;
+  p.packed = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 && rows < 512LL * a->B ? 1 : 0;
   p.max_tiles = static_cast<int>((p.packed ? 2 : 1) * (rows / kRows + 1) + a->B + 1);
-  p.G = sm_count();
+  p.G = pair_count();
   const size_t slots = 2 * static_cast<size_t>(p.G) + (p.packed ? p.max_tiles : 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   p.off_tiles = 0;
@@ -842,7 +936,7 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   if (!status) return DSA_ERR_CUDA;
   CUtensorMap tc, tr;
   const long long slots = std::max(1LL, static_cast<long long>(a->num_pages) * a->page_size);
-  const int box = std::min(a->page_size, kKeys);
+  const int box = std::min(a->page_size, 64);
   if (!key_map(&tc, a->cache_c, slots, kRank, box) || !key_map(&tr, a->cache_r, slots, kRope, box)) return DSA_ERR_CUDA;
   Args k{};
   k.B = a->B;
@@ -878,12 +972,9 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.part_o = reinterpret_cast<float*>(ws + p.off_o);
   k.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaFuncSetAttribute(prefix_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
+  cudaError_t e = launch_pdl(prefix_mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  e = launch_pdl(prefix_mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, k);
-  if (e != cudaSuccess) return DSA_ERR_CUDA;
-  e = launch_pdl(prefix_mla_kernel, dim3(p.G), dim3(kThreads), kSmem, s, tc, tr, k);
+  e = launch_pdl(prefix_mla_kernel, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   // few rows: one CTA each, for latency; many: eight a CTA, most of which find nothing to join
   const long long rows = static_cast<long long>(a->total_q) * a->H;
