@@ -18,13 +18,14 @@
 //   S [128 rows x 128 keys] = Q . K^T       each CTA stages its rows of Q and 64 of the keys
 //   O [128 rows x 512]     += P . V         each CTA stages its rows of P and, of all 128 keys,
 //                                           its half of the latent columns (MN-major)
-//   warp 4      keys of S (9 columns of 64 bf16, in three groups with barriers of their own);
-//   warp 5      keys of P . V (2 x 2 columns); both by TMA, one lane per page piece and column;
-//   warps 6, 7  the piece's query rows (16-byte cp.async, any strides);
-//   warp 8      TMEM; lane 0 of the even CTA issues the MMAs, whichever product has its inputs;
-//   warps 0..3  softmax.  A thread holds one row and one half: 64 of the block's keys, 256 of the
-//               row's latent sums (the row's halves meet in shared memory).  The reference maximum
-//               moves only when a block's maximum passes it by 8 (a factor 256).
+//   warps 0..7  softmax.  A thread holds one row and a quarter: 32 of the block's keys, 128 of the
+//               row's latent sums (the quarters meet in shared memory).  The reference maximum
+//               moves only when a block's maximum passes it by 8 (a factor 256);
+//   warps 8..10 keys of S, three groups of 3 columns of 64 bf16, and warps 11, 12 keys of P . V,
+//               two groups of 2 columns: a warp per group, so that a group's buffer is refilled
+//               as soon as its MMAs are done; TMA, one lane per page piece and column;
+//   warps 13,14 the piece's query rows (16-byte cp.async, any strides);
+//   warp 15     TMEM; in the even CTA one lane issues the MMAs, whichever product has its inputs.
 // A tile done in one piece is normalised and written; the others leave (O, m, l) in fp32.
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
@@ -46,12 +47,12 @@ namespace {
 constexpr int kRank = 512, kRope = 64, kAtoms = 9;        // 576 = 9 columns of 64 bf16
 constexpr int kRows = 128;                                // rows per tile, 64 in each CTA of a pair
 constexpr int kKeys = 128;                                // keys per block
-constexpr int kThreads = 288;                             // warps 0-3 softmax, 4 K, 5 V, 6-7 queries, 8 MMA
+constexpr int kThreads = 512;                             // 8 softmax, 3 K, 2 V, 2 query warps, 1 MMA
 constexpr uint32_t kAtomBytes = 64 * 128;                 // a column of 64 rows or keys
 constexpr uint32_t kKGroup = 3 * kAtomBytes, kVGroup = 2 * 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtoms * kAtomBytes;
 constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
-constexpr size_t kSmem = kOffMisc + 2560;
+constexpr size_t kSmem = kOffMisc + 3072;
 constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -77,7 +78,7 @@ struct Args {
   Tile* tiles;
   long long* u0;           // [max_tiles + 1] first block of each tile in the line of all blocks
   int* head;               // [0] tiles, [1] packed prefix tiles, [2 + b] first own tile of request b
-  float *part_o, *part_ml; // pieces: [slot][64][512], [slot][64][2]
+  float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
   unsigned* status;
 };
 
@@ -88,7 +89,7 @@ struct Bars {
   uint64_t kfull[3], kempty[3];  // L: each CTA's copies
   uint64_t vfull[2], vempty[2];  // L
   uint64_t vown[2];              // this CTA's copies of a block with rows to clear
-  uint64_t sfull[2], sempty[2];  // sempty L: 4 softmax warps of each CTA
+  uint64_t sfull[2], sempty[2];  // sempty L: 8 softmax warps of each CTA
   uint64_t pfull, ofree, done;   // pfull, done L
 };
 
@@ -322,8 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 260);
   volatile int* first_tile = reinterpret_cast<volatile int*>(smem + kOffMisc + 264);
-  float* xmax = reinterpret_cast<float*>(smem + kOffMisc + 512);   // [2][2][64] by block parity, half, row
-  float* xsum = reinterpret_cast<float*>(smem + kOffMisc + 1536);  // [2][64]
+  float* xmax = reinterpret_cast<float*>(smem + kOffMisc + 512);  // [2][4][64] by block parity, quarter, row
   const int rank = static_cast<int>(ptx::cluster_ctarank());
 
   if (threadIdx.x == 0) {
@@ -338,19 +338,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars->vempty[g], 1);
       ptx::mbar_init(&bars->vown[g], 1);
       ptx::mbar_init(&bars->sfull[g], 1);
-      ptx::mbar_init(&bars->sempty[g], 8);
+      ptx::mbar_init(&bars->sempty[g], 16);
     }
-    ptx::mbar_init(&bars->pfull, 8);
+    ptx::mbar_init(&bars->pfull, 16);
     ptx::mbar_init(&bars->ofree, 1);
     ptx::mbar_init(&bars->done, 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 15) {
     ptx::tmem_alloc_pair(tmem_holder, 512);
     ptx::tmem_relinquish_pair();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     ptx::prefetch_tmap(&tmap_c);
     ptx::prefetch_tmap(&tmap_r);
   }
@@ -375,193 +375,186 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Piece p{i_first, 0, 0, 0};
   Tile t;
 
-  if (warp == 8) {
+  if (warp == 15) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {  // the whole warp walks the blocks; one lane issues
       const uint32_t sbase = ptx::smem_u32(smem);
       const uint32_t id1 = ptx::idesc_f32acc(128, kKeys, true);
       const uint32_t id2 = ptx::idesc_f32acc_bf16_bmn(128, 256);
       const uint64_t q0 = ptx::sw128_kmajor_desc(sbase + kOffQ), k0 = ptx::sw128_kmajor_desc(sbase + kOffK);
       const uint64_t p0 = ptx::sw128_kmajor_desc(sbase + kOffP);
       const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + kOffV, 128 * 128);
+      auto ready = [](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity)) != 0;
+      };
       bool ok = true;
       uint32_t n1 = 0, n2 = 0, g1 = 0, g2 = 0;  // blocks (and groups of the next) issued, over all pieces
       uint32_t seg = 0;
       for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
-        if (!ptx::mbar_wait_cluster(&bars->qfull, seg & 1, abort, a.status, kStatusTimeout)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->qfull, seg & 1, abort, a.status, kStatusTimeout)) != 0;
+        if (!ok) break;
         const uint32_t s_begin = n1, s_end = n1 + (p.k1 - p.k0);
         uint64_t t0 = ptx::globaltimer();
         for (uint32_t spin = 0; ok && n2 < s_end; ++spin) {
           bool progress = false;
-          if (n2 < n1 && (g2 > 0 || ptx::mbar_test_wait_cluster(&bars->pfull, n2 & 1)) &&
-              ptx::mbar_test_wait_cluster(&bars->vfull[g2], n2 & 1)) {
+          if (n2 < n1 && (g2 > 0 || ready(&bars->pfull, n2 & 1)) && ready(&bars->vfull[g2], n2 & 1)) {
             ptx::tc_fence_after();
-            const uint64_t v = v0 + g2 * (kVGroup >> 4);
-            const uint32_t d = tmem_base + kOCol0 + g2 * 128;
+            if (ptx::elect_one()) {
+              const uint64_t v = v0 + g2 * (kVGroup >> 4);
+              const uint32_t d = tmem_base + kOCol0 + g2 * 128;
 #pragma unroll
-            for (int s = 0; s < 8; ++s)  // 16 keys per MMA: two 8-key groups of 1024 bytes
-              ptx::mma_bf16_pair(d, p0 + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4), v + ((s * 2048) >> 4), id2,
-                                 (n2 > s_begin || s > 0) ? 1u : 0u);
-            ptx::mma_commit_pair(&bars->vempty[g2], 3);
-            if (++g2 == 2) {
-              ptx::mma_commit_pair(&bars->ofree, 3);
-              g2 = 0;
-              ++n2;
+              for (int s = 0; s < 8; ++s)  // 16 keys per MMA: two 8-key groups of 1024 bytes
+                ptx::mma_bf16_pair(d, p0 + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4), v + ((s * 2048) >> 4), id2,
+                                   (n2 > s_begin || s > 0) ? 1u : 0u);
+              ptx::mma_commit_pair(&bars->vempty[g2], 3);
+              if (g2 == 1) ptx::mma_commit_pair(&bars->ofree, 3);
             }
+            __syncwarp();
+            n2 += g2;
+            g2 ^= 1;
             progress = true;
           }
-          if (n1 < s_end && n1 <= n2 + 1 &&
-              (g1 > 0 || ptx::mbar_test_wait_cluster(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1)) &&
-              ptx::mbar_test_wait_cluster(&bars->kfull[g1], n1 & 1)) {
+          if (n1 < s_end && n1 <= n2 + 1 && (g1 > 0 || ready(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1)) &&
+              ready(&bars->kfull[g1], n1 & 1)) {
             ptx::tc_fence_after();
-            const uint32_t d = tmem_base + (n1 & 1) * 64;
-            const uint64_t go = g1 * (kKGroup >> 4);
+            if (ptx::elect_one()) {
+              const uint32_t d = tmem_base + (n1 & 1) * 64;
+              const uint64_t go = g1 * (kKGroup >> 4);
 #pragma unroll
-            for (int s = 0; s < 12; ++s) {  // 16 values of K per MMA, four in a column
-              const uint64_t off = go + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4);
-              ptx::mma_bf16_pair(d, q0 + off, k0 + off, id1, (g1 > 0 || s > 0) ? 1u : 0u);
+              for (int s = 0; s < 12; ++s) {  // 16 values of K per MMA, four in a column
+                const uint64_t off = go + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4);
+                ptx::mma_bf16_pair(d, q0 + off, k0 + off, id1, (g1 > 0 || s > 0) ? 1u : 0u);
+              }
+              ptx::mma_commit_pair(&bars->kempty[g1], 3);
+              if (g1 == 2) ptx::mma_commit_pair(&bars->sfull[n1 & 1], 3);
+              if (g1 == 2 && n1 + 1 == s_end) ptx::mma_commit_pair(&bars->qempty, 3);
             }
-            ptx::mma_commit_pair(&bars->kempty[g1], 3);
+            __syncwarp();
             if (++g1 == 3) {
-              ptx::mma_commit_pair(&bars->sfull[n1 & 1], 3);
               g1 = 0;
-              if (++n1 == s_end) ptx::mma_commit_pair(&bars->qempty, 3);
+              ++n1;
             }
             progress = true;
           }
           if (progress) {
             t0 = ptx::globaltimer();
           } else if ((spin & 63u) == 63u) {
-            if (*abort) ok = false;
-            else if (ptx::globaltimer() - t0 > 2000000000ull) {
+            bool stop = *abort != 0;
+            if (!stop && ptx::globaltimer() - t0 > 2000000000ull) {
               *abort = 1;
               atomicOr(a.status, kStatusTimeout);
-              ok = false;
+              stop = true;
             }
+            ok = !__any_sync(0xffffffffu, stop);
           }
         }
       }
-      ptx::mma_commit_pair(&bars->done, 1);
-      ptx::mbar_wait_cluster_drain(&bars->done, 0, a.status, kStatusTimeout, 200000000ull);
+      if (ptx::elect_one()) ptx::mma_commit_pair(&bars->done, 1);
+      __syncwarp();
+      ptx::mbar_wait_drain(&bars->done, 0, a.status, kStatusTimeout, 200000000ull);
     }
     __syncwarp();
-  } else if (warp == 4) {
-    // ------------------------------------------------------------ keys of S: this CTA's 64 of a block
-    const int per = 64 / box;
+  } else if (warp >= 8 && warp < 11) {
+    // ------------------------------------------------------------ keys of S: columns 3 g .. 3 g + 2 of this CTA's 64
+    const int per = 64 / box, g = warp - 8;
+    const int at = 3 * g + lane / per, j = lane & (per - 1);  // the lane's column, box of the column
+    const bool mine = lane / per < 3;
+    uint8_t* dst = smem + kOffK + at * kAtomBytes + j * box * 128;
+    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
     uint32_t n = 0;
     bool ok = true;
     for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
-      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
+      for (int k = p.k0; k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
-        const int row = cache_row(a, t, b, b.s0 + rank * 64 + (lane & (per - 1)) * box, box, &bad);
+        const int row = cache_row(a, t, b, b.s0 + rank * 64 + j * box, box, &bad);
         if (bad) atomicOr(a.status, kStatusBadPage);
-        const int at = lane / per, j = lane & (per - 1);  // column of the group, box of the column
-        for (int g = 0; g < 3; ++g) {
-          int good = 1;
-          if (lane == 0)
-            good = ptx::mbar_wait_cluster(&bars->kempty[g], (n & 1) ^ 1, abort, a.status, kStatusTimeout);
-          good = __shfl_sync(0xffffffffu, good, 0);
-          if (!good) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
-          if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
-          __syncwarp();
-          if (at < 3) {
-            uint8_t* dst = smem + kOffK + (3 * g + at) * kAtomBytes + j * box * 128;
-            if (3 * g + at < 8) ptx::tma_load_2d_pair(dst, &tmap_c, full, (3 * g + at) * 64, row);
-            else ptx::tma_load_2d_pair(dst, &tmap_r, full, 0, row);
-          }
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
+                                                            kStatusTimeout)) != 0;
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
+        __syncwarp();
+        if (mine) {
+          if (at < 8) ptx::tma_load_2d_pair(dst, &tmap_c, full, at * 64, row);
+          else ptx::tma_load_2d_pair(dst, &tmap_r, full, 0, row);
         }
       }
     }
-    // every copy lands before the pair can exit, whatever happened
+    // after a failure: every copy lands before the pair can exit
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      for (int g = 0; g < 3; ++g)
-        ptx::mbar_wait_cluster_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
+      ptx::mbar_wait_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
     __syncwarp();
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ keys of P . V: 256 latent columns of all 128
-    const int per = 128 / box;
+  } else if (warp >= 11 && warp < 13) {
+    // ------------------------------------------------------------ keys of P . V: 2 of this CTA's 4 columns, all 128
+    const int per = 128 / box, g = warp - 11;
+    const int j = lane & (per - 1);
+    const bool mine = lane / per < 2;
+    uint8_t* base = smem + kOffV + g * kVGroup;
+    uint8_t* dst = base + (lane / per) * (128 * 128) + j * box * 128;
+    const int x = rank * 256 + (2 * g + lane / per) * 64;
+    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
     uint32_t n = 0, cleared = 0;
     bool ok = true;
     for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
-      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
+      for (int k = p.k0; k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
-        const int row = cache_row(a, t, b, b.s0 + (lane & (per - 1)) * box, box, &bad);
-        const int at = lane / per, j = lane & (per - 1);
+        const int row = cache_row(a, t, b, b.s0 + j * box, box, &bad);
         // rows that no row of this tile sees may hold anything: their weights are 0, and the
         // values are cleared so that the products are
         const bool clear = b.s0 < b.lo || b.s0 + kKeys > b.hi;
-        for (int g = 0; g < 2; ++g) {
-          int good = 1;
-          if (lane == 0)
-            good = ptx::mbar_wait_cluster(&bars->vempty[g], (n & 1) ^ 1, abort, a.status, kStatusTimeout);
-          good = __shfl_sync(0xffffffffu, good, 0);
-          if (!good) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
-          uint8_t* base = smem + kOffV + g * kVGroup;
-          if (lane == 0) {
-            if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
-            else ptx::mbar_arrive_expect_tx_cluster(full, kVGroup);
-          }
-          __syncwarp();
-          if (at < 2) {
-            uint8_t* dst = base + at * (128 * 128) + j * box * 128;
-            const int x = rank * 256 + (2 * g + at) * 64;
-            if (clear) ptx::tma_load_2d(dst, &tmap_c, &bars->vown[g], x, row);
-            else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
-          }
-          if (clear) {
-            good = ptx::mbar_wait_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout, 2000000000ull);
-            if (!__all_sync(0xffffffffu, good != 0)) {
-              ok = false;
-              break;
-            }
-            for (int e = lane; e < 2 * 128 * 8; e += 32) {  // column, row, 16-byte chunk
-              const int key = (e >> 3) & 127;
-              if (b.s0 + key < b.lo || b.s0 + key >= b.hi)
-                *reinterpret_cast<uint4*>(base + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(full);
-          }
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
+                                                            kStatusTimeout)) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
+          else ptx::mbar_arrive_expect_tx_cluster(full, kVGroup);
         }
-        if (clear) ++cleared;
+        __syncwarp();
+        if (mine) {
+          if (clear) ptx::tma_load_2d(dst, &tmap_c, &bars->vown[g], x, row);
+          else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
+        }
+        if (clear) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout,
+                                                            2000000000ull)) != 0;
+          if (!ok) break;
+          ++cleared;
+          const int from = max(b.lo - b.s0, 0), to = min(b.hi - b.s0, kKeys);  // rows [from, to) stay
+          const int n_clear = from + kKeys - to;
+          for (int e = lane; e < n_clear * 16; e += 32) {  // 16 chunks of 16 bytes a row, in two columns
+            const int r = e >> 4, key = r < from ? r : to + (r - from);
+            *reinterpret_cast<uint4*>(base + ((e >> 3) & 1) * (128 * 128) + key * 128 + (e & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(full);
+        }
       }
     }
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      for (int g = 0; g < 2; ++g)
-        ptx::mbar_wait_cluster_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
+      ptx::mbar_wait_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
     __syncwarp();
-  } else if (warp > 5) {
+  } else if (warp >= 13) {
     // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
-    const int gt = threadIdx.x - 192;
+    const int gt = threadIdx.x - 13 * 32;
+    const int c16 = gt & 7;
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
     uint32_t seg = 0;
     for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
-      const bool good = ptx::mbar_wait_cluster(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
+      const bool good = ptx::mbar_wait(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
       if (!__all_sync(0xffffffffu, good)) break;
-      for (int e = gt; e < 64 * 72; e += 64) {
-        const int r = e / 72, ch = e - r * 72;
-        const int at = ch >> 3, c16 = ch & 7;
+      for (int r = gt >> 3; r < 64; r += 8) {  // eight threads a row, 128 bytes at a time
         const bool live = rank * 64 + r < t.nrows;
         const int row = t.row0 + (live ? rank * 64 + r : 0);
         const int tq = row / a.H, h = row - tq * a.H;
-        const __nv_bfloat16* src = at < 8 ? a.qn + tq * a.qn_t + h * a.qn_h + at * 64 + c16 * 8
-                                          : a.qr + tq * a.qr_t + h * a.qr_h + c16 * 8;
-        ptx::cp_async_16(smem + kOffQ + at * kAtomBytes + r * 128 + ((c16 ^ (r & 7)) << 4), src, live ? 16u : 0u);
+        const __nv_bfloat16* qn = a.qn + tq * a.qn_t + h * a.qn_h + c16 * 8;
+        const __nv_bfloat16* qr = a.qr + tq * a.qr_t + h * a.qr_h + c16 * 8;
+        uint8_t* dst = smem + kOffQ + r * 128 + ((c16 ^ (r & 7)) << 4);
+#pragma unroll
+        for (int at = 0; at < kAtoms; ++at)
+          ptx::cp_async_16(dst + at * kAtomBytes, at < 8 ? qn + at * 64 : qr, live ? 16u : 0u);
       }
       cp_async_wait_all();
       ptx::fence_proxy_async_smem();
@@ -569,17 +562,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive_cluster(full);
     }
   } else {
-    // ------------------------------------------------------------ softmax, rescale, output (warps 0..3)
-    const int row = (warp & 1) * 32 + lane, half = warp >> 1;  // TMEM lane = 64 half + row
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t pair_bar = 2 + (warp & 1);                  // warps w and w + 2: the halves of the same rows
-    const int per = 64 / box;
+    // ------------------------------------------------------------ softmax, rescale, output (warps 0..7)
+    const int row = (warp & 1) * 32 + lane, half = (warp >> 1) & 1;  // TMEM lane = 64 half + row
+    const int part = warp >> 2, quarter = 2 * half + part;           // columns 32 part of S, 128 part of O
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t row_bar = 2 + (warp & 1);                         // the four warps of the same rows
+    const int per = max(32 / box, 1);                                // boxes under this thread's keys
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->pfull), 0);
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&bars->sempty[0]), 0);
     bool ok = true;
     uint32_t n = 0;
     for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
-      float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this half's sum
+      float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this quarter's sum
       int lim = 0;                   // keys this row sees
       const int trow = rank * 64 + row;
       if (trow < t.nrows) {
@@ -590,50 +584,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const int tb = n & 1;
         const Block b = block_at(a, t, k);
-        const int s0 = b.s0 + half * 64;  // this thread's 64 keys
+        const int s0 = b.s0 + half * 64 + part * 32;  // this thread's 32 keys
         bool bad = false;
-        const int crow = cache_row(a, t, b, s0 + (lane & (per - 1)) * box, box, &bad);
-        const unsigned there = __ballot_sync(0xffffffffu, crow != a.past_row);
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
+        const int s_box = (s0 & ~(box - 1)) + (lane & (per - 1)) * box;
+        const unsigned there = __ballot_sync(0xffffffffu, cache_row(a, t, b, s_box, box, &bad) != a.past_row);
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
                                                                     kStatusTimeout)) != 0;
-        float x[64];
+        float x[32];
         float mb = -INFINITY;
         if (ok) {
           ptx::tc_fence_after();
-          uint32_t x0[32], x1[32];
-          ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * 64, x0);
-          ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * 64 + 32, x1);
-          ptx::tmem_ld_wait_regs(x0);
-          ptx::tmem_ld_wait_regs(x1);
+          uint32_t xr[32];
+          ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + tb * 64 + part * 32, xr);
+          ptx::tmem_ld_wait_regs(xr);
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive_cluster(empty0 + tb * 8);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(x0[i]);
-            x[32 + i] = __uint_as_float(x1[i]);
-          }
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(xr[i]);
           const int end = min(b.hi, lim);
           const unsigned all = (1u << per) - 1u;
-          if (s0 < b.lo || s0 + 64 > end || (there & all) != all) {
+          if (s0 < b.lo || s0 + 32 > end || (there & all) != all) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
+            for (int i = 0; i < 32; ++i) {
               const int s = s0 + i;
-              const bool v = s >= b.lo && s < end && ((there >> (i >> box_log2)) & 1u);
+              const bool v = s >= b.lo && s < end && ((there >> ((i >> box_log2) & (per - 1))) & 1u);
               x[i] = v ? x[i] : -INFINITY;
             }
           }
 #pragma unroll
-          for (int i = 0; i < 64; ++i) mb = fmaxf(mb, x[i]);
+          for (int i = 0; i < 32; ++i) mb = fmaxf(mb, x[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = -INFINITY;
+          for (int i = 0; i < 32; ++i) x[i] = -INFINITY;
         }
-        // the row's block maximum over both halves
-        float* xm = xmax + tb * 128;
-        xm[half * 64 + row] = mb;
-        ptx::named_bar_sync(pair_bar, 64);
-        mb = fmaxf(mb, xm[(half ^ 1) * 64 + row]) * a.scale_log2;
+        // the row's block maximum over its quarters
+        float* xm = xmax + tb * 256 + row;
+        xm[quarter * 64] = mb;
+        ptx::named_bar_sync(row_bar, 128);
+        mb = fmaxf(fmaxf(xm[0], xm[64]), fmaxf(xm[128], xm[192])) * a.scale_log2;
         // The reference maximum moves only when the block's maximum exceeds it by more than 8
         // (a factor 256 in probability): p stays below 256 and the output, which divides by
         // the sum taken against the same reference, is unchanged.
@@ -642,9 +631,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float cr = (m == -INFINITY || mn == m) ? 1.f : ptx::ex2(m - mn);
         const float off = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every x is -inf, p = 0
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const float p0 = ptx::ex2(fmaf(x[2 * i], a.scale_log2, -off));
           const float p1 = ptx::ex2(fmaf(x[2 * i + 1], a.scale_log2, -off));
           ls[(2 * i) & 3] += p0;
@@ -656,25 +645,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         m = mn;
         // P and O are free once the previous block's P . V has completed
         if (n > 0 && ok)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->ofree, (n - 1) & 1, abort, a.status,
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                               kStatusTimeout)) != 0;
         if (ok) {
-          // row of P: this half's 64 keys = 8 chunks of 16 bytes, swizzled by the row
+          // row of P: this quarter's 32 keys = 4 chunks of 16 bytes, swizzled by the row
           uint8_t* prow = smem + kOffP + half * kAtomBytes + row * 128;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4*>(prow + ((q ^ (row & 7)) << 4)) =
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(prow + (((part * 4 + q) ^ (row & 7)) << 4)) =
                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
           ptx::fence_proxy_async_smem();
           if (k > p.k0 && __any_sync(0xffffffffu, cr != 1.f)) {
             ptx::tc_fence_after();
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t col = tmem_base + lane_addr + kOCol0 + part * 128 + q * 32;
               uint32_t r[32];
-              ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
+              ptx::tmem_ld_32x32b_x32(col, r);
               ptx::tmem_ld_wait_regs(r);
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * cr);
-              ptx::tmem_st_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
+              ptx::tmem_st_32x32b_x32(col, r);
             }
             ptx::tmem_st_wait();
           }
@@ -687,25 +677,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool at_start = p.k0 == 0;
       const bool whole = at_start && p.u + (p.k1 - p.k0) == __ldcg(a.u0 + p.i + 1);
       const bool direct = whole && !a.packed;
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(&bars->ofree, (n - 1) & 1, abort, a.status,
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                                   kStatusTimeout)) != 0;
-      xsum[half * 64 + row] = l;
-      ptx::named_bar_sync(pair_bar, 64);
-      l += xsum[(half ^ 1) * 64 + row];
-      ptx::named_bar_sync(pair_bar, 64);  // read before the next piece writes them
+      float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
+      xs[quarter * 64] = l;
+      ptx::named_bar_sync(row_bar, 128);
+      l = (xs[0] + xs[64]) + (xs[128] + xs[192]);
+      ptx::named_bar_sync(row_bar, 128);  // read before the next piece writes there
       const bool live = trow < t.nrows && ok;
-      const long long prow = piece_slot(a.G, c, p.i, at_start, whole) * kRows + trow;
-      if (live && half == 0) {
-        if (!direct) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m, l);
+      const long long slot = piece_slot(a.G, c, p.i, at_start, whole);
+      if (live && quarter == 0) {
+        if (!direct) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + trow) * 2) = make_float2(m, l);
         else if (a.lse) a.lse[t.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       ptx::tc_fence_after();
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < 4; ++q) {
         uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + q * 32, r);
+        ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + part * 128 + q * 32, r);
         ptx::tmem_ld_wait_regs(r);
-        const int lat = half * 256 + q * 32;
+        const int lat = half * 256 + part * 128 + q * 32;
         if (live && direct) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + (t.row0 + trow) * static_cast<long long>(kRank) + lat);
 #pragma unroll
@@ -720,9 +711,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * kRank + lat);
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + (slot * (kRank / 4) + lat / 4) * kRows + trow;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            dst[i * kRows] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
         }
       }
       ptx::tc_fence_before();
@@ -731,39 +723,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // no CTA leaves while its peer may still touch its memory, barriers or TMEM
-  if (warp == 8) {
+  if (warp == 15) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
 // ------------------------------------------------------------------ join
-// A CTA takes rows_per rows of a group of 128 (a packed prefix tile, or a tile); a thread four
-// latent values.
-__global__ void __launch_bounds__(128) prefix_mla_join_kernel(const Args a, int rows_per) {
+// An item is 16 latent columns of a group of 128 rows: a packed prefix tile, or a tile that a part
+// begins inside (the first such part names it).  Thread (r, y) takes row r and the pieces y, y + 4,
+// ..; the four meet in shared memory.  Tiles without any block get zeros.
+constexpr int kJoinCols = 4;  // columns of 4
+__global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
+  __shared__ float4 acc_s[3][kJoinCols][kRows];
+  __shared__ float2 ml_s[3][kRows];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int per = kRows / rows_per;
-  const int g = blockIdx.x / per, r0 = (blockIdx.x - g * per) * rows_per;
+  const int r = threadIdx.x & (kRows - 1), y = threadIdx.x >> 7;
   const int n_tiles = __ldcg(a.head);
-  const int n_groups = a.packed ? __ldcg(a.head + 1) : n_tiles;
-  if (g >= n_groups) return;
   const long long U = __ldcg(a.u0 + n_tiles);
   const int G = parts(a, U);
-  const Tile t = a.tiles[g];
-  const long long g0 = __ldcg(a.u0 + g), g1 = __ldcg(a.u0 + g + 1);
-  const int gc0 = g1 > g0 ? part_of(U, G, g0) : 0, gc1 = g1 > g0 ? part_of(U, G, g1 - 1) : -1;
-  if (!a.packed && g1 > g0 && gc0 == gc1) return;  // done in one piece: already written
-  for (int r = r0; r < min(r0 + rows_per, t.nrows); ++r) {
-    const int row = t.row0 + r;
+  constexpr int kSplit = kRank / 4 / kJoinCols;
+  const int groups = a.packed ? __ldcg(a.head + 1) : G;
+  for (int item = blockIdx.x; item < groups * kSplit; item += gridDim.x) {
+    const int col0 = (item % kSplit) * kJoinCols;  // neighbouring CTAs: other columns of the same rows
+    int g = item / kSplit;
+    if (!a.packed) {
+      if (g == 0) continue;
+      const long long u = part_begin(U, G, g);
+      g = find_tile(a.u0, n_tiles, u);
+      if (__ldcg(a.u0 + g) == u) continue;                                         // begins with a tile
+      if (part_begin(U, G, item / kSplit - 1) > __ldcg(a.u0 + g)) continue;        // an earlier part named it
+    }
+    const int row0 = __ldcg(&a.tiles[g].row0), nrows = __ldcg(&a.tiles[g].nrows);
+    const int row = row0 + r;
+    const bool live = r < nrows;
     // up to two tiles hold this row's pieces
-    int ti[2] = {g, -1}, rr[2] = {r, 0}, c0[2] = {gc0, 0}, c1[2] = {gc1, -1};
-    if (a.packed) {
+    int ti[2] = {g, -1}, rr[2] = {r, 0}, c0[2] = {0, 0}, c1[2] = {-1, -1};
+    const long long g0 = __ldcg(a.u0 + g), g1 = __ldcg(a.u0 + g + 1);
+    if (g1 > g0) {
+      c0[0] = part_of(U, G, g0);
+      c1[0] = part_of(U, G, g1 - 1);
+    }
+    if (a.packed && live) {
       const int tq = row / a.H;
       const int b = request_of(a, tq);
-      const int q0 = __ldg(a.cu + b);
       if (tq < __ldg(a.cu + b + 1)) {
-        const int local = row - q0 * a.H;
+        const int local = row - __ldg(a.cu + b) * a.H;
         ti[1] = __ldcg(a.head + 2 + b) + local / kRows;
         rr[1] = local % kRows;
         if (ti[1] < n_tiles) {
@@ -775,37 +781,92 @@ __global__ void __launch_bounds__(128) prefix_mla_join_kernel(const Args a, int 
         }
       }
     }
-    float M = -INFINITY;
+    // running maximum, sum and columns over this thread's pieces
+    const int n0 = c1[0] - c0[0] + 1, np = n0 + c1[1] - c0[1] + 1;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[kJoinCols];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      for (int c = c0[q]; c <= c1[q]; ++c) {
-        const long long s = piece_slot(a.G, c, ti[q], c == c0[q], c0[q] == c1[q]);
-        M = fmaxf(M, __ldcg(a.part_ml + (s * kRows + rr[q]) * 2));
-      }
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
+    for (int q = 0; q < kJoinCols; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+#pragma unroll 2
+      for (int k = y; k < np; k += 4) {
+        const int w = k < n0 ? 0 : 1, c = c0[w] + k - (w ? n0 : 0);
+        const long long s = piece_slot(a.G, c, ti[w], c == c0[w], c0[w] == c1[w]);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + s * kRows + rr[w]);
+        const float4* src = reinterpret_cast<const float4*>(a.part_o) + (s * (kRank / 4) + col0) * kRows + rr[w];
+        float4 o[kJoinCols];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll 4
-        for (int c = c0[q]; c <= c1[q]; ++c) {
-          const long long s = piece_slot(a.G, c, ti[q], c == c0[q], c0[q] == c1[q]) * kRows + rr[q];
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + s * 2));
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + s * kRank) + threadIdx.x);
-          const float w = exp2f(ml.x - M);  // 0 for a piece in which the row saw nothing
-          L = fmaf(w, ml.y, L);
-          acc.x = fmaf(w, o.x, acc.x);
-          acc.y = fmaf(w, o.y, acc.y);
-          acc.z = fmaf(w, o.z, acc.z);
-          acc.w = fmaf(w, o.w, acc.w);
+        for (int q = 0; q < kJoinCols; ++q) o[q] = __ldcg(src + q * kRows);
+        if (ml.x == -INFINITY) continue;  // a piece in which the row saw nothing
+        const float Mn = fmaxf(M, ml.x);
+        const float f = exp2f(M - Mn), e = exp2f(ml.x - Mn);  // f = 0 the first time
+        M = Mn;
+        L = L * f + e * ml.y;
+#pragma unroll
+        for (int q = 0; q < kJoinCols; ++q) {
+          acc[q].x = acc[q].x * f + e * o[q].x;
+          acc[q].y = acc[q].y * f + e * o[q].y;
+          acc[q].z = acc[q].z * f + e * o[q].z;
+          acc[q].w = acc[q].w * f + e * o[q].w;
         }
+      }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kRank)[threadIdx.x] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    __syncthreads();  // the last item's reads are done
+    if (y > 0) {
+      ml_s[y - 1][r] = make_float2(M, L);
+#pragma unroll
+      for (int q = 0; q < kJoinCols; ++q) acc_s[y - 1][q][r] = acc[q];
+    }
+    __syncthreads();
+    if (y == 0 && live) {
+      float2 ml[3];
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        ml[k] = ml_s[k][r];
+        Mn = fmaxf(Mn, ml[k].x);
+      }
+      const float none = Mn == -INFINITY ? 0.f : Mn;
+      const float f = exp2f(M - none);
+      L *= f;
+#pragma unroll
+      for (int q = 0; q < kJoinCols; ++q)
+        acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const float e = exp2f(ml[k].x - none);
+        L += e * ml[k].y;
+#pragma unroll
+        for (int q = 0; q < kJoinCols; ++q) {
+          const float4 o = acc_s[k][q][r];
+          acc[q].x += e * o.x;
+          acc[q].y += e * o.y;
+          acc[q].z += e * o.z;
+          acc[q].w += e * o.w;
+        }
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      uint32_t w[2 * kJoinCols];
+#pragma unroll
+      for (int q = 0; q < kJoinCols; ++q) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * inv, acc[q].y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * inv, acc[q].w * inv);
+        w[2 * q] = *reinterpret_cast<const uint32_t*>(&lo);
+        w[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<long long>(row) * kRank + col0 * 4);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if (a.lse && col0 == 0) a.lse[row] = L > 0.f ? (Mn + log2f(L)) * kLn2 : -INFINITY;
+    }
+  }
+  if (a.packed) return;  // every row lies in a packed tile
+  for (int i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+    if (__ldcg(a.u0 + i) != __ldcg(a.u0 + i + 1)) continue;
+    const int row0 = __ldcg(&a.tiles[i].row0), nrows = __ldcg(&a.tiles[i].nrows);
+    for (int e = threadIdx.x; e < nrows * (kRank / 8); e += blockDim.x)
+      reinterpret_cast<uint4*>(a.out + static_cast<long long>(row0) * kRank)[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse && threadIdx.x < nrows) a.lse[row0 + threadIdx.x] = -INFINITY;
   }
 }
 
@@ -976,12 +1037,10 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   e = launch_pdl(prefix_mla_kernel, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  // few rows: one CTA each, for latency; many: eight a CTA, most of which find nothing to join
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  const int rows_per = rows <= 16384 ? 1 : 8;
-  const long long groups = p.packed ? (rows + kRows - 1) / kRows : p.max_tiles;
-  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(groups * (kRows / rows_per))), dim3(128), 0, s, k,
-                 rows_per);
+  const long long groups = p.packed ? (rows + kRows - 1) / kRows : p.G;
+  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(std::min(groups * (kRank / 4 / kJoinCols), 608LL))),
+                 dim3(512), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
