@@ -377,81 +377,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 15) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0) {  // the whole warp walks the blocks; one lane issues
+    // The whole warp walks the blocks, one lane issues.  S of block k + 1 goes before P . V of
+    // block k, whose weights are computed meanwhile.
+    if (rank == 0) {
       const uint32_t sbase = ptx::smem_u32(smem);
       const uint32_t id1 = ptx::idesc_f32acc(128, kKeys, true);
       const uint32_t id2 = ptx::idesc_f32acc_bf16_bmn(128, 256);
-      const uint64_t q0 = ptx::sw128_kmajor_desc(sbase + kOffQ), k0 = ptx::sw128_kmajor_desc(sbase + kOffK);
-      const uint64_t p0 = ptx::sw128_kmajor_desc(sbase + kOffP);
-      const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + kOffV, 128 * 128);
-      auto ready = [](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity)) != 0;
-      };
+      const uint32_t q0 = ptx::desc_lo(sbase + kOffQ, 16), k0 = ptx::desc_lo(sbase + kOffK, 16);
+      const uint32_t p0 = ptx::desc_lo(sbase + kOffP, 16), v0 = ptx::desc_lo(sbase + kOffV, 128 * 128);
       bool ok = true;
-      uint32_t n1 = 0, n2 = 0, g1 = 0, g2 = 0;  // blocks (and groups of the next) issued, over all pieces
-      uint32_t seg = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout)) != 0;
+      };
+      uint32_t n1 = 0, n2 = 0, seg = 0;  // blocks whose S / P . V was issued, pieces
       for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->qfull, seg & 1, abort, a.status, kStatusTimeout)) != 0;
-        if (!ok) break;
-        const uint32_t s_begin = n1, s_end = n1 + (p.k1 - p.k0);
-        uint64_t t0 = ptx::globaltimer();
-        for (uint32_t spin = 0; ok && n2 < s_end; ++spin) {
-          bool progress = false;
-          if (n2 < n1 && (g2 > 0 || ready(&bars->pfull, n2 & 1)) && ready(&bars->vfull[g2], n2 & 1)) {
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint64_t v = v0 + g2 * (kVGroup >> 4);
-              const uint32_t d = tmem_base + kOCol0 + g2 * 128;
+        wait(&bars->qfull, seg & 1);
+        const int nblk = p.k1 - p.k0;
+        for (int i = 0; ok && i <= nblk; ++i) {
+          if (i < nblk) {
+            const uint32_t d = tmem_base + (n1 & 1) * 64;
+            wait(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1);
 #pragma unroll
-              for (int s = 0; s < 8; ++s)  // 16 keys per MMA: two 8-key groups of 1024 bytes
-                ptx::mma_bf16_pair(d, p0 + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4), v + ((s * 2048) >> 4), id2,
-                                   (n2 > s_begin || s > 0) ? 1u : 0u);
-              ptx::mma_commit_pair(&bars->vempty[g2], 3);
-              if (g2 == 1) ptx::mma_commit_pair(&bars->ofree, 3);
-            }
-            __syncwarp();
-            n2 += g2;
-            g2 ^= 1;
-            progress = true;
-          }
-          if (n1 < s_end && n1 <= n2 + 1 && (g1 > 0 || ready(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1)) &&
-              ready(&bars->kfull[g1], n1 & 1)) {
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint32_t d = tmem_base + (n1 & 1) * 64;
-              const uint64_t go = g1 * (kKGroup >> 4);
+            for (int g = 0; g < 3; ++g) {
+              wait(&bars->kfull[g], n1 & 1);
+              ptx::tc_fence_after();
+              if (ok && ptx::elect_one()) {
+                uint32_t qa = q0, kb = k0;
+                asm volatile("" : "+r"(qa), "+r"(kb));  // descriptors are added up here, not kept over the loop
 #pragma unroll
-              for (int s = 0; s < 12; ++s) {  // 16 values of K per MMA, four in a column
-                const uint64_t off = go + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4);
-                ptx::mma_bf16_pair(d, q0 + off, k0 + off, id1, (g1 > 0 || s > 0) ? 1u : 0u);
+                for (int s = 0; s < 12; ++s) {  // 16 values of K per MMA, four in a column
+                  const uint32_t off = ((3 * g + (s >> 2)) * kAtomBytes + (s & 3) * 32) >> 4;
+                  ptx::mma_bf16_pair(d, qa + off, kb + off, id1, (g > 0 || s > 0) ? 1u : 0u);
+                }
+                ptx::mma_commit_pair(&bars->kempty[g], 3);
+                if (g == 2) {
+                  ptx::mma_commit_pair(&bars->sfull[n1 & 1], 3);
+                  if (i + 1 == nblk) ptx::mma_commit_pair(&bars->qempty, 3);
+                }
               }
-              ptx::mma_commit_pair(&bars->kempty[g1], 3);
-              if (g1 == 2) ptx::mma_commit_pair(&bars->sfull[n1 & 1], 3);
-              if (g1 == 2 && n1 + 1 == s_end) ptx::mma_commit_pair(&bars->qempty, 3);
+              __syncwarp();
             }
-            __syncwarp();
-            if (++g1 == 3) {
-              g1 = 0;
-              ++n1;
-            }
-            progress = true;
+            ++n1;
           }
-          if (progress) {
-            t0 = ptx::globaltimer();
-          } else if ((spin & 63u) == 63u) {
-            bool stop = *abort != 0;
-            if (!stop && ptx::globaltimer() - t0 > 2000000000ull) {
-              *abort = 1;
-              atomicOr(a.status, kStatusTimeout);
-              stop = true;
+          if (i > 0) {
+            wait(&bars->pfull, n2 & 1);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              wait(&bars->vfull[g], n2 & 1);
+              ptx::tc_fence_after();
+              if (ok && ptx::elect_one()) {
+                uint32_t pa = p0, vb = v0;
+                asm volatile("" : "+r"(pa), "+r"(vb));
+#pragma unroll
+                for (int s = 0; s < 8; ++s)  // 16 keys per MMA: two 8-key groups of 1024 bytes
+                  ptx::mma_bf16_pair(tmem_base + kOCol0 + g * 128,
+                                     pa + (((s >> 2) * kAtomBytes + (s & 3) * 32) >> 4),
+                                     vb + ((g * kVGroup + s * 2048) >> 4), id2, (i > 1 || s > 0) ? 1u : 0u);
+                ptx::mma_commit_pair(&bars->vempty[g], 3);
+                if (g == 1) ptx::mma_commit_pair(&bars->ofree, 3);
+              }
+              __syncwarp();
             }
-            ok = !__any_sync(0xffffffffu, stop);
+            ++n2;
           }
         }
       }
       if (ptx::elect_one()) ptx::mma_commit_pair(&bars->done, 1);
       __syncwarp();
-      ptx::mbar_wait_drain(&bars->done, 0, a.status, kStatusTimeout, 200000000ull);
+      ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     }
     __syncwarp();
   } else if (warp >= 8 && warp < 11) {
@@ -469,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool bad = false;
         const int row = cache_row(a, t, b, b.s0 + rank * 64 + j * box, box, &bad);
         if (bad) atomicOr(a.status, kStatusBadPage);
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
+        ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
                                                             kStatusTimeout)) != 0;
         if (!ok) break;
         if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
@@ -482,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // after a failure: every copy lands before the pair can exit
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      ptx::mbar_wait_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
+      ptx::mbar_spin_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     __syncwarp();
   } else if (warp >= 11 && warp < 13) {
     // ------------------------------------------------------------ keys of P . V: 2 of this CTA's 4 columns, all 128
@@ -503,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // rows that no row of this tile sees may hold anything: their weights are 0, and the
         // values are cleared so that the products are
         const bool clear = b.s0 < b.lo || b.s0 + kKeys > b.hi;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
+        ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
                                                             kStatusTimeout)) != 0;
         if (!ok) break;
         if (lane == 0) {
@@ -516,8 +509,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
         }
         if (clear) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout,
-                                                            2000000000ull)) != 0;
+          ok = __all_sync(0xffffffffu, ptx::mbar_spin_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout,
+                                                            ptx::kWaitCycles)) != 0;
           if (!ok) break;
           ++cleared;
           const int from = max(b.lo - b.s0, 0), to = min(b.hi - b.s0, kKeys);  // rows [from, to) stay
@@ -534,7 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      ptx::mbar_wait_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, 200000000ull);
+      ptx::mbar_spin_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     __syncwarp();
   } else if (warp >= 13) {
     // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
@@ -543,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
     uint32_t seg = 0;
     for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
-      const bool good = ptx::mbar_wait(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
+      const bool good = ptx::mbar_spin(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
       if (!__all_sync(0xffffffffu, good)) break;
       for (int r = gt >> 3; r < 64; r += 8) {  // eight threads a row, 128 bytes at a time
         const bool live = rank * 64 + r < t.nrows;
@@ -588,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool bad = false;
         const int s_box = (s0 & ~(box - 1)) + (lane & (per - 1)) * box;
         const unsigned there = __ballot_sync(0xffffffffu, cache_row(a, t, b, s_box, box, &bad) != a.past_row);
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
                                                                     kStatusTimeout)) != 0;
         float x[32];
         float mb = -INFINITY;
@@ -645,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         m = mn;
         // P and O are free once the previous block's P . V has completed
         if (n > 0 && ok)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
+          ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                               kStatusTimeout)) != 0;
         if (ok) {
           // row of P: this quarter's 32 keys = 4 chunks of 16 bytes, swizzled by the row
@@ -677,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool at_start = p.k0 == 0;
       const bool whole = at_start && p.u + (p.k1 - p.k0) == __ldcg(a.u0 + p.i + 1);
       const bool direct = whole && !a.packed;
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->ofree, (n - 1) & 1, abort, a.status,
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                                   kStatusTimeout)) != 0;
       float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
       xs[quarter * 64] = l;

@@ -295,12 +295,44 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   return d;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
+}
+// Bounded wait like mbar_wait, its limit counted in SM cycles (about 2 s): reading the cycle
+// counter takes some 20 cycles, the global timer about 1000, which every wait that does not
+// succeed at once would add (and a wait on the critical path often just misses).
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status,
+                                          unsigned timeout_bit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kWaitCycles) {
+        *abort = 1;
+        atomicOr(status, timeout_bit);
+        return false;
+      }
+    }
+  }
+}
+// The same for copies or MMAs already in flight before the CTA exits: ignores the abort flag.
+__device__ __forceinline__ bool mbar_spin_drain(uint64_t* bar, uint32_t parity, unsigned* status,
+                                                unsigned timeout_bit, long long cycles) {
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0 && clock64() - t0 > cycles) {
+      atomicOr(status, timeout_bit);
+      return false;
+    }
+  }
 }
 // One lane of a converged warp, always the same.  MMAs are issued under this and not under a
 // comparison of the lane id: the compiler then keeps descriptors in uniform registers, and an MMA
@@ -337,14 +369,21 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
 }
 // 2-SM MMA: D (rows split over the pair's TMEM) (+)= A (each CTA's rows) x B^T (N split in
 // halves over the pair's shared memory; one descriptor, the same offsets in both CTAs).
-// Issued by the even CTA.
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// Issued by the even CTA.  The operands are 128-byte swizzled tiles, given by the low words of
+// their descriptors (start address >> 4, leading byte offset >> 4 in bits 16-29); the high word
+// (stride byte offset 1024, version 1, swizzle mode 2) is the same for K-major and MN-major.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lead_bytes) {
+  return ((smem_addr >> 4) & 0x3FFFu) | ((lead_bytes >> 4) << 16);
 }
 // Arrive once on the mbarrier at this offset in every CTA of `mask` when the pair's
 // earlier MMAs (issued by this thread) complete.
