@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -172,13 +173,13 @@ def lib():
         L.dsa_sparse_mla.restype = I
         L.dsa_sparse_mla.argtypes = [ctypes.POINTER(dsa_sparse_mla_args), P]
         L.dsa_page_plan.restype = I
-        L.dsa_page_plan.argtypes = [ctypes.POINTER(dsa_page_plan_args), P]
+        L.dsa_page_plan.argtypes = [P, P]
         L.dsa_mla_cache_append.restype = I
-        L.dsa_mla_cache_append.argtypes = [ctypes.POINTER(dsa_mla_cache_append_args), P]
+        L.dsa_mla_cache_append.argtypes = [P, P]
         L.dsa_prefix_mla_workspace_size.restype = I
-        L.dsa_prefix_mla_workspace_size.argtypes = [ctypes.POINTER(dsa_prefix_mla_args), ctypes.POINTER(S)]
+        L.dsa_prefix_mla_workspace_size.argtypes = [P, ctypes.POINTER(S)]
         L.dsa_prefix_mla.restype = I
-        L.dsa_prefix_mla.argtypes = [ctypes.POINTER(dsa_prefix_mla_args), P]
+        L.dsa_prefix_mla.argtypes = [P, P]
         L.dsa_test_arm_score_timeout.restype = I
         L.dsa_test_arm_score_timeout.argtypes = [ctypes.c_ulonglong]
         _LIB = L
@@ -685,13 +686,47 @@ def dsa_sparse_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
 
 # ---- a batch that shares its prompt: page plan, latent cache append, attention --------------
 
+# These calls are often short against what it takes to make them, so their arguments are packed
+# with struct (in the layout of the C structs above) and every check is one comparison that
+# succeeds; the messages are put together only when one fails.
+_PLAN_ARGS = struct.Struct("@6i9P")
+_APPEND_ARGS = struct.Struct("@7if2P2q7P")
+_PREFIX_ARGS = struct.Struct("@10if2P4q9PN")
+assert _PLAN_ARGS.size == ctypes.sizeof(dsa_page_plan_args)
+assert _APPEND_ARGS.size == ctypes.sizeof(dsa_mla_cache_append_args)
+assert _PREFIX_ARGS.size == ctypes.sizeof(dsa_prefix_mla_args)
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape) -> int:
+    """Device pointer of a contiguous CUDA tensor of this type and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != shape:
+        _expect([(t, name, shape)])
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, dtype)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, shape) -> int:
+    """Device pointer of a bf16 tensor whose last dimension is dense, the others in any strides."""
+    if t.shape != shape:
+        _expect([(t, name, shape)])
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return t.data_ptr()
+
+
 def _record(tensors, stream) -> None:
     """Memory of these tensors must not be reused ahead of `stream`'s kernels (torch's
     allocator only knows the stream a tensor was allocated on)."""
-    if stream is not None:
-        for t in tensors:
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor, free_pages: torch.Tensor,
@@ -705,44 +740,32 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     of free_pages in request order, -1 behind.  total_q: the outputs' length, at least the
     sum of q_lens (the rest is -1).  Returns (cu_q_lens [B + 1] int32, slot_mapping [total_q]
     int64, positions [total_q] int32, used [1] int32: the free pages taken)."""
-    _expect([(q_lens, "q_lens", (None,))])
-    B = q_lens.shape[0]
-    _expect([(seq_lens, "seq_lens", (B,)), (block_tables, "block_tables", (B, None)),
+    _expect([(q_lens, "q_lens", (None,)), (block_tables, "block_tables", (q_lens.shape[0], None)),
              (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
-    dev = block_tables.device
-    if cu_q_lens is None:
-        cu_q_lens = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    if slot_mapping is None:
-        slot_mapping = torch.empty(total_q, dtype=torch.int64, device=dev)
-    if positions is None:
-        positions = torch.empty(total_q, dtype=torch.int32, device=dev)
-    if used is None:
-        used = torch.empty(1, dtype=torch.int32, device=dev)
-    _expect([(cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
-             (positions, "positions", (total_q,)), (used, "used", (1,))])
+    B, width = block_tables.shape
     i32 = torch.int32
-    a = dsa_page_plan_args(
-        B, int(total_q), int(page_size), block_tables.shape[1], 0 if prefix_pages is None else prefix_pages.shape[0],
-        free_pages.shape[0], _dev(q_lens, "q_lens", i32), _dev(seq_lens, "seq_lens", i32),
-        _dev(prefix_pages, "prefix_pages", i32), _dev(free_pages, "free_pages", i32),
-        _dev(block_tables, "block_tables", i32), _dev(cu_q_lens, "cu_q_lens", i32),
-        _dev(slot_mapping, "slot_mapping", torch.int64), _dev(positions, "positions", i32), _dev(used, "used", i32))
-    _check(lib().dsa_page_plan(ctypes.byref(a), _stream_ptr(stream)), "dsa_page_plan")
-    _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
-            stream)
+    n_free, n_prefix = free_pages.shape[0], 0 if prefix_pages is None else prefix_pages.shape[0]
+    lens = (_ptr(q_lens, "q_lens", i32, (B,)), _ptr(seq_lens, "seq_lens", i32, (B,)),
+            _ptr(prefix_pages, "prefix_pages", i32, (n_prefix,)), _ptr(free_pages, "free_pages", i32, (n_free,)),
+            _ptr(block_tables, "block_tables", i32, (B, width)))
+    new = block_tables.new_empty
+    if cu_q_lens is None:
+        cu_q_lens = new(B + 1)
+    if slot_mapping is None:
+        slot_mapping = new(total_q, dtype=torch.int64)
+    if positions is None:
+        positions = new(total_q)
+    if used is None:
+        used = new(1)
+    args = _PLAN_ARGS.pack(B, total_q, page_size, width, n_prefix, n_free, *lens,
+                           _ptr(cu_q_lens, "cu_q_lens", i32, (B + 1,)),
+                           _ptr(slot_mapping, "slot_mapping", torch.int64, (total_q,)),
+                           _ptr(positions, "positions", i32, (total_q,)), _ptr(used, "used", i32, (1,)))
+    _check(lib().dsa_page_plan(args, _stream_ptr(stream)), "dsa_page_plan")
+    if stream is not None:
+        _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
+                stream)
     return cu_q_lens, slot_mapping, positions, used
-
-
-def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16) -> int:
-    """Device pointer of a tensor whose last dimension is dense; the others may have any
-    strides that are multiples of 16 bytes."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
-    return t.data_ptr()
 
 
 def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor, cache_c: torch.Tensor,
@@ -756,64 +779,25 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
     when given; row t without positions) into cache_r [num_pages, page_size, 64], at the slots
     slot_mapping [n] (int64, page * page_size + row; negative = skip).  c_kv and k_rope may be
     views of one [n, 576] projection output."""
-    _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (cache_c, "cache_c", (None, None, None))])
+    _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (cache_c, "cache_c", (None, None, None)),
+             (rope_cos, "rope_cos", (None, None))])
     n, R = c_kv.shape
     rd = k_rope.shape[1]
     num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
-    _expect([(k_rope, "k_rope", (n, rd)), (slot_mapping, "slot_mapping", (n,)),
-             (cache_c, "cache_c", (num_pages, page_size, R)), (cache_r, "cache_r", (num_pages, page_size, rd)),
-             (norm_weight, "norm_weight", (R,)), (rope_cos, "rope_cos", (None, rd // 2)),
-             (positions, "positions", (n,))])
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin go together")
     rows = 0 if rope_cos is None else rope_cos.shape[0]
-    _expect([(rope_sin, "rope_sin", (rows, rd // 2))])
-    f32 = torch.float32
-    a = dsa_mla_cache_append_args(
-        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, float(norm_eps), _rows(c_kv, "c_kv"),
-        _rows(k_rope, "k_rope"), c_kv.stride(0), k_rope.stride(0), _dev(slot_mapping, "slot_mapping", torch.int64),
-        _dev(norm_weight, "norm_weight", f32), _dev(rope_cos, "rope_cos", f32), _dev(rope_sin, "rope_sin", f32),
-        _dev(positions, "positions", torch.int32), _dev(cache_c, "cache_c", torch.bfloat16),
-        _dev(cache_r, "cache_r", torch.bfloat16))
-    _check(lib().dsa_mla_cache_append(ctypes.byref(a), _stream_ptr(stream)), "dsa_mla_cache_append")
-    _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
-
-
-def make_prefix_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages=None, *,
-                         prefix_len: int, scale: float, out=None, lse=None, workspace=None):
-    """dsa_prefix_mla_args for these tensors (every shape checked); returns (args, kept
-    tensors, (out, lse)).  out, lse and the workspace are allocated when not given."""
-    _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
-             (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,))])
-    total_q, H, R = q_nope.shape
-    rd = q_rope.shape[2]
-    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
-    B = seq_lens.shape[0]
-    _expect([(q_rope, "q_rope", (total_q, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
-             (cache_r, "cache_r", (num_pages, page_size, rd)), (cu_q_lens, "cu_q_lens", (B + 1,)),
-             (block_tables, "block_tables", (B, None)), (prefix_pages, "prefix_pages", (None,))])
-    dev = q_nope.device
-    if out is None:
-        out = torch.empty((total_q, H, R), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
-    _expect([(out, "out", (total_q, H, R)), (lse, "lse", (total_q, H))])
-    i32, bf16 = torch.int32, torch.bfloat16
-    a = dsa_prefix_mla_args(
-        B, total_q, H, R, rd, page_size, num_pages, block_tables.shape[1], int(prefix_len),
-        0 if prefix_pages is None else prefix_pages.shape[0], float(scale), _rows(q_nope, "q_nope"),
-        _rows(q_rope, "q_rope"), q_nope.stride(0), q_nope.stride(1), q_rope.stride(0), q_rope.stride(1),
-        _dev(cache_c, "cache_c", bf16), _dev(cache_r, "cache_r", bf16), _dev(prefix_pages, "prefix_pages", i32),
-        _dev(block_tables, "block_tables", i32), _dev(cu_q_lens, "cu_q_lens", i32), _dev(seq_lens, "seq_lens", i32),
-        _dev(out, "out", bf16), _dev(lse, "lse", torch.float32))
-    if workspace is None:
-        n = ctypes.c_size_t(0)
-        _check(lib().dsa_prefix_mla_workspace_size(ctypes.byref(a), ctypes.byref(n)), "dsa_prefix_mla_workspace_size")
-        workspace = torch.empty(max(n.value, 16), dtype=torch.uint8, device=dev)
-    a.workspace = _dev(workspace, "workspace")
-    a.workspace_bytes = workspace.numel() * workspace.element_size()
-    return a, (q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
-               workspace), (out, lse)
+    f32, bf16 = torch.float32, torch.bfloat16
+    args = _APPEND_ARGS.pack(
+        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv", (n, R)),
+        _rows(k_rope, "k_rope", (n, rd)), c_kv.stride(0), k_rope.stride(0),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, (n,)), _ptr(norm_weight, "norm_weight", f32, (R,)),
+        _ptr(rope_cos, "rope_cos", f32, (rows, rd // 2)), _ptr(rope_sin, "rope_sin", f32, (rows, rd // 2)),
+        _ptr(positions, "positions", torch.int32, (n,)), _ptr(cache_c, "cache_c", bf16, (num_pages, page_size, R)),
+        _ptr(cache_r, "cache_r", bf16, (num_pages, page_size, rd)))
+    _check(lib().dsa_mla_cache_append(args, _stream_ptr(stream)), "dsa_mla_cache_append")
+    if stream is not None:
+        _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
 
 
 def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages=None, *,
@@ -821,13 +805,42 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     """Latent attention of a batch whose sequences share their first prefix_len tokens (their
     pages in prefix_pages; the rest through block_tables): (out [total_q, H, 512] bf16,
     lse [total_q, H] fp32, the natural logarithm of the sum of exponentials).  q_nope and
-    q_rope may be views of one [total_q, H, 576] tensor."""
-    a, keep, res = make_prefix_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens,
-                                        prefix_pages, prefix_len=prefix_len, scale=scale, out=out, lse=lse,
-                                        workspace=workspace)
-    _check(lib().dsa_prefix_mla(ctypes.byref(a), _stream_ptr(stream)), "dsa_prefix_mla")
-    _record(keep, stream)
-    return res
+    q_rope may be views of one [total_q, H, 576] tensor.  out, lse and the workspace
+    (dsa_prefix_mla_workspace_size bytes) are allocated when not given."""
+    _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
+             (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,)),
+             (block_tables, "block_tables", (None, None)), (prefix_pages, "prefix_pages", (None,))])
+    T, H, R = q_nope.shape
+    rd = q_rope.shape[2]
+    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
+    B, width = seq_lens.shape[0], block_tables.shape[1]
+    n_prefix = 0 if prefix_pages is None else prefix_pages.shape[0]
+    i32, bf16 = torch.int32, torch.bfloat16
+    sizes = (B, T, H, R, rd, page_size, num_pages, width, prefix_len, n_prefix, scale)
+    tensors = (_rows(q_nope, "q_nope", (T, H, R)), _rows(q_rope, "q_rope", (T, H, rd)), q_nope.stride(0),
+               q_nope.stride(1), q_rope.stride(0), q_rope.stride(1),
+               _ptr(cache_c, "cache_c", bf16, (num_pages, page_size, R)),
+               _ptr(cache_r, "cache_r", bf16, (num_pages, page_size, rd)),
+               _ptr(prefix_pages, "prefix_pages", i32, (n_prefix,)),
+               _ptr(block_tables, "block_tables", i32, (B, width)), _ptr(cu_q_lens, "cu_q_lens", i32, (B + 1,)),
+               _ptr(seq_lens, "seq_lens", i32, (B,)))
+    if out is None:
+        out = cache_c.new_empty((T, H, R))
+    if lse is None:
+        lse = cache_c.new_empty((T, H), dtype=torch.float32)
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(lib().dsa_prefix_mla_workspace_size(_PREFIX_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need)),
+               "dsa_prefix_mla_workspace_size")
+        workspace = cache_c.new_empty(max(need.value, 16), dtype=torch.uint8)
+    args = _PREFIX_ARGS.pack(*sizes, *tensors, _ptr(out, "out", bf16, (T, H, R)),
+                             _ptr(lse, "lse", torch.float32, (T, H)), _dev(workspace, "workspace"),
+                             workspace.numel() * workspace.element_size())
+    _check(lib().dsa_prefix_mla(args, _stream_ptr(stream)), "dsa_prefix_mla")
+    if stream is not None:
+        _record((q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
+                 workspace), stream)
+    return out, lse
 
 
 def dsa_test_arm_score_timeout(limit_ns: int) -> None:

@@ -61,7 +61,13 @@ struct Tile {
   int b;             // request, -1: rows of several requests (prefix only)
   int n_pre;         // blocks of the prefix; the rest are the request's own
   int limit;         // the most keys any of its rows sees
-  int pad[3];
+  int c0, c1;        // the parts that its blocks lie in (c1 < c0: none)
+  int pad;
+};
+// A query of a packed batch: its request's first own tile, its first row among the request's
+// rows, the keys it sees.
+struct Query {
+  int tile, row, sees, pad;
 };
 
 struct Args {
@@ -78,6 +84,8 @@ struct Args {
   Tile* tiles;
   long long* u0;           // [max_tiles + 1] first block of each tile in the line of all blocks
   int* head;               // [0] tiles, [1] packed prefix tiles, [2 + b] first own tile of request b
+  int* part_tile;          // [G] the tile that each part begins in
+  Query* queries;          // [total_q], packed batches only
   float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
   unsigned* status;
 };
@@ -116,6 +124,22 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
     n = room;
   }
   return static_cast<int>(max(n, 0LL));
+}
+
+// The line of U blocks in G = min(CTA pairs, U) parts, none of them empty: part c is
+// [c U / G, (c + 1) U / G).
+__device__ __forceinline__ int parts(const Args& a, long long U) {
+  return static_cast<int>(min(static_cast<long long>(a.G), U));
+}
+__device__ __forceinline__ long long part_begin(long long U, int G, int c) { return U * c / G; }
+__device__ __forceinline__ int part_of(long long U, int G, long long u) {
+  return static_cast<int>(((u + 1) * G - 1) / U);
+}
+// Where a piece of tile i in part c leaves its result: pieces that begin inside a tile are the
+// first of their part, those that only end inside one the last, so two slots a part hold them;
+// whole tiles come behind (they leave one only where rows are joined over two tiles).
+__device__ __forceinline__ long long piece_slot(int G, int c, int i, bool at_start, bool whole) {
+  return whole ? 2LL * G + i : 2LL * c + (at_start ? 1 : 0);
 }
 
 // ------------------------------------------------------------------ plan
@@ -164,7 +188,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
     const long long at = block_scan(n, wsum, &total);
     if (b < nreq) a.head[2 + b] = base + static_cast<int>(at);
     base += static_cast<int>(total);
-    __syncthreads();
   }
   const int n_tiles = min(base, a.max_tiles);
   if (tid == 0) {
@@ -173,9 +196,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
     a.head[2 + nreq] = base;
   }
   __syncthreads();
+  bool bad = false;
+  if (a.packed) {
+    for (int q = tid; q < a.total_q; q += kPlanThreads) {
+      const int b = request_of(a, q);
+      Query r;
+      r.sees = sees(a, b, q, &bad);
+      const int q0 = __ldg(a.cu + b);
+      const bool mine = q >= q0 && q < __ldg(a.cu + b + 1);
+      r.tile = mine ? a.head[2 + b] : n_tiles;  // n_tiles: no own keys (padding)
+      r.row = mine ? (q - q0) * a.H : 0;
+      r.pad = 0;
+      *reinterpret_cast<int4*>(a.queries + q) = *reinterpret_cast<const int4*>(&r);
+    }
+    __syncthreads();
+  }
   const int kO = a.prefix_len / kKeys;  // first block with own keys
   long long u = 0;
-  bool bad = false;
   for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
     long long units = 0;
@@ -186,12 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
         t.row0 = i * kRows;
         t.nrows = min(kRows, a.total_q * a.H - t.row0);
         t.b = -1;
-        const int tq0 = t.row0 / a.H, tq1 = (t.row0 + t.nrows - 1) / a.H;
-        int b = request_of(a, tq0);
-        for (int q = tq0; q <= tq1; ++q) {
-          while (b + 1 < a.B && __ldg(a.cu + b + 1) <= q) ++b;
-          t.limit = max(t.limit, sees(a, b, q, &bad));
-        }
+        for (int q = t.row0 / a.H; q <= (t.row0 + t.nrows - 1) / a.H; ++q) t.limit = max(t.limit, a.queries[q].sees);
       } else {
         int lo = 0, hi = nreq;  // the last b with head[2 + b] <= i
         while (hi - lo > 1) {
@@ -214,42 +246,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
     const long long at = block_scan(units, wsum, &total);
     if (i < n_tiles) a.u0[i] = u + at;
     u += total;
-    __syncthreads();
   }
   if (tid == 0) a.u0[n_tiles] = u;
   if (bad) atomicOr(a.status, kStatusUncovered);
-}
-
-// The line of U blocks in G = min(CTA pairs, U) parts, none of them empty: part c is
-// [c U / G, (c + 1) U / G).
-__device__ __forceinline__ int parts(const Args& a, long long U) {
-  return static_cast<int>(min(static_cast<long long>(a.G), U));
-}
-__device__ __forceinline__ long long part_begin(long long U, int G, int c) { return U * c / G; }
-__device__ __forceinline__ int part_of(long long U, int G, long long u) {
-  return static_cast<int>(((u + 1) * G - 1) / U);
-}
-// Where a piece of tile i in part c leaves its result: pieces that begin inside a tile are the
-// first of their part, those that only end inside one the last, so two slots a part hold them;
-// whole tiles come behind (they leave one only where rows are joined over two tiles).
-__device__ __forceinline__ long long piece_slot(int G, int c, int i, bool at_start, bool whole) {
-  return whole ? 2LL * G + i : 2LL * c + (at_start ? 1 : 0);
-}
-
-// Last tile i with u0[i] <= u, all lanes of a warp probing: a factor 32 a step.
-__device__ __forceinline__ int find_tile(const long long* u0, int n, long long u) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;  // u0[lo] <= u, u < u0[hi] (u0[n] = U)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int p = min(lo + lane * step, hi - 1);
-    const unsigned m = __ballot_sync(0xffffffffu, __ldcg(u0 + p) <= u);
-    const int last = 31 - __clz(m);  // lane 0 always holds
-    const int nlo = min(lo + last * step, hi - 1);
-    hi = last == 31 ? hi : min(lo + (last + 1) * step, hi);
-    lo = nlo;
+  __syncthreads();
+  // which parts each tile lies in, and the tile each part begins in
+  const int G = parts(a, u);
+  for (int i = tid; i < n_tiles; i += kPlanThreads) {
+    const long long b0 = a.u0[i], b1 = a.u0[i + 1];
+    int c0 = 0, c1 = -1;
+    if (b1 > b0) {
+      c0 = part_of(u, G, b0);
+      c1 = part_of(u, G, b1 - 1);
+      for (int c = part_begin(u, G, c0) == b0 ? c0 : c0 + 1; c <= c1; ++c) a.part_tile[c] = i;
+    }
+    a.tiles[i].c0 = c0;
+    a.tiles[i].c1 = c1;
   }
-  return lo;
 }
 
 // ------------------------------------------------------------------ attend
@@ -322,7 +335,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffMisc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 260);
-  volatile int* first_tile = reinterpret_cast<volatile int*>(smem + kOffMisc + 264);
   float* xmax = reinterpret_cast<float*>(smem + kOffMisc + 512);  // [2][4][64] by block parity, quarter, row
   const int rank = static_cast<int>(ptx::cluster_ctarank());
 
@@ -359,17 +371,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int n_tiles = __ldcg(a.head);
   const long long U = __ldcg(a.u0 + n_tiles);
   const int c = blockIdx.x >> 1, G = parts(a, U);
+  const int i_first = c < G ? __ldcg(a.part_tile + c) : 0;
   const long long u_lo = c < G ? part_begin(U, G, c) : 0, u_hi = c < G ? part_begin(U, G, c + 1) : 0;
-  if (warp == 0 && u_lo < u_hi) {
-    const int i = find_tile(a.u0, n_tiles, u_lo);
-    if (lane == 0) *first_tile = i;
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int i_first = u_lo < u_hi ? *first_tile : 0;
   const int box = min(a.page_size, 64);  // rows of one copy
   const int box_log2 = 31 - __clz(box);
   Piece p{i_first, 0, 0, 0};
@@ -571,8 +579,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int trow = rank * 64 + row;
       if (trow < t.nrows) {
         const int tq = (t.row0 + trow) / a.H;
-        bool bad = false;
-        lim = min(sees(a, t.b >= 0 ? t.b : request_of(a, tq), tq, &bad), t.limit);
+        bool bad = false;  // counted by the plan
+        lim = min(a.packed ? __ldcg(&a.queries[tq].sees) : sees(a, t.b, tq, &bad), t.limit);
       }
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const int tb = n & 1;
@@ -723,144 +731,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// An item is 16 latent columns of a group of 128 rows: a packed prefix tile, or a tile that a part
-// begins inside (the first such part names it).  Thread (r, y) takes row r and the pieces y, y + 4,
-// ..; the four meet in shared memory.  Tiles without any block get zeros.
-constexpr int kJoinCols = 4;  // columns of 4
+// A CTA of 512 threads joins some latent columns (of 4) of the 128 rows of a tile.
+// Packed batches: blockIdx = 32 * prefix tile + column group of 4; a row has the pieces of that
+// tile and of one of its request's own.  Otherwise blockIdx = 8 * part + g for every part that
+// begins inside a tile; the parts of a tile share its columns (1, 2 or 4 of them: 16, 8 or 4
+// columns a CTA), so that a tile of many pieces has many CTAs.  A thread takes row r; the four
+// threads of a row split the columns when there are up to four pieces, else the pieces, and meet
+// in shared memory.  Tiles without any block get zeros.
+constexpr int kCols = 4;  // columns (of 4) a thread
 __global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
-  __shared__ float4 acc_s[3][kJoinCols][kRows];
+  __shared__ float4 acc_s[3][kCols][kRows];
   __shared__ float2 ml_s[3][kRows];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int r = threadIdx.x & (kRows - 1), y = threadIdx.x >> 7;
   const int n_tiles = __ldcg(a.head);
-  const long long U = __ldcg(a.u0 + n_tiles);
-  const int G = parts(a, U);
-  constexpr int kSplit = kRank / 4 / kJoinCols;
-  const int groups = a.packed ? __ldcg(a.head + 1) : G;
-  for (int item = blockIdx.x; item < groups * kSplit; item += gridDim.x) {
-    const int col0 = (item % kSplit) * kJoinCols;  // neighbouring CTAs: other columns of the same rows
-    int g = item / kSplit;
-    if (!a.packed) {
-      if (g == 0) continue;
-      const long long u = part_begin(U, G, g);
-      g = find_tile(a.u0, n_tiles, u);
-      if (__ldcg(a.u0 + g) == u) continue;                                         // begins with a tile
-      if (part_begin(U, G, item / kSplit - 1) > __ldcg(a.u0 + g)) continue;        // an earlier part named it
+  int i, col0, n_col = kCols;
+  bool by_piece = true;
+  if (a.packed) {
+    i = blockIdx.x >> 5;
+    col0 = (blockIdx.x & 31) * kCols;
+    if (i >= __ldcg(a.head + 1)) return;
+  } else {
+    // zeros for tiles without blocks
+    for (int z = blockIdx.x; z < n_tiles; z += gridDim.x) {
+      if (__ldcg(&a.tiles[z].c1) >= 0) continue;
+      const int row0 = __ldcg(&a.tiles[z].row0), nrows = __ldcg(&a.tiles[z].nrows);
+      for (int e = threadIdx.x; e < nrows * (kRank / 8); e += blockDim.x)
+        reinterpret_cast<uint4*>(a.out + static_cast<long long>(row0) * kRank)[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.lse && threadIdx.x < nrows) a.lse[row0 + threadIdx.x] = -INFINITY;
     }
-    const int row0 = __ldcg(&a.tiles[g].row0), nrows = __ldcg(&a.tiles[g].nrows);
-    const int row = row0 + r;
-    const bool live = r < nrows;
-    // up to two tiles hold this row's pieces
-    int ti[2] = {g, -1}, rr[2] = {r, 0}, c0[2] = {0, 0}, c1[2] = {-1, -1};
-    const long long g0 = __ldcg(a.u0 + g), g1 = __ldcg(a.u0 + g + 1);
-    if (g1 > g0) {
-      c0[0] = part_of(U, G, g0);
-      c1[0] = part_of(U, G, g1 - 1);
+    const long long U = __ldcg(a.u0 + n_tiles);
+    const int c = blockIdx.x >> 3;
+    if (c >= parts(a, U)) return;
+    i = __ldcg(a.part_tile + c);
+    const int first = c - __ldcg(&a.tiles[i].c0) - 1;  // which of the parts that begin inside the tile
+    const int pieces = __ldcg(&a.tiles[i].c1) - __ldcg(&a.tiles[i].c0) + 1;
+    const int share = pieces > 4 ? 4 : (pieces > 2 ? 2 : 1);
+    if (first < 0 || first >= share) return;           // begins with the tile (first = -1), or not needed
+    const int width = 16 / share;
+    col0 = ((blockIdx.x & 7) * share + first) * width;
+    by_piece = pieces > 4;
+    if (!by_piece) {
+      n_col = width / 4;
+      col0 += y * n_col;
     }
-    if (a.packed && live) {
-      const int tq = row / a.H;
-      const int b = request_of(a, tq);
-      if (tq < __ldg(a.cu + b + 1)) {
-        const int local = row - __ldg(a.cu + b) * a.H;
-        ti[1] = __ldcg(a.head + 2 + b) + local / kRows;
-        rr[1] = local % kRows;
-        if (ti[1] < n_tiles) {
-          const long long b0 = __ldcg(a.u0 + ti[1]), b1 = __ldcg(a.u0 + ti[1] + 1);
-          if (b1 > b0) {
-            c0[1] = part_of(U, G, b0);
-            c1[1] = part_of(U, G, b1 - 1);
-          }
-        }
-      }
+  }
+  const int row0 = __ldcg(&a.tiles[i].row0), nrows = __ldcg(&a.tiles[i].nrows);
+  const int row = row0 + r;
+  const bool live = r < nrows;
+  // up to two tiles hold this row's pieces
+  int ti[2] = {i, -1}, rr[2] = {r, 0}, c0[2] = {__ldcg(&a.tiles[i].c0), 0}, c1[2] = {__ldcg(&a.tiles[i].c1), -1};
+  if (a.packed && live) {
+    const int tq = row / a.H;
+    const int4 q = __ldcg(reinterpret_cast<const int4*>(a.queries + tq));
+    const int local = q.y + row - tq * a.H;
+    ti[1] = q.x + local / kRows;
+    rr[1] = local % kRows;
+    if (ti[1] < n_tiles) {
+      c0[1] = __ldcg(&a.tiles[ti[1]].c0);
+      c1[1] = __ldcg(&a.tiles[ti[1]].c1);
     }
-    // running maximum, sum and columns over this thread's pieces
-    const int n0 = c1[0] - c0[0] + 1, np = n0 + c1[1] - c0[1] + 1;
-    float M = -INFINITY, L = 0.f;
-    float4 acc[kJoinCols];
+  }
+  // running maximum, sum and columns over this thread's pieces
+  const int n0 = c1[0] - c0[0] + 1, np = n0 + c1[1] - c0[1] + 1;
+  float M = -INFINITY, L = 0.f;
+  float4 acc[kCols];
 #pragma unroll
-    for (int q = 0; q < kJoinCols; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
+  for (int q = 0; q < kCols; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
 #pragma unroll 2
-      for (int k = y; k < np; k += 4) {
-        const int w = k < n0 ? 0 : 1, c = c0[w] + k - (w ? n0 : 0);
-        const long long s = piece_slot(a.G, c, ti[w], c == c0[w], c0[w] == c1[w]);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + s * kRows + rr[w]);
-        const float4* src = reinterpret_cast<const float4*>(a.part_o) + (s * (kRank / 4) + col0) * kRows + rr[w];
-        float4 o[kJoinCols];
+    for (int k = by_piece ? y : 0; k < np; k += by_piece ? 4 : 1) {
+      const int w = k < n0 ? 0 : 1, c = c0[w] + k - (w ? n0 : 0);
+      const long long s = piece_slot(a.G, c, ti[w], c == c0[w], c0[w] == c1[w]);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + s * kRows + rr[w]);
+      const float4* src = reinterpret_cast<const float4*>(a.part_o) + (s * (kRank / 4) + col0) * kRows + rr[w];
+      float4 o[kCols];
 #pragma unroll
-        for (int q = 0; q < kJoinCols; ++q) o[q] = __ldcg(src + q * kRows);
-        if (ml.x == -INFINITY) continue;  // a piece in which the row saw nothing
-        const float Mn = fmaxf(M, ml.x);
-        const float f = exp2f(M - Mn), e = exp2f(ml.x - Mn);  // f = 0 the first time
-        M = Mn;
-        L = L * f + e * ml.y;
+      for (int q = 0; q < kCols; ++q) o[q] = q < n_col ? __ldcg(src + q * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ml.x == -INFINITY) continue;  // a piece in which the row saw nothing
+      const float Mn = fmaxf(M, ml.x);
+      const float f = exp2f(M - Mn), e = exp2f(ml.x - Mn);  // f = 0 the first time
+      M = Mn;
+      L = L * f + e * ml.y;
 #pragma unroll
-        for (int q = 0; q < kJoinCols; ++q) {
-          acc[q].x = acc[q].x * f + e * o[q].x;
-          acc[q].y = acc[q].y * f + e * o[q].y;
-          acc[q].z = acc[q].z * f + e * o[q].z;
-          acc[q].w = acc[q].w * f + e * o[q].w;
-        }
+      for (int q = 0; q < kCols; ++q) {
+        acc[q].x = acc[q].x * f + e * o[q].x;
+        acc[q].y = acc[q].y * f + e * o[q].y;
+        acc[q].z = acc[q].z * f + e * o[q].z;
+        acc[q].w = acc[q].w * f + e * o[q].w;
       }
     }
-    __syncthreads();  // the last item's reads are done
+  }
+  if (by_piece) {  // the four threads of a row meet
     if (y > 0) {
       ml_s[y - 1][r] = make_float2(M, L);
 #pragma unroll
-      for (int q = 0; q < kJoinCols; ++q) acc_s[y - 1][q][r] = acc[q];
+      for (int q = 0; q < kCols; ++q) acc_s[y - 1][q][r] = acc[q];
     }
     __syncthreads();
-    if (y == 0 && live) {
-      float2 ml[3];
-      float Mn = M;
+    if (y > 0) return;
+    float2 ml[3];
+    float Mn = M;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        ml[k] = ml_s[k][r];
-        Mn = fmaxf(Mn, ml[k].x);
-      }
-      const float none = Mn == -INFINITY ? 0.f : Mn;
-      const float f = exp2f(M - none);
-      L *= f;
-#pragma unroll
-      for (int q = 0; q < kJoinCols; ++q)
-        acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float e = exp2f(ml[k].x - none);
-        L += e * ml[k].y;
-#pragma unroll
-        for (int q = 0; q < kJoinCols; ++q) {
-          const float4 o = acc_s[k][q][r];
-          acc[q].x += e * o.x;
-          acc[q].y += e * o.y;
-          acc[q].z += e * o.z;
-          acc[q].w += e * o.w;
-        }
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      uint32_t w[2 * kJoinCols];
-#pragma unroll
-      for (int q = 0; q < kJoinCols; ++q) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * inv, acc[q].y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * inv, acc[q].w * inv);
-        w[2 * q] = *reinterpret_cast<const uint32_t*>(&lo);
-        w[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-      }
-      uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<long long>(row) * kRank + col0 * 4);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      if (a.lse && col0 == 0) a.lse[row] = L > 0.f ? (Mn + log2f(L)) * kLn2 : -INFINITY;
+    for (int k = 0; k < 3; ++k) {
+      ml[k] = ml_s[k][r];
+      Mn = fmaxf(Mn, ml[k].x);
     }
+    const float none = Mn == -INFINITY ? 0.f : Mn;
+    const float f = exp2f(M - none);
+    L *= f;
+#pragma unroll
+    for (int q = 0; q < kCols; ++q)
+      acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const float e = exp2f(ml[k].x - none);
+      L += e * ml[k].y;
+#pragma unroll
+      for (int q = 0; q < kCols; ++q) {
+        const float4 o = acc_s[k][q][r];
+        acc[q].x += e * o.x;
+        acc[q].y += e * o.y;
+        acc[q].z += e * o.z;
+        acc[q].w += e * o.w;
+      }
+    }
+    M = Mn;
   }
-  if (a.packed) return;  // every row lies in a packed tile
-  for (int i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-    if (__ldcg(a.u0 + i) != __ldcg(a.u0 + i + 1)) continue;
-    const int row0 = __ldcg(&a.tiles[i].row0), nrows = __ldcg(&a.tiles[i].nrows);
-    for (int e = threadIdx.x; e < nrows * (kRank / 8); e += blockDim.x)
-      reinterpret_cast<uint4*>(a.out + static_cast<long long>(row0) * kRank)[e] = make_uint4(0u, 0u, 0u, 0u);
-    if (a.lse && threadIdx.x < nrows) a.lse[row0 + threadIdx.x] = -INFINITY;
+  if (!live) return;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kRank + col0 * 4);
+#pragma unroll
+  for (int q = 0; q < kCols; ++q) {
+    if (q >= n_col) break;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * inv, acc[q].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * inv, acc[q].w * inv);
+    dst[q] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
+  if (a.lse && col0 == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 bool key_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
@@ -929,7 +938,7 @@ dsa_status validate(const dsa_prefix_mla_args* a) {
 
 struct Layout {
   int packed, max_tiles, G;
-  size_t off_tiles, off_u0, off_head, off_ml, off_o, total;
+  size_t off_tiles, off_u0, off_head, off_parts, off_queries, off_ml, off_o, total;
 };
 
 Layout layout(const dsa_prefix_mla_args* a) {
@@ -945,7 +954,9 @@ Layout layout(const dsa_prefix_mla_args* a) {
   p.off_tiles = 0;
   p.off_u0 = up(p.off_tiles + sizeof(Tile) * p.max_tiles);
   p.off_head = up(p.off_u0 + 8 * (static_cast<size_t>(p.max_tiles) + 1));
-  p.off_ml = up(p.off_head + 4 * (static_cast<size_t>(a->B) + 4));
+  p.off_parts = up(p.off_head + 4 * (static_cast<size_t>(a->B) + 4));
+  p.off_queries = up(p.off_parts + 4 * static_cast<size_t>(p.G));
+  p.off_ml = up(p.off_queries + (p.packed ? sizeof(Query) * a->total_q : 0));
   p.off_o = up(p.off_ml + slots * kRows * 8);
   p.total = up(p.off_o + slots * kRows * kRank * 4);
   return p;
@@ -1022,6 +1033,8 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.tiles = reinterpret_cast<Tile*>(ws + p.off_tiles);
   k.u0 = reinterpret_cast<long long*>(ws + p.off_u0);
   k.head = reinterpret_cast<int*>(ws + p.off_head);
+  k.part_tile = reinterpret_cast<int*>(ws + p.off_parts);
+  k.queries = reinterpret_cast<Query*>(ws + p.off_queries);
   k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
   k.part_o = reinterpret_cast<float*>(ws + p.off_o);
   k.status = status;
@@ -1031,9 +1044,8 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   e = launch_pdl(prefix_mla_kernel, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  const long long groups = p.packed ? (rows + kRows - 1) / kRows : p.G;
-  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(std::min(groups * (kRank / 4 / kJoinCols), 608LL))),
-                 dim3(512), 0, s, k);
+  const long long ctas = p.packed ? (rows + kRows - 1) / kRows * 32 : p.G * 8LL;
+  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
