@@ -697,21 +697,17 @@ assert _APPEND_ARGS.size == ctypes.sizeof(dsa_mla_cache_append_args)
 assert _PREFIX_ARGS.size == ctypes.sizeof(dsa_prefix_mla_args)
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape) -> int:
-    """Device pointer of a contiguous CUDA tensor of this type and shape (0 for None)."""
+def _ptr(t: Optional[torch.Tensor], name: str, dtype) -> int:
+    """Device pointer of a contiguous CUDA tensor of this type (0 for None)."""
     if t is None:
         return 0
-    if t.shape != shape:
-        _expect([(t, name, shape)])
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         _dev(t, name, dtype)
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, shape) -> int:
+def _rows(t: torch.Tensor, name: str) -> int:
     """Device pointer of a bf16 tensor whose last dimension is dense, the others in any strides."""
-    if t.shape != shape:
-        _expect([(t, name, shape)])
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
@@ -719,6 +715,11 @@ def _rows(t: torch.Tensor, name: str, shape) -> int:
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be dense in its last dimension")
     return t.data_ptr()
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """Raw cudaStream_t of `stream`, or of the current stream on the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
 
 
 def _record(tensors, stream) -> None:
@@ -740,28 +741,30 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     of free_pages in request order, -1 behind.  total_q: the outputs' length, at least the
     sum of q_lens (the rest is -1).  Returns (cu_q_lens [B + 1] int32, slot_mapping [total_q]
     int64, positions [total_q] int32, used [1] int32: the free pages taken)."""
-    _expect([(q_lens, "q_lens", (None,)), (block_tables, "block_tables", (q_lens.shape[0], None)),
-             (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
-    B, width = block_tables.shape
-    i32 = torch.int32
-    n_free, n_prefix = free_pages.shape[0], 0 if prefix_pages is None else prefix_pages.shape[0]
-    lens = (_ptr(q_lens, "q_lens", i32, (B,)), _ptr(seq_lens, "seq_lens", i32, (B,)),
-            _ptr(prefix_pages, "prefix_pages", i32, (n_prefix,)), _ptr(free_pages, "free_pages", i32, (n_free,)),
-            _ptr(block_tables, "block_tables", i32, (B, width)))
-    new = block_tables.new_empty
+    width = block_tables.shape[-1]
+    B = q_lens.shape[0] if q_lens.dim() == 1 else -1
+    if not (q_lens.shape == seq_lens.shape == (B,) and block_tables.shape == (B, width) and free_pages.dim() == 1
+            and (prefix_pages is None or prefix_pages.dim() == 1)):
+        _expect([(q_lens, "q_lens", (None,)), (seq_lens, "seq_lens", (B,)), (block_tables, "block_tables", (B, None)),
+                 (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
+    i32, dev = torch.int32, block_tables.device
+    lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
+            _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
     if cu_q_lens is None:
-        cu_q_lens = new(B + 1)
+        cu_q_lens = torch.empty(B + 1, dtype=i32, device=dev)
     if slot_mapping is None:
-        slot_mapping = new(total_q, dtype=torch.int64)
+        slot_mapping = torch.empty(total_q, dtype=torch.int64, device=dev)
     if positions is None:
-        positions = new(total_q)
+        positions = torch.empty(total_q, dtype=i32, device=dev)
     if used is None:
-        used = new(1)
-    args = _PLAN_ARGS.pack(B, total_q, page_size, width, n_prefix, n_free, *lens,
-                           _ptr(cu_q_lens, "cu_q_lens", i32, (B + 1,)),
-                           _ptr(slot_mapping, "slot_mapping", torch.int64, (total_q,)),
-                           _ptr(positions, "positions", i32, (total_q,)), _ptr(used, "used", i32, (1,)))
-    _check(lib().dsa_page_plan(args, _stream_ptr(stream)), "dsa_page_plan")
+        used = torch.empty(1, dtype=i32, device=dev)
+    _expect([(cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
+             (positions, "positions", (total_q,)), (used, "used", (1,))])
+    args = _PLAN_ARGS.pack(B, total_q, page_size, width, 0 if prefix_pages is None else prefix_pages.shape[0],
+                           free_pages.shape[0], *lens, _ptr(cu_q_lens, "cu_q_lens", i32),
+                           _ptr(slot_mapping, "slot_mapping", torch.int64), _ptr(positions, "positions", i32),
+                           _ptr(used, "used", i32))
+    _check(lib().dsa_page_plan(args, _stream_of(block_tables, stream)), "dsa_page_plan")
     if stream is not None:
         _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
                 stream)
@@ -779,23 +782,31 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
     when given; row t without positions) into cache_r [num_pages, page_size, 64], at the slots
     slot_mapping [n] (int64, page * page_size + row; negative = skip).  c_kv and k_rope may be
     views of one [n, 576] projection output."""
-    _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (cache_c, "cache_c", (None, None, None)),
-             (rope_cos, "rope_cos", (None, None))])
+    if not (c_kv.dim() == k_rope.dim() == 2 and cache_c.dim() == 3 and (rope_cos is None or rope_cos.dim() == 2)):
+        _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)),
+                 (cache_c, "cache_c", (None, None, None)), (rope_cos, "rope_cos", (None, None))])
     n, R = c_kv.shape
     rd = k_rope.shape[1]
-    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
+    num_pages, page_size = cache_c.shape[:2]
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin go together")
     rows = 0 if rope_cos is None else rope_cos.shape[0]
+    table = (rows, rd // 2)
+    if not (k_rope.shape[0] == n and slot_mapping.shape == (n,) and cache_c.shape[2] == R
+            and cache_r.shape == (num_pages, page_size, rd) and (norm_weight is None or norm_weight.shape == (R,))
+            and (rope_cos is None or rope_cos.shape == rope_sin.shape == table)
+            and (positions is None or positions.shape == (n,))):
+        _expect([(k_rope, "k_rope", (n, rd)), (slot_mapping, "slot_mapping", (n,)),
+                 (cache_c, "cache_c", (num_pages, page_size, R)), (cache_r, "cache_r", (num_pages, page_size, rd)),
+                 (norm_weight, "norm_weight", (R,)), (rope_cos, "rope_cos", table), (rope_sin, "rope_sin", table),
+                 (positions, "positions", (n,))])
     f32, bf16 = torch.float32, torch.bfloat16
     args = _APPEND_ARGS.pack(
-        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv", (n, R)),
-        _rows(k_rope, "k_rope", (n, rd)), c_kv.stride(0), k_rope.stride(0),
-        _ptr(slot_mapping, "slot_mapping", torch.int64, (n,)), _ptr(norm_weight, "norm_weight", f32, (R,)),
-        _ptr(rope_cos, "rope_cos", f32, (rows, rd // 2)), _ptr(rope_sin, "rope_sin", f32, (rows, rd // 2)),
-        _ptr(positions, "positions", torch.int32, (n,)), _ptr(cache_c, "cache_c", bf16, (num_pages, page_size, R)),
-        _ptr(cache_r, "cache_r", bf16, (num_pages, page_size, rd)))
-    _check(lib().dsa_mla_cache_append(args, _stream_ptr(stream)), "dsa_mla_cache_append")
+        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv"),
+        _rows(k_rope, "k_rope"), c_kv.stride(0), k_rope.stride(0), _ptr(slot_mapping, "slot_mapping", torch.int64),
+        _ptr(norm_weight, "norm_weight", f32), _ptr(rope_cos, "rope_cos", f32), _ptr(rope_sin, "rope_sin", f32),
+        _ptr(positions, "positions", torch.int32), _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16))
+    _check(lib().dsa_mla_cache_append(args, _stream_of(cache_c, stream)), "dsa_mla_cache_append")
     if stream is not None:
         _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
 
@@ -807,36 +818,40 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     lse [total_q, H] fp32, the natural logarithm of the sum of exponentials).  q_nope and
     q_rope may be views of one [total_q, H, 576] tensor.  out, lse and the workspace
     (dsa_prefix_mla_workspace_size bytes) are allocated when not given."""
-    _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
-             (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,)),
-             (block_tables, "block_tables", (None, None)), (prefix_pages, "prefix_pages", (None,))])
+    if not (q_nope.dim() == q_rope.dim() == cache_c.dim() == 3 and seq_lens.dim() == 1 and block_tables.dim() == 2
+            and (prefix_pages is None or prefix_pages.dim() == 1)):
+        _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
+                 (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,)),
+                 (block_tables, "block_tables", (None, None)), (prefix_pages, "prefix_pages", (None,))])
     T, H, R = q_nope.shape
     rd = q_rope.shape[2]
-    num_pages, page_size = cache_c.shape[0], cache_c.shape[1]
+    num_pages, page_size = cache_c.shape[:2]
     B, width = seq_lens.shape[0], block_tables.shape[1]
-    n_prefix = 0 if prefix_pages is None else prefix_pages.shape[0]
-    i32, bf16 = torch.int32, torch.bfloat16
-    sizes = (B, T, H, R, rd, page_size, num_pages, width, prefix_len, n_prefix, scale)
-    tensors = (_rows(q_nope, "q_nope", (T, H, R)), _rows(q_rope, "q_rope", (T, H, rd)), q_nope.stride(0),
-               q_nope.stride(1), q_rope.stride(0), q_rope.stride(1),
-               _ptr(cache_c, "cache_c", bf16, (num_pages, page_size, R)),
-               _ptr(cache_r, "cache_r", bf16, (num_pages, page_size, rd)),
-               _ptr(prefix_pages, "prefix_pages", i32, (n_prefix,)),
-               _ptr(block_tables, "block_tables", i32, (B, width)), _ptr(cu_q_lens, "cu_q_lens", i32, (B + 1,)),
-               _ptr(seq_lens, "seq_lens", i32, (B,)))
+    i32, f32, bf16, dev = torch.int32, torch.float32, torch.bfloat16, cache_c.device
+    if not (q_rope.shape[:2] == (T, H) and cache_c.shape[2] == R and cache_r.shape == (num_pages, page_size, rd)
+            and block_tables.shape[0] == B and cu_q_lens.shape == (B + 1,)
+            and (out is None or out.shape == (T, H, R)) and (lse is None or lse.shape == (T, H))):
+        _expect([(q_rope, "q_rope", (T, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
+                 (cache_r, "cache_r", (num_pages, page_size, rd)), (block_tables, "block_tables", (B, None)),
+                 (cu_q_lens, "cu_q_lens", (B + 1,)), (out, "out", (T, H, R)), (lse, "lse", (T, H))])
+    sizes = (B, T, H, R, rd, page_size, num_pages, width, prefix_len,
+             0 if prefix_pages is None else prefix_pages.shape[0], scale)
+    tensors = (_rows(q_nope, "q_nope"), _rows(q_rope, "q_rope"), *q_nope.stride()[:2], *q_rope.stride()[:2],
+               _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16),
+               _ptr(prefix_pages, "prefix_pages", i32), _ptr(block_tables, "block_tables", i32),
+               _ptr(cu_q_lens, "cu_q_lens", i32), _ptr(seq_lens, "seq_lens", i32))
     if out is None:
-        out = cache_c.new_empty((T, H, R))
+        out = torch.empty((T, H, R), dtype=bf16, device=dev)
     if lse is None:
-        lse = cache_c.new_empty((T, H), dtype=torch.float32)
+        lse = torch.empty((T, H), dtype=f32, device=dev)
     if workspace is None:
         need = ctypes.c_size_t(0)
         _check(lib().dsa_prefix_mla_workspace_size(_PREFIX_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need)),
                "dsa_prefix_mla_workspace_size")
-        workspace = cache_c.new_empty(max(need.value, 16), dtype=torch.uint8)
-    args = _PREFIX_ARGS.pack(*sizes, *tensors, _ptr(out, "out", bf16, (T, H, R)),
-                             _ptr(lse, "lse", torch.float32, (T, H)), _dev(workspace, "workspace"),
-                             workspace.numel() * workspace.element_size())
-    _check(lib().dsa_prefix_mla(args, _stream_ptr(stream)), "dsa_prefix_mla")
+        workspace = torch.empty(max(need.value, 16), dtype=torch.uint8, device=dev)
+    args = _PREFIX_ARGS.pack(*sizes, *tensors, _ptr(out, "out", bf16), _ptr(lse, "lse", f32),
+                             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    _check(lib().dsa_prefix_mla(args, _stream_of(cache_c, stream)), "dsa_prefix_mla")
     if stream is not None:
         _record((q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
                  workspace), stream)

@@ -54,6 +54,7 @@ constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtom
 constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
 constexpr size_t kSmem = kOffMisc + 3072;
 constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
+constexpr int kSetup = 3;                                 // what a tile costs beside its blocks, in blocks
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Tile {
@@ -82,7 +83,7 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   Tile* tiles;
-  long long* u0;           // [max_tiles + 1] first block of each tile in the line of all blocks
+  long long* u0;           // [max_tiles + 1] where each tile begins in the line of all blocks
   int* head;               // [0] tiles, [1] packed prefix tiles, [2 + b] first own tile of request b
   int* part_tile;          // [G] the tile that each part begins in
   Query* queries;          // [total_q], packed batches only
@@ -126,8 +127,11 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
   return static_cast<int>(max(n, 0LL));
 }
 
-// The line of U blocks in G = min(CTA pairs, U) parts, none of them empty: part c is
-// [c U / G, (c + 1) U / G).
+// The line of all tiles, U long: a tile's blocks stand behind kSetup places for what it costs to
+// begin and end one (its queries, its first copies, its result: about 5 us).  Without them the
+// parts with many short tiles end last: 64 requests x 64 heads behind 8192 keys took 100 us in
+// this kernel, with them ATTEND_B64_US.  The line is cut into G = min(CTA pairs, U) parts, part c
+// being [c U / G, (c + 1) U / G); a part may hold no block.
 __device__ __forceinline__ int parts(const Args& a, long long U) {
   return static_cast<int>(min(static_cast<long long>(a.G), U));
 }
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
         own = t.limit > a.prefix_len ? (t.limit + kKeys - 1) / kKeys - kO : 0;
       }
       t.n_pre = (a.packed && i >= n_pre_tiles) ? 0 : (min(t.limit, a.prefix_len) + kKeys - 1) / kKeys;
-      units = t.n_pre + own;
+      units = t.n_pre + own > 0 ? t.n_pre + own + kSetup : 0;
       a.tiles[i] = t;
     }
     long long total;
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
   if (tid == 0) a.u0[n_tiles] = u;
   if (bad) atomicOr(a.status, kStatusUncovered);
   __syncthreads();
-  // which parts each tile lies in, and the tile each part begins in
+  // the parts that each tile's blocks lie in, and the tile that each part begins in
   const int G = parts(a, u);
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
     const long long b0 = a.u0[i], b1 = a.u0[i + 1];
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
       c0 = part_of(u, G, b0);
       c1 = part_of(u, G, b1 - 1);
       for (int c = part_begin(u, G, c0) == b0 ? c0 : c0 + 1; c <= c1; ++c) a.part_tile[c] = i;
+      c0 = part_of(u, G, b0 + kSetup);
     }
     a.tiles[i].c0 = c0;
     a.tiles[i].c1 = c1;
@@ -269,26 +274,30 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
 // The part's pieces: tile i, its blocks [k0, k1).  Every role walks the same list.
 struct Piece {
   int i, k0, k1;
-  long long u;   // first block of the piece in the line
+  bool whole;       // all the tile's blocks
+  long long next;   // where the next piece begins in the line
 };
-__device__ __forceinline__ bool next_piece(const Args& a, Piece& p, long long u, long long u_hi, Tile& t) {
-  if (u >= u_hi) return false;
-  long long b0 = __ldcg(a.u0 + p.i), b1 = __ldcg(a.u0 + p.i + 1);
-  while (b1 <= u) {  // tiles without blocks, and the one just done
-    ++p.i;
-    b0 = b1;
-    b1 = __ldcg(a.u0 + p.i + 1);
+__device__ __forceinline__ bool next_piece(const Args& a, Piece& p, long long u_hi, Tile& t) {
+  while (p.next < u_hi) {
+    const long long b0 = __ldcg(a.u0 + p.i), b1 = __ldcg(a.u0 + p.i + 1);
+    const long long first = b0 + kSetup, from = p.next, to = min(b1, u_hi);
+    if (b1 > from) {
+      const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
+      t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
+      t.row0 = w.x;
+      t.nrows = w.y;
+      t.b = w.z;
+      t.n_pre = w.w;
+      p.k0 = static_cast<int>(max(from - first, 0LL));
+      p.k1 = static_cast<int>(max(to - first, 0LL));
+      p.whole = p.k0 == 0 && to == b1;
+      p.next = to;
+      if (p.k1 > p.k0) return true;
+      if (to == u_hi) return false;  // the part ends before the tile's first block
+    }
+    ++p.i;  // done, or without blocks
   }
-  p.u = u;
-  p.k0 = static_cast<int>(u - b0);
-  p.k1 = static_cast<int>(min(b1, u_hi) - b0);
-  const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
-  t.row0 = w.x;
-  t.nrows = w.y;
-  t.b = w.z;
-  t.n_pre = w.w;
-  t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
-  return true;
+  return false;
 }
 
 // Block k of a tile: its first position, and the positions [lo, hi) of it that the tile sees.
@@ -380,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
   const int box = min(a.page_size, 64);  // rows of one copy
   const int box_log2 = 31 - __clz(box);
-  Piece p{i_first, 0, 0, 0};
+  Piece p{i_first, 0, 0, false, u_lo};
   Tile t;
 
   if (warp == 15) {
@@ -398,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout)) != 0;
       };
       uint32_t n1 = 0, n2 = 0, seg = 0;  // blocks whose S / P . V was issued, pieces
-      for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
+      for (; ok && next_piece(a, p, u_hi, t); ++seg) {
         wait(&bars->qfull, seg & 1);
         const int nblk = p.k1 - p.k0;
         for (int i = 0; ok && i <= nblk; ++i) {
@@ -464,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
     uint32_t n = 0;
     bool ok = true;
-    for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+    while (ok && next_piece(a, p, u_hi, t)) {
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
@@ -496,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
     uint32_t n = 0, cleared = 0;
     bool ok = true;
-    for (long long u = u_lo; ok && next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+    while (ok && next_piece(a, p, u_hi, t)) {
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
@@ -543,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int c16 = gt & 7;
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
     uint32_t seg = 0;
-    for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0), ++seg) {
+    for (; next_piece(a, p, u_hi, t); ++seg) {
       const bool good = ptx::mbar_spin(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
       if (!__all_sync(0xffffffffu, good)) break;
       for (int r = gt >> 3; r < 64; r += 8) {  // eight threads a row, 128 bytes at a time
@@ -573,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&bars->sempty[0]), 0);
     bool ok = true;
     uint32_t n = 0;
-    for (long long u = u_lo; next_piece(a, p, u, u_hi, t); u = p.u + (p.k1 - p.k0)) {
+    while (next_piece(a, p, u_hi, t)) {
       float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this quarter's sum
       int lim = 0;                   // keys this row sees
       const int trow = rank * 64 + row;
@@ -676,8 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the piece's result
       const bool at_start = p.k0 == 0;
-      const bool whole = at_start && p.u + (p.k1 - p.k0) == __ldcg(a.u0 + p.i + 1);
-      const bool direct = whole && !a.packed;
+      const bool direct = p.whole && !a.packed;
       if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                                   kStatusTimeout)) != 0;
       float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
@@ -686,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       l = (xs[0] + xs[64]) + (xs[128] + xs[192]);
       ptx::named_bar_sync(row_bar, 128);  // read before the next piece writes there
       const bool live = trow < t.nrows && ok;
-      const long long slot = piece_slot(a.G, c, p.i, at_start, whole);
+      const long long slot = piece_slot(a.G, c, p.i, at_start, p.whole);
       if (live && quarter == 0) {
         if (!direct) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + trow) * 2) = make_float2(m, l);
         else if (a.lse) a.lse[t.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
