@@ -750,6 +750,10 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     i32, dev = torch.int32, block_tables.device
     lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
             _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
+    for t, name, shape in ((cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
+                           (positions, "positions", (total_q,)), (used, "used", (1,))):
+        if t is not None and t.shape != shape:
+            _expect([(t, name, shape)])
     if cu_q_lens is None:
         cu_q_lens = torch.empty(B + 1, dtype=i32, device=dev)
     if slot_mapping is None:
@@ -758,8 +762,6 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
         positions = torch.empty(total_q, dtype=i32, device=dev)
     if used is None:
         used = torch.empty(1, dtype=i32, device=dev)
-    _expect([(cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
-             (positions, "positions", (total_q,)), (used, "used", (1,))])
     args = _PLAN_ARGS.pack(B, total_q, page_size, width, 0 if prefix_pages is None else prefix_pages.shape[0],
                            free_pages.shape[0], *lens, _ptr(cu_q_lens, "cu_q_lens", i32),
                            _ptr(slot_mapping, "slot_mapping", torch.int64), _ptr(positions, "positions", i32),

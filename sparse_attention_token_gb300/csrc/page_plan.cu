@@ -136,11 +136,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const dsa_page_
   const int W = a.max_pages_per_seq;
   const int vec = (W % 4 == 0 && (reinterpret_cast<uintptr_t>(a.block_tables) & 15u) == 0) ? 4 : 1;
   const int per_row = W / vec;
-  const long long units = static_cast<long long>(nb) * per_row;
   const long long step = static_cast<long long>(gridDim.y) * kPlanThreads;
-  for (long long u = static_cast<long long>(blockIdx.y) * kPlanThreads + tid; u < units; u += step) {
-    const int i = static_cast<int>(u / per_row);
-    const int j0 = static_cast<int>(u - static_cast<long long>(i) * per_row) * vec;
+  // (i, j) advance by step without a division an entry
+  const int step_i = per_row > 0 ? static_cast<int>(step / per_row) : 0;
+  const int step_j = per_row > 0 ? static_cast<int>(step - static_cast<long long>(step_i) * per_row) : 0;
+  const int start = blockIdx.y * kPlanThreads + tid;
+  int i = per_row > 0 ? start / per_row : nb, j = per_row > 0 ? start - i * per_row : 0;
+  for (; i < nb; i += step_i, j += step_j) {
+    if (j >= per_row) {
+      j -= per_row;
+      if (++i >= nb) break;
+    }
+    const int j0 = j * vec;
     int32_t* row = a.block_tables + static_cast<long long>(b0 + i) * W;
     const int held = s_held[i], have = s_have[i];
     const int f = have > 0 ? min(a.num_prefix_pages, W) : 0;  // have = 0: an empty request
@@ -148,9 +155,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const dsa_page_
       *reinterpret_cast<int4*>(row + j0) = make_int4(-1, -1, -1, -1);
       continue;
     }
-    for (int j = j0; j < j0 + vec; ++j) {
-      if (j >= f && j < held) continue;
-      row[j] = j < have ? page_at(i, j) : -1;
+    for (int e = j0; e < j0 + vec; ++e) {
+      if (e >= f && e < held) continue;
+      row[e] = e < have ? page_at(i, e) : -1;
     }
   }
 

@@ -65,6 +65,10 @@ struct Tile {
   int c0, c1;        // the parts that its blocks lie in (c1 < c0: none)
   int pad;
 };
+// The tile that a part begins in.
+struct Part {
+  int tile, c0, c1, row0, nrows, pad[3];
+};
 // A query of a packed batch: its request's first own tile, its first row among the request's
 // rows, the keys it sees.
 struct Query {
@@ -84,8 +88,8 @@ struct Args {
   float* lse;
   Tile* tiles;
   long long* u0;           // [max_tiles + 1] where each tile begins in the line of all blocks
-  int* head;               // [0] tiles, [1] packed prefix tiles, [2 + b] first own tile of request b
-  int* part_tile;          // [G] the tile that each part begins in
+  int* head;               // [0] tiles, [1] tiles without blocks, [2 + b] first own tile of request b
+  Part* parts;             // [G]
   Query* queries;          // [total_q], packed batches only
   float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
   unsigned* status;
@@ -130,13 +134,14 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
 // The line of all tiles, U long: a tile's blocks stand behind kSetup places for what it costs to
 // begin and end one (its queries, its first copies, its result: about 5 us).  Without them the
 // parts with many short tiles end last: 64 requests x 64 heads behind 8192 keys took 100 us in
-// this kernel, with them ATTEND_B64_US.  The line is cut into G = min(CTA pairs, U) parts, part c
+// the attention kernel, with them 75.  The line is cut into G = min(CTA pairs, U) parts, part c
 // being [c U / G, (c + 1) U / G); a part may hold no block.
 __device__ __forceinline__ int parts(const Args& a, long long U) {
   return static_cast<int>(min(static_cast<long long>(a.G), U));
 }
 __device__ __forceinline__ long long part_begin(long long U, int G, int c) { return U * c / G; }
 __device__ __forceinline__ int part_of(long long U, int G, long long u) {
+  if (U * G < (1LL << 32)) return static_cast<uint32_t>((u + 1) * G - 1) / static_cast<uint32_t>(U);
   return static_cast<int>(((u + 1) * G - 1) / U);
 }
 // Where a piece of tile i in part c leaves its result: pieces that begin inside a tile are the
@@ -171,8 +176,11 @@ __device__ __forceinline__ long long block_scan(long long v, long long* wsum, lo
   return before + s - v;
 }
 
+// One CTA; what a batch of up to 1024 requests, queries and tiles needs stays in shared memory and
+// registers (a round trip through L2 between two steps costs about 0.4 us).
 __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Args a) {
   __shared__ long long wsum[32];
+  __shared__ int s_head[kPlanThreads + 1], s_sees[kPlanThreads];
   const int tid = threadIdx.x;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -189,17 +197,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
       n = (static_cast<int>(q1 - q0) * a.H + kRows - 1) / kRows;
     }
     long long total;
-    const long long at = block_scan(n, wsum, &total);
-    if (b < nreq) a.head[2 + b] = base + static_cast<int>(at);
+    const int at = base + static_cast<int>(block_scan(n, wsum, &total));
+    if (b < nreq) a.head[2 + b] = at;
+    if (b < kPlanThreads) s_head[b] = at;
     base += static_cast<int>(total);
   }
   const int n_tiles = min(base, a.max_tiles);
-  if (tid == 0) {
-    a.head[0] = n_tiles;
-    a.head[1] = n_pre_tiles;
-    a.head[2 + nreq] = base;
-  }
   __syncthreads();
+  auto head = [&](int b) { return b < kPlanThreads ? s_head[b] : a.head[2 + b]; };
   bool bad = false;
   if (a.packed) {
     for (int q = tid; q < a.total_q; q += kPlanThreads) {
@@ -208,35 +213,39 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
       r.sees = sees(a, b, q, &bad);
       const int q0 = __ldg(a.cu + b);
       const bool mine = q >= q0 && q < __ldg(a.cu + b + 1);
-      r.tile = mine ? a.head[2 + b] : n_tiles;  // n_tiles: no own keys (padding)
+      r.tile = mine ? head(b) : n_tiles;  // n_tiles: no own keys (padding)
       r.row = mine ? (q - q0) * a.H : 0;
       r.pad = 0;
       *reinterpret_cast<int4*>(a.queries + q) = *reinterpret_cast<const int4*>(&r);
+      if (q < kPlanThreads) s_sees[q] = r.sees;
     }
     __syncthreads();
   }
   const int kO = a.prefix_len / kKeys;  // first block with own keys
-  long long u = 0;
+  long long u = 0, my_b0 = 0, my_units = 0;
+  int empty = 0;
+  Tile t{};
   for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
     long long units = 0;
     if (i < n_tiles) {
-      Tile t{};
+      t = Tile{};
       int own = 0;
       if (i < n_pre_tiles) {
         t.row0 = i * kRows;
         t.nrows = min(kRows, a.total_q * a.H - t.row0);
         t.b = -1;
-        for (int q = t.row0 / a.H; q <= (t.row0 + t.nrows - 1) / a.H; ++q) t.limit = max(t.limit, a.queries[q].sees);
+        for (int q = t.row0 / a.H; q <= (t.row0 + t.nrows - 1) / a.H; ++q)
+          t.limit = max(t.limit, q < kPlanThreads ? s_sees[q] : a.queries[q].sees);
       } else {
-        int lo = 0, hi = nreq;  // the last b with head[2 + b] <= i
+        int lo = 0, hi = nreq;  // the last b with head(b) <= i
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (a.head[2 + mid] <= i) lo = mid; else hi = mid;
+          if (head(mid) <= i) lo = mid; else hi = mid;
         }
         const int q0 = min(max(__ldg(a.cu + lo), 0), a.total_q);
         const int q1 = lo < a.B ? min(max(__ldg(a.cu + lo + 1), q0), a.total_q) : a.total_q;
-        t.row0 = q0 * a.H + (i - a.head[2 + lo]) * kRows;
+        t.row0 = q0 * a.H + (i - head(lo)) * kRows;
         t.nrows = min(kRows, q1 * a.H - t.row0);
         t.b = min(lo, a.B - 1);
         t.limit = lo < a.B ? sees(a, lo, (t.row0 + t.nrows - 1) / a.H, &bad) : 0;
@@ -244,29 +253,48 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
       }
       t.n_pre = (a.packed && i >= n_pre_tiles) ? 0 : (min(t.limit, a.prefix_len) + kKeys - 1) / kKeys;
       units = t.n_pre + own > 0 ? t.n_pre + own + kSetup : 0;
-      a.tiles[i] = t;
+      empty += units == 0;
     }
     long long total;
     const long long at = block_scan(units, wsum, &total);
-    if (i < n_tiles) a.u0[i] = u + at;
+    if (i < n_tiles) {
+      if (n_tiles > kPlanThreads) a.tiles[i] = t;
+      a.u0[i] = u + at;
+    }
+    my_b0 = u + at;
+    my_units = units;
     u += total;
   }
   if (tid == 0) a.u0[n_tiles] = u;
+  empty = __syncthreads_count(empty > 0);
+  if (tid == 0) {
+    a.head[0] = n_tiles;
+    a.head[1] = empty;  // whether there are any
+  }
   if (bad) atomicOr(a.status, kStatusUncovered);
-  __syncthreads();
   // the parts that each tile's blocks lie in, and the tile that each part begins in
   const int G = parts(a, u);
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    const long long b0 = a.u0[i], b1 = a.u0[i + 1];
-    int c0 = 0, c1 = -1;
-    if (b1 > b0) {
-      c0 = part_of(u, G, b0);
-      c1 = part_of(u, G, b1 - 1);
-      for (int c = part_begin(u, G, c0) == b0 ? c0 : c0 + 1; c <= c1; ++c) a.part_tile[c] = i;
-      c0 = part_of(u, G, b0 + kSetup);
+    if (n_tiles > kPlanThreads) {
+      t = a.tiles[i];
+      my_b0 = a.u0[i];
+      my_units = a.u0[i + 1] - my_b0;
     }
-    a.tiles[i].c0 = c0;
-    a.tiles[i].c1 = c1;
+    t.c0 = 0;
+    t.c1 = -1;
+    if (my_units > 0) {
+      const int before = part_of(u, G, my_b0);
+      t.c0 = part_of(u, G, my_b0 + kSetup);
+      t.c1 = part_of(u, G, my_b0 + my_units - 1);
+      for (int c = part_begin(u, G, before) == my_b0 ? before : before + 1; c <= t.c1; ++c) {
+        int4* p = reinterpret_cast<int4*>(a.parts + c);
+        p[0] = make_int4(i, t.c0, t.c1, t.row0);
+        p[1] = make_int4(t.nrows, 0, 0, 0);
+      }
+    }
+    int4* p = reinterpret_cast<int4*>(a.tiles + i);
+    p[0] = make_int4(t.row0, t.nrows, t.b, t.n_pre);
+    p[1] = make_int4(t.limit, t.c0, t.c1, 0);
   }
 }
 
@@ -380,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int n_tiles = __ldcg(a.head);
   const long long U = __ldcg(a.u0 + n_tiles);
   const int c = blockIdx.x >> 1, G = parts(a, U);
-  const int i_first = c < G ? __ldcg(a.part_tile + c) : 0;
+  const int i_first = c < G ? __ldcg(&a.parts[c].tile) : 0;
   const long long u_lo = c < G ? part_begin(U, G, c) : 0, u_hi = c < G ? part_begin(U, G, c + 1) : 0;
   ptx::tc_fence_before();
   __syncthreads();
@@ -742,8 +770,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // A CTA of 512 threads joins some latent columns (of 4) of the 128 rows of a tile.
 // Packed batches: blockIdx = 32 * prefix tile + column group of 4; a row has the pieces of that
 // tile and of one of its request's own.  Otherwise blockIdx = 8 * part + g for every part that
-// begins inside a tile; the parts of a tile share its columns (1, 2 or 4 of them: 16, 8 or 4
-// columns a CTA), so that a tile of many pieces has many CTAs.  A thread takes row r; the four
+// begins inside a tile; the parts of a tile share its columns (1, 2, 4 or 16 of them: 16, 8, 4 or
+// 1 columns a CTA), so that a tile of many pieces has many CTAs.  A thread takes row r; the four
 // threads of a row split the columns when there are up to four pieces, else the pieces, and meet
 // in shared memory.  Tiles without any block get zeros.
 constexpr int kCols = 4;  // columns (of 4) a thread
@@ -753,54 +781,62 @@ __global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int r = threadIdx.x & (kRows - 1), y = threadIdx.x >> 7;
-  const int n_tiles = __ldcg(a.head);
-  int i, col0, n_col = kCols;
+  int i, col0, n_col = kCols, row0, nrows;
   bool by_piece = true;
+  // up to two tiles hold a row's pieces
+  int ti[2] = {-1, -1}, rr[2] = {r, 0}, c0[2] = {0, 0}, c1[2] = {-1, -1};
   if (a.packed) {
     i = blockIdx.x >> 5;
     col0 = (blockIdx.x & 31) * kCols;
-    if (i >= __ldcg(a.head + 1)) return;
-  } else {
-    // zeros for tiles without blocks
-    for (int z = blockIdx.x; z < n_tiles; z += gridDim.x) {
-      if (__ldcg(&a.tiles[z].c1) >= 0) continue;
-      const int row0 = __ldcg(&a.tiles[z].row0), nrows = __ldcg(&a.tiles[z].nrows);
-      for (int e = threadIdx.x; e < nrows * (kRank / 8); e += blockDim.x)
-        reinterpret_cast<uint4*>(a.out + static_cast<long long>(row0) * kRank)[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse && threadIdx.x < nrows) a.lse[row0 + threadIdx.x] = -INFINITY;
+    row0 = i * kRows;
+    nrows = min(kRows, a.total_q * a.H - row0);
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + i) + 1);
+    c0[0] = w.y;
+    c1[0] = w.z;
+    if (r < nrows) {
+      const int tq = (row0 + r) / a.H;
+      const int4 q = __ldcg(reinterpret_cast<const int4*>(a.queries + tq));
+      const int local = q.y + row0 + r - tq * a.H;
+      ti[1] = q.x + local / kRows;
+      rr[1] = local % kRows;
+      if (ti[1] < __ldcg(a.head)) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.tiles + ti[1]) + 1);
+        c0[1] = v.y;
+        c1[1] = v.z;
+      }
     }
-    const long long U = __ldcg(a.u0 + n_tiles);
+  } else {
     const int c = blockIdx.x >> 3;
-    if (c >= parts(a, U)) return;
-    i = __ldcg(a.part_tile + c);
-    const int first = c - __ldcg(&a.tiles[i].c0) - 1;  // which of the parts that begin inside the tile
-    const int pieces = __ldcg(&a.tiles[i].c1) - __ldcg(&a.tiles[i].c0) + 1;
-    const int share = pieces > 4 ? 4 : (pieces > 2 ? 2 : 1);
-    if (first < 0 || first >= share) return;           // begins with the tile (first = -1), or not needed
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.parts + c));
+    nrows = __ldcg(&a.parts[c].nrows);
+    const int n_tiles = __ldcg(a.head);
+    if (__ldcg(a.head + 1) > 0) {  // zeros for tiles without blocks
+      for (int z = blockIdx.x; z < n_tiles; z += gridDim.x) {
+        if (__ldcg(&a.tiles[z].c1) >= 0) continue;
+        const int z0 = __ldcg(&a.tiles[z].row0), zn = __ldcg(&a.tiles[z].nrows);
+        for (int e = threadIdx.x; e < zn * (kRank / 8); e += blockDim.x)
+          reinterpret_cast<uint4*>(a.out + static_cast<long long>(z0) * kRank)[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && threadIdx.x < zn) a.lse[z0 + threadIdx.x] = -INFINITY;
+      }
+    }
+    if (c >= parts(a, __ldcg(a.u0 + n_tiles))) return;
+    i = w.x;
+    c0[0] = w.y;
+    c1[0] = w.z;
+    row0 = w.w;
+    const int first = c - w.y - 1;  // which of the parts that begin inside the tile's blocks
+    const int pieces = w.z - w.y + 1;
+    const int share = pieces > 16 ? 16 : (pieces > 4 ? 4 : (pieces > 2 ? 2 : 1));
+    if (first < 0 || first >= share) return;  // begins with the tile (first < 0), or not needed
     const int width = 16 / share;
     col0 = ((blockIdx.x & 7) * share + first) * width;
     by_piece = pieces > 4;
-    if (!by_piece) {
-      n_col = width / 4;
-      col0 += y * n_col;
-    }
+    n_col = by_piece ? width : width / 4;
+    if (!by_piece) col0 += y * n_col;
   }
-  const int row0 = __ldcg(&a.tiles[i].row0), nrows = __ldcg(&a.tiles[i].nrows);
+  ti[0] = i;
   const int row = row0 + r;
   const bool live = r < nrows;
-  // up to two tiles hold this row's pieces
-  int ti[2] = {i, -1}, rr[2] = {r, 0}, c0[2] = {__ldcg(&a.tiles[i].c0), 0}, c1[2] = {__ldcg(&a.tiles[i].c1), -1};
-  if (a.packed && live) {
-    const int tq = row / a.H;
-    const int4 q = __ldcg(reinterpret_cast<const int4*>(a.queries + tq));
-    const int local = q.y + row - tq * a.H;
-    ti[1] = q.x + local / kRows;
-    rr[1] = local % kRows;
-    if (ti[1] < n_tiles) {
-      c0[1] = __ldcg(&a.tiles[ti[1]].c0);
-      c1[1] = __ldcg(&a.tiles[ti[1]].c1);
-    }
-  }
   // running maximum, sum and columns over this thread's pieces
   const int n0 = c1[0] - c0[0] + 1, np = n0 + c1[1] - c0[1] + 1;
   float M = -INFINITY, L = 0.f;
@@ -808,7 +844,7 @@ __global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
 #pragma unroll
   for (int q = 0; q < kCols; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) {
-#pragma unroll 2
+#pragma unroll 4
     for (int k = by_piece ? y : 0; k < np; k += by_piece ? 4 : 1) {
       const int w = k < n0 ? 0 : 1, c = c0[w] + k - (w ? n0 : 0);
       const long long s = piece_slot(a.G, c, ti[w], c == c0[w], c0[w] == c1[w]);
@@ -963,7 +999,7 @@ Layout layout(const dsa_prefix_mla_args* a) {
   p.off_u0 = up(p.off_tiles + sizeof(Tile) * p.max_tiles);
   p.off_head = up(p.off_u0 + 8 * (static_cast<size_t>(p.max_tiles) + 1));
   p.off_parts = up(p.off_head + 4 * (static_cast<size_t>(a->B) + 4));
-  p.off_queries = up(p.off_parts + 4 * static_cast<size_t>(p.G));
+  p.off_queries = up(p.off_parts + sizeof(Part) * p.G);
   p.off_ml = up(p.off_queries + (p.packed ? sizeof(Query) * a->total_q : 0));
   p.off_o = up(p.off_ml + slots * kRows * 8);
   p.total = up(p.off_o + slots * kRows * kRank * 4);
@@ -1041,7 +1077,7 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.tiles = reinterpret_cast<Tile*>(ws + p.off_tiles);
   k.u0 = reinterpret_cast<long long*>(ws + p.off_u0);
   k.head = reinterpret_cast<int*>(ws + p.off_head);
-  k.part_tile = reinterpret_cast<int*>(ws + p.off_parts);
+  k.parts = reinterpret_cast<Part*>(ws + p.off_parts);
   k.queries = reinterpret_cast<Query*>(ws + p.off_queries);
   k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
   k.part_o = reinterpret_cast<float*>(ws + p.off_o);
