@@ -21,11 +21,13 @@
 //   warps 0..7  softmax.  A thread holds one row and a quarter: 32 of the block's keys, 128 of the
 //               row's latent sums (the quarters meet in shared memory).  The reference maximum
 //               moves only when a block's maximum passes it by 8 (a factor 256);
-//   warps 8..10 keys of S, three groups of 3 columns of 64 bf16, and warps 11, 12 keys of P . V,
-//               two groups of 2 columns: a warp per group, so that a group's buffer is refilled
-//               as soon as its MMAs are done; TMA, one lane per page piece and column;
-//   warps 13,14 the piece's query rows (16-byte cp.async, any strides);
-//   warp 15     TMEM; in the even CTA one lane issues the MMAs, whichever product has its inputs.
+//   warp 8      keys of S, three groups of 3 columns of 64 bf16, and warp 9 keys of P . V, two
+//               groups of 2 columns: each group refilled as soon as its MMAs are done; TMA, one
+//               lane per page piece and column;
+//   warp 10     the piece's query rows (16-byte cp.async, any strides);
+//   warp 11     TMEM; in the even CTA one lane issues the MMAs.
+// 12 warps leave 168 registers a thread; with a warp for every group they were 128, which the
+// softmax warps spilled.
 // A tile done in one piece is normalised and written; the others leave (O, m, l) in fp32.
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
@@ -47,7 +49,7 @@ namespace {
 constexpr int kRank = 512, kRope = 64, kAtoms = 9;        // 576 = 9 columns of 64 bf16
 constexpr int kRows = 128;                                // rows per tile, 64 in each CTA of a pair
 constexpr int kKeys = 128;                                // keys per block
-constexpr int kThreads = 512;                             // 8 softmax, 3 K, 2 V, 2 query warps, 1 MMA
+constexpr int kThreads = 384;                             // 8 softmax warps, K, V, queries, MMA
 constexpr uint32_t kAtomBytes = 64 * 128;                 // a column of 64 rows or keys
 constexpr uint32_t kKGroup = 3 * kAtomBytes, kVGroup = 2 * 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtoms * kAtomBytes;
@@ -76,7 +78,7 @@ struct Query {
 };
 
 struct Args {
-  int B, total_q, H, page_size, num_pages, max_pages, prefix_len, num_prefix_pages;
+  int B, total_q, H, page_size, page_log2, num_pages, max_pages, prefix_len, num_prefix_pages;
   int packed;              // small requests: prefix tiles packed across requests
   int max_tiles, G;        // tiles there is room for; CTA pairs
   int past_row;            // a row coordinate past the cache: copies from there are zeros
@@ -98,7 +100,7 @@ struct Args {
 // Barriers of a CTA.  L: the even CTA's, waited for by the issuer; the others are waited for in
 // each CTA and completed by the issuer's commits in both.
 struct Bars {
-  uint64_t qfull, qempty;        // L: 2 query warps of each CTA
+  uint64_t qfull, qempty;        // qfull L: the query warp of each CTA
   uint64_t kfull[3], kempty[3];  // L: each CTA's copies
   uint64_t vfull[2], vempty[2];  // L
   uint64_t vown[2];              // this CTA's copies of a block with rows to clear
@@ -345,7 +347,7 @@ __device__ __forceinline__ Block block_at(const Args& a, const Tile& t, int k) {
 // there: past_row (zeros) when the tile sees none of them, or the page is not there (*bad).
 __device__ __forceinline__ int cache_row(const Args& a, const Tile& t, const Block& b, int s, int box, bool* bad) {
   if (s >= b.hi || s + box <= b.lo) return a.past_row;
-  const int j = s / a.page_size;
+  const int j = s >> a.page_log2;
   int pg = -1;
   if (b.pre) {
     if (j < a.num_prefix_pages) pg = __ldg(a.prefix_pages + j);
@@ -376,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = static_cast<int>(ptx::cluster_ctarank());
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(&bars->qfull, 4);
+    ptx::mbar_init(&bars->qfull, 2);
     ptx::mbar_init(&bars->qempty, 1);
     for (int g = 0; g < 3; ++g) {
       ptx::mbar_init(&bars->kfull[g], 2);
@@ -395,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 15) {
+  if (warp == 11) {
     ptx::tmem_alloc_pair(tmem_holder, 512);
     ptx::tmem_relinquish_pair();
   }
@@ -420,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Piece p{i_first, 0, 0, false, u_lo};
   Tile t;
 
-  if (warp == 15) {
+  if (warp == 11) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     // The whole warp walks the blocks, one lane issues.  S of block k + 1 goes before P . V of
     // block k, whose weights are computed meanwhile.
@@ -434,8 +436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout)) != 0;
       };
-      uint32_t n1 = 0, n2 = 0, seg = 0;  // blocks whose S / P . V was issued, pieces
-      for (; ok && next_piece(a, p, u_hi, t); ++seg) {
+      uint32_t n1 = 0, n2 = 0;  // blocks whose S / P . V was issued
+      bool more = next_piece(a, p, u_hi, t);
+      for (uint32_t seg = 0; ok && more; ++seg) {
         wait(&bars->qfull, seg & 1);
         const int nblk = p.k1 - p.k0;
         for (int i = 0; ok && i <= nblk; ++i) {
@@ -464,6 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++n1;
           }
+          if (i == nblk) more = next_piece(a, p, u_hi, t);  // its loads pass behind the last block's softmax
           if (i > 0) {
             wait(&bars->pfull, n2 & 1);
 #pragma unroll
@@ -492,74 +496,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     }
     __syncwarp();
-  } else if (warp >= 8 && warp < 11) {
-    // ------------------------------------------------------------ keys of S: columns 3 g .. 3 g + 2 of this CTA's 64
-    const int per = 64 / box, g = warp - 8;
-    const int at = 3 * g + lane / per, j = lane & (per - 1);  // the lane's column, box of the column
-    const bool mine = lane / per < 3;
-    uint8_t* dst = smem + kOffK + at * kAtomBytes + j * box * 128;
-    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ keys of S: this CTA's 64 of a block
+    const int per = 64 / box, j = lane & (per - 1), at = lane / per;  // box of a column, column of a group
     uint32_t n = 0;
     bool ok = true;
     while (ok && next_piece(a, p, u_hi, t)) {
-      for (int k = p.k0; k < p.k1; ++k, ++n) {
+      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
         const int row = cache_row(a, t, b, b.s0 + rank * 64 + j * box, box, &bad);
         if (bad) atomicOr(a.status, kStatusBadPage);
-        ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
                                                             kStatusTimeout)) != 0;
-        if (!ok) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
-        __syncwarp();
-        if (mine) {
-          if (at < 8) ptx::tma_load_2d_pair(dst, &tmap_c, full, at * 64, row);
-          else ptx::tma_load_2d_pair(dst, &tmap_r, full, 0, row);
+          if (!ok) break;
+          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
+          if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
+          __syncwarp();
+          if (at < 3) {
+            uint8_t* dst = smem + kOffK + (3 * g + at) * kAtomBytes + j * box * 128;
+            if (3 * g + at < 8) ptx::tma_load_2d_pair(dst, &tmap_c, full, (3 * g + at) * 64, row);
+            else ptx::tma_load_2d_pair(dst, &tmap_r, full, 0, row);
+          }
         }
       }
     }
     // after a failure: every copy lands before the pair can exit
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      ptx::mbar_spin_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+      for (int g = 0; g < 3; ++g)
+        ptx::mbar_spin_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     __syncwarp();
-  } else if (warp >= 11 && warp < 13) {
-    // ------------------------------------------------------------ keys of P . V: 2 of this CTA's 4 columns, all 128
-    const int per = 128 / box, g = warp - 11;
-    const int j = lane & (per - 1);
-    const bool mine = lane / per < 2;
-    uint8_t* base = smem + kOffV + g * kVGroup;
-    uint8_t* dst = base + (lane / per) * (128 * 128) + j * box * 128;
-    const int x = rank * 256 + (2 * g + lane / per) * 64;
-    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ keys of P . V: this CTA's 4 columns, all 128
+    const int per = 128 / box, j = lane & (per - 1), at = lane / per;
     uint32_t n = 0, cleared = 0;
     bool ok = true;
     while (ok && next_piece(a, p, u_hi, t)) {
-      for (int k = p.k0; k < p.k1; ++k, ++n) {
+      for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
         bool bad = false;
         const int row = cache_row(a, t, b, b.s0 + j * box, box, &bad);
         // rows that no row of this tile sees may hold anything: their weights are 0, and the
         // values are cleared so that the products are
         const bool clear = b.s0 < b.lo || b.s0 + kKeys > b.hi;
-        ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
                                                             kStatusTimeout)) != 0;
-        if (!ok) break;
-        if (lane == 0) {
-          if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
-          else ptx::mbar_arrive_expect_tx_cluster(full, kVGroup);
-        }
-        __syncwarp();
-        if (mine) {
-          if (clear) ptx::tma_load_2d(dst, &tmap_c, &bars->vown[g], x, row);
-          else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
-        }
-        if (clear) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_spin_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout,
-                                                            ptx::kWaitCycles)) != 0;
           if (!ok) break;
-          ++cleared;
-          const int from = max(b.lo - b.s0, 0), to = min(b.hi - b.s0, kKeys);  // rows [from, to) stay
-          const int n_clear = from + kKeys - to;
+          const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
+          if (lane == 0) {
+            if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
+            else ptx::mbar_arrive_expect_tx_cluster(full, kVGroup);
+          }
+          __syncwarp();
+          if (at < 2) {
+            uint8_t* dst = smem + kOffV + g * kVGroup + at * (128 * 128) + j * box * 128;
+            const int x = rank * 256 + (2 * g + at) * 64;
+            if (clear) ptx::tma_load_2d(dst, &tmap_c, &bars->vown[g], x, row);
+            else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
+          }
+        }
+        if (!clear) continue;
+        const int from = min(max(b.lo - b.s0, 0), kKeys), to = max(min(b.hi - b.s0, kKeys), from);  // [from, to) stay
+        const int n_clear = from + kKeys - to;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin_drain(&bars->vown[g], cleared & 1, a.status,
+                                                                  kStatusTimeout, ptx::kWaitCycles)) != 0;
+          if (!ok) break;
+          uint8_t* base = smem + kOffV + g * kVGroup;
           for (int e = lane; e < n_clear * 16; e += 32) {  // 16 chunks of 16 bytes a row, in two columns
             const int r = e >> 4, key = r < from ? r : to + (r - from);
             *reinterpret_cast<uint4*>(base + ((e >> 3) & 1) * (128 * 128) + key * 128 + (e & 7) * 16) =
@@ -567,23 +575,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(full);
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0));
         }
+        ++cleared;
       }
     }
     if (rank == 0 && lane == 0 && n > 0 && !ok)
-      ptx::mbar_spin_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+      for (int g = 0; g < 2; ++g)
+        ptx::mbar_spin_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     __syncwarp();
-  } else if (warp >= 13) {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
-    const int gt = threadIdx.x - 13 * 32;
-    const int c16 = gt & 7;
+    const int c16 = lane & 7;
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
     uint32_t seg = 0;
     for (; next_piece(a, p, u_hi, t); ++seg) {
       const bool good = ptx::mbar_spin(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
       if (!__all_sync(0xffffffffu, good)) break;
-      for (int r = gt >> 3; r < 64; r += 8) {  // eight threads a row, 128 bytes at a time
+      for (int r = lane >> 3; r < 64; r += 4) {  // eight lanes a row, 128 bytes at a time
         const bool live = rank * 64 + r < t.nrows;
         const int row = t.row0 + (live ? rank * 64 + r : 0);
         const int tq = row / a.H, h = row - tq * a.H;
@@ -610,22 +619,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&bars->sempty[0]), 0);
     bool ok = true;
     uint32_t n = 0;
-    while (next_piece(a, p, u_hi, t)) {
+    const int trow = rank * 64 + row;
+    auto limit_of = [&](const Tile& tile) {  // keys this row sees
+      if (trow >= tile.nrows) return 0;
+      const int tq = (tile.row0 + trow) / a.H;
+      bool bad = false;  // counted by the plan
+      return min(a.packed ? __ldcg(&a.queries[tq].sees) : sees(a, tile.b, tq, &bad), tile.limit);
+    };
+    auto row_at = [&](const Tile& tile, int k) {  // cache row of the lane's box under this warp's keys
+      const Block b = block_at(a, tile, k);
+      const int s0 = b.s0 + half * 64 + part * 32;
+      bool bad = false;  // counted by the copies
+      return cache_row(a, tile, b, (s0 & ~(box - 1)) + (lane & (per - 1)) * box, box, &bad);
+    };
+    bool more = next_piece(a, p, u_hi, t);
+    int lim = more ? limit_of(t) : 0, crow = more ? row_at(t, p.k0) : 0;
+    while (more) {
       float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this quarter's sum
-      int lim = 0;                   // keys this row sees
-      const int trow = rank * 64 + row;
-      if (trow < t.nrows) {
-        const int tq = (t.row0 + trow) / a.H;
-        bool bad = false;  // counted by the plan
-        lim = min(a.packed ? __ldcg(&a.queries[tq].sees) : sees(a, t.b, tq, &bad), t.limit);
-      }
       for (int k = p.k0; k < p.k1; ++k, ++n) {
         const int tb = n & 1;
         const Block b = block_at(a, t, k);
         const int s0 = b.s0 + half * 64 + part * 32;  // this thread's 32 keys
-        bool bad = false;
-        const int s_box = (s0 & ~(box - 1)) + (lane & (per - 1)) * box;
-        const unsigned there = __ballot_sync(0xffffffffu, cache_row(a, t, b, s_box, box, &bad) != a.past_row);
+        if (k > p.k0) crow = row_at(t, k);            // passes while S is computed
+        const unsigned there = __ballot_sync(0xffffffffu, crow != a.past_row);
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
                                                                     kStatusTimeout)) != 0;
         float x[32];
@@ -711,9 +727,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(full);
       }
+      // the next piece, its loads behind the last P . V
+      const Piece pc = p;
+      const Tile tc = t;
+      more = next_piece(a, p, u_hi, t);
+      lim = more ? limit_of(t) : 0;
+      crow = more ? row_at(t, p.k0) : 0;
       // the piece's result
-      const bool at_start = p.k0 == 0;
-      const bool direct = p.whole && !a.packed;
+      const bool at_start = pc.k0 == 0;
+      const bool direct = pc.whole && !a.packed;
       if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
                                                                   kStatusTimeout)) != 0;
       float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
@@ -721,11 +743,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::named_bar_sync(row_bar, 128);
       l = (xs[0] + xs[64]) + (xs[128] + xs[192]);
       ptx::named_bar_sync(row_bar, 128);  // read before the next piece writes there
-      const bool live = trow < t.nrows && ok;
-      const long long slot = piece_slot(a.G, c, p.i, at_start, p.whole);
+      const bool live = trow < tc.nrows && ok;
+      const long long slot = piece_slot(a.G, c, pc.i, at_start, pc.whole);
       if (live && quarter == 0) {
         if (!direct) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + trow) * 2) = make_float2(m, l);
-        else if (a.lse) a.lse[t.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        else if (a.lse) a.lse[tc.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       ptx::tc_fence_after();
@@ -734,8 +756,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_ld_32x32b_x32(tmem_base + lane_addr + kOCol0 + part * 128 + q * 32, r);
         ptx::tmem_ld_wait_regs(r);
         const int lat = half * 256 + part * 128 + q * 32;
-        if (live && direct) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (t.row0 + trow) * static_cast<long long>(kRank) + lat);
+        if (direct) {
+          // through the rows' own places in P, so that four lanes write 64 bytes of a row together
+          // (a lane's 16 bytes a store, 1024 apart, took the piece's end from 1.5 to 5 us)
+          uint8_t* place = smem + kOffP + half * kAtomBytes + row * 128;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
@@ -745,8 +769,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                              __uint_as_float(r[8 * i + 2 * j + 1]) * inv);
               w[j] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(place + (((part * 4 + i) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          ptx::named_bar_sync(row_bar, 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // this warp's 8 rows x 2 halves of 128 bytes, 4 a step
+            const int sg = i * 4 + (lane >> 3), hf = sg & 1, ch = lane & 7;
+            const int rw = (warp & 1) * 32 + (warp >> 1) * 8 + (sg >> 1);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffP + hf * kAtomBytes + rw * 128 +
+                                                            ((ch ^ (rw & 7)) << 4));
+            if (ok && rank * 64 + rw < tc.nrows)
+              *reinterpret_cast<uint4*>(a.out + (tc.row0 + rank * 64 + rw) * static_cast<long long>(kRank) + hf * 256 +
+                                        (ch >> 2) * 128 + q * 32 + (ch & 3) * 8) = v;
+          }
+          ptx::named_bar_sync(row_bar, 128);  // read before it is written again
         } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(a.part_o) + (slot * (kRank / 4) + lat / 4) * kRows + trow;
 #pragma unroll
@@ -760,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // no CTA leaves while its peer may still touch its memory, barriers or TMEM
-  if (warp == 15) {
+  if (warp == 11) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, 512);
   }
@@ -1052,6 +1088,7 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.total_q = a->total_q;
   k.H = a->H;
   k.page_size = a->page_size;
+  k.page_log2 = a->page_size == 16 ? 4 : (a->page_size == 32 ? 5 : (a->page_size == 64 ? 6 : 7));
   k.num_pages = a->num_pages;
   k.max_pages = a->max_pages_per_seq;
   k.prefix_len = a->prefix_len;
