@@ -67,7 +67,7 @@ struct Tile {
   int c0, c1;        // the parts that its blocks lie in (c1 < c0: none)
   int pad;
 };
-// The tile that a part begins in.
+// The tile that a part begins in (tile < 0: no such part).
 struct Part {
   int tile, c0, c1, row0, nrows, pad[3];
 };
@@ -135,13 +135,17 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
 
 // The line of all tiles, U long: a tile's blocks stand behind kSetup places for what it costs to
 // begin and end one (its queries, its first copies, its result: about 5 us).  Without them the
-// parts with many short tiles end last: 64 requests x 64 heads behind 8192 keys took 100 us in
-// the attention kernel, with them 75.  The line is cut into G = min(CTA pairs, U) parts, part c
+// parts with many short tiles end last: of 0, 1, 2, 3, 4, 6 places 64 requests x 64 heads behind
+// 8192 keys took 109, 98, 90, 84, 84, 87 us, 128 x 16 heads behind 32768 180, 176, 173, 167, 168,
+// 173 us.  The line is cut into G = min(CTA pairs, U) parts, part c
 // being [c U / G, (c + 1) U / G); a part may hold no block.
 __device__ __forceinline__ int parts(const Args& a, long long U) {
   return static_cast<int>(min(static_cast<long long>(a.G), U));
 }
-__device__ __forceinline__ long long part_begin(long long U, int G, int c) { return U * c / G; }
+__device__ __forceinline__ long long part_begin(long long U, int G, int c) {
+  if (U * G < (1LL << 32)) return static_cast<uint32_t>(U * c) / static_cast<uint32_t>(G);
+  return U * c / G;
+}
 __device__ __forceinline__ int part_of(long long U, int G, long long u) {
   if (U * G < (1LL << 32)) return static_cast<uint32_t>((u + 1) * G - 1) / static_cast<uint32_t>(U);
   return static_cast<int>(((u + 1) * G - 1) / U);
@@ -276,6 +280,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
   if (bad) atomicOr(a.status, kStatusUncovered);
   // the parts that each tile's blocks lie in, and the tile that each part begins in
   const int G = parts(a, u);
+  for (int c = G + tid; c < a.G; c += kPlanThreads) a.parts[c].tile = -1;
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
     if (n_tiles > kPlanThreads) {
       t = a.tiles[i];
@@ -803,46 +808,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// A CTA of 512 threads joins some latent columns (of 4) of the 128 rows of a tile.
-// Packed batches: blockIdx = 32 * prefix tile + column group of 4; a row has the pieces of that
-// tile and of one of its request's own.  Otherwise blockIdx = 8 * part + g for every part that
-// begins inside a tile; the parts of a tile share its columns (1, 2, 4 or 16 of them: 16, 8, 4 or
-// 1 columns a CTA), so that a tile of many pieces has many CTAs.  A thread takes row r; the four
-// threads of a row split the columns when there are up to four pieces, else the pieces, and meet
-// in shared memory.  Tiles without any block get zeros.
-constexpr int kCols = 4;  // columns (of 4) a thread
-__global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
-  __shared__ float4 acc_s[3][kCols][kRows];
+// A CTA of 512 threads (128 rows x 4) joins some of the 128 latent columns (of 4) of a tile's rows.
+// Packed batches: a row has the pieces of its prefix tile and of one of its request's own tiles;
+// blockIdx = per_tile * prefix tile + columns.  Otherwise blockIdx = 2 * part + columns for every
+// part that begins inside a tile; the parts of a tile share its columns (up to 64 of them), so that
+// a tile of many pieces has many CTAs.  The four threads of a row split the columns when the pieces
+// are few, else the pieces, and meet in shared memory.  About one wave of CTAs, a few trips to L2.
+// Tiles without any block get zeros.
+constexpr int kBatch = 4, kAcc = 8;  // pieces whose loads go out together, columns (of 4) at once
+__global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, int per_tile) {
+  extern __shared__ float4 acc_s[];  // [3][kAcc][128]
   __shared__ float2 ml_s[3][kRows];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int r = threadIdx.x & (kRows - 1), y = threadIdx.x >> 7;
-  int i, col0, n_col = kCols, row0, nrows;
-  bool by_piece = true;
-  // up to two tiles hold a row's pieces
-  int ti[2] = {-1, -1}, rr[2] = {r, 0}, c0[2] = {0, 0}, c1[2] = {-1, -1};
+  int col0, n_col, row0, nrows;
+  bool by_piece;
+  // up to two tiles hold a row's pieces: parts a0 .. a1 of tile ta (row r), b0 .. b1 of tb (row rb)
+  int ta, a0, a1, tb = 0, rb = 0, b0 = 0, b1 = -1;
   if (a.packed) {
-    i = blockIdx.x >> 5;
-    col0 = (blockIdx.x & 31) * kCols;
-    row0 = i * kRows;
+    ta = blockIdx.x / per_tile;
+    const int width = 128 / per_tile;
+    by_piece = per_tile == 32;
+    col0 = (blockIdx.x - ta * per_tile) * width;
+    n_col = by_piece ? width : width / 4;
+    if (!by_piece) col0 += y * n_col;
+    row0 = ta * kRows;
     nrows = min(kRows, a.total_q * a.H - row0);
-    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + i) + 1);
-    c0[0] = w.y;
-    c1[0] = w.z;
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + ta) + 1);
+    a0 = w.y;
+    a1 = w.z;
     if (r < nrows) {
       const int tq = (row0 + r) / a.H;
       const int4 q = __ldcg(reinterpret_cast<const int4*>(a.queries + tq));
       const int local = q.y + row0 + r - tq * a.H;
-      ti[1] = q.x + local / kRows;
-      rr[1] = local % kRows;
-      if (ti[1] < __ldcg(a.head)) {
-        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.tiles + ti[1]) + 1);
-        c0[1] = v.y;
-        c1[1] = v.z;
+      tb = q.x + local / kRows;
+      rb = local % kRows;
+      if (tb < __ldcg(a.head)) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.tiles + tb) + 1);
+        b0 = v.y;
+        b1 = v.z;
       }
     }
   } else {
-    const int c = blockIdx.x >> 3;
+    const int c = blockIdx.x >> 1;
     const int4 w = __ldcg(reinterpret_cast<const int4*>(a.parts + c));
     nrows = __ldcg(&a.parts[c].nrows);
     const int n_tiles = __ldcg(a.head);
@@ -855,102 +864,142 @@ __global__ void __launch_bounds__(512) prefix_mla_join_kernel(const Args a) {
         if (a.lse && threadIdx.x < zn) a.lse[z0 + threadIdx.x] = -INFINITY;
       }
     }
-    if (c >= parts(a, __ldcg(a.u0 + n_tiles))) return;
-    i = w.x;
-    c0[0] = w.y;
-    c1[0] = w.z;
+    if (w.x < 0) return;
+    ta = w.x;
+    a0 = w.y;
+    a1 = w.z;
     row0 = w.w;
-    const int first = c - w.y - 1;  // which of the parts that begin inside the tile's blocks
-    const int pieces = w.z - w.y + 1;
-    const int share = pieces > 16 ? 16 : (pieces > 4 ? 4 : (pieces > 2 ? 2 : 1));
+    const int first = c - a0 - 1;  // which of the parts that begin inside the tile's blocks
+    const int pieces = a1 - a0 + 1;
+    const int share = pieces > 64 ? 64 : (pieces > 16 ? 16 : (pieces > 4 ? 4 : (pieces > 2 ? 2 : 1)));
     if (first < 0 || first >= share) return;  // begins with the tile (first < 0), or not needed
-    const int width = 16 / share;
-    col0 = ((blockIdx.x & 7) * share + first) * width;
+    const int width = 64 / share;
     by_piece = pieces > 4;
     n_col = by_piece ? width : width / 4;
-    if (!by_piece) col0 += y * n_col;
+    col0 = ((blockIdx.x & 1) * share + first) * width + (by_piece ? 0 : y * n_col);
   }
-  ti[0] = i;
   const int row = row0 + r;
   const bool live = r < nrows;
-  // running maximum, sum and columns over this thread's pieces
-  const int n0 = c1[0] - c0[0] + 1, np = n0 + c1[1] - c0[1] + 1;
-  float M = -INFINITY, L = 0.f;
-  float4 acc[kCols];
+  const int na = a1 - a0 + 1, np = live ? na + b1 - b0 + 1 : 0;
+  const int k0 = by_piece ? y : 0, step = by_piece ? 4 : 1;
+  const float2* part_ml = reinterpret_cast<const float2*>(a.part_ml);
+  const float4* part_o = reinterpret_cast<const float4*>(a.part_o);
+  const int whole = 2 * a.G;
+  auto slot_of = [&](int k) -> int {  // of piece k
+    const bool in_a = k < na;
+    const int kk = in_a ? k : k - na, first = in_a ? a0 : b0;
+    if (first == (in_a ? a1 : b1)) return whole + (in_a ? ta : tb);
+    return 2 * (first + kk) + (kk == 0 ? 1 : 0);
+  };
+
+  for (int q0 = 0; q0 < n_col; q0 += kAcc) {
+    // running maximum, sum and columns over this thread's pieces
+    float M = -INFINITY, L = 0.f;
+    float4 acc[kAcc];
 #pragma unroll
-  for (int q = 0; q < kCols; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-#pragma unroll 4
-    for (int k = by_piece ? y : 0; k < np; k += by_piece ? 4 : 1) {
-      const int w = k < n0 ? 0 : 1, c = c0[w] + k - (w ? n0 : 0);
-      const long long s = piece_slot(a.G, c, ti[w], c == c0[w], c0[w] == c1[w]);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + s * kRows + rr[w]);
-      const float4* src = reinterpret_cast<const float4*>(a.part_o) + (s * (kRank / 4) + col0) * kRows + rr[w];
-      float4 o[kCols];
+    for (int q = 0; q < kAcc; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = k0; k < np; k += kBatch * step) {
+      float2 ml[kBatch];
+      const float4* src[kBatch];
+      float w[kBatch];
 #pragma unroll
-      for (int q = 0; q < kCols; ++q) o[q] = q < n_col ? __ldcg(src + q * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ml.x == -INFINITY) continue;  // a piece in which the row saw nothing
-      const float Mn = fmaxf(M, ml.x);
-      const float f = exp2f(M - Mn), e = exp2f(ml.x - Mn);  // f = 0 the first time
+      for (int h = 0; h < kBatch; ++h) {
+        const int kk = k + h * step;
+        const long long slot = slot_of(min(kk, np - 1));
+        const int rr = min(kk, np - 1) < na ? r : rb;
+        ml[h] = part_ml[slot * kRows + rr];
+        if (kk >= np) ml[h] = make_float2(-INFINITY, 0.f);
+        src[h] = part_o + (slot * (kRank / 4) + col0 + q0) * kRows + rr;
+      }
+      float Mn = M;
+#pragma unroll
+      for (int h = 0; h < kBatch; ++h) Mn = fmaxf(Mn, ml[h].x);
+      const float base = Mn == -INFINITY ? 0.f : Mn;  // nothing seen so far: every weight is 0
+      const float f = ptx::ex2(M - base);
       M = Mn;
-      L = L * f + e * ml.y;
+      L *= f;
 #pragma unroll
-      for (int q = 0; q < kCols; ++q) {
-        acc[q].x = acc[q].x * f + e * o[q].x;
-        acc[q].y = acc[q].y * f + e * o[q].y;
-        acc[q].z = acc[q].z * f + e * o[q].z;
-        acc[q].w = acc[q].w * f + e * o[q].w;
+      for (int h = 0; h < kBatch; ++h) {
+        w[h] = ptx::ex2(ml[h].x - base);
+        L = fmaf(w[h], ml[h].y, L);
+      }
+#pragma unroll
+      for (int q = 0; q < kAcc; q += 2) {
+        if (q0 + q >= n_col) break;
+        float4 o[kBatch][2];
+#pragma unroll
+        for (int h = 0; h < kBatch; ++h) {
+          const bool in = k + h * step < np;
+          o[h][0] = in ? src[h][q * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+          o[h][1] = in && q0 + q + 1 < n_col ? src[h][(q + 1) * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float4 v = make_float4(acc[q + e].x * f, acc[q + e].y * f, acc[q + e].z * f, acc[q + e].w * f);
+#pragma unroll
+          for (int h = 0; h < kBatch; ++h) {
+            v.x = fmaf(w[h], o[h][e].x, v.x);
+            v.y = fmaf(w[h], o[h][e].y, v.y);
+            v.z = fmaf(w[h], o[h][e].z, v.z);
+            v.w = fmaf(w[h], o[h][e].w, v.w);
+          }
+          acc[q + e] = v;
+        }
       }
     }
-  }
-  if (by_piece) {  // the four threads of a row meet
-    if (y > 0) {
-      ml_s[y - 1][r] = make_float2(M, L);
+    if (by_piece) {  // the four threads of a row meet
+      if (y > 0) {
+        ml_s[y - 1][r] = make_float2(M, L);
 #pragma unroll
-      for (int q = 0; q < kCols; ++q) acc_s[y - 1][q][r] = acc[q];
-    }
-    __syncthreads();
-    if (y > 0) return;
-    float2 ml[3];
-    float Mn = M;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      ml[k] = ml_s[k][r];
-      Mn = fmaxf(Mn, ml[k].x);
-    }
-    const float none = Mn == -INFINITY ? 0.f : Mn;
-    const float f = exp2f(M - none);
-    L *= f;
-#pragma unroll
-    for (int q = 0; q < kCols; ++q)
-      acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const float e = exp2f(ml[k].x - none);
-      L += e * ml[k].y;
-#pragma unroll
-      for (int q = 0; q < kCols; ++q) {
-        const float4 o = acc_s[k][q][r];
-        acc[q].x += e * o.x;
-        acc[q].y += e * o.y;
-        acc[q].z += e * o.z;
-        acc[q].w += e * o.w;
+        for (int q = 0; q < kAcc; ++q)
+          if (q0 + q < n_col) acc_s[((y - 1) * kAcc + q) * kRows + r] = acc[q];
       }
-    }
-    M = Mn;
-  }
-  if (!live) return;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  uint2* dst = reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kRank + col0 * 4);
+      __syncthreads();
+      if (y == 0) {
+        float Mn = M;
 #pragma unroll
-  for (int q = 0; q < kCols; ++q) {
-    if (q >= n_col) break;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * inv, acc[q].y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * inv, acc[q].w * inv);
-    dst[q] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        for (int h = 0; h < 3; ++h) Mn = fmaxf(Mn, ml_s[h][r].x);
+        const float base = Mn == -INFINITY ? 0.f : Mn;
+        const float f = ptx::ex2(M - base);
+        M = Mn;
+        L *= f;
+#pragma unroll
+        for (int q = 0; q < kAcc; ++q) acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          const float w = ptx::ex2(ml_s[h][r].x - base);
+          L = fmaf(w, ml_s[h][r].y, L);
+#pragma unroll
+          for (int q = 0; q < kAcc; ++q) {
+            if (q0 + q >= n_col) break;
+            const float4 v = acc_s[(h * kAcc + q) * kRows + r];
+            acc[q].x = fmaf(w, v.x, acc[q].x);
+            acc[q].y = fmaf(w, v.y, acc[q].y);
+            acc[q].z = fmaf(w, v.z, acc[q].z);
+            acc[q].w = fmaf(w, v.w, acc[q].w);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (!live || (by_piece && y > 0)) continue;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kRank + (col0 + q0) * 4);
+    auto packed = [&](const float4& v) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+      return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    };
+#pragma unroll
+    for (int q = 0; q < kAcc; q += 2) {  // columns come in pairs, but for a single one
+      if (q0 + q >= n_col) break;
+      const uint2 u = packed(acc[q]), v = packed(acc[q + 1]);
+      if (n_col == 1) dst[q] = u;
+      else *reinterpret_cast<uint4*>(dst + q) = make_uint4(u.x, u.y, v.x, v.y);
+    }
+    if (a.lse && col0 + q0 == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
-  if (a.lse && col0 == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
+constexpr int kJoinSmem = 3 * kAcc * kRows * 16;
 
 bool key_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
@@ -992,6 +1041,8 @@ int pair_count() {
     cfg.numAttrs = 1;
     if (cudaFuncSetAttribute(prefix_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(prefix_mla_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem) !=
+            cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, prefix_mla_kernel, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       return 76;
@@ -1125,8 +1176,11 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   e = launch_pdl(prefix_mla_kernel, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  const long long ctas = p.packed ? (rows + kRows - 1) / kRows * 32 : p.G * 8LL;
-  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), 0, s, k);
+  // Few packed tiles have many pieces each: 32 CTAs a tile, which split them.
+  const long long groups = (rows + kRows - 1) / kRows;
+  const int per_tile = groups * 32 <= 2LL * p.G ? 32 : (groups * 8 <= 2LL * p.G ? 8 : 4);
+  const long long ctas = p.packed ? groups * per_tile : p.G * 2LL;
+  e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), kJoinSmem, s, k, per_tile);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
