@@ -171,6 +171,40 @@ def test_latent_append(n, norm, rope, interleaved, views):
         assert np.array_equal(gc, ref_c)
 
 
+@pytest.mark.parametrize("n", [8195, 16387])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_latent_append_many_tokens(n, interleaved):
+    # several tokens a warp: every row against the oracle's formula, written with numpy at once
+    g = torch.Generator(device="cuda").manual_seed(n)
+    page, pages = 32, 600
+    kv = torch.randn((n, 576), generator=g, device="cuda").to(torch.bfloat16)
+    slots = torch.randperm(page * pages, generator=g, device="cuda")[:n]
+    slots[3::1000] = -1
+    pos = torch.randint(0, 300, (n,), generator=g, device="cuda", dtype=torch.int32)
+    ang = torch.rand((300, 32), generator=g, device="cuda") * 6.28
+    w = 1 + 0.1 * torch.randn(512, generator=g, device="cuda")
+    gc = torch.full((pages, page, 512), 9.0, dtype=torch.bfloat16, device="cuda")
+    gr = torch.full((pages, page, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_mla_cache_append(kv[:, :512], kv[:, 512:], slots, gc, gr, norm_weight=w, rope_cos=ang.cos(),
+                             rope_sin=ang.sin(), positions=pos, rope_interleaved=interleaved)
+    _ok()
+    c, r = kv[:, :512].double().cpu().numpy(), kv[:, 512:].double().cpu().numpy()
+    c = c / np.sqrt((c * c).mean(1, keepdims=True) + 1e-6) * w.double().cpu().numpy()
+    p = pos.cpu().numpy()
+    cos, sin = ang.cos().double().cpu().numpy()[p], ang.sin().double().cpu().numpy()[p]
+    ia, ib = (np.arange(0, 64, 2), np.arange(1, 64, 2)) if interleaved else (np.arange(32), np.arange(32, 64))
+    out = r.copy()
+    out[:, ia], out[:, ib] = r[:, ia] * cos - r[:, ib] * sin, r[:, ia] * sin + r[:, ib] * cos
+    sl = slots.cpu().numpy()
+    live = sl >= 0
+    fc, fr = gc.double().cpu().numpy().reshape(-1, 512), gr.double().cpu().numpy().reshape(-1, 64)
+    assert np.all(np.abs(fc[sl[live]] - c[live]) <= (H16 + 2.0 ** -20) * np.abs(c[live]) + 1e-30)
+    assert np.all(np.abs(fr[sl[live]] - out[live]) <= H16 * np.abs(out[live]) + 2.0 ** -22 * np.abs(out).max())
+    rest = np.ones(len(fc), dtype=bool)
+    rest[sl[live]] = False
+    assert np.all(fc[rest] == 9) and np.all(fr[rest] == 9)
+
+
 def test_latent_append_without_positions_uses_the_token_row():
     g = torch.Generator().manual_seed(2)
     kv = torch.randn((9, 576), generator=g).to(torch.bfloat16)
@@ -279,6 +313,11 @@ class Case:
     (32, 32, 300, [(1, 301 + 17 * i) for i in range(9)]),
     (64, 128, 2000, [(1, 2001)]),
     (17, 16, 256, [(13, 280), (33, 300)]),
+    (128, 64, 20000, [(1, 20001)]),
+    (16, 16, 9000, [(1, 9001), (3, 9003), (1, 9777), (2, 9129)]),
+    (48, 32, 640, [(1, 641 + 31 * i) for i in range(40)]),
+    (100, 64, 1280, [(2, 1290), (9, 1400), (1, 1281)]),
+    (2, 128, 384, [(200, 584), (1, 385), (64, 500)]),
 ], ids=str)
 def test_attend(H, page, prefix, reqs):
     Case(H, page, prefix, reqs, seed=H + prefix).check()
