@@ -706,6 +706,16 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype) -> int:
     return t.data_ptr()
 
 
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape:
+        _expect([(t, name, shape)])
+    _ptr(t, name, dtype)
+    return t
+
+
 def _rows(t: torch.Tensor, name: str) -> int:
     """Device pointer of a bf16 tensor whose last dimension is dense, the others in any strides."""
     if not t.is_cuda:
@@ -750,22 +760,13 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     i32, dev = torch.int32, block_tables.device
     lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
             _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
-    for t, name, shape in ((cu_q_lens, "cu_q_lens", (B + 1,)), (slot_mapping, "slot_mapping", (total_q,)),
-                           (positions, "positions", (total_q,)), (used, "used", (1,))):
-        if t is not None and t.shape != shape:
-            _expect([(t, name, shape)])
-    if cu_q_lens is None:
-        cu_q_lens = torch.empty(B + 1, dtype=i32, device=dev)
-    if slot_mapping is None:
-        slot_mapping = torch.empty(total_q, dtype=torch.int64, device=dev)
-    if positions is None:
-        positions = torch.empty(total_q, dtype=i32, device=dev)
-    if used is None:
-        used = torch.empty(1, dtype=i32, device=dev)
+    cu_q_lens = _out(cu_q_lens, "cu_q_lens", (B + 1,), i32, dev)
+    slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev)
+    positions = _out(positions, "positions", (total_q,), i32, dev)
+    used = _out(used, "used", (1,), i32, dev)
     args = _PLAN_ARGS.pack(B, total_q, page_size, width, 0 if prefix_pages is None else prefix_pages.shape[0],
-                           free_pages.shape[0], *lens, _ptr(cu_q_lens, "cu_q_lens", i32),
-                           _ptr(slot_mapping, "slot_mapping", torch.int64), _ptr(positions, "positions", i32),
-                           _ptr(used, "used", i32))
+                           free_pages.shape[0], *lens, cu_q_lens.data_ptr(), slot_mapping.data_ptr(),
+                           positions.data_ptr(), used.data_ptr())
     _check(lib().dsa_page_plan(args, _stream_of(block_tables, stream)), "dsa_page_plan")
     if stream is not None:
         _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
@@ -813,6 +814,14 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
         _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
 
 
+def dsa_prefix_mla_workspace_size(B: int, total_q: int, H: int, *, prefix_len: int) -> int:
+    """Bytes of workspace that dsa_prefix_mla takes for a batch of these sizes."""
+    need = ctypes.c_size_t(0)
+    args = _PREFIX_ARGS.pack(B, total_q, H, 512, 64, 64, 0, 0, prefix_len, -(-prefix_len // 64), 1.0, *[0] * 16)
+    _check(lib().dsa_prefix_mla_workspace_size(args, ctypes.byref(need)), "dsa_prefix_mla_workspace_size")
+    return int(need.value)
+
+
 def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages=None, *,
                    prefix_len: int, scale: float, out=None, lse=None, workspace=None, stream=None):
     """Latent attention of a batch whose sequences share their first prefix_len tokens (their
@@ -829,30 +838,26 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     rd = q_rope.shape[2]
     num_pages, page_size = cache_c.shape[:2]
     B, width = seq_lens.shape[0], block_tables.shape[1]
-    i32, f32, bf16, dev = torch.int32, torch.float32, torch.bfloat16, cache_c.device
+    i32, bf16, dev = torch.int32, torch.bfloat16, cache_c.device
     if not (q_rope.shape[:2] == (T, H) and cache_c.shape[2] == R and cache_r.shape == (num_pages, page_size, rd)
-            and block_tables.shape[0] == B and cu_q_lens.shape == (B + 1,)
-            and (out is None or out.shape == (T, H, R)) and (lse is None or lse.shape == (T, H))):
+            and block_tables.shape[0] == B and cu_q_lens.shape == (B + 1,)):
         _expect([(q_rope, "q_rope", (T, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
                  (cache_r, "cache_r", (num_pages, page_size, rd)), (block_tables, "block_tables", (B, None)),
-                 (cu_q_lens, "cu_q_lens", (B + 1,)), (out, "out", (T, H, R)), (lse, "lse", (T, H))])
+                 (cu_q_lens, "cu_q_lens", (B + 1,))])
     sizes = (B, T, H, R, rd, page_size, num_pages, width, prefix_len,
              0 if prefix_pages is None else prefix_pages.shape[0], scale)
     tensors = (_rows(q_nope, "q_nope"), _rows(q_rope, "q_rope"), *q_nope.stride()[:2], *q_rope.stride()[:2],
                _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16),
                _ptr(prefix_pages, "prefix_pages", i32), _ptr(block_tables, "block_tables", i32),
                _ptr(cu_q_lens, "cu_q_lens", i32), _ptr(seq_lens, "seq_lens", i32))
-    if out is None:
-        out = torch.empty((T, H, R), dtype=bf16, device=dev)
-    if lse is None:
-        lse = torch.empty((T, H), dtype=f32, device=dev)
+    out, lse = _out(out, "out", (T, H, R), bf16, dev), _out(lse, "lse", (T, H), torch.float32, dev)
     if workspace is None:
         need = ctypes.c_size_t(0)
         _check(lib().dsa_prefix_mla_workspace_size(_PREFIX_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need)),
                "dsa_prefix_mla_workspace_size")
         workspace = torch.empty(max(need.value, 16), dtype=torch.uint8, device=dev)
-    args = _PREFIX_ARGS.pack(*sizes, *tensors, _ptr(out, "out", bf16), _ptr(lse, "lse", f32),
-                             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    args = _PREFIX_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"),
+                             workspace.numel() * workspace.element_size())
     _check(lib().dsa_prefix_mla(args, _stream_of(cache_c, stream)), "dsa_prefix_mla")
     if stream is not None:
         _record((q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
