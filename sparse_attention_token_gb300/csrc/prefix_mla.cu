@@ -429,9 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 11) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    // The whole warp walks the blocks, one lane issues.  S of block k + 1 goes before P . V of
-    // block k, whose weights are computed meanwhile.
-    if (rank == 0) {
+    // S of block k + 1 goes before P . V of block k, whose weights are computed meanwhile.
+    if (rank == 0 && ptx::elect_one()) {
       const uint32_t sbase = ptx::smem_u32(smem);
       const uint32_t id1 = ptx::idesc_f32acc(128, kKeys, true);
       const uint32_t id2 = ptx::idesc_f32acc_bf16_bmn(128, 256);
@@ -439,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t p0 = ptx::desc_lo(sbase + kOffP, 16), v0 = ptx::desc_lo(sbase + kOffV, 128 * 128);
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout)) != 0;
+        ok = ok && ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout);
       };
       uint32_t n1 = 0, n2 = 0;  // blocks whose S / P . V was issued
       bool more = next_piece(a, p, u_hi, t);
@@ -454,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 3; ++g) {
               wait(&bars->kfull[g], n1 & 1);
               ptx::tc_fence_after();
-              if (ok && ptx::elect_one()) {
+              if (ok) {
                 uint32_t qa = q0, kb = k0;
                 asm volatile("" : "+r"(qa), "+r"(kb));  // descriptors are added up here, not kept over the loop
 #pragma unroll
@@ -468,7 +467,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   if (i + 1 == nblk) ptx::mma_commit_pair(&bars->qempty, 3);
                 }
               }
-              __syncwarp();
             }
             ++n1;
           }
@@ -479,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 2; ++g) {
               wait(&bars->vfull[g], n2 & 1);
               ptx::tc_fence_after();
-              if (ok && ptx::elect_one()) {
+              if (ok) {
                 uint32_t pa = p0, vb = v0;
                 asm volatile("" : "+r"(pa), "+r"(vb));
 #pragma unroll
@@ -490,14 +488,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ptx::mma_commit_pair(&bars->vempty[g], 3);
                 if (g == 1) ptx::mma_commit_pair(&bars->ofree, 3);
               }
-              __syncwarp();
             }
             ++n2;
           }
         }
       }
-      if (ptx::elect_one()) ptx::mma_commit_pair(&bars->done, 1);
-      __syncwarp();
+      ptx::mma_commit_pair(&bars->done, 1);
       ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     }
     __syncwarp();
