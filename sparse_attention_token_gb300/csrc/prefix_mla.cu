@@ -160,33 +160,34 @@ __device__ __forceinline__ long long piece_slot(int G, int c, int i, bool at_sta
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ long long block_scan(long long v, long long* wsum, long long* total) {  // exclusive
+// Exclusive scan over the CTA: within the warps, then every warp scans the warps' sums.
+template <typename V>
+__device__ __forceinline__ V block_scan(V v, V* wsum, V* total) {
+  static_assert(kPlanThreads == 32 * 32, "one sum per lane");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long s = v;
+  auto scan = [&](V s) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const V u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    return s;
+  };
+  const V s = scan(v);
   __syncthreads();
   if (lane == 31) wsum[warp] = s;
   __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll 8
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const long long x = wsum[w];
-    if (w < warp) before += x;
-    all += x;
-  }
-  *total = all;
-  return before + s - v;
+  const V w = scan(wsum[lane]);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const V before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return (warp > 0 ? before : V(0)) + s - v;
 }
 
 // One CTA; what a batch of up to 1024 requests, queries and tiles needs stays in shared memory and
 // registers (a round trip through L2 between two steps costs about 0.4 us).
 __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Args a) {
   __shared__ long long wsum[32];
-  __shared__ int s_head[kPlanThreads + 1], s_sees[kPlanThreads];
+  __shared__ int wsum_n[32], s_head[kPlanThreads + 1], s_sees[kPlanThreads];
   const int tid = threadIdx.x;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -202,11 +203,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
       const int q1 = b < a.B ? min(max(__ldg(a.cu + b + 1), q0), a.total_q) : a.total_q;
       n = (static_cast<int>(q1 - q0) * a.H + kRows - 1) / kRows;
     }
-    long long total;
-    const int at = base + static_cast<int>(block_scan(n, wsum, &total));
+    int total;
+    const int at = base + block_scan(n, wsum_n, &total);
     if (b < nreq) a.head[2 + b] = at;
     if (b < kPlanThreads) s_head[b] = at;
-    base += static_cast<int>(total);
+    base += total;
   }
   const int n_tiles = min(base, a.max_tiles);
   __syncthreads();
