@@ -30,6 +30,16 @@
 // softmax warps spilled.
 // A tile done in one piece is normalised and written; the others leave (O, m, l) in fp32.
 //
+// What bounds it: the refill of the key buffers, with the tensor pipe close behind.  A block's
+// products are 36 MMAs of N = 128 (35 cycles each) and 16 of N = 256 (64 each), 2284 cycles; it
+// takes 2700 to 3050.  A buffer's MMAs, the commit to both CTAs, the next copy and its arrival at the
+// issuer take some 3000 (870 from a V group's first MMA to the next copy, 2000 to 2250 from there).
+// Keys are staged twice, once for S and once for P . V (the MMAs of a pair read the same offsets in
+// both CTAs, so one copy cannot be split by keys and by columns), which fills shared memory with one
+// block; nine K and four V groups cost the two copying warps and the issuer more than they save.
+// 1781 x 64 rows behind 6000 keys take 0.98 ms, 1.60 PFLOP/s (0.87 to 0.92 ms, 1.71 to 1.80 PFLOP/s,
+// launch after launch in a graph), the tensor pipe active 76 % of its cycles under the profiler.
+//
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
 //
 // Every wait is bounded; after one gives up, every role stops, copies and MMAs in flight are
@@ -1072,9 +1082,14 @@ struct Layout {
 Layout layout(const dsa_prefix_mla_args* a) {
   Layout p{};
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  // Requests of few rows share prefix tiles: with H a multiple of 128, or 512 rows a request on
-  // average, a request's own tiles are (nearly) full and the join would be extra traffic.
-  p.packed = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 && rows < 512LL * a->B ? 1 : 0;
+  // Requests share prefix tiles where their own tiles would stand too empty: by more than 15 % for
+  // a request of the average number of rows (none are empty with H a multiple of 128).  Behind 8192
+  // keys, shared and own tiles took: 64 rows a request (half empty) 75 and 111 us, 128 (none) 67 and
+  // 60, 256 (none) 113 and 100, 320 (20 %) 143 and 153, 448 (14 %) 197 and 191, 576 (11 %) 245 and
+  // 230; 16 rows a request behind 32768 keys 150 and 732 us.
+  const long long full = static_cast<long long>(kRows) * std::max(a->B, 1), filled = (rows + full - 1) / full;
+  p.packed = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 &&
+             100 * filled * full > 115 * rows ? 1 : 0;
   p.max_tiles = static_cast<int>((p.packed ? 2 : 1) * (rows / kRows + 1) + a->B + 1);
   p.G = pair_count();
   const size_t slots = 2 * static_cast<size_t>(p.G) + (p.packed ? p.max_tiles : 0);
