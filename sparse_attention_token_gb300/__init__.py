@@ -727,9 +727,9 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    """Raw cudaStream_t of `stream`, or of the current stream on the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+def _stream_of(device: torch.device, stream) -> int:
+    """Raw cudaStream_t of `stream`, or of the current stream on the device."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _record(tensors, stream) -> None:
@@ -751,12 +751,13 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     of free_pages in request order, -1 behind.  total_q: the outputs' length, at least the
     sum of q_lens (the rest is -1).  Returns (cu_q_lens [B + 1] int32, slot_mapping [total_q]
     int64, positions [total_q] int32, used [1] int32: the free pages taken)."""
-    width = block_tables.shape[-1]
-    B = q_lens.shape[0] if q_lens.dim() == 1 else -1
-    if not (q_lens.shape == seq_lens.shape == (B,) and block_tables.shape == (B, width) and free_pages.dim() == 1
-            and (prefix_pages is None or prefix_pages.dim() == 1)):
+    bs, qs, fs = block_tables.shape, q_lens.shape, free_pages.shape
+    n_prefix = 0 if prefix_pages is None else prefix_pages.shape[0] if prefix_pages.dim() == 1 else -1
+    if len(qs) != 1 or len(bs) != 2 or len(fs) != 1 or n_prefix < 0 or bs[0] != qs[0] or seq_lens.shape != qs:
+        B = qs[0] if len(qs) == 1 else None
         _expect([(q_lens, "q_lens", (None,)), (seq_lens, "seq_lens", (B,)), (block_tables, "block_tables", (B, None)),
                  (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
+    B, width = bs
     i32, dev = torch.int32, block_tables.device
     lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
             _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
@@ -764,10 +765,11 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev)
     positions = _out(positions, "positions", (total_q,), i32, dev)
     used = _out(used, "used", (1,), i32, dev)
-    args = _PLAN_ARGS.pack(B, total_q, page_size, width, 0 if prefix_pages is None else prefix_pages.shape[0],
-                           free_pages.shape[0], *lens, cu_q_lens.data_ptr(), slot_mapping.data_ptr(),
-                           positions.data_ptr(), used.data_ptr())
-    _check(lib().dsa_page_plan(args, _stream_of(block_tables, stream)), "dsa_page_plan")
+    args = _PLAN_ARGS.pack(B, total_q, page_size, width, n_prefix, fs[0], *lens, cu_q_lens.data_ptr(),
+                           slot_mapping.data_ptr(), positions.data_ptr(), used.data_ptr())
+    status = lib().dsa_page_plan(args, _stream_of(dev, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_page_plan")
     if stream is not None:
         _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
                 stream)
@@ -809,7 +811,9 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
         _rows(k_rope, "k_rope"), c_kv.stride(0), k_rope.stride(0), _ptr(slot_mapping, "slot_mapping", torch.int64),
         _ptr(norm_weight, "norm_weight", f32), _ptr(rope_cos, "rope_cos", f32), _ptr(rope_sin, "rope_sin", f32),
         _ptr(positions, "positions", torch.int32), _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16))
-    _check(lib().dsa_mla_cache_append(args, _stream_of(cache_c, stream)), "dsa_mla_cache_append")
+    status = lib().dsa_mla_cache_append(args, _stream_of(cache_c.device, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_mla_cache_append")
     if stream is not None:
         _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
 
@@ -829,36 +833,44 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     lse [total_q, H] fp32, the natural logarithm of the sum of exponentials).  q_nope and
     q_rope may be views of one [total_q, H, 576] tensor.  out, lse and the workspace
     (dsa_prefix_mla_workspace_size bytes) are allocated when not given."""
-    if not (q_nope.dim() == q_rope.dim() == cache_c.dim() == 3 and seq_lens.dim() == 1 and block_tables.dim() == 2
-            and (prefix_pages is None or prefix_pages.dim() == 1)):
+    qs, rs, cs, bs = q_nope.shape, q_rope.shape, cache_c.shape, block_tables.shape
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    n_prefix = 0 if prefix_pages is None else prefix_pages.shape[0] if prefix_pages.dim() == 1 else -1
+    if len(qs) != 3 or len(rs) != 3 or len(cs) != 3 or len(bs) != 2 or B < 0 or n_prefix < 0:
         _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
                  (cache_c, "cache_c", (None, None, None)), (seq_lens, "seq_lens", (None,)),
                  (block_tables, "block_tables", (None, None)), (prefix_pages, "prefix_pages", (None,))])
-    T, H, R = q_nope.shape
-    rd = q_rope.shape[2]
-    num_pages, page_size = cache_c.shape[:2]
-    B, width = seq_lens.shape[0], block_tables.shape[1]
-    i32, bf16, dev = torch.int32, torch.bfloat16, cache_c.device
-    if not (q_rope.shape[:2] == (T, H) and cache_c.shape[2] == R and cache_r.shape == (num_pages, page_size, rd)
-            and block_tables.shape[0] == B and cu_q_lens.shape == (B + 1,)):
+    T, H, R = qs
+    rd = rs[2]
+    num_pages, page_size, row = cs
+    if (row != R or rs != (T, H, rd) or cache_r.shape != (num_pages, page_size, rd) or bs[0] != B
+            or cu_q_lens.shape != (B + 1,)):
         _expect([(q_rope, "q_rope", (T, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
                  (cache_r, "cache_r", (num_pages, page_size, rd)), (block_tables, "block_tables", (B, None)),
                  (cu_q_lens, "cu_q_lens", (B + 1,))])
-    sizes = (B, T, H, R, rd, page_size, num_pages, width, prefix_len,
-             0 if prefix_pages is None else prefix_pages.shape[0], scale)
-    tensors = (_rows(q_nope, "q_nope"), _rows(q_rope, "q_rope"), *q_nope.stride()[:2], *q_rope.stride()[:2],
-               _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16),
-               _ptr(prefix_pages, "prefix_pages", i32), _ptr(block_tables, "block_tables", i32),
-               _ptr(cu_q_lens, "cu_q_lens", i32), _ptr(seq_lens, "seq_lens", i32))
+    i32, bf16, dev = torch.int32, torch.bfloat16, cache_c.device
+    sizes = (B, T, H, R, rd, page_size, num_pages, bs[1], prefix_len, n_prefix, scale)
+    qt, qh, _ = q_nope.stride()
+    rt, rh, _ = q_rope.stride()
+    tensors = (_rows(q_nope, "q_nope"), _rows(q_rope, "q_rope"), qt, qh, rt, rh, _ptr(cache_c, "cache_c", bf16),
+               _ptr(cache_r, "cache_r", bf16), _ptr(prefix_pages, "prefix_pages", i32),
+               _ptr(block_tables, "block_tables", i32), _ptr(cu_q_lens, "cu_q_lens", i32),
+               _ptr(seq_lens, "seq_lens", i32))
     out, lse = _out(out, "out", (T, H, R), bf16, dev), _out(lse, "lse", (T, H), torch.float32, dev)
+    L = lib()
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _check(lib().dsa_prefix_mla_workspace_size(_PREFIX_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need)),
-               "dsa_prefix_mla_workspace_size")
-        workspace = torch.empty(max(need.value, 16), dtype=torch.uint8, device=dev)
-    args = _PREFIX_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"),
-                             workspace.numel() * workspace.element_size())
-    _check(lib().dsa_prefix_mla(args, _stream_of(cache_c, stream)), "dsa_prefix_mla")
+        status = L.dsa_prefix_mla_workspace_size(_PREFIX_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need))
+        if status != DSA_OK:
+            raise DsaError(status, "dsa_prefix_mla_workspace_size")
+        room = need.value or 16
+        workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+    else:
+        room = workspace.numel() * workspace.element_size()
+    args = _PREFIX_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"), room)
+    status = L.dsa_prefix_mla(args, _stream_of(dev, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_prefix_mla")
     if stream is not None:
         _record((q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
                  workspace), stream)

@@ -323,6 +323,14 @@ def test_attend(H, page, prefix, reqs):
     Case(H, page, prefix, reqs, seed=H + prefix).check()
 
 
+@pytest.mark.parametrize("H,prefix", [(128, 20), (16, 40), (64, 0)])
+def test_attend_more_requests_queries_and_tiles_than_a_plan_thread_each(H, prefix):
+    # 1100 requests: own tiles, packed tiles, and no prefix; some idle, some seeing nothing
+    reqs = [(1 if i % 7 else i % 3, prefix + 1 + i % 5 if i % 11 else 0) for i in range(1100)]
+    reqs = [(q, max(n, q) if n else 0) for q, n in reqs]
+    Case(H, 16, prefix, reqs, pad=3, seed=H).check()
+
+
 @pytest.mark.parametrize("prefix", [127, 128, 129, 255, 256, 257])
 @pytest.mark.parametrize("page", [16, 64, 128])
 def test_attend_around_tile_borders(prefix, page):
