@@ -404,7 +404,8 @@ dsa_status dsa_sparse_mla(const dsa_sparse_mla_args* args, dsa_stream_t stream);
  * total_q is the outputs' length: at least the sum of q_lens; entries past the sum (a step
  * padded to a captured graph's size) are -1 in both.
  * Only whole pages of a shared prompt can be shared: a request writes its own pages, so a
- * partly filled last prompt page is each request's own.
+ * partly filled last prompt page is each request's own, and c is num_prefix_pages * P at
+ * least (new tokens before that would get slots of the shared pages).
  * Recorded in the device status word (DSA_ERR_DEVICE_CHECK), never out of bounds: a
  * free list that is too short (its entries and slots become -1; used[0] is still what the
  * step needs), a page id < 0, a length that is negative, exceeds the table, or q_lens[b] >
@@ -474,8 +475,8 @@ dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_strea
  *   strides (multiples of 8; the last dimension dense); cache_c, cache_r as in dsa_sparse_mla;
  *   block_tables [B, max_pages_per_seq]; out [total_q, H, 512] bf16 dense; lse [total_q, H].
  * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0.
- * Cache rows that no query sees may hold anything, NaN included; rows of positions below
- * seq_lens[b] must be finite.  A page outside the cache, or a position past the table, is
+ * Cache rows that no query sees may hold anything, NaN included; rows that some query sees
+ * must be finite.  A page outside the cache, or a position past the table, is
  * skipped and reported through dsa_check_device_status.  Probabilities enter P.V rounded to
  * bf16; statistics and sums are fp32.  Results do not depend on the run (no atomics on data).
  * workspace: dsa_prefix_mla_workspace_size bytes, 16-byte aligned like the other pointers.

@@ -64,7 +64,7 @@ constexpr uint32_t kAtomBytes = 64 * 128;                 // a column of 64 rows
 constexpr uint32_t kKGroup = 3 * kAtomBytes, kVGroup = 2 * 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtoms * kAtomBytes;
 constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
-constexpr size_t kSmem = kOffMisc + 3072;
+constexpr size_t kSmem = kOffMisc + 3 * 1024;
 constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
 constexpr int kSetup = 3;                                 // what a tile costs beside its blocks, in blocks
 constexpr float kLn2 = 0.6931471805599453f;
@@ -77,9 +77,10 @@ struct Tile {
   int c0, c1;        // the parts that its blocks lie in (c1 < c0: none)
   int pad;
 };
-// The tile that a part begins in (tile < 0: no such part).
+// A part, and the tile it begins in (tile < 0: no such part): all that its first piece needs.
 struct Part {
-  int tile, c0, c1, row0, nrows, pad[3];
+  int tile, c0, c1, row0, nrows, b, n_pre, limit;
+  long long begin, end, tile_begin, tile_end;
 };
 // A query of a packed batch: its request's first own tile, its first row among the request's
 // rows, the keys it sees.
@@ -91,6 +92,7 @@ struct Args {
   int B, total_q, H, page_size, page_log2, num_pages, max_pages, prefix_len, num_prefix_pages;
   int packed;              // small requests: prefix tiles packed across requests
   int max_tiles, G;        // tiles there is room for; CTA pairs
+  int narrow;              // the line is shorter than 2^31 places, whatever the lengths
   int past_row;            // a row coordinate past the cache: copies from there are zeros
   float scale_log2;        // scale * log2(e)
   const __nv_bfloat16 *qn, *qr;
@@ -198,6 +200,7 @@ __device__ __forceinline__ V block_scan(V v, V* wsum, V* total) {
 __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Args a) {
   __shared__ long long wsum[32];
   __shared__ int wsum_n[32], s_head[kPlanThreads + 1], s_sees[kPlanThreads];
+  __shared__ long long s_b0[kPlanThreads];
   const int tid = threadIdx.x;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -265,15 +268,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
         t.row0 = q0 * a.H + (i - head(lo)) * kRows;
         t.nrows = min(kRows, q1 * a.H - t.row0);
         t.b = min(lo, a.B - 1);
-        t.limit = lo < a.B ? sees(a, lo, (t.row0 + t.nrows - 1) / a.H, &bad) : 0;
+        const int last = (t.row0 + t.nrows - 1) / a.H;
+        if (lo < a.B)
+          t.limit = !a.packed ? sees(a, lo, last, &bad) : (last < kPlanThreads ? s_sees[last] : a.queries[last].sees);
         own = t.limit > a.prefix_len ? (t.limit + kKeys - 1) / kKeys - kO : 0;
       }
       t.n_pre = (a.packed && i >= n_pre_tiles) ? 0 : (min(t.limit, a.prefix_len) + kKeys - 1) / kKeys;
       units = t.n_pre + own > 0 ? t.n_pre + own + kSetup : 0;
       empty += units == 0;
     }
-    long long total;
-    const long long at = block_scan(units, wsum, &total);
+    long long total, at;
+    if (a.narrow) {
+      int sum;
+      at = block_scan(static_cast<int>(units), wsum_n, &sum);
+      total = sum;
+    } else {
+      at = block_scan(units, wsum, &total);
+    }
     if (i < n_tiles) {
       if (n_tiles > kPlanThreads) a.tiles[i] = t;
       a.u0[i] = u + at;
@@ -289,30 +300,45 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
     a.head[1] = empty;  // whether there are any
   }
   if (bad) atomicOr(a.status, kStatusUncovered);
-  // the parts that each tile's blocks lie in, and the tile that each part begins in
+  // the parts that each tile's blocks lie in
   const int G = parts(a, u);
-  for (int c = G + tid; c < a.G; c += kPlanThreads) a.parts[c].tile = -1;
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
     if (n_tiles > kPlanThreads) {
       t = a.tiles[i];
       my_b0 = a.u0[i];
       my_units = a.u0[i + 1] - my_b0;
+    } else {
+      s_b0[i] = my_b0;
     }
     t.c0 = 0;
     t.c1 = -1;
     if (my_units > 0) {
-      const int before = part_of(u, G, my_b0);
       t.c0 = part_of(u, G, my_b0 + kSetup);
       t.c1 = part_of(u, G, my_b0 + my_units - 1);
-      for (int c = part_begin(u, G, before) == my_b0 ? before : before + 1; c <= t.c1; ++c) {
-        int4* p = reinterpret_cast<int4*>(a.parts + c);
-        p[0] = make_int4(i, t.c0, t.c1, t.row0);
-        p[1] = make_int4(t.nrows, 0, 0, 0);
-      }
     }
     int4* p = reinterpret_cast<int4*>(a.tiles + i);
     p[0] = make_int4(t.row0, t.nrows, t.b, t.n_pre);
     p[1] = make_int4(t.limit, t.c0, t.c1, 0);
+  }
+  __syncthreads();
+  // the tile that each part begins in: the last with b0 <= begin (the ones before it that share
+  // its place have no blocks)
+  for (int c = tid; c < a.G; c += kPlanThreads) {
+    if (c >= G) {
+      a.parts[c].tile = -1;
+      continue;
+    }
+    const long long begin = part_begin(u, G, c);
+    auto b0 = [&](int i) { return n_tiles > kPlanThreads ? a.u0[i] : s_b0[i]; };
+    int lo = 0, hi = n_tiles;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (b0(mid) <= begin) lo = mid; else hi = mid;
+    }
+    const int4* w = reinterpret_cast<const int4*>(a.tiles + lo);
+    const int4 w0 = w[0], w1 = w[1];
+    a.parts[c] = Part{lo, w1.y, w1.z, w0.x, w0.y, w0.z, w0.w, w1.x, begin, part_begin(u, G, c + 1), b0(lo),
+                      lo + 1 < n_tiles ? b0(lo + 1) : u};
   }
 }
 
@@ -320,28 +346,30 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
 // The part's pieces: tile i, its blocks [k0, k1).  Every role walks the same list.
 struct Piece {
   int i, k0, k1;
-  bool whole;       // all the tile's blocks
-  long long next;   // where the next piece begins in the line
+  bool whole;          // all the tile's blocks
+  long long b0, b1;    // the tile's places in the line
+  long long next;      // where the next piece begins
 };
 __device__ __forceinline__ bool next_piece(const Args& a, Piece& p, long long u_hi, Tile& t) {
   while (p.next < u_hi) {
-    const long long b0 = __ldcg(a.u0 + p.i), b1 = __ldcg(a.u0 + p.i + 1);
-    const long long first = b0 + kSetup, from = p.next, to = min(b1, u_hi);
-    if (b1 > from) {
-      const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
-      t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
-      t.row0 = w.x;
-      t.nrows = w.y;
-      t.b = w.z;
-      t.n_pre = w.w;
+    const long long first = p.b0 + kSetup, from = p.next, to = min(p.b1, u_hi);
+    if (to > from) {
       p.k0 = static_cast<int>(max(from - first, 0LL));
       p.k1 = static_cast<int>(max(to - first, 0LL));
-      p.whole = p.k0 == 0 && to == b1;
+      p.whole = p.k0 == 0 && to == p.b1;
       p.next = to;
       if (p.k1 > p.k0) return true;
       if (to == u_hi) return false;  // the part ends before the tile's first block
     }
     ++p.i;  // done, or without blocks
+    p.b0 = p.b1;
+    p.b1 = __ldcg(a.u0 + p.i + 1);
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + p.i));
+    t.limit = __ldcg(reinterpret_cast<const int*>(a.tiles + p.i) + 4);
+    t.row0 = w.x;
+    t.nrows = w.y;
+    t.b = w.z;
+    t.n_pre = w.w;
   }
   return false;
 }
@@ -423,11 +451,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int n_tiles = __ldcg(a.head);
-  const long long U = __ldcg(a.u0 + n_tiles);
-  const int c = blockIdx.x >> 1, G = parts(a, U);
-  const int i_first = c < G ? __ldcg(&a.parts[c].tile) : 0;
-  const long long u_lo = c < G ? part_begin(U, G, c) : 0, u_hi = c < G ? part_begin(U, G, c + 1) : 0;
+  const int c = blockIdx.x >> 1;
+  const int4* rec = reinterpret_cast<const int4*>(a.parts + c);
+  const int4 r0 = __ldcg(rec), r1 = __ldcg(rec + 1);
+  const longlong2 r2 = __ldcg(reinterpret_cast<const longlong2*>(rec + 2));
+  const longlong2 r3 = __ldcg(reinterpret_cast<const longlong2*>(rec + 3));
+  const long long u_hi = r0.x >= 0 ? r2.y : 0;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
@@ -435,8 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
   const int box = min(a.page_size, 64);  // rows of one copy
   const int box_log2 = 31 - __clz(box);
-  Piece p{i_first, 0, 0, false, u_lo};
-  Tile t;
+  Piece p{r0.x, 0, 0, false, r3.x, r3.y, r0.x >= 0 ? r2.x : 0};
+  Tile t{r0.w, r1.x, r1.y, r1.z, r1.w, 0, 0, 0};
 
   if (warp == 11) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -1160,6 +1189,9 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.max_tiles = p.max_tiles;
   k.G = p.G;
   k.past_row = static_cast<int>(slots);
+  const long long most = std::max(static_cast<long long>(a->max_pages_per_seq) * a->page_size,
+                                  static_cast<long long>(a->prefix_len)) / kKeys + 2 + kSetup;
+  k.narrow = most * p.max_tiles < (1LL << 31) ? 1 : 0;
   k.scale_log2 = a->scale * 1.4426950408889634f;
   k.qn = static_cast<const __nv_bfloat16*>(a->q_nope);
   k.qr = static_cast<const __nv_bfloat16*>(a->q_rope);
