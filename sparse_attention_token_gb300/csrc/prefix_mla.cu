@@ -449,6 +449,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tmap_c);
     ptx::prefetch_tmap(&tmap_r);
   }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int c = blockIdx.x >> 1;
@@ -457,11 +462,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const longlong2 r2 = __ldcg(reinterpret_cast<const longlong2*>(rec + 2));
   const longlong2 r3 = __ldcg(reinterpret_cast<const longlong2*>(rec + 3));
   const long long u_hi = r0.x >= 0 ? r2.y : 0;
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
-  ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
   const int box = min(a.page_size, 64);  // rows of one copy
   const int box_log2 = 31 - __clz(box);
   Piece p{r0.x, 0, 0, false, r3.x, r3.y, r0.x >= 0 ? r2.x : 0};
