@@ -405,6 +405,23 @@ __device__ __forceinline__ int cache_row(const Args& a, const Tile& t, const Blo
   return pg * a.page_size + (s & (a.page_size - 1));
 }
 
+// This CTA's rows r0, r0 + step, .. of the tile's queries (16-byte cp.async, zeros past its rows);
+// eight lanes a row (ch: which), 128 bytes at a time, swizzled.
+__device__ __forceinline__ void load_q(const Args& a, uint8_t* smem, const Tile& t, int rank, int r0, int step,
+                                       int ch) {
+  for (int r = r0; r < 64; r += step) {
+    const bool live = rank * 64 + r < t.nrows;
+    const int row = t.row0 + (live ? rank * 64 + r : 0);
+    const int tq = row / a.H, h = row - tq * a.H;
+    const __nv_bfloat16* qn = a.qn + tq * a.qn_t + h * a.qn_h + ch * 8;
+    const __nv_bfloat16* qr = a.qr + tq * a.qr_t + h * a.qr_h + ch * 8;
+    uint8_t* dst = smem + kOffQ + r * 128 + ((ch ^ (r & 7)) << 4);
+#pragma unroll
+    for (int at = 0; at < kAtoms; ++at)
+      ptx::cp_async_16(dst + at * kAtomBytes, at < 8 ? qn + at * 64 : qr, live ? 16u : 0u);
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_mla_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r,
                       const Args a) {
@@ -627,23 +644,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
-    const int c16 = lane & 7;
+    // (the softmax warps, idle until then, bring the first piece's: 4 x 16 heads behind 1000 took
+    // 18.3 us when this warp did, 17.0 now, longer calls the same within 0.6)
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
-    uint32_t seg = 0;
-    for (; next_piece(a, p, u_hi, t); ++seg) {
+    next_piece(a, p, u_hi, t);
+    for (uint32_t seg = 1; next_piece(a, p, u_hi, t); ++seg) {
       const bool good = ptx::mbar_spin(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
       if (!__all_sync(0xffffffffu, good)) break;
-      for (int r = lane >> 3; r < 64; r += 4) {  // eight lanes a row, 128 bytes at a time
-        const bool live = rank * 64 + r < t.nrows;
-        const int row = t.row0 + (live ? rank * 64 + r : 0);
-        const int tq = row / a.H, h = row - tq * a.H;
-        const __nv_bfloat16* qn = a.qn + tq * a.qn_t + h * a.qn_h + c16 * 8;
-        const __nv_bfloat16* qr = a.qr + tq * a.qr_t + h * a.qr_h + c16 * 8;
-        uint8_t* dst = smem + kOffQ + r * 128 + ((c16 ^ (r & 7)) << 4);
-#pragma unroll
-        for (int at = 0; at < kAtoms; ++at)
-          ptx::cp_async_16(dst + at * kAtomBytes, at < 8 ? qn + at * 64 : qr, live ? 16u : 0u);
-      }
+      load_q(a, smem, t, rank, lane >> 3, 4, lane & 7);
       cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -674,6 +682,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return cache_row(a, tile, b, (s0 & ~(box - 1)) + (lane & (per - 1)) * box, box, &bad);
     };
     bool more = next_piece(a, p, u_hi, t);
+    if (more) {  // the first piece's queries: eight warps at once
+      load_q(a, smem, t, rank, threadIdx.x >> 3, 32, lane & 7);
+      cp_async_wait_all();
+      ptx::fence_proxy_async_smem();
+      ptx::named_bar_sync(4, 256);
+      if (threadIdx.x == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0));
+    }
     int lim = more ? limit_of(t) : 0, crow = more ? row_at(t, p.k0) : 0;
     while (more) {
       float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this quarter's sum
