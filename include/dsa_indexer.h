@@ -476,8 +476,9 @@ dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_strea
  *   block_tables [B, max_pages_per_seq]; out [total_q, H, 512] bf16 dense; lse [total_q, H].
  * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0.
  * Cache rows that no query sees may hold anything, NaN included; rows that some query sees
- * must be finite.  A page outside the cache, or a position past the table, is
- * skipped and reported through dsa_check_device_status.  Probabilities enter P.V rounded to
+ * must be finite.  A NaN in a query makes out and lse of its (t, h) NaN and no others.  A page
+ * outside the cache, or a position past the table, is skipped and reported through
+ * dsa_check_device_status.  Probabilities enter P.V rounded to
  * bf16; statistics and sums are fp32.  Results do not depend on the run (no atomics on data).
  * workspace: dsa_prefix_mla_workspace_size bytes, 16-byte aligned like the other pointers.
  */

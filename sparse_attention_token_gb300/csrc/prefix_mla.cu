@@ -803,9 +803,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const long long slot = piece_slot(a.G, c, pc.i, at_start, pc.whole);
       if (live && quarter == 0) {
         if (!direct) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + trow) * 2) = make_float2(m, l);
-        else if (a.lse) a.lse[tc.row0 + trow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        else if (a.lse) a.lse[tc.row0 + trow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: 0; a NaN stays one
       ptx::tc_fence_after();
       for (int q = 0; q < 4; ++q) {
         uint32_t r[32];
@@ -1034,7 +1034,7 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
       __syncthreads();
     }
     if (!live || (by_piece && y > 0)) continue;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     uint2* dst = reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kRank + (col0 + q0) * 4);
     auto packed = [&](const float4& v) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
       if (n_col == 1) dst[q] = u;
       else *reinterpret_cast<uint4*>(dst + q) = make_uint4(u.x, u.y, v.x, v.y);
     }
-    if (a.lse && col0 + q0 == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (a.lse && col0 + q0 == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
 }
 constexpr int kJoinSmem = 3 * kAcc * kRows * 16;

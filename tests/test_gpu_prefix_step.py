@@ -348,6 +348,34 @@ def test_attend_rows_nobody_sees_may_hold_anything(junk, H):
     Case(H, 64, 70, [(1, 71), (2, 200), (1, 133), (60, 190)], seed=6, junk=junk).check()
 
 
+@pytest.mark.parametrize("H,prefix,reqs", [
+    (128, 0, [(1, 100), (2, 90), (1, 1)]),          # tiles of one block, written without a join
+    (64, 500, [(130, 700), (70, 900)]),             # tiles of a request, joined
+    (16, 500, [(1, 501), (3, 700), (1, 800)]),      # tiles of several requests, joined with their own
+], ids=str)
+def test_attend_a_nan_in_a_query_stays_with_its_row(H, prefix, reqs):
+    c = Case(H, 32, prefix, reqs, seed=12)
+    out, lse = c.gpu()
+    t, h = 2, H - 3
+    for q in (c.qn, c.qr):
+        q[t, h, 5] = math.nan
+        got, got_lse = c.gpu()
+        assert torch.all(torch.isnan(got[t, h])) and torch.isnan(got_lse[t, h])
+        rest = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+        rest[t, h] = False
+        assert torch.equal(got[rest], out[rest]) and torch.equal(got_lse[rest], lse[rest])
+
+
+@pytest.mark.parametrize("H,prefix", [(128, 0), (64, 200), (16, 200)])
+def test_attend_a_nan_in_a_key_reaches_every_row_of_its_request(H, prefix):
+    c = Case(H, 32, prefix, [(1, prefix + 90), (1, prefix + 70)], seed=13)
+    s = prefix + 60
+    c.cr[int(c.bt[0, s // 32]), s % 32, 7] = math.nan
+    out, lse = c.gpu()
+    assert torch.all(torch.isnan(out[0])) and torch.all(torch.isnan(lse[0]))
+    assert torch.all(torch.isfinite(out[1])) and torch.all(torch.isfinite(lse[1]))
+
+
 def test_attend_one_key_is_its_row():
     c = Case(64, 16, 0, [(1, 1), (1, 1), (1, 1)], seed=7)
     out, lse = c.gpu()
