@@ -24,7 +24,7 @@
 //   warp 8      keys of S, three groups of 3 columns of 64 bf16, and warp 9 keys of P . V, two
 //               groups of 2 columns: each group refilled as soon as its MMAs are done; TMA, one
 //               lane per page piece and column;
-//   warp 10     the piece's query rows (16-byte cp.async, any strides);
+//   warp 10     the query rows of every piece but the first (16-byte cp.async, any strides);
 //   warp 11     TMEM; in the even CTA one lane issues the MMAs.
 // 12 warps leave 168 registers a thread; with a warp for every group they were 128, which the
 // softmax warps spilled.
@@ -37,7 +37,7 @@
 // Keys are staged twice, once for S and once for P . V (the MMAs of a pair read the same offsets in
 // both CTAs, so one copy cannot be split by keys and by columns), which fills shared memory with one
 // block; nine K and four V groups cost the two copying warps and the issuer more than they save.
-// 1781 x 64 rows behind 6000 keys take 0.98 ms, 1.60 PFLOP/s (0.87 to 0.92 ms, 1.71 to 1.80 PFLOP/s,
+// 1781 x 64 rows behind 6000 keys take 0.98 ms, 1.60 PFLOP/s (0.87 to 0.93 ms, 1.70 to 1.80 PFLOP/s,
 // launch after launch in a graph), the tensor pipe active 76 % of its cycles under the profiler.
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
@@ -112,7 +112,7 @@ struct Args {
 // Barriers of a CTA.  L: the even CTA's, waited for by the issuer; the others are waited for in
 // each CTA and completed by the issuer's commits in both.
 struct Bars {
-  uint64_t qfull, qempty;        // qfull L: the query warp of each CTA
+  uint64_t qfull, qempty;        // qfull L: each CTA, its query rows
   uint64_t kfull[3], kempty[3];  // L: each CTA's copies
   uint64_t vfull[2], vempty[2];  // L
   uint64_t vown[2];              // this CTA's copies of a block with rows to clear
