@@ -11,12 +11,16 @@ Function names mirror the C ABI:
   dsa_resolve_indexer_sources, dsa_indexer_stack, dsa_check_device_status,
   dsa_topk_width, dsa_status_string, dsa_version (and the others the header declares;
   dsa_clock_sample is a diagnostic for measuring the SM clock over an interval).
+Calls that take `stream` run on it (default: the current stream): what they allocate comes from
+that stream's memory, and the caller orders the stream behind the kernels that made the inputs and
+before those that read the results, as with torch's own operators under torch.cuda.stream(stream).
 Host helpers from the GLM5 TensorCast adaptation design ("Sparse MLA 配置兼容",
 "GLM-5.2 IndexShare"): resolve_topk_limit, extend_indexer_types_for_mtp,
 indexer_types_to_codes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -232,6 +236,27 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _on(stream):
+    """Where a call allocates: on the stream that its kernels run on.  A block of another stream's
+    memory may still be in use by kernels queued there, which nothing orders before this call's."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _hold(stream, inputs, results=()) -> None:
+    """After a call on a given stream: the caller may drop its tensors, and use and drop the
+    results on its current stream, without their memory being reused ahead of either's kernels
+    (the allocator itself only knows the stream that a tensor was allocated on)."""
+    if stream is None:
+        return
+    here = torch.cuda.current_stream()
+    if here == stream:
+        return
+    for tensors, on in ((inputs, stream), (results, here)):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(on)
+
+
 def _expect(checks) -> None:
     """Raise ValueError unless every (tensor or None, name, shape) matches; a shape entry
     of None accepts any size in that dimension.  The C ABI sees only pointers and sizes."""
@@ -258,7 +283,8 @@ def dsa_indexer_scores(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, *, q_p
     if ld is None:
         ld = (S + 3) // 4 * 4
     if scores is None:
-        scores = torch.full((T, ld), fill, dtype=torch.float32, device=q.device)
+        with _on(stream):
+            scores = torch.full((T, ld), fill, dtype=torch.float32, device=q.device)
     _expect([(k, "k", (S, D)), (w, "w", (T, H)), (q_scale, "q_scale", (T, H)), (k_scale, "k_scale", (S,)),
              (scores, "scores", (T, None))])
     if scores.shape[1] < S:
@@ -268,6 +294,7 @@ def dsa_indexer_scores(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, *, q_p
         _dev(k, "k"), _dtype_code(k), _dev(k_scale, "k_scale", torch.float32),
         _dev(w, "w", torch.float32), T, S, H, D, int(q_pos0), _dev(scores, "scores", torch.float32),
         int(scores.stride(0)), _stream_ptr(stream)), "dsa_indexer_scores")
+    _hold(stream, (q, k, w, q_scale, k_scale, scores), (scores,))
     return scores
 
 
@@ -313,7 +340,8 @@ def dsa_indexer_dense_host(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, *,
              (topk, "topk", (T, k_out))])
     need = dsa_indexer_dense_host_workspace_size(T, S, H, D, _dtype_code(q), k_out, chunk_rows)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
     if not workspace.is_cuda or workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a CUDA uint8 tensor")
     _check(lib().dsa_indexer_dense_host(
@@ -322,6 +350,7 @@ def dsa_indexer_dense_host(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, *,
         _host(w, "w", torch.float32), T, S, H, D, int(q_pos0), int(topk_limit), int(k_out), int(order),
         int(chunk_rows), _host(topk, "topk", torch.int32), workspace.data_ptr(), workspace.numel(),
         _stream_ptr(stream)), "dsa_indexer_dense_host")
+    _hold(stream, (workspace,))
     return topk
 
 
@@ -332,13 +361,15 @@ def dsa_indexer_topk(scores: torch.Tensor, *, T: int, S: int, q_pos0: int, topk_
     if k_out is None:
         k_out = topk_limit
     if topk is None:
-        topk = torch.empty((T, k_out), dtype=torch.int32, device=scores.device)
+        with _on(stream):
+            topk = torch.empty((T, k_out), dtype=torch.int32, device=scores.device)
     _expect([(scores, "scores", (None, None)), (topk, "topk", (T, k_out))])
     if scores.shape[0] < T or scores.shape[1] < S:
         raise ValueError(f"scores must hold at least [{T}, {S}], got {tuple(scores.shape)}")
     _check(lib().dsa_indexer_topk(_dev(scores, "scores", torch.float32), int(scores.stride(0)), T, S,
                                   int(q_pos0), int(topk_limit), int(k_out), int(order),
                                   _dev(topk, "topk", torch.int32), _stream_ptr(stream)), "dsa_indexer_topk")
+    _hold(stream, (scores, topk), (topk,))
     return topk
 
 
@@ -410,11 +441,13 @@ def dsa_indexer(q, w, k_cache, cu_q_lens, seq_lens, block_tables, *, max_seq_len
     """Fused paged indexer for a varlen batch; returns topk [total_q, k_out] int32.
     With k_new [total_q, D] bf16 and slot_mapping [total_q] int64 the step's keys are
     first written into k_cache (and k_scale_cache), in place."""
-    a, keep = make_indexer_args(q, w, k_cache, cu_q_lens, seq_lens, block_tables, max_seq_len=max_seq_len,
-                                topk_limit=topk_limit, k_out=k_out, q_scale=q_scale,
-                                k_scale_cache=k_scale_cache, topk=topk, workspace=workspace, order=order,
-                                k_new=k_new, slot_mapping=slot_mapping)
+    with _on(stream):
+        a, keep = make_indexer_args(q, w, k_cache, cu_q_lens, seq_lens, block_tables, max_seq_len=max_seq_len,
+                                    topk_limit=topk_limit, k_out=k_out, q_scale=q_scale,
+                                    k_scale_cache=k_scale_cache, topk=topk, workspace=workspace, order=order,
+                                    k_new=k_new, slot_mapping=slot_mapping)
     _check(lib().dsa_indexer(ctypes.byref(a), _stream_ptr(stream)), "dsa_indexer")
+    _hold(stream, keep, (keep[8],))
     return keep[8]
 
 
@@ -432,6 +465,7 @@ def dsa_indexer_cache_append(k_new: torch.Tensor, slot_mapping: torch.Tensor, k_
         _dev(k_new, "k_new", torch.bfloat16), n, D, _dev(slot_mapping, "slot_mapping", torch.int64),
         _dev(k_cache, "k_cache"), _dtype_code(k_cache), _dev(k_scale_cache, "k_scale_cache", torch.float32),
         page_size, num_pages, _stream_ptr(stream)), "dsa_indexer_cache_append")
+    _hold(stream, (k_new, slot_mapping, k_cache, k_scale_cache))
 
 
 def make_prepare_args(hidden: torch.Tensor, qa_normed: torch.Tensor, rope_cos: Optional[torch.Tensor],
@@ -506,16 +540,13 @@ def dsa_indexer_prepare(hidden: torch.Tensor, qa_normed: torch.Tensor, rope_cos:
                         stream=None):
     """The indexer front-end through the C ABI: returns (q, q_scale, w) for dsa_indexer
     and writes this step's keys (and on an e4m3 cache their scales) through slot_mapping."""
-    a, keep, out = make_prepare_args(hidden, qa_normed, rope_cos, rope_sin, wq_b, wk, weights_proj, k_norm_weight,
-                                     k_cache, slot_mapping, H=H, rope_dim=rope_dim, rope_interleaved=rope_interleaved,
-                                     k_norm_bias=k_norm_bias, k_norm_eps=k_norm_eps, k_scale_cache=k_scale_cache,
-                                     workspace=workspace)
+    with _on(stream):
+        a, keep, out = make_prepare_args(
+            hidden, qa_normed, rope_cos, rope_sin, wq_b, wk, weights_proj, k_norm_weight, k_cache, slot_mapping, H=H,
+            rope_dim=rope_dim, rope_interleaved=rope_interleaved, k_norm_bias=k_norm_bias, k_norm_eps=k_norm_eps,
+            k_scale_cache=k_scale_cache, workspace=workspace)
     _check(lib().dsa_indexer_prepare(ctypes.byref(a), _stream_ptr(stream)), "dsa_indexer_prepare")
-    if stream is not None:  # memory freed here must not be reused ahead of that stream's kernels
-        for t in keep:
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
-    del keep
+    _hold(stream, keep, out)
     return out
 
 
@@ -581,16 +612,18 @@ def dsa_indexer_shard_candidates(q: torch.Tensor, k_shard: torch.Tensor, w: torc
     nbytes = ctypes.c_size_t(0)
     _check(lib().dsa_indexer_shard_candidates_workspace_size(T, S, ctypes.byref(nbytes)),
            "dsa_indexer_shard_candidates_workspace_size")
-    if workspace is None:
-        workspace = torch.empty(max(nbytes.value, 16), dtype=torch.uint8, device=q.device)
-    cand_idx = torch.empty((T, k_cand), dtype=torch.int32, device=q.device)
-    cand_scores = torch.empty((T, k_cand), dtype=torch.float32, device=q.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(nbytes.value, 16), dtype=torch.uint8, device=q.device)
+        cand_idx = torch.empty((T, k_cand), dtype=torch.int32, device=q.device)
+        cand_scores = torch.empty((T, k_cand), dtype=torch.float32, device=q.device)
     _check(lib().dsa_indexer_shard_candidates(
         _dev(q, "q"), _dtype_code(q), _dev(q_scale, "q_scale", torch.float32), _dev(k_shard, "k_shard"),
         _dtype_code(k_shard), _dev(k_scale, "k_scale", torch.float32), _dev(w, "w", torch.float32), T, S, H, D,
         int(q_pos0), int(key_offset), int(k_cand), cand_idx.data_ptr(), cand_scores.data_ptr(),
         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
         "dsa_indexer_shard_candidates")
+    _hold(stream, (q, k_shard, w, q_scale, k_scale, workspace), (cand_idx, cand_scores))
     return cand_idx, cand_scores
 
 
@@ -602,12 +635,14 @@ def dsa_indexer_merge_candidates(cand_scores: torch.Tensor, cand_idx: torch.Tens
     k_out = topk_limit if k_out is None else k_out
     _expect([(cand_scores, "cand_scores", (n_shards, T, k_cand))])
     if topk is None:
-        topk = torch.empty((T, k_out), dtype=torch.int32, device=cand_idx.device)
+        with _on(stream):
+            topk = torch.empty((T, k_out), dtype=torch.int32, device=cand_idx.device)
     _expect([(topk, "topk", (T, k_out))])
     _check(lib().dsa_indexer_merge_candidates(
         _dev(cand_scores, "cand_scores", torch.float32), _dev(cand_idx, "cand_idx", torch.int32), n_shards, T,
         k_cand, int(topk_limit), int(k_out), int(order), _dev(topk, "topk", torch.int32), _stream_ptr(stream)),
         "dsa_indexer_merge_candidates")
+    _hold(stream, (cand_scores, cand_idx, topk), (topk,))
     return topk
 
 
@@ -634,7 +669,8 @@ def dsa_indexer_key_sharded(q: torch.Tensor, k_shard: torch.Tensor, w: torch.Ten
     ci, cs = dsa_indexer_shard_candidates(q, k_shard, w, q_pos0=q_pos0, key_offset=key_offset,
                                           k_cand=min(topk_limit, k_out), q_scale=q_scale, k_scale=k_scale,
                                           stream=stream)
-    all_idx, all_sc = gather_shard_candidates(ci, cs, group)
+    with _on(stream):  # the gather reads what the call above writes on that stream
+        all_idx, all_sc = gather_shard_candidates(ci, cs, group)
     return dsa_indexer_merge_candidates(all_sc, all_idx, topk_limit=topk_limit, k_out=k_out, order=order,
                                         stream=stream)
 
@@ -678,9 +714,11 @@ def make_sparse_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_le
 def dsa_sparse_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, topk, *, scale: float,
                    out=None, workspace=None, stream=None) -> torch.Tensor:
     """Latent attention output [total_q, H, kv_rank] fp32 of each query over its selected keys."""
-    a, keep = make_sparse_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, topk,
-                                   scale=scale, out=out, workspace=workspace)
+    with _on(stream):
+        a, keep = make_sparse_mla_args(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, topk,
+                                       scale=scale, out=out, workspace=workspace)
     _check(lib().dsa_sparse_mla(ctypes.byref(a), _stream_ptr(stream)), "dsa_sparse_mla")
+    _hold(stream, keep, (keep[8],))
     return keep[8]
 
 
@@ -706,10 +744,18 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype) -> int:
     return t.data_ptr()
 
 
-def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for the call's kernels, from the memory of the stream they run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device, stream) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device, stream)
     if t.shape != shape:
         _expect([(t, name, shape)])
     _ptr(t, name, dtype)
@@ -730,14 +776,6 @@ def _rows(t: torch.Tensor, name: str) -> int:
 def _stream_of(device: torch.device, stream) -> int:
     """Raw cudaStream_t of `stream`, or of the current stream on the device."""
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _record(tensors, stream) -> None:
-    """Memory of these tensors must not be reused ahead of `stream`'s kernels (torch's
-    allocator only knows the stream a tensor was allocated on)."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
 
 
 def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor, free_pages: torch.Tensor,
@@ -761,19 +799,19 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
     i32, dev = torch.int32, block_tables.device
     lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
             _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
-    cu_q_lens = _out(cu_q_lens, "cu_q_lens", (B + 1,), i32, dev)
-    slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev)
-    positions = _out(positions, "positions", (total_q,), i32, dev)
-    used = _out(used, "used", (1,), i32, dev)
+    cu_q_lens = _out(cu_q_lens, "cu_q_lens", (B + 1,), i32, dev, stream)
+    slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev, stream)
+    positions = _out(positions, "positions", (total_q,), i32, dev, stream)
+    used = _out(used, "used", (1,), i32, dev, stream)
     args = _PLAN_ARGS.pack(B, total_q, page_size, width, n_prefix, fs[0], *lens, cu_q_lens.data_ptr(),
                            slot_mapping.data_ptr(), positions.data_ptr(), used.data_ptr())
     status = lib().dsa_page_plan(args, _stream_of(dev, stream))
     if status != DSA_OK:
         raise DsaError(status, "dsa_page_plan")
+    results = (cu_q_lens, slot_mapping, positions, used)
     if stream is not None:
-        _record((q_lens, seq_lens, block_tables, free_pages, prefix_pages, cu_q_lens, slot_mapping, positions, used),
-                stream)
-    return cu_q_lens, slot_mapping, positions, used
+        _hold(stream, (q_lens, seq_lens, block_tables, free_pages, prefix_pages) + results, results)
+    return results
 
 
 def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor, cache_c: torch.Tensor,
@@ -815,7 +853,7 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
     if status != DSA_OK:
         raise DsaError(status, "dsa_mla_cache_append")
     if stream is not None:
-        _record((c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions), stream)
+        _hold(stream, (c_kv, k_rope, slot_mapping, cache_c, cache_r, norm_weight, rope_cos, rope_sin, positions))
 
 
 def dsa_prefix_mla_workspace_size(B: int, total_q: int, H: int, *, prefix_len: int) -> int:
@@ -856,7 +894,8 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
                _ptr(cache_r, "cache_r", bf16), _ptr(prefix_pages, "prefix_pages", i32),
                _ptr(block_tables, "block_tables", i32), _ptr(cu_q_lens, "cu_q_lens", i32),
                _ptr(seq_lens, "seq_lens", i32))
-    out, lse = _out(out, "out", (T, H, R), bf16, dev), _out(lse, "lse", (T, H), torch.float32, dev)
+    out = _out(out, "out", (T, H, R), bf16, dev, stream)
+    lse = _out(lse, "lse", (T, H), torch.float32, dev, stream)
     L = lib()
     if workspace is None:
         need = ctypes.c_size_t(0)
@@ -864,7 +903,7 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
         if status != DSA_OK:
             raise DsaError(status, "dsa_prefix_mla_workspace_size")
         room = need.value or 16
-        workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+        workspace = _new(room, torch.uint8, dev, stream)
     else:
         room = workspace.numel() * workspace.element_size()
     args = _PREFIX_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"), room)
@@ -872,8 +911,8 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     if status != DSA_OK:
         raise DsaError(status, "dsa_prefix_mla")
     if stream is not None:
-        _record((q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
-                 workspace), stream)
+        _hold(stream, (q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
+                       workspace), (out, lse))
     return out, lse
 
 
@@ -892,8 +931,10 @@ def dsa_check_device_status(stream=None) -> int:
 def dsa_clock_sample(n_ctas: int, stream=None):
     """Device tensor [n_ctas, 3] int64 of (SM id, SM cycle counter, global ns timer), one
     row per one-thread block; two samples bracket an interval (diagnostic)."""
-    out = torch.empty((n_ctas, 3), dtype=torch.int64, device="cuda")
+    with _on(stream):
+        out = torch.empty((n_ctas, 3), dtype=torch.int64, device="cuda")
     _check(lib().dsa_clock_sample(out.data_ptr(), int(n_ctas), _stream_ptr(stream)), "dsa_clock_sample")
+    _hold(stream, (), (out,))
     return out
 
 
@@ -938,13 +979,15 @@ def dsa_indexer_static(q, w, k_cache, cu_q_lens, seq_lens, block_tables, *, max_
     step).  The library keeps the scratch in a fixed device array of
     DSA_STATIC_WORKSPACE_BYTES; larger problems raise DsaError(DSA_ERR_WORKSPACE).
     Calls that overlap on the GPU share that array and must be serialised."""
-    a, keep = make_indexer_args(q, w, k_cache, cu_q_lens, seq_lens, block_tables, max_seq_len=max_seq_len,
-                                topk_limit=topk_limit, k_out=k_out, q_scale=q_scale,
-                                k_scale_cache=k_scale_cache, topk=topk,
-                                workspace=torch.empty(0, dtype=torch.uint8, device=q.device), order=order)
+    with _on(stream):
+        a, keep = make_indexer_args(q, w, k_cache, cu_q_lens, seq_lens, block_tables, max_seq_len=max_seq_len,
+                                    topk_limit=topk_limit, k_out=k_out, q_scale=q_scale,
+                                    k_scale_cache=k_scale_cache, topk=topk,
+                                    workspace=torch.empty(0, dtype=torch.uint8, device=q.device), order=order)
     a.workspace, a.workspace_bytes = None, 0
     fn = lib().dsa_indexer_static
     fn.restype = ctypes.c_int
     fn.argtypes = [ctypes.POINTER(dsa_indexer_args), ctypes.c_void_p]
     _check(fn(ctypes.byref(a), _stream_ptr(stream)), "dsa_indexer_static")
+    _hold(stream, keep, (keep[8],))
     return keep[8]
