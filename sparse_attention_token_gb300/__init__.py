@@ -215,11 +215,20 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported element type {t.dtype} (bf16 or float8_e4m3fn)")
 
 
+def _on_current_device(t: torch.Tensor, name: str) -> None:
+    """The library launches on the calling thread's current device, so every tensor lies there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    here = torch._C._cuda_getDevice()
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on cuda:{t.get_device()} but the current device is cuda:{here}: call under "
+                         f"torch.cuda.device({t.get_device()})")
+
+
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    _on_current_device(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -233,6 +242,9 @@ def _stream_ptr(stream) -> Optional[int]:
         if not torch.cuda.is_available():
             return None
         stream = torch.cuda.current_stream()
+    elif stream.device_index != torch._C._cuda_getDevice():
+        raise ValueError(f"stream is one of cuda:{stream.device_index} but the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
     return stream.cuda_stream
 
 
@@ -344,6 +356,7 @@ def dsa_indexer_dense_host(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, *,
             workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
     if not workspace.is_cuda or workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a CUDA uint8 tensor")
+    _on_current_device(workspace, "workspace")
     _check(lib().dsa_indexer_dense_host(
         _host(q, "q"), _dtype_code(q), _host(q_scale, "q_scale", torch.float32),
         _host(k, "k"), _dtype_code(k), _host(k_scale, "k_scale", torch.float32),
@@ -735,11 +748,17 @@ assert _APPEND_ARGS.size == ctypes.sizeof(dsa_mla_cache_append_args)
 assert _PREFIX_ARGS.size == ctypes.sizeof(dsa_prefix_mla_args)
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype) -> int:
-    """Device pointer of a contiguous CUDA tensor of this type (0 for None)."""
+def _here(t: torch.Tensor) -> int:
+    """Index of the current device, which every tensor of a call must lie on (no index where t,
+    one of them, is no CUDA tensor: there may be no device to ask for)."""
+    return torch._C._cuda_getDevice() if t.is_cuda else -2
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, here: int) -> int:
+    """Device pointer of a contiguous tensor of this type on device `here` (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype != dtype or t.get_device() != here or not t.is_contiguous():
         _dev(t, name, dtype)
     return t.data_ptr()
 
@@ -752,20 +771,21 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device, stream) -> torch.Tensor:
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device, here, stream) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
         return _new(shape, dtype, device, stream)
     if t.shape != shape:
         _expect([(t, name, shape)])
-    _ptr(t, name, dtype)
+    _ptr(t, name, dtype, here)
     return t
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    """Device pointer of a bf16 tensor whose last dimension is dense, the others in any strides."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _rows(t: torch.Tensor, name: str, here: int) -> int:
+    """Device pointer of a bf16 tensor on device `here` whose last dimension is dense, the others
+    in any strides."""
+    if t.get_device() != here:
+        _on_current_device(t, name)
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -773,9 +793,9 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _stream_of(device: torch.device, stream) -> int:
-    """Raw cudaStream_t of `stream`, or of the current stream on the device."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _stream_of(here: int, stream) -> int:
+    """Raw cudaStream_t of `stream`, or of the current stream on device `here`."""
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream_ptr(stream)
 
 
 def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor, free_pages: torch.Tensor,
@@ -796,16 +816,17 @@ def dsa_page_plan(q_lens: torch.Tensor, seq_lens: torch.Tensor, block_tables: to
         _expect([(q_lens, "q_lens", (None,)), (seq_lens, "seq_lens", (B,)), (block_tables, "block_tables", (B, None)),
                  (free_pages, "free_pages", (None,)), (prefix_pages, "prefix_pages", (None,))])
     B, width = bs
-    i32, dev = torch.int32, block_tables.device
-    lens = (_ptr(q_lens, "q_lens", i32), _ptr(seq_lens, "seq_lens", i32), _ptr(prefix_pages, "prefix_pages", i32),
-            _ptr(free_pages, "free_pages", i32), _ptr(block_tables, "block_tables", i32))
-    cu_q_lens = _out(cu_q_lens, "cu_q_lens", (B + 1,), i32, dev, stream)
-    slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev, stream)
-    positions = _out(positions, "positions", (total_q,), i32, dev, stream)
-    used = _out(used, "used", (1,), i32, dev, stream)
+    i32, dev, here = torch.int32, block_tables.device, _here(block_tables)
+    lens = (_ptr(q_lens, "q_lens", i32, here), _ptr(seq_lens, "seq_lens", i32, here),
+            _ptr(prefix_pages, "prefix_pages", i32, here), _ptr(free_pages, "free_pages", i32, here),
+            _ptr(block_tables, "block_tables", i32, here))
+    cu_q_lens = _out(cu_q_lens, "cu_q_lens", (B + 1,), i32, dev, here, stream)
+    slot_mapping = _out(slot_mapping, "slot_mapping", (total_q,), torch.int64, dev, here, stream)
+    positions = _out(positions, "positions", (total_q,), i32, dev, here, stream)
+    used = _out(used, "used", (1,), i32, dev, here, stream)
     args = _PLAN_ARGS.pack(B, total_q, page_size, width, n_prefix, fs[0], *lens, cu_q_lens.data_ptr(),
                            slot_mapping.data_ptr(), positions.data_ptr(), used.data_ptr())
-    status = lib().dsa_page_plan(args, _stream_of(dev, stream))
+    status = lib().dsa_page_plan(args, _stream_of(here, stream))
     if status != DSA_OK:
         raise DsaError(status, "dsa_page_plan")
     results = (cu_q_lens, slot_mapping, positions, used)
@@ -843,13 +864,15 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
                  (cache_c, "cache_c", (num_pages, page_size, R)), (cache_r, "cache_r", (num_pages, page_size, rd)),
                  (norm_weight, "norm_weight", (R,)), (rope_cos, "rope_cos", table), (rope_sin, "rope_sin", table),
                  (positions, "positions", (n,))])
-    f32, bf16 = torch.float32, torch.bfloat16
+    f32, bf16, here = torch.float32, torch.bfloat16, _here(cache_c)
     args = _APPEND_ARGS.pack(
-        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv"),
-        _rows(k_rope, "k_rope"), c_kv.stride(0), k_rope.stride(0), _ptr(slot_mapping, "slot_mapping", torch.int64),
-        _ptr(norm_weight, "norm_weight", f32), _ptr(rope_cos, "rope_cos", f32), _ptr(rope_sin, "rope_sin", f32),
-        _ptr(positions, "positions", torch.int32), _ptr(cache_c, "cache_c", bf16), _ptr(cache_r, "cache_r", bf16))
-    status = lib().dsa_mla_cache_append(args, _stream_of(cache_c.device, stream))
+        n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv", here),
+        _rows(k_rope, "k_rope", here), c_kv.stride(0), k_rope.stride(0),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, here), _ptr(norm_weight, "norm_weight", f32, here),
+        _ptr(rope_cos, "rope_cos", f32, here), _ptr(rope_sin, "rope_sin", f32, here),
+        _ptr(positions, "positions", torch.int32, here), _ptr(cache_c, "cache_c", bf16, here),
+        _ptr(cache_r, "cache_r", bf16, here))
+    status = lib().dsa_mla_cache_append(args, _stream_of(here, stream))
     if status != DSA_OK:
         raise DsaError(status, "dsa_mla_cache_append")
     if stream is not None:
@@ -857,7 +880,7 @@ def dsa_mla_cache_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
 
 
 def dsa_prefix_mla_workspace_size(B: int, total_q: int, H: int, *, prefix_len: int) -> int:
-    """Bytes of workspace that dsa_prefix_mla takes for a batch of these sizes."""
+    """Bytes of workspace that dsa_prefix_mla takes for a batch of these sizes on the current device."""
     need = ctypes.c_size_t(0)
     args = _PREFIX_ARGS.pack(B, total_q, H, 512, 64, 64, 0, 0, prefix_len, -(-prefix_len // 64), 1.0, *[0] * 16)
     _check(lib().dsa_prefix_mla_workspace_size(args, ctypes.byref(need)), "dsa_prefix_mla_workspace_size")
@@ -886,16 +909,16 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
         _expect([(q_rope, "q_rope", (T, H, rd)), (cache_c, "cache_c", (num_pages, page_size, R)),
                  (cache_r, "cache_r", (num_pages, page_size, rd)), (block_tables, "block_tables", (B, None)),
                  (cu_q_lens, "cu_q_lens", (B + 1,))])
-    i32, bf16, dev = torch.int32, torch.bfloat16, cache_c.device
+    i32, bf16, dev, here = torch.int32, torch.bfloat16, cache_c.device, _here(cache_c)
     sizes = (B, T, H, R, rd, page_size, num_pages, bs[1], prefix_len, n_prefix, scale)
     qt, qh, _ = q_nope.stride()
     rt, rh, _ = q_rope.stride()
-    tensors = (_rows(q_nope, "q_nope"), _rows(q_rope, "q_rope"), qt, qh, rt, rh, _ptr(cache_c, "cache_c", bf16),
-               _ptr(cache_r, "cache_r", bf16), _ptr(prefix_pages, "prefix_pages", i32),
-               _ptr(block_tables, "block_tables", i32), _ptr(cu_q_lens, "cu_q_lens", i32),
-               _ptr(seq_lens, "seq_lens", i32))
-    out = _out(out, "out", (T, H, R), bf16, dev, stream)
-    lse = _out(lse, "lse", (T, H), torch.float32, dev, stream)
+    tensors = (_rows(q_nope, "q_nope", here), _rows(q_rope, "q_rope", here), qt, qh, rt, rh,
+               _ptr(cache_c, "cache_c", bf16, here), _ptr(cache_r, "cache_r", bf16, here),
+               _ptr(prefix_pages, "prefix_pages", i32, here), _ptr(block_tables, "block_tables", i32, here),
+               _ptr(cu_q_lens, "cu_q_lens", i32, here), _ptr(seq_lens, "seq_lens", i32, here))
+    out = _out(out, "out", (T, H, R), bf16, dev, here, stream)
+    lse = _out(lse, "lse", (T, H), torch.float32, dev, here, stream)
     L = lib()
     if workspace is None:
         need = ctypes.c_size_t(0)
@@ -907,7 +930,7 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     else:
         room = workspace.numel() * workspace.element_size()
     args = _PREFIX_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"), room)
-    status = L.dsa_prefix_mla(args, _stream_of(dev, stream))
+    status = L.dsa_prefix_mla(args, _stream_of(here, stream))
     if status != DSA_OK:
         raise DsaError(status, "dsa_prefix_mla")
     if stream is not None:

@@ -1,4 +1,5 @@
-"""Where the bindings' memory comes from when a call is given a stream, without a GPU.
+"""Where the bindings' memory comes from when a call is given a stream, and that every tensor of
+a call lies on the current device, without a GPU.
 
 The tensors are CPU tensors that answer as CUDA ones, the C entry points are stand-ins that
 return DSA_OK (workspace sizes come from the real ones), and torch's allocation and stream calls
@@ -13,23 +14,29 @@ import torch
 
 
 class Cuda(torch.Tensor):
-    """A CPU tensor that answers as one on cuda:0."""
+    """A CPU tensor that answers as one on cuda:0 (or the device set as `index`)."""
     __torch_function__ = torch._C._disabled_torch_function_impl
+    index = 0
     is_cuda = property(lambda self: True)
-    device = property(lambda self: torch.device("cuda", 0))
+    device = property(lambda self: torch.device("cuda", self.index))
 
     def get_device(self):
-        return 0
+        return self.index
 
     def record_stream(self, stream):
         LOG.setdefault(id(self), []).append(stream.name)
 
 
 LOG = {}
+AWAY = {}  # "left": tensors still to be made before the one that lies on cuda:1
 
 
 def cuda(t):
-    return torch.Tensor._make_subclass(Cuda, t)
+    t = torch.Tensor._make_subclass(Cuda, t)
+    if AWAY:
+        t.index = 1 if AWAY["left"] == 0 else 0
+        AWAY["left"] -= 1
+    return t
 
 
 class Stream:
@@ -78,6 +85,7 @@ def box(monkeypatch):
         return make
 
     LOG.clear()
+    AWAY.clear()
     fake = Lib()
     monkeypatch.setattr(dsa, "lib", lambda: fake)
     monkeypatch.setattr(torch, "empty", alloc(torch.empty))
@@ -97,7 +105,7 @@ b16 = lambda *s: cuda(torch.zeros(s, dtype=torch.bfloat16))
 
 
 def _paged():
-    return (b16(2, 32, 128), f32(2, 32), b16(4, 64, 128), i32(3), i32(2), i32(2, 2)), dict(max_seq_len=128, topk_limit=64)
+    return b16(2, 32, 128), f32(2, 32), b16(4, 64, 128), i32(3), i32(2), i32(2, 2)
 
 
 CALLS = {
@@ -108,8 +116,8 @@ CALLS = {
                                                        i32(2, 2), i32(3), i32(2), i32(1), prefix_len=60, scale=0.1, **kw),
     "dsa_indexer_scores": lambda d, **kw: d.dsa_indexer_scores(b16(4, 32, 128), b16(8, 128), f32(4, 32), **kw),
     "dsa_indexer_topk": lambda d, **kw: d.dsa_indexer_topk(f32(4, 8), T=4, S=8, q_pos0=4, topk_limit=4, **kw),
-    "dsa_indexer": lambda d, **kw: d.dsa_indexer(*_paged()[0], **_paged()[1], **kw),
-    "dsa_indexer_static": lambda d, **kw: d.dsa_indexer_static(*_paged()[0], **_paged()[1], **kw),
+    "dsa_indexer": lambda d, **kw: d.dsa_indexer(*_paged(), max_seq_len=128, topk_limit=64, **kw),
+    "dsa_indexer_static": lambda d, **kw: d.dsa_indexer_static(*_paged(), max_seq_len=128, topk_limit=64, **kw),
     "dsa_indexer_cache_append": lambda d, **kw: d.dsa_indexer_cache_append(b16(3, 128), i64(3), b16(2, 16, 128), **kw),
     "dsa_indexer_prepare": lambda d, **kw: d.dsa_indexer_prepare(
         b16(2, 256), b16(2, 128), f32(2, 32), f32(2, 32), b16(32 * 128, 128), b16(128, 256), b16(32, 256), f32(128),
@@ -158,3 +166,32 @@ def test_the_host_pipeline_allocates_its_workspace_there(box):
     h = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
     box.dsa.dsa_indexer_dense_host(h(4, 32, 128), h(8, 128), h(4, 32, dtype=torch.float32), topk_limit=4, stream=box.side)
     assert [where for _, where in box.made] == ["side"] and box.launches == [("dsa_indexer_dense_host", 77)]
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "dsa_clock_sample"])
+def test_tensors_of_another_device_are_refused(box, name):
+    CALLS[name](box.dsa)                       # all of them on the current device
+    box.launches.clear()
+    n = 0
+    while True:                                # the n-th tensor that is made lies on the other device
+        AWAY["left"] = n
+        box.made.clear()
+        try:
+            CALLS[name](box.dsa)
+            refused = False
+        except ValueError as e:
+            refused = "cuda:1" in str(e) and "current device" in str(e) and not box.launches
+        if AWAY["left"] >= 0 or any(t.index for t, _ in box.made):
+            break                              # past the caller's tensors
+        assert refused, f"tensor {n}"
+        n += 1
+    assert n >= 1
+
+
+def test_a_stream_of_another_device_is_refused(box):
+    other = Stream("other", 99)
+    other.device_index = 1
+    for name in CALLS:
+        with pytest.raises(ValueError, match="stream"):
+            CALLS[name](box.dsa, stream=other)
+    assert not box.launches
