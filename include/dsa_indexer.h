@@ -585,6 +585,18 @@ dsa_status dsa_clock_sample(uint64_t* out, int n_ctas, dsa_stream_t stream);
  */
 dsa_status dsa_test_arm_score_timeout(unsigned long long limit_ns);
 
+/*
+ * dsa_test_arm_prefix_mla_timeout -- the same for the attention kernel of dsa_prefix_mla,
+ * which runs on pairs of CTAs: in the next dsa_prefix_mla launch of the calling host thread
+ * one role (in the same CTA of every pair) waits on an internal barrier that nothing ever
+ * completes, for about limit_ns (at most 1e9).  site:
+ *   1 MMA issuer, before its block of keys number `at`; 2 copies of the keys for the logits,
+ *   3 copies of the keys for the output, before the first; 4 query rows, before piece `at`
+ *   (1 and up); 5 softmax, at its start; 10 .. 13 are 2 .. 5 in the odd CTAs.
+ * DSA_ERR_INVALID_ARGUMENT for another site or limit; limit_ns = 0 disarms.
+ */
+dsa_status dsa_test_arm_prefix_mla_timeout(int site, unsigned at, unsigned long long limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

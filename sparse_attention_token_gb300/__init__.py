@@ -186,6 +186,8 @@ def lib():
         L.dsa_prefix_mla.argtypes = [P, P]
         L.dsa_test_arm_score_timeout.restype = I
         L.dsa_test_arm_score_timeout.argtypes = [ctypes.c_ulonglong]
+        L.dsa_test_arm_prefix_mla_timeout.restype = I
+        L.dsa_test_arm_prefix_mla_timeout.argtypes = [I, ctypes.c_uint, ctypes.c_ulonglong]
         _LIB = L
     return _LIB
 
@@ -944,6 +946,13 @@ def dsa_test_arm_score_timeout(limit_ns: int) -> None:
     waits up to limit_ns on a barrier nothing completes, then records DSA_ERR_TIMEOUT,
     drains and returns (its outputs are unspecified).  0 disarms."""
     _check(lib().dsa_test_arm_score_timeout(int(limit_ns)), "dsa_test_arm_score_timeout")
+
+
+def dsa_test_arm_prefix_mla_timeout(site: int, at: int, limit_ns: int) -> None:
+    """The same for the attention kernel of the next dsa_prefix_mla: a wait of one role runs out (1 MMAs
+    before block `at`, 2 keys, 3 values, 4 queries before piece `at`, 5 softmax; + 8 in the odd CTAs)."""
+    _check(lib().dsa_test_arm_prefix_mla_timeout(int(site), int(at), int(limit_ns)),
+           "dsa_test_arm_prefix_mla_timeout")
 
 
 def dsa_check_device_status(stream=None) -> int:

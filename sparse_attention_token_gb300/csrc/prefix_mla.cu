@@ -42,8 +42,8 @@
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
 //
-// Every wait is bounded; after one gives up, every role stops, copies and MMAs in flight are
-// drained (bounded) and TMEM is freed.
+// Every wait is bounded; after one gives up, every role of both CTAs stops, the MMAs and copies in
+// flight are drained (bounded) and TMEM is freed.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
@@ -107,7 +107,24 @@ struct Args {
   Query* queries;          // [total_q], packed batches only
   float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
   unsigned* status;
+  // failure-path test hook (probe_site 0: off): a role waits, at probe_at, for what never comes
+  int probe_site;
+  uint32_t probe_at;
+  long long probe_cycles;
 };
+
+// Roles whose waits the test hook can let run out (the issuer's at a block, the queries' at a piece, the
+// others' at their start); + kProbeOdd: in the pairs' odd CTAs.
+enum : int { kProbeMma = 1, kProbeKeys = 2, kProbeValues = 3, kProbeQueries = 4, kProbeSoftmax = 5, kProbeOdd = 8 };
+struct Probe {
+  int site;
+  uint32_t at;
+  unsigned long long limit_ns;
+};
+Probe& armed_probe() {
+  static thread_local Probe p{0, 0, 0};
+  return p;
+}
 
 // Barriers of a CTA.  L: the even CTA's, waited for by the issuer; the others are waited for in
 // each CTA and completed by the issuer's commits in both.
@@ -117,8 +134,11 @@ struct Bars {
   uint64_t vfull[2], vempty[2];  // L
   uint64_t vown[2];              // this CTA's copies of a block with rows to clear
   uint64_t sfull[2], sempty[2];  // sempty L: 8 softmax warps of each CTA
-  uint64_t pfull, ofree, done;   // pfull, done L
+  uint64_t pfull, ofree, done;   // pfull L; done: the issuer's last commit, in both
+  uint64_t never;                // test hook: nothing arrives
+  uint32_t kissued, vissued;     // this CTA's arrivals at kfull / vfull, all groups together; for the drain
 };
+static_assert(sizeof(Bars) <= 256, "the words behind the barriers begin at 256");
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -437,6 +457,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 260);
   float* xmax = reinterpret_cast<float*>(smem + kOffMisc + 512);  // [2][4][64] by block parity, quarter, row
   const int rank = static_cast<int>(ptx::cluster_ctarank());
+  // A wait that gives up ends the roles of its CTA, and each of them then those of the other CTA.
+  auto give_up = [&]() {
+    *abort = 1;
+    ptx::st_shared_cluster(ptx::mapa_shared(ptx::smem_u32(const_cast<int*>(abort)), ptx::cluster_ctarank() ^ 1u), 1u);
+  };
+  auto spin = [&](uint64_t* bar, uint32_t parity, long long cycles = ptx::kWaitCycles) {
+    return ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout, cycles);
+  };
+  auto probed = [&](int site) { return a.probe_site == site + (rank != 0 ? kProbeOdd : 0); };
+  auto stop_at = [&](int site) { return probed(site) ? a.probe_at : ~0u; };
+  // (The copying warps ask before their first block only: asked in their loops, for every group, it took
+  // 64 x 64 heads behind 8192 keys from 74 to 82 us and 1781 prompt tokens from 0.91 to 1.09 ms.)
+  auto run_out = [&]() { return __all_sync(0xffffffffu, spin(&bars->never, 0, a.probe_cycles)) != 0; };
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(&bars->qfull, 2);
@@ -455,6 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&bars->pfull, 16);
     ptx::mbar_init(&bars->ofree, 1);
     ptx::mbar_init(&bars->done, 1);
+    ptx::mbar_init(&bars->never, 1);
+    bars->kissued = bars->vissued = 0;
     *abort = 0;
     ptx::fence_mbar_init();
   }
@@ -494,9 +529,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t q0 = ptx::desc_lo(sbase + kOffQ, 16), k0 = ptx::desc_lo(sbase + kOffK, 16);
       const uint32_t p0 = ptx::desc_lo(sbase + kOffP, 16), v0 = ptx::desc_lo(sbase + kOffV, 128 * 128);
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout);
-      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && spin(bar, parity); };
+      const uint32_t stop = stop_at(kProbeMma);
       uint32_t n1 = 0, n2 = 0;  // blocks whose S / P . V was issued
       bool more = next_piece(a, p, u_hi, t);
       for (uint32_t seg = 0; ok && more; ++seg) {
@@ -505,6 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i <= nblk; ++i) {
           if (i < nblk) {
             const uint32_t d = tmem_base + (n1 & 1) * 64;
+            if (n1 == stop) ok = ok && spin(&bars->never, 0, a.probe_cycles);
             wait(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1);
 #pragma unroll
             for (int g = 0; g < 3; ++g) {
@@ -550,15 +585,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      ptx::mma_commit_pair(&bars->done, 1);
+      if (!ok) give_up();
+      ptx::mma_commit_pair(&bars->done, 3);
       ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
     }
     __syncwarp();
   } else if (warp == 8) {
     // ------------------------------------------------------------ keys of S: this CTA's 64 of a block
     const int per = 64 / box, j = lane & (per - 1), at = lane / per;  // box of a column, column of a group
-    uint32_t n = 0;
-    bool ok = true;
+    uint32_t n = 0, left = 0;  // left: arrivals when a wait gave up
+    bool ok = !probed(kProbeKeys) || run_out();
     while (ok && next_piece(a, p, u_hi, t)) {
       for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
@@ -567,9 +603,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (bad) atomicOr(a.status, kStatusBadPage);
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
-          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(&bars->kempty[g], (n & 1) ^ 1, abort, a.status,
-                                                            kStatusTimeout)) != 0;
-          if (!ok) break;
+          ok = ok && __all_sync(0xffffffffu, spin(&bars->kempty[g], (n & 1) ^ 1)) != 0;
+          if (!ok) {
+            left = 3 * n + g;
+            break;
+          }
           const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->kfull[g]), 0);
           if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(full, kKGroup);
           __syncwarp();
@@ -581,16 +619,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-    // after a failure: every copy lands before the pair can exit
-    if (rank == 0 && lane == 0 && n > 0 && !ok)
-      for (int g = 0; g < 3; ++g)
-        ptx::mbar_spin_drain(&bars->kfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+    if (!ok) give_up();
+    if (lane == 0) bars->kissued = ok ? 3 * n : left;
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ keys of P . V: this CTA's 4 columns, all 128
     const int per = 128 / box, j = lane & (per - 1), at = lane / per;
-    uint32_t n = 0, cleared = 0;
-    bool ok = true;
+    uint32_t n = 0, cleared = 0, left = 0;
+    bool ok = !probed(kProbeValues) || run_out();
     while (ok && next_piece(a, p, u_hi, t)) {
       for (int k = p.k0; ok && k < p.k1; ++k, ++n) {
         const Block b = block_at(a, t, k);
@@ -601,9 +637,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool clear = b.s0 < b.lo || b.s0 + kKeys > b.hi;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin(&bars->vempty[g], (n & 1) ^ 1, abort, a.status,
-                                                            kStatusTimeout)) != 0;
-          if (!ok) break;
+          ok = ok && __all_sync(0xffffffffu, spin(&bars->vempty[g], (n & 1) ^ 1)) != 0;
+          if (!ok) {
+            left = 2 * n + (clear ? 0 : g);
+            if (clear && g > 0)  // the first group's copy lands on this CTA's own barrier
+              ptx::mbar_spin_drain(&bars->vown[0], cleared & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+            break;
+          }
           const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->vfull[g]), 0);
           if (lane == 0) {
             if (clear) ptx::mbar_arrive_expect_tx(&bars->vown[g], kVGroup);
@@ -617,14 +657,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             else ptx::tma_load_2d_pair(dst, &tmap_c, full, x, row);
           }
         }
-        if (!clear) continue;
+        if (!clear || !ok) continue;
         const int from = min(max(b.lo - b.s0, 0), kKeys), to = max(min(b.hi - b.s0, kKeys), from);  // [from, to) stay
         const int n_clear = from + kKeys - to;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          ok = ok && __all_sync(0xffffffffu, ptx::mbar_spin_drain(&bars->vown[g], cleared & 1, a.status,
-                                                                  kStatusTimeout, ptx::kWaitCycles)) != 0;
-          if (!ok) break;
+          const bool landed = ptx::mbar_spin_drain(&bars->vown[g], cleared & 1, a.status, kStatusTimeout,
+                                                   ok ? ptx::kWaitCycles : ptx::kWaitCycles / 10);
+          if (!__all_sync(0xffffffffu, landed) && ok) {
+            ok = false;
+            left = 2 * n + g;
+          }
+          if (!ok) continue;  // the other group's copy is waited for all the same
           uint8_t* base = smem + kOffV + g * kVGroup;
           for (int e = lane; e < n_clear * 16; e += 32) {  // 16 chunks of 16 bytes a row, in two columns
             const int r = e >> 4, key = r < from ? r : to + (r - from);
@@ -638,19 +682,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++cleared;
       }
     }
-    if (rank == 0 && lane == 0 && n > 0 && !ok)
-      for (int g = 0; g < 2; ++g)
-        ptx::mbar_spin_drain(&bars->vfull[g], (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+    if (!ok) give_up();
+    if (lane == 0) bars->vissued = ok ? 2 * n : left;
     __syncwarp();
   } else if (warp == 10) {
     // ------------------------------------------------------------ queries: this CTA's 64 rows of the tile
     // (the softmax warps, idle until then, bring the first piece's: 4 x 16 heads behind 1000 took
     // 18.3 us when this warp did, 17.0 now, longer calls the same within 0.6)
     const uint32_t full = ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0);
+    const uint32_t stop = stop_at(kProbeQueries);
     next_piece(a, p, u_hi, t);
     for (uint32_t seg = 1; next_piece(a, p, u_hi, t); ++seg) {
-      const bool good = ptx::mbar_spin(&bars->qempty, (seg & 1) ^ 1, abort, a.status, kStatusTimeout);
-      if (!__all_sync(0xffffffffu, good)) break;
+      bool good = seg != stop || spin(&bars->never, 0, a.probe_cycles);
+      good = good && spin(&bars->qempty, (seg & 1) ^ 1);
+      if (!__all_sync(0xffffffffu, good)) {
+        give_up();
+        break;
+      }
       load_q(a, smem, t, rank, lane >> 3, 4, lane & 7);
       cp_async_wait_all();
       ptx::fence_proxy_async_smem();
@@ -689,6 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::named_bar_sync(4, 256);
       if (threadIdx.x == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0));
     }
+    if (probed(kProbeSoftmax) && warp == 0) ok = run_out();
     int lim = more ? limit_of(t) : 0, crow = more ? row_at(t, p.k0) : 0;
     while (more) {
       float m = -INFINITY, l = 0.f;  // reference maximum (scaled, base 2), this quarter's sum
@@ -698,8 +747,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int s0 = b.s0 + half * 64 + part * 32;  // this thread's 32 keys
         if (k > p.k0) crow = row_at(t, k);            // passes while S is computed
         const unsigned there = __ballot_sync(0xffffffffu, crow != a.past_row);
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->sfull[tb], (n >> 1) & 1, abort, a.status,
-                                                                    kStatusTimeout)) != 0;
+        if (ok) ok = __all_sync(0xffffffffu, spin(&bars->sfull[tb], (n >> 1) & 1)) != 0;
         float x[32];
         float mb = -INFINITY;
         if (ok) {
@@ -754,9 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l = l * cr + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
         m = mn;
         // P and O are free once the previous block's P . V has completed
-        if (n > 0 && ok)
-          ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
-                                                              kStatusTimeout)) != 0;
+        if (n > 0 && ok) ok = __all_sync(0xffffffffu, spin(&bars->ofree, (n - 1) & 1)) != 0;
         if (ok) {
           // row of P: this quarter's 32 keys = 4 chunks of 16 bytes, swizzled by the row
           uint8_t* prow = smem + kOffP + half * kAtomBytes + row * 128;
@@ -792,8 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the piece's result
       const bool at_start = pc.k0 == 0;
       const bool direct = pc.whole && !a.packed;
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_spin(&bars->ofree, (n - 1) & 1, abort, a.status,
-                                                                  kStatusTimeout)) != 0;
+      if (ok) ok = __all_sync(0xffffffffu, spin(&bars->ofree, (n - 1) & 1)) != 0;
       float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
       xs[quarter * 64] = l;
       ptx::named_bar_sync(row_bar, 128);
@@ -848,10 +893,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_before();
     }
+    if (!ok) give_up();
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // the issuer has waited for its last commit in its own CTA; its arrival here comes from outside too
+  if (rank != 0 && threadIdx.x == 0)
+    ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
   ptx::cluster_sync();  // no CTA leaves while its peer may still touch its memory, barriers or TMEM
+  if (*abort) {
+    // Set in both CTAs if in one.  The MMAs have waited for every copy unless a role gave up.  Then a
+    // group's last full phase may have the arrival of one CTA only, no more than one phase apart
+    // (a copy of a block waits for the MMAs on the block before, and those for both CTAs' copies):
+    // arrive for the other, so that the phase ends as soon as the copies that were issued have landed.
+    if (rank == 0 && threadIdx.x == 0) {
+      const uint32_t k0 = bars->kissued, v0 = bars->vissued;
+      const uint32_t k1 = ptx::ld_shared_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->kissued), 1));
+      const uint32_t v1 = ptx::ld_shared_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->vissued), 1));
+      auto drain = [&](uint64_t* bar, uint32_t n0, uint32_t n1) {  // phases with this and the other CTA's arrival
+        if (n0 != n1) ptx::mbar_arrive(bar);
+        const uint32_t n = max(n0, n1);
+        if (n > 0) ptx::mbar_spin_drain(bar, (n - 1) & 1, a.status, kStatusTimeout, ptx::kWaitCycles / 10);
+      };
+      for (uint32_t g = 0; g < 3; ++g) drain(&bars->kfull[g], (k0 + 2 - g) / 3, (k1 + 2 - g) / 3);
+      for (uint32_t g = 0; g < 2; ++g) drain(&bars->vfull[g], (v0 + 1 - g) / 2, (v1 + 1 - g) / 2);
+    }
+    ptx::cluster_sync();
+  }
   if (warp == 11) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, 512);
@@ -1229,6 +1297,11 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
   k.part_o = reinterpret_cast<float*>(ws + p.off_o);
   k.status = status;
+  const Probe probe = armed_probe();
+  armed_probe() = Probe{0, 0, 0};
+  k.probe_site = probe.site;
+  k.probe_at = probe.at;
+  k.probe_cycles = 2 * static_cast<long long>(probe.limit_ns);  // some 2 cycles a nanosecond
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(prefix_mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
@@ -1241,6 +1314,14 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   const long long ctas = p.packed ? groups * per_tile : p.G * 2LL;
   e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), kJoinSmem, s, k, per_tile);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_test_arm_prefix_mla_timeout(int site, unsigned at, unsigned long long limit_ns) {
+  const int role = site & ~kProbeOdd;
+  if (role < kProbeMma || role > kProbeSoftmax || site == kProbeMma + kProbeOdd || limit_ns > 1000000000ull)
+    return DSA_ERR_INVALID_ARGUMENT;
+  armed_probe() = limit_ns == 0 ? Probe{0, 0, 0} : Probe{site, at, limit_ns};
+  return DSA_OK;
 }
 
 }  // extern "C"

@@ -302,19 +302,28 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_a
                "r"(bytes)
                : "memory");
 }
+// 32-bit words of shared memory anywhere in the cluster.
+__device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_cluster(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 // Bounded wait like mbar_wait, its limit counted in SM cycles (about 2 s): reading the cycle
 // counter takes some 20 cycles, the global timer about 1000, which every wait that does not
 // succeed at once would add (and a wait on the critical path often just misses).
 constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status,
-                                          unsigned timeout_bit) {
+                                          unsigned timeout_bit, long long cycles = kWaitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 15u) == 0) {
       if (*abort) return false;
-      if (clock64() - t0 > kWaitCycles) {
+      if (clock64() - t0 > cycles) {
         *abort = 1;
         atomicOr(status, timeout_bit);
         return false;
