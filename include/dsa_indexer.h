@@ -481,8 +481,8 @@ dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_strea
  * dsa_check_device_status.  Probabilities enter P.V rounded to
  * bf16; statistics and sums are fp32.  Results do not depend on the run (no atomics on data).
  * workspace: dsa_prefix_mla_workspace_size bytes, 16-byte aligned like the other pointers; some
- * 40 MB on a GB300 (two results of 128 rows for each pair of SMs), and where requests share tiles
- * about 4 KB more for every (query, head) row.
+ * 40 MB on a GB300 (two results of 128 rows for each pair of SMs), and where requests may share
+ * tiles (H no multiple of 128, at most some 850 rows a request) 4 KB more for every row.
  */
 typedef struct {
   int B, total_q, H, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq;

@@ -6,10 +6,10 @@
 // Three launches.
 //
 // plan (one CTA): the (query, head) rows are cut into tiles of up to 128 rows, and every tile's
-// keys into blocks of 128.  A request of many rows fills tiles of its own, which walk the prefix
-// and then the request's keys.  Small requests (few heads, one query) share: tiles packed across
-// requests walk the prefix, further tiles, one request each, walk its own keys, and the two are
-// joined.  The blocks of all tiles stand in one line, cut into equal parts, one per pair of SMs:
+// keys into blocks of 128.  Requests of many rows fill tiles of their own, which walk the prefix
+// and then the request's keys.  Where such tiles would stand too empty (few heads, one query; also
+// a few long prompts among many of these) the batch shares: tiles packed across requests walk the
+// prefix, further tiles, one request each, walk its own keys, and the two are joined.  The blocks of all tiles stand in one line, cut into equal parts, one per pair of SMs:
 // a part may start and end inside a tile, so one long prefix fills every SM.
 //
 // attend (a cluster of two CTAs on two SMs per part, each holding 64 rows of a tile): the 512
@@ -90,7 +90,7 @@ struct Query {
 
 struct Args {
   int B, total_q, H, page_size, page_log2, num_pages, max_pages, prefix_len, num_prefix_pages;
-  int packed;              // small requests: prefix tiles packed across requests
+  int may_pack;            // the plan may pack the prefix tiles across requests
   int max_tiles, G;        // tiles there is room for; CTA pairs
   int narrow;              // the line is shorter than 2^31 places, whatever the lengths
   int past_row;            // a row coordinate past the cache: copies from there are zeros
@@ -102,7 +102,7 @@ struct Args {
   float* lse;
   Tile* tiles;
   long long* u0;           // [max_tiles + 1] where each tile begins in the line of all blocks
-  int* head;               // [0] tiles, [1] tiles without blocks, [2 + b] first own tile of request b
+  int* head;               // [0] tiles, [1] whether some have no blocks, [2] packed, [3 + b] own tiles before request b
   Part* parts;             // [G]
   Query* queries;          // [total_q], packed batches only
   float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
@@ -163,6 +163,12 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
     n = room;
   }
   return static_cast<int>(max(n, 0LL));
+}
+
+// Whether a tile's rows are joined over two tiles, its own being one of a packed batch: tiles of
+// several requests, and those that begin with own keys although there is a prefix.
+__device__ __forceinline__ bool joined(const Args& a, const Tile& t) {
+  return t.b < 0 || (t.n_pre == 0 && a.prefix_len > 0);
 }
 
 // The line of all tiles, U long: a tile's blocks stand behind kSetup places for what it costs to
@@ -227,34 +233,47 @@ __device__ __forceinline__ V block_scan(V v, V* wsum, V* total) {
 // registers (a round trip through L2 between two steps costs about 0.4 us).
 __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Args a) {
   __shared__ long long wsum[32];
-  __shared__ int wsum_n[32], s_head[kPlanThreads + 1], s_sees[kPlanThreads];
+  __shared__ unsigned wsum_n[32];
+  __shared__ int s_head[kPlanThreads + 1], s_sees[kPlanThreads];
   __shared__ long long s_b0[kPlanThreads];
   const int tid = threadIdx.x;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  // rows beyond the last request (padding) count as one more request that sees nothing
-  const int n_pre_tiles = a.packed ? (a.total_q * a.H + kRows - 1) / kRows : 0;
-  int base = n_pre_tiles;
-  const int nreq = a.packed ? a.B : a.B + 1;
-  for (int b0 = 0; b0 < nreq; b0 += kPlanThreads) {
+  const int q_end = min(max(__ldg(a.cu + a.B), 0), a.total_q);
+  // every request's own tiles
+  unsigned own_tiles = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int n = 0;
-    if (b < nreq) {
-      const int q0 = min(max(__ldg(a.cu + b), 0), a.total_q);
-      const int q1 = b < a.B ? min(max(__ldg(a.cu + b + 1), q0), a.total_q) : a.total_q;
-      n = (static_cast<int>(q1 - q0) * a.H + kRows - 1) / kRows;
+    unsigned n = 0, total;
+    if (b < a.B) {
+      const int q0 = min(max(__ldg(a.cu + b), 0), a.total_q), q1 = min(max(__ldg(a.cu + b + 1), q0), a.total_q);
+      n = ((q1 - q0) * a.H + kRows - 1) / kRows;
     }
-    int total;
-    const int at = base + block_scan(n, wsum_n, &total);
-    if (b < nreq) a.head[2 + b] = at;
-    if (b < kPlanThreads) s_head[b] = at;
-    base += total;
+    const int at = static_cast<int>(own_tiles + block_scan(n, wsum_n, &total));
+    own_tiles += total;
+    if (b < a.B) a.head[3 + b] = at;
+    if (b < min(a.B, kPlanThreads)) s_head[b] = at;
   }
-  const int n_tiles = min(base, a.max_tiles);
+  // Requests share prefix tiles where their own tiles would stand too empty: by more than 15 % of the
+  // rows there are (none are with H a multiple of 128).  Behind 8192 keys, shared and own tiles took:
+  // 64 rows a request (half empty) 75 and 111 us, 128 (none) 67 and 60, 256 (none) 113 and 100, 320
+  // (20 %) 143 and 153, 448 (14 %) 197 and 191, 576 (11 %) 245 and 230; 16 rows a request behind 32768
+  // keys 150 and 732 us.
+  const bool packed = a.may_pack && 100LL * kRows * own_tiles > 115LL * q_end * a.H;
+  // rows beyond the last request (padding) count as one more request that sees nothing
+  const int n_pad = packed ? 0 : ((a.total_q - q_end) * a.H + kRows - 1) / kRows;
+  const int n_pre_tiles = packed ? (a.total_q * a.H + kRows - 1) / kRows : 0;
+  const int nreq = packed ? a.B : a.B + 1;
+  const int n_tiles = static_cast<int>(min(n_pre_tiles + n_pad + own_tiles, static_cast<unsigned>(a.max_tiles)));
+  if (tid == 0) {
+    a.head[2] = packed;
+    a.head[3 + a.B] = static_cast<int>(own_tiles);
+    if (a.B < kPlanThreads) s_head[a.B] = static_cast<int>(own_tiles);
+  }
   __syncthreads();
-  auto head = [&](int b) { return b < kPlanThreads ? s_head[b] : a.head[2 + b]; };
+  auto head = [&](int b) { return n_pre_tiles + (b < kPlanThreads ? s_head[b] : a.head[3 + b]); };
   bool bad = false;
-  if (a.packed) {
+  if (packed) {
     for (int q = tid; q < a.total_q; q += kPlanThreads) {
       const int b = request_of(a, q);
       Query r;
@@ -293,22 +312,24 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
         }
         const int q0 = min(max(__ldg(a.cu + lo), 0), a.total_q);
         const int q1 = lo < a.B ? min(max(__ldg(a.cu + lo + 1), q0), a.total_q) : a.total_q;
-        t.row0 = q0 * a.H + (i - head(lo)) * kRows;
-        t.nrows = min(kRows, q1 * a.H - t.row0);
+        const int k = i - head(lo), rows = (q1 - q0) * a.H;  // (offsets that do not rise make any k)
+        const bool in = k >= 0 && k < (rows + kRows - 1) / kRows;
+        t.row0 = q0 * a.H + (in ? k * kRows : 0);
+        t.nrows = in ? min(kRows, rows - k * kRows) : 0;
         t.b = min(lo, a.B - 1);
         const int last = (t.row0 + t.nrows - 1) / a.H;
-        if (lo < a.B)
-          t.limit = !a.packed ? sees(a, lo, last, &bad) : (last < kPlanThreads ? s_sees[last] : a.queries[last].sees);
+        if (lo < a.B && in)
+          t.limit = !packed ? sees(a, lo, last, &bad) : (last < kPlanThreads ? s_sees[last] : a.queries[last].sees);
         own = t.limit > a.prefix_len ? (t.limit + kKeys - 1) / kKeys - kO : 0;
       }
-      t.n_pre = (a.packed && i >= n_pre_tiles) ? 0 : (min(t.limit, a.prefix_len) + kKeys - 1) / kKeys;
+      t.n_pre = (packed && i >= n_pre_tiles) ? 0 : (min(t.limit, a.prefix_len) + kKeys - 1) / kKeys;
       units = t.n_pre + own > 0 ? t.n_pre + own + kSetup : 0;
       empty += units == 0;
     }
     long long total, at;
     if (a.narrow) {
-      int sum;
-      at = block_scan(static_cast<int>(units), wsum_n, &sum);
+      unsigned sum;
+      at = block_scan(static_cast<unsigned>(units), wsum_n, &sum);
       total = sum;
     } else {
       at = block_scan(units, wsum, &total);
@@ -729,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (trow >= tile.nrows) return 0;
       const int tq = (tile.row0 + trow) / a.H;
       bool bad = false;  // counted by the plan
-      return min(a.packed ? __ldcg(&a.queries[tq].sees) : sees(a, tile.b, tq, &bad), tile.limit);
+      return min(joined(a, tile) ? __ldcg(&a.queries[tq].sees) : sees(a, tile.b, tq, &bad), tile.limit);
     };
     auto row_at = [&](const Tile& tile, int k) {  // cache row of the lane's box under this warp's keys
       const Block b = block_at(a, tile, k);
@@ -845,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       crow = more ? row_at(t, p.k0) : 0;
       // the piece's result
       const bool at_start = pc.k0 == 0;
-      const bool direct = pc.whole && !a.packed;
+      const bool direct = pc.whole && !joined(a, tc);
       if (ok) ok = __all_sync(0xffffffffu, spin(&bars->ofree, (n - 1) & 1)) != 0;
       float* xs = xmax + (n & 1) * 256 + row;  // the side that the last block did not use
       xs[quarter * 64] = l;
@@ -939,7 +960,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ join
 // A CTA of 512 threads (128 rows x 4) joins some of the 128 latent columns (of 4) of a tile's rows.
 // Packed batches: a row has the pieces of its prefix tile and of one of its request's own tiles;
-// blockIdx = per_tile * prefix tile + columns.  Otherwise blockIdx = 2 * part + columns for every
+// blockIdx = per_tile * prefix tile + columns (the grid has room for either kind).  Otherwise blockIdx = 2 * part + columns for every
 // part that begins inside a tile; the parts of a tile share its columns (up to 64 of them), so that
 // a tile of many pieces has many CTAs.  The four threads of a row split the columns when the pieces
 // are few, else the pieces, and meet in shared memory.  About one wave of CTAs, a few trips to L2.
@@ -955,8 +976,19 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
   bool by_piece;
   // up to two tiles hold a row's pieces: parts a0 .. a1 of tile ta (row r), b0 .. b1 of tb (row rb)
   int ta, a0, a1, tb = 0, rb = 0, b0 = 0, b1 = -1;
-  if (a.packed) {
+  // what a packed batch needs first is read together with whether it is one: one trip to L2
+  int packed = 0;
+  int4 wa{}, qr{};
+  if (a.may_pack) {
+    packed = __ldcg(a.head + 2);
+    const int rows = a.total_q * a.H;
+    const int row_a = min(static_cast<int>(blockIdx.x) / per_tile * kRows + r, rows - 1);
+    wa = __ldcg(reinterpret_cast<const int4*>(a.tiles + row_a / kRows) + 1);
+    qr = __ldcg(reinterpret_cast<const int4*>(a.queries + row_a / a.H));
+  }
+  if (packed) {
     ta = blockIdx.x / per_tile;
+    if (ta * kRows >= a.total_q * a.H) return;
     const int width = 128 / per_tile;
     by_piece = per_tile == 32;
     col0 = (blockIdx.x - ta * per_tile) * width;
@@ -964,14 +996,11 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
     if (!by_piece) col0 += y * n_col;
     row0 = ta * kRows;
     nrows = min(kRows, a.total_q * a.H - row0);
-    const int4 w = __ldcg(reinterpret_cast<const int4*>(a.tiles + ta) + 1);
-    a0 = w.y;
-    a1 = w.z;
+    a0 = wa.y;
+    a1 = wa.z;
     if (r < nrows) {
-      const int tq = (row0 + r) / a.H;
-      const int4 q = __ldcg(reinterpret_cast<const int4*>(a.queries + tq));
-      const int local = q.y + row0 + r - tq * a.H;
-      tb = q.x + local / kRows;
+      const int local = qr.y + (row0 + r) % a.H;
+      tb = qr.x + local / kRows;
       rb = local % kRows;
       if (tb < __ldcg(a.head)) {
         const int4 v = __ldcg(reinterpret_cast<const int4*>(a.tiles + tb) + 1);
@@ -980,7 +1009,7 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
       }
     }
   } else {
-    const int c = blockIdx.x >> 1;
+    const int c = min(static_cast<int>(blockIdx.x >> 1), a.G - 1);
     const int4 w = __ldcg(reinterpret_cast<const int4*>(a.parts + c));
     nrows = __ldcg(&a.parts[c].nrows);
     const int n_tiles = __ldcg(a.head);
@@ -993,7 +1022,7 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
         if (a.lse && threadIdx.x < zn) a.lse[z0 + threadIdx.x] = -INFINITY;
       }
     }
-    if (w.x < 0) return;
+    if (w.x < 0 || blockIdx.x >= 2 * a.G) return;
     ta = w.x;
     a0 = w.y;
     a1 = w.z;
@@ -1195,31 +1224,27 @@ dsa_status validate(const dsa_prefix_mla_args* a) {
 
 
 struct Layout {
-  int packed, max_tiles, G;
+  int may_pack, max_tiles, G;
   size_t off_tiles, off_u0, off_head, off_parts, off_queries, off_ml, off_o, total;
 };
 
 Layout layout(const dsa_prefix_mla_args* a) {
   Layout p{};
   const long long rows = static_cast<long long>(a->total_q) * a->H;
-  // Requests share prefix tiles where their own tiles would stand too empty: by more than 15 % for
-  // a request of the average number of rows (none are empty with H a multiple of 128).  Behind 8192
-  // keys, shared and own tiles took: 64 rows a request (half empty) 75 and 111 us, 128 (none) 67 and
-  // 60, 256 (none) 113 and 100, 320 (20 %) 143 and 153, 448 (14 %) 197 and 191, 576 (11 %) 245 and
-  // 230; 16 rows a request behind 32768 keys 150 and 732 us.
-  const long long full = static_cast<long long>(kRows) * std::max(a->B, 1), filled = (rows + full - 1) / full;
-  p.packed = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 &&
-             100 * filled * full > 115 * rows ? 1 : 0;
-  p.max_tiles = static_cast<int>((p.packed ? 2 : 1) * (rows / kRows + 1) + a->B + 1);
+  // Whether requests share prefix tiles is for the plan to say, from the lengths: where their own
+  // tiles, sum ceil(rows / 128), come to more than 1.15 times the rows.  That sum is at most
+  // (rows + 127 B) / 128, so batches of 15 rows > 12700 B never do, and need no room for it.
+  p.may_pack = a->prefix_len > 0 && a->B > 1 && a->H % kRows != 0 && 15 * rows <= 12700LL * a->B ? 1 : 0;
+  p.max_tiles = static_cast<int>((p.may_pack ? 2 : 1) * (rows / kRows + 1) + a->B + 1);
   p.G = pair_count();
-  const size_t slots = 2 * static_cast<size_t>(p.G) + (p.packed ? 2 * ((rows + kRows - 1) / kRows) : 0);
+  const size_t slots = 2 * static_cast<size_t>(p.G) + (p.may_pack ? 2 * ((rows + kRows - 1) / kRows) : 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   p.off_tiles = 0;
   p.off_u0 = up(p.off_tiles + sizeof(Tile) * p.max_tiles);
   p.off_head = up(p.off_u0 + 8 * (static_cast<size_t>(p.max_tiles) + 1));
   p.off_parts = up(p.off_head + 4 * (static_cast<size_t>(a->B) + 4));
   p.off_queries = up(p.off_parts + sizeof(Part) * p.G);
-  p.off_ml = up(p.off_queries + (p.packed ? sizeof(Query) * a->total_q : 0));
+  p.off_ml = up(p.off_queries + (p.may_pack ? sizeof(Query) * a->total_q : 0));
   p.off_o = up(p.off_ml + slots * kRows * 8);
   p.total = up(p.off_o + slots * kRows * kRank * 4);
   return p;
@@ -1276,7 +1301,7 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.max_pages = a->max_pages_per_seq;
   k.prefix_len = a->prefix_len;
   k.num_prefix_pages = a->num_prefix_pages;
-  k.packed = p.packed;
+  k.may_pack = p.may_pack;
   k.max_tiles = p.max_tiles;
   k.G = p.G;
   k.past_row = static_cast<int>(slots);
@@ -1319,7 +1344,7 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   // Few packed tiles have many pieces each: 32 CTAs a tile, which split them.
   const long long groups = (rows + kRows - 1) / kRows;
   const int per_tile = groups * 32 <= 2LL * p.G ? 32 : (groups * 8 <= 2LL * p.G ? 8 : 4);
-  const long long ctas = p.packed ? groups * per_tile : p.G * 2LL;
+  const long long ctas = std::max(p.may_pack ? groups * per_tile : 0LL, p.G * 2LL);
   e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), kJoinSmem, s, k, per_tile);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
