@@ -68,7 +68,8 @@ def latent_append(c_kv, k_rope, slot_mapping, cache_c, cache_r, *, norm_weight=N
 def prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, *, prefix_len,
                scale):
     """dict of out [T, H, R], lse [T, H], cond [T, H, R] = sum_s p_s |c_s| and reach [T, H] =
-    max_s scale * sum_d |q_d k_d| (what the logits' rounding is relative to), n [T] keys seen."""
+    max_s scale * sum_d |q_d k_d| (what the logits' rounding is relative to), n [T] keys seen.
+    Positions that no table entry covers, or whose page is outside the cache, are left out."""
     qn, qr, cc, cr = _f64(q_nope), _f64(q_rope), _f64(cache_c), _f64(cache_r)
     page = cc.shape[1]
     bt, cu, lens = block_tables.cpu().numpy(), cu_q_lens.cpu().numpy(), seq_lens.cpu().numpy()
@@ -83,7 +84,12 @@ def prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_le
             if n <= 0:
                 continue
             pos = np.arange(n)
-            pg = np.array([pp[s // page] if s < prefix_len else bt[b, s // page] for s in pos])
+            tables = [pp if s < prefix_len else bt[b] for s in pos]
+            pg = np.array([tab[s // page] if s // page < len(tab) else -1 for s, tab in zip(pos, tables)])
+            there = (pg >= 0) & (pg < len(cc))
+            if not there.any():
+                continue
+            pos, pg, n = pos[there], pg[there], int(there.sum())
             c, r = cc[pg, pos % page], cr[pg, pos % page]
             x = scale * (qn[t] @ c.T + qr[t] @ r.T)
             m = x.max(axis=1, keepdims=True)

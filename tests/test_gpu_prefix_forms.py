@@ -75,3 +75,44 @@ def test_a_chunk_among_single_tokens_shares_the_prefix():
     together = batch([1] * 127 + [800])
     assert dsa.dsa_check_device_status() == dsa.DSA_OK
     assert together < 1.3 * apart, (together, apart)
+
+
+def _check_reported(c):
+    """The call reports what is not there, and its results are those of the keys that are."""
+    d = lambda t: t.cuda()
+    got = dsa.dsa_prefix_mla(d(c.qn), d(c.qr), d(c.cc), d(c.cr), d(c.bt), d(c.cu), d(c.lens), d(c.pp),
+                             prefix_len=c.prefix, scale=c.scale)
+    assert dsa.dsa_check_device_status() == dsa.DSA_ERR_DEVICE_CHECK
+    c.check(got)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("H", [16, 128])  # prefix tiles shared by the requests, and tiles of their own
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+def test_pages_that_are_not_there_are_left_out(page, H, bad):
+    prefix = 3 * page + 5
+    reqs = [(1, prefix + 200), (3, prefix + 150), (1, prefix + 1), (2, prefix + 2 * page)]
+    c = Case(H, page, prefix, reqs, seed=page)
+    c.bt[0, 4] = bad                    # a whole page of one request
+    c.bt[1, (prefix + 149) // page] = bad  # its newest keys
+    c.bt[3, 3] = bad                    # the page that begins with the prefix's last keys
+    _check_reported(c)
+    c = Case(H, page, prefix, reqs, seed=page + 1)
+    c.pp[1] = bad                       # a page of the prefix, for all of them
+    _check_reported(c)
+    c = Case(H, page, prefix, [(1, 3)] + reqs[1:], seed=page + 2)
+    c.pp[0] = len(c.cc)                 # the first page behind the cache: all that a short request sees
+    _check_reported(c)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("H", [16, 128])
+def test_lengths_past_the_table_are_cut(page, H):
+    prefix = 2 * page
+    c = Case(H, page, prefix, [(1, prefix + page), (2, prefix + 50), (4, prefix + 3 * page)], seed=page)
+    width = c.bt.shape[1]
+    c.bt[0, 3:] = torch.arange(1, width - 2)   # the request's table is full: every page somebody's
+    c.lens[0] = width * page + 7               # and its length beyond it
+    c.lens[2] = width * page + 2               # some of its queries see all of the table, some less
+    c.bt[2, c.bt[2] < 0] = 0
+    _check_reported(c)
