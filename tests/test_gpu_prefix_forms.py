@@ -116,3 +116,105 @@ def test_lengths_past_the_table_are_cut(page, H):
     c.lens[2] = width * page + 2               # some of its queries see all of the table, some less
     c.bt[2, c.bt[2] < 0] = 0
     _check_reported(c)
+
+
+def test_the_callers_buffers():
+    c = Case(20, 32, 300, [(1, 301 + 40 * i) for i in range(9)] + [(30, 400)], pad=3, seed=21)
+    ref = c.gpu()
+    T, H = c.qn.shape[:2]
+    need = dsa.dsa_prefix_mla_workspace_size(len(c.lens), T, H, prefix_len=c.prefix)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((T + 2, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 2, H), 7.0, device="cuda")
+    got = c.gpu(out=out[1:-1], lse=lse[1:-1], workspace=ws[:need])
+    assert got[0].data_ptr() == out[1].data_ptr() and got[1].data_ptr() == lse[1].data_ptr()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    # nothing written beside them
+    assert torch.all(ws[need:] == 0xA5)
+    assert torch.all(out[0] == 7) and torch.all(out[-1] == 7) and torch.all(lse[0] == 7) and torch.all(lse[-1] == 7)
+    # a workspace that another batch left behind
+    ws[:need] = 0xFF
+    again = c.gpu(out=out[1:-1], lse=lse[1:-1], workspace=ws[:need])
+    assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
+    with pytest.raises(dsa.DsaError) as e:
+        c.gpu(workspace=ws[: need - 1])
+    assert e.value.status == dsa.DSA_ERR_WORKSPACE
+
+
+def test_a_long_prompt_behind_a_prefix():
+    Case(8, 64, 200, [(1000, 1200), (1, 260), (333, 533)], seed=22).check()
+    Case(128, 32, 0, [(300, 300)], seed=23).check()
+
+
+def test_calls_side_by_side_on_two_streams():
+    cases = [Case(64, 64, 900, [(1, 950), (2, 1400), (1, 901)], seed=24),
+             Case(16, 32, 500, [(1, 501 + i) for i in range(40)], seed=25)]
+    d = lambda t: t.cuda()
+    args = [[d(t) for t in (c.qn, c.qr, c.cc, c.cr, c.bt, c.cu, c.lens, c.pp)] for c in cases]
+    kw = [dict(prefix_len=c.prefix, scale=c.scale) for c in cases]
+    ref = [dsa.dsa_prefix_mla(*a, **k) for a, k in zip(args, kw)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        for a, k, s in zip(args, kw, streams):
+            got.append(dsa.dsa_prefix_mla(*a, stream=s, **k))
+    torch.cuda.synchronize()
+    assert dsa.dsa_check_device_status() == dsa.DSA_OK
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, ref[i % 2][0]) and torch.equal(lse, ref[i % 2][1])
+
+
+@pytest.mark.parametrize("H,reqs,width", [
+    (128, [(140, 190)], 16_000_000),                               # own tiles, written without a join
+    (80, [(5, 60 + 9 * i) for i in range(20)], 15_000_000),       # shared tiles
+])
+def test_tables_so_wide_that_the_plan_counts_in_64_bits(H, reqs, width):
+    """Tables of 15 million pages of 128 rows: 2^31 blocks of keys and more over the tiles there is
+    room for, whatever the lengths turn out to be."""
+    c = Case(H, 128, 40, reqs, seed=26)
+    wide = torch.full((len(reqs), width), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.bt.shape[1]] = c.bt.cuda()
+    d = lambda t: t.cuda()
+    got = dsa.dsa_prefix_mla(d(c.qn), d(c.qr), d(c.cc), d(c.cr), wide, d(c.cu), d(c.lens), d(c.pp),
+                             prefix_len=c.prefix, scale=c.scale)
+    assert dsa.dsa_check_device_status() == dsa.DSA_OK
+    c.check(got)
+
+
+@pytest.mark.slow
+def test_so_many_blocks_that_the_plan_cuts_them_in_64_bits():
+    """1024 tiles behind 7.3 million keys (some 57000 blocks each; about a second): more than 2^32
+    places times parts.  The keys are 1024 rows over and over, so query i sees each of them
+    `times` - 1 times and the first i + 1 once more, and the sums are known.
+
+    A running sum takes one fp32 addition a block, 57000 * 2^-24 = 0.0034 relative at most, the
+    logits 576 * 2^-23 * reach; a lost, doubled or misplaced piece moves lse by far more."""
+    times, rows, H, page = 7130, 1024, 128, 128
+    prefix = times * rows
+    g = torch.Generator(device="cuda").manual_seed(27)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    cc, cr, q = rnd(rows // page, page, 512), rnd(rows // page, page, 64), rnd(rows, H, 576)
+    i32 = lambda t: t.to(torch.int32).cuda()
+    scale = 576 ** -0.5
+    out, lse = dsa.dsa_prefix_mla(q[..., :512], q[..., 512:], cc, cr, torch.full((1, 1), -1, dtype=torch.int32, device="cuda"),
+                                  i32(torch.tensor([0, rows])), i32(torch.tensor([prefix])),
+                                  i32(torch.arange(prefix // page) % (rows // page)), prefix_len=prefix, scale=scale)
+    assert dsa.dsa_check_device_status() == dsa.DSA_OK
+    k = torch.cat([cc.view(rows, 512), cr.view(rows, 64)], 1).double()
+    for i in range(0, rows, 64):
+        qi = q[i: i + 64].double()
+        x = torch.einsum("thd,sd->ths", qi, k) * scale
+        reach = (qi.abs().float().flatten(0, 1) @ k.abs().float().T).amax(1).view(64, H).double() * scale * 1.001
+        count = (times - 1) + (torch.arange(rows, device="cuda") <= torch.arange(i, i + 64, device="cuda")[:, None]).double()
+        ref = torch.logsumexp(x + count.log()[:, None, :], 2)
+        tol = 576 * 2.0 ** -23 * reach + 57100 * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * ref.abs()
+        assert torch.all((lse[i: i + 64].double() - ref).abs() <= tol)
+        if i % 256:
+            continue
+        p = torch.exp(x + count.log()[:, None, :] - ref[:, :, None])
+        # 8 fp32 additions a block into the tile's sums, each of at most 2^-23 of what is there
+        cond = torch.einsum("ths,sd->thd", p, k[:, :512].abs())
+        o = torch.einsum("ths,sd->thd", p, k[:, :512])
+        bound = (2.0 ** -8 + 2 * tol.amax() + 8 * 57100 * 2.0 ** -23) * cond + 2.0 ** -8 * o.abs()
+        assert torch.all((out[i: i + 64].double() - o).abs() <= bound)

@@ -29,3 +29,30 @@ def test_workspace_follows_the_rows(dsa, B, H):
     blocks, tiles = -(-B * H // 128), 2 * (B * H // 128 + 1) + B + 1
     most = alone + 2 * blocks * 128 * row + 64 * B + 40 * tiles + 4 * B + 4096
     assert dsa.dsa_prefix_mla_workspace_size(B, B, H, prefix_len=1000) <= most
+
+
+@pytest.mark.parametrize("short", [1, 4096])
+def test_a_workspace_that_is_too_small(dsa, short):
+    import ctypes
+    from test_prefix_step import _attend_args
+    n = ctypes.c_size_t(0)
+    assert dsa.lib().dsa_prefix_mla_workspace_size(ctypes.byref(_attend_args(dsa)), ctypes.byref(n)) == dsa.DSA_OK
+    a = _attend_args(dsa, workspace_bytes=n.value - short)
+    assert dsa.lib().dsa_prefix_mla(ctypes.byref(a), None) == dsa.DSA_ERR_WORKSPACE
+    for bad in (dict(workspace=None), dict(workspace=(1 << 20) + 8)):
+        a = _attend_args(dsa, workspace_bytes=n.value, **bad)
+        assert dsa.lib().dsa_prefix_mla(ctypes.byref(a), None) == dsa.DSA_ERR_WORKSPACE
+
+
+def test_the_size_helper_answers_for_the_call(dsa):
+    import ctypes
+    from test_prefix_step import _attend_args
+    for B, T, H, prefix, page in ((1, 1, 128, 0, 16), (5, 9, 20, 1000, 128), (64, 64, 64, 8192, 64), (2, 900, 17, 33, 32)):
+        n = ctypes.c_size_t(0)
+        a = _attend_args(dsa, B=B, total_q=T, H=H, prefix_len=prefix, page_size=page, num_prefix_pages=-(-prefix // page),
+                         max_pages_per_seq=77)
+        assert dsa.lib().dsa_prefix_mla_workspace_size(ctypes.byref(a), ctypes.byref(n)) == dsa.DSA_OK
+        assert dsa.dsa_prefix_mla_workspace_size(B, T, H, prefix_len=prefix) == n.value
+    assert dsa.dsa_prefix_mla_workspace_size(3, 0, 64, prefix_len=10) == 0
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_prefix_mla_workspace_size(3, 4, 129, prefix_len=10)
