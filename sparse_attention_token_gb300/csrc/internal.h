@@ -139,6 +139,18 @@ cudaError_t launch_score(const ScoreArgs& a, const CUtensorMap* tmap_q, const CU
 size_t score_smem_bytes(const ScoreArgs& a, int num_k_stages);
 cudaError_t launch_topk(const TopkArgs& a, int max_row_len, cudaStream_t st);
 unsigned* device_status_ptr();  // address of the status word on the current device
+// Tensor map of a row-major [rows, D] bf16 or e4m3 operand, 128-byte swizzled boxes of {128 bytes, box_rows}.
+bool make_map_2d(CUtensorMap* m, const void* base, bool fp8, int D, long long rows, int box_rows);
+
+// Sequence of query row t: the last b < B with cu[b] <= t.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 // New indexer keys through slot_mapping into the paged cache (bf16 copy or per-token
 // e4m3 quantisation with its scale); slots >= n_slots set kStatusBadPage.
 cudaError_t launch_cache_append(const void* k_new, int n, int D, const int64_t* slots, void* cache, bool fp8,

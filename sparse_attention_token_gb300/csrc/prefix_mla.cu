@@ -44,7 +44,6 @@
 //
 // Every wait is bounded; after one gives up, every role of both CTAs stops, the MMAs and copies in
 // flight are drained (bounded) and TMEM is freed.
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -139,18 +138,6 @@ struct Bars {
   uint32_t kissued, vissued;     // this CTA's arrivals at kfull / vfull, all groups together; for the drain
 };
 static_assert(sizeof(Bars) <= 256, "the words behind the barriers begin at 256");
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Request of query t: the last b with cu[b] <= t.
-__device__ __forceinline__ int request_of(const Args& a, int t) {
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 // Keys that query t of request b sees, cut to what the table covers (and counted as bad then).
 __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
@@ -275,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
   bool bad = false;
   if (packed) {
     for (int q = tid; q < a.total_q; q += kPlanThreads) {
-      const int b = request_of(a, q);
+      const int b = sequence_of(a.cu, a.B, q);
       Query r;
       r.sees = sees(a, b, q, &bad);
       const int q0 = __ldg(a.cu + b);
@@ -729,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       load_q(a, smem, t, rank, lane >> 3, 4, lane & 7);
-      cp_async_wait_all();
+      ptx::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(full);
@@ -761,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool more = next_piece(a, p, u_hi, t);
     if (more) {  // the first piece's queries: eight warps at once
       load_q(a, smem, t, rank, threadIdx.x >> 3, 32, lane & 7);
-      cp_async_wait_all();
+      ptx::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       ptx::named_bar_sync(4, 256);
       if (threadIdx.x == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&bars->qfull), 0));
@@ -1157,26 +1144,6 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
 }
 constexpr int kJoinSmem = 3 * kAcc * kRows * 16;
 
-bool key_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  if (!enc) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // CTA pairs that run at once (one per two SMs, less where a cluster does not fit), per device.
 int pair_count() {
   int dev = 0;
@@ -1290,7 +1257,8 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   CUtensorMap tc, tr;
   const long long slots = std::max(1LL, static_cast<long long>(a->num_pages) * a->page_size);
   const int box = std::min(a->page_size, 64);
-  if (!key_map(&tc, a->cache_c, slots, kRank, box) || !key_map(&tr, a->cache_r, slots, kRope, box)) return DSA_ERR_CUDA;
+  if (!make_map_2d(&tc, a->cache_c, false, kRank, slots, box) || !make_map_2d(&tr, a->cache_r, false, kRope, slots, box))
+    return DSA_ERR_CUDA;
   Args k{};
   k.B = a->B;
   k.total_q = a->total_q;

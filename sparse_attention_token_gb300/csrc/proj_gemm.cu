@@ -24,7 +24,6 @@
 //               the fp32 round trip through memory.
 // Every wait is bounded; on a timeout every role stops, in-flight copies and MMAs are
 // drained (bounded) and TMEM is freed.
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -331,26 +330,6 @@ __global__ void __launch_bounds__(kPThreads, 1) proj_kernel(const __grid_constan
   }
 }
 
-bool proj_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  if (!enc) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(kPK), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
@@ -363,9 +342,9 @@ template <int BN, int OUT, int HALF, bool INTER>
 cudaError_t launch_proj_t(const void* A, const void* B, ProjArgs a, cudaStream_t st, const void* B2 = nullptr) {
   CUtensorMap ta, tb, tb2;
   a.b_box = OUT == kOutDual ? 128 : (a.N < BN ? a.N : BN);
-  if (!proj_map(&ta, A, a.M, a.K, kPM) || !proj_map(&tb, B, OUT == kOutDual ? 128 : a.N, a.K, a.b_box))
+  if (!make_map_2d(&ta, A, false, a.K, a.M, kPM) || !make_map_2d(&tb, B, false, a.K, OUT == kOutDual ? 128 : a.N, a.b_box))
     return cudaErrorInvalidValue;
-  if (OUT == kOutDual ? !proj_map(&tb2, B2, a.n2, a.K, a.n2) : false) return cudaErrorInvalidValue;
+  if (OUT == kOutDual ? !make_map_2d(&tb2, B2, false, a.K, a.n2, a.n2) : false) return cudaErrorInvalidValue;
   if (OUT != kOutDual) tb2 = tb;
   const size_t stage = static_cast<size_t>(kPM) * 128 + static_cast<size_t>(BN) * 128;
   a.stages = static_cast<int>((kPSmemBudget - 256) / stage);

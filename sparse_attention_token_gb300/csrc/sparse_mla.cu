@@ -31,7 +31,6 @@
 // A second kernel combines the splits: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
 // Every wait is bounded; on a timeout every role stops, copies and MMAs in flight are
 // drained (bounded) and TMEM is freed.
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -74,17 +73,6 @@ struct MlaArgs {
 struct MlaBars {
   uint64_t qfull, tfull[2], tempty[2], sfull[2], sempty[2], pfull, ofree, done;
 };
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ int seq_of_row(const MlaArgs& a, int r) {
-  int lo = 0, hi = a.B;  // last b with cu_q_lens[b] <= r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu_q_lens + mid) <= r) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 __global__ void __launch_bounds__(kMlaThreads, 1) sparse_mla_kernel(const __grid_constant__ CUtensorMap tmap_qn,
                                                                      const __grid_constant__ CUtensorMap tmap_qr,
@@ -141,7 +129,7 @@ __global__ void __launch_bounds__(kMlaThreads, 1) sparse_mla_kernel(const __grid
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
-  const int b = seq_of_row(a, t);
+  const int b = sequence_of(a.cu_q_lens, a.B, t);
   const int seq_len = __ldg(a.seq_lens + b);
   const int32_t* sel = a.topk + static_cast<long long>(t) * a.k + key0;
   const long long part = (static_cast<long long>(t) * a.splits + j) * a.H + g * kHeadsPerCta;  // first head row
@@ -260,7 +248,7 @@ __global__ void __launch_bounds__(kMlaThreads, 1) sparse_mla_kernel(const __grid
         uint8_t* dst = tile + at * kAtomBytes + key * 128 + ((c16 ^ (key & 7)) << 4);
         ptx::cp_async_16(dst, src, sl < 0 ? 0u : 16u);
       }
-      cp_async_wait_all();
+      ptx::cp_async_wait_all();
       ptx::fence_proxy_async_smem();  // the MMA reads the tile through the async proxy
       ptx::mbar_arrive(&bars->tfull[tb]);
     }
@@ -438,26 +426,6 @@ __global__ void sparse_mla_combine_kernel(const float* __restrict__ part_o, cons
   }
 }
 
-bool mla_map(CUtensorMap* m, const void* base, long long rows, int cols) {
-  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  if (!enc) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {64, 64};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct MlaPlan {
   int splits, keys_per_split, groups;
   size_t off_o, off_ml, total;
@@ -546,7 +514,8 @@ dsa_status dsa_sparse_mla(const dsa_sparse_mla_args* a, dsa_stream_t stream) {
   if (!status) return DSA_ERR_CUDA;
   CUtensorMap tqn, tqr;
   const long long qrows = static_cast<long long>(a->total_q) * a->H;
-  if (!mla_map(&tqn, a->q_nope, qrows, kKvRank) || !mla_map(&tqr, a->q_rope, qrows, kRopeDim)) return DSA_ERR_CUDA;
+  if (!make_map_2d(&tqn, a->q_nope, false, kKvRank, qrows, 64) || !make_map_2d(&tqr, a->q_rope, false, kRopeDim, qrows, 64))
+    return DSA_ERR_CUDA;
   MlaArgs k{};
   k.total_q = a->total_q;
   k.B = a->B;
