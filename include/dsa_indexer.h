@@ -440,7 +440,8 @@ dsa_status dsa_page_plan(const dsa_page_plan_args* args, dsa_stream_t stream);
  * dsa_indexer_prepare.  slot_mapping [n] int64, negative: the token is skipped.  A slot past
  * the cache, or a position outside the tables, skips the token and is reported through
  * dsa_check_device_status.  Two tokens with one slot leave either's values there.
- * Pointers 16-byte aligned (slot_mapping 8, positions 4), strides multiples of 8 elements.
+ * Pointers 16-byte aligned (slot_mapping 8, positions 4), strides multiples of 8 elements
+ * (any when n = 1).
  */
 typedef struct {
   int n, kv_rank, rope_dim, page_size, num_pages, rope_interleaved, rope_rows;
@@ -472,7 +473,7 @@ dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_strea
  * rows nobody reads) and may be 0; a sequence may be shorter than it.  A query that sees
  * nothing (p < 0) and the rows t >= cu_q_lens[B] (padding) give zeros and lse = -inf.
  *   q_nope [total_q, H, 512] bf16 and q_rope [total_q, H, 64] bf16 with the given element
- *   strides (multiples of 8; the last dimension dense); cache_c, cache_r as in dsa_sparse_mla;
+ *   strides (multiples of 8, any in a dimension of size 1; the last dimension dense); cache_c, cache_r as in dsa_sparse_mla;
  *   block_tables [B, max_pages_per_seq]; out [total_q, H, 512] bf16 dense; lse [total_q, H].
  * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0.
  * Cache rows that no query sees may hold anything, NaN included; rows that some query sees

@@ -186,7 +186,8 @@ extern "C" dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* a, d
   if ((a->rope_cos == nullptr) != (a->rope_sin == nullptr)) return DSA_ERR_INVALID_ARGUMENT;
   if (a->rope_cos && (a->rope_rows < 1 || (!a->positions && a->rope_rows < a->n))) return DSA_ERR_INVALID_ARGUMENT;
   if (a->norm_weight && !(a->norm_eps >= 0.f)) return DSA_ERR_INVALID_ARGUMENT;
-  if (a->c_stride < 0 || a->r_stride < 0 || a->c_stride % 8 != 0 || a->r_stride % 8 != 0)
+  // (one token's strides lead nowhere)
+  if (a->n > 1 && (a->c_stride < 0 || a->r_stride < 0 || a->c_stride % 8 != 0 || a->r_stride % 8 != 0))
     return DSA_ERR_INVALID_ARGUMENT;
   auto al = [](const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
   if (!al(a->c_kv, 16) || !al(a->k_rope, 16) || !al(a->cache_c, 16) || !al(a->cache_r, 16) ||

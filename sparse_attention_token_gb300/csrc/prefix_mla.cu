@@ -1245,7 +1245,9 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
       !al(a->lse, 4) || !al(a->prefix_pages, 4) || !al(a->block_tables, 4) || !al(a->cu_q_lens, 4) ||
       !al(a->seq_lens, 4))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (a->qn_stride_t % 8 || a->qn_stride_h % 8 || a->qr_stride_t % 8 || a->qr_stride_h % 8)
+  // (strides of one query, of one head, lead nowhere)
+  if ((a->total_q > 1 && (a->qn_stride_t % 8 || a->qr_stride_t % 8)) ||
+      (a->H > 1 && (a->qn_stride_h % 8 || a->qr_stride_h % 8)))
     return DSA_ERR_INVALID_ARGUMENT;
   if (static_cast<long long>(a->total_q) * a->H > 0x7FFFFFFFLL - kRows ||
       static_cast<long long>(a->num_pages) * a->page_size > 0x7FFFFFFFLL - kKeys)

@@ -221,3 +221,24 @@ def test_so_many_blocks_that_the_plan_cuts_them_in_64_bits():
         o = torch.einsum("ths,sd->thd", p, k[:, :512])
         bound = (2.0 ** -8 + 2 * tol.amax() + 8 * 57100 * 2.0 ** -23) * cond + 2.0 ** -8 * o.abs()
         assert torch.all((out[i: i + 64].double() - o).abs() <= bound)
+
+
+def test_one_token_and_one_head_in_tensors_of_odd_strides():
+    g = torch.Generator(device="cuda").manual_seed(28)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    # one token's row in a tensor whose rows are no multiples of 16 bytes apart
+    kv = rnd(1, 577)
+    gc, gr = torch.zeros((2, 16, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_mla_cache_append(kv[:, :512], kv[:, 512:576], torch.tensor([19], device="cuda"), gc, gr)
+    assert dsa.dsa_check_device_status() == dsa.DSA_OK
+    assert torch.equal(gc[1, 3], kv[0, :512]) and torch.equal(gr[1, 3], kv[0, 512:576])
+    for H, reqs in ((16, [(1, 200)]), (1, [(3, 200), (1, 150)])):
+        c = Case(H, 32, 90, reqs, seed=29)
+        T = c.qn.shape[0]
+        store = torch.zeros(T * H * 600 + 8, dtype=torch.bfloat16, device="cuda")
+        # rows 592 apart; the stride of the dimension of size 1 is 577
+        st, sh = (577, 592) if T == 1 else (592, 577)
+        qn, qr = store.as_strided((T, H, 512), (st, sh, 1)), store.as_strided((T, H, 64), (st, sh, 1), 512)
+        qn.copy_(c.qn)
+        qr.copy_(c.qr)
+        c.check(c.gpu(qn=qn, qr=qr))

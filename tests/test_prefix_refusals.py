@@ -56,3 +56,17 @@ def test_the_size_helper_answers_for_the_call(dsa):
     assert dsa.dsa_prefix_mla_workspace_size(3, 0, 64, prefix_len=10) == 0
     with pytest.raises(dsa.DsaError):
         dsa.dsa_prefix_mla_workspace_size(3, 4, 129, prefix_len=10)
+
+
+def test_strides_of_dimensions_of_size_one_do_not_count(dsa):
+    import ctypes
+    from test_prefix_step import _attend_args
+    # the workspace is asked for last: what gets there was accepted so far
+    call = lambda **kw: dsa.lib().dsa_prefix_mla(ctypes.byref(_attend_args(dsa, workspace_bytes=0, **kw)), None)
+    odd = dict(qn_stride_t=577, qr_stride_t=65)
+    assert call(total_q=1, **odd) == dsa.DSA_ERR_WORKSPACE
+    assert call(total_q=2, **odd) == dsa.DSA_ERR_INVALID_ARGUMENT
+    odd = dict(qn_stride_h=577, qr_stride_h=65)
+    assert call(H=1, **odd) == dsa.DSA_ERR_WORKSPACE
+    assert call(H=2, **odd) == dsa.DSA_ERR_INVALID_ARGUMENT
+    assert call(total_q=1, H=2, **odd) == dsa.DSA_ERR_INVALID_ARGUMENT
