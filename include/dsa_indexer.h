@@ -475,7 +475,9 @@ dsa_status dsa_mla_cache_append(const dsa_mla_cache_append_args* args, dsa_strea
  *   q_nope [total_q, H, 512] bf16 and q_rope [total_q, H, 64] bf16 with the given element
  *   strides (multiples of 8, any in a dimension of size 1; the last dimension dense); cache_c, cache_r as in dsa_sparse_mla;
  *   block_tables [B, max_pages_per_seq]; out [total_q, H, 512] bf16 dense; lse [total_q, H].
- * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0.
+ * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, page_size 16, 32, 64 or 128, scale > 0; total_q * H,
+ * num_pages * page_size and the keys that a query sees below 2^31 - 128 (a longer sequence is cut
+ * there and reported like one that passes its table).
  * Cache rows that no query sees may hold anything, NaN included; rows that some query sees
  * must be finite.  A NaN in a query makes out and lse of its (t, h) NaN and no others.  A page
  * outside the cache, or a position past the table, is skipped and reported through

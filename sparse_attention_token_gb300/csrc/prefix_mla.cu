@@ -65,6 +65,7 @@ constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtom
 constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
 constexpr size_t kSmem = kOffMisc + 3 * 1024;
 constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
+constexpr int kMaxKeys = 0x7FFFFFFF - kKeys;              // that a query sees
 constexpr int kSetup = 3;                                 // what a tile costs beside its blocks, in blocks
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -144,7 +145,9 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
   const int q0 = __ldg(a.cu + b), q1 = __ldg(a.cu + b + 1);
   if (t < q0 || t >= q1) return 0;
   long long n = static_cast<long long>(__ldg(a.lens + b)) - (q1 - q0) + (t - q0) + 1;
-  const long long room = max(static_cast<long long>(a.max_pages) * a.page_size, static_cast<long long>(a.prefix_len));
+  // (no more than kMaxKeys, so that the border of the last block stays in 32 bits)
+  const long long room = min(max(static_cast<long long>(a.max_pages) * a.page_size, static_cast<long long>(a.prefix_len)),
+                             static_cast<long long>(kMaxKeys));
   if (n > room) {
     *bad = true;
     n = room;
@@ -1186,9 +1189,12 @@ dsa_status validate(const dsa_prefix_mla_args* a) {
   if (a->H > 128) return DSA_ERR_UNSUPPORTED;
   if (a->page_size != 16 && a->page_size != 32 && a->page_size != 64 && a->page_size != 128)
     return DSA_ERR_UNSUPPORTED;
+  // rows, cache rows and positions are counted in 32 bits, with room for a tile or block behind them
+  if (static_cast<long long>(a->total_q) * a->H > 0x7FFFFFFFLL - kRows ||
+      static_cast<long long>(a->num_pages) * a->page_size > 0x7FFFFFFFLL - kKeys || a->prefix_len > kMaxKeys)
+    return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
-
 
 struct Layout {
   int may_pack, max_tiles, G;
@@ -1249,9 +1255,6 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   if ((a->total_q > 1 && (a->qn_stride_t % 8 || a->qr_stride_t % 8)) ||
       (a->H > 1 && (a->qn_stride_h % 8 || a->qr_stride_h % 8)))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (static_cast<long long>(a->total_q) * a->H > 0x7FFFFFFFLL - kRows ||
-      static_cast<long long>(a->num_pages) * a->page_size > 0x7FFFFFFFLL - kKeys)
-    return DSA_ERR_UNSUPPORTED;
   const Layout p = layout(a);
   if (!a->workspace || a->workspace_bytes < p.total || !al(a->workspace, 16)) return DSA_ERR_WORKSPACE;
   unsigned* status = device_status_ptr();

@@ -242,3 +242,20 @@ def test_one_token_and_one_head_in_tensors_of_odd_strides():
         qn.copy_(c.qn)
         qr.copy_(c.qr)
         c.check(c.gpu(qn=qn, qr=qr))
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("H,reqs", [(1, [(1, 300)]), (16, [(1, 300), (2, 200)])])
+def test_a_length_at_the_end_of_32_bits(H, reqs):
+    """A table of 2^24 + 2 pages of 128 rows covers 2^31 + 256 positions; a length of 2^31 - 1 is cut
+    where the block counts still fit, and the pages that are there give the result."""
+    c = Case(H, 128, 140, reqs, seed=30)
+    wide = torch.full((len(reqs), (1 << 24) + 2), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.bt.shape[1]] = c.bt.cuda()
+    c.lens[0] = (1 << 31) - 1
+    d = lambda t: t.cuda()
+    got = dsa.dsa_prefix_mla(d(c.qn), d(c.qr), d(c.cc), d(c.cr), wide, d(c.cu), d(c.lens), d(c.pp),
+                             prefix_len=c.prefix, scale=c.scale)
+    assert dsa.dsa_check_device_status() == dsa.DSA_ERR_DEVICE_CHECK
+    c.lens[0] = c.bt.shape[1] * 128  # the oracle: all that the pages hold
+    c.check(got)

@@ -70,3 +70,18 @@ def test_strides_of_dimensions_of_size_one_do_not_count(dsa):
     assert call(H=1, **odd) == dsa.DSA_ERR_WORKSPACE
     assert call(H=2, **odd) == dsa.DSA_ERR_INVALID_ARGUMENT
     assert call(total_q=1, H=2, **odd) == dsa.DSA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("big", [dict(total_q=1 << 24), dict(total_q=(1 << 31) - 1, H=1), dict(total_q=(1 << 31) - 1, H=128),
+                                 dict(num_pages=1 << 25), dict(prefix_len=(1 << 31) - 128, num_prefix_pages=1 << 25)])
+def test_sizes_that_pass_32_bits(dsa, big):
+    """Refused by the call and by its workspace size alike (a size from overflown tile counts would be
+    of no use to anybody)."""
+    import ctypes
+    from test_prefix_step import _attend_args
+    a = _attend_args(dsa, **{"H": 128, **big})
+    n = ctypes.c_size_t(5)
+    assert dsa.lib().dsa_prefix_mla_workspace_size(ctypes.byref(a), ctypes.byref(n)) == dsa.DSA_ERR_UNSUPPORTED
+    assert n.value == 5
+    a.workspace_bytes = 0  # the workspace is asked for last
+    assert dsa.lib().dsa_prefix_mla(ctypes.byref(a), None) == dsa.DSA_ERR_UNSUPPORTED
