@@ -65,7 +65,7 @@ constexpr uint32_t kOffQ = 0, kOffK = kAtoms * kAtomBytes, kOffV = kOffK + kAtom
 constexpr uint32_t kOffP = kOffV + 2 * kVGroup, kOffMisc = kOffP + 2 * kAtomBytes;
 constexpr size_t kSmem = kOffMisc + 3 * 1024;
 constexpr uint32_t kOCol0 = 128;                          // O behind the two S buffers of 64 columns
-constexpr int kMaxKeys = 0x7FFFFFFF - kKeys;              // that a query sees
+constexpr int kMaxKeys = 0x7FFFFFFF - kKeys;              // that a query sees: the last block's border fits 32 bits
 constexpr int kSetup = 3;                                 // what a tile costs beside its blocks, in blocks
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -92,6 +92,8 @@ struct Args {
   int B, total_q, H, page_size, page_log2, num_pages, max_pages, prefix_len, num_prefix_pages;
   int may_pack;            // the plan may pack the prefix tiles across requests
   int max_tiles, G;        // tiles there is room for; CTA pairs
+  int row_blocks;          // of 128 of the batch's rows
+  int room;                // keys that the tables cover, at most kMaxKeys
   int narrow;              // the line is shorter than 2^31 places, whatever the lengths
   int past_row;            // a row coordinate past the cache: copies from there are zeros
   float scale_log2;        // scale * log2(e)
@@ -107,7 +109,7 @@ struct Args {
   Query* queries;          // [total_q], packed batches only
   float *part_o, *part_ml; // pieces: [slot][128 columns of 4][128 rows][4], [slot][128 rows][2]
   unsigned* status;
-  // failure-path test hook (probe_site 0: off): a role waits, at probe_at, for what never comes
+  // failure-path test hook: a role waits, at probe_at, for what never comes
   int probe_site;
   uint32_t probe_at;
   long long probe_cycles;
@@ -145,20 +147,17 @@ __device__ __forceinline__ int sees(const Args& a, int b, int t, bool* bad) {
   const int q0 = __ldg(a.cu + b), q1 = __ldg(a.cu + b + 1);
   if (t < q0 || t >= q1) return 0;
   long long n = static_cast<long long>(__ldg(a.lens + b)) - (q1 - q0) + (t - q0) + 1;
-  // (no more than kMaxKeys, so that the border of the last block stays in 32 bits)
-  const long long room = min(max(static_cast<long long>(a.max_pages) * a.page_size, static_cast<long long>(a.prefix_len)),
-                             static_cast<long long>(kMaxKeys));
-  if (n > room) {
+  if (n > a.room) {
     *bad = true;
-    n = room;
+    n = a.room;
   }
   return static_cast<int>(max(n, 0LL));
 }
 
 // Whether a tile's rows are joined over two tiles, its own being one of a packed batch: tiles of
-// several requests, and those that begin with own keys although there is a prefix.
+// several requests, and those that begin with own keys (may_pack: there is a prefix).
 __device__ __forceinline__ bool joined(const Args& a, const Tile& t) {
-  return t.b < 0 || (t.n_pre == 0 && a.prefix_len > 0);
+  return a.may_pack && (t.b < 0 || t.n_pre == 0);
 }
 
 // The line of all tiles, U long: a tile's blocks stand behind kSetup places for what it costs to
@@ -189,8 +188,7 @@ struct Place {
 };
 __device__ __forceinline__ Place place(const Args& a, int c, bool at_start, bool whole, bool own, int row, int r) {
   if (!whole) return {2 * c + (at_start ? 1 : 0), r};
-  const int blocks = (a.total_q * a.H + kRows - 1) / kRows;
-  return {2 * a.G + (own ? blocks : 0) + row / kRows, row % kRows};
+  return {2 * a.G + (own ? a.row_blocks : 0) + (row >> 7), row & (kRows - 1)};
 }
 
 // ------------------------------------------------------------------ plan
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_mla_plan_kernel(const Arg
   const bool packed = a.may_pack && 100LL * kRows * own_tiles > 115LL * q_end * a.H;
   // rows beyond the last request (padding) count as one more request that sees nothing
   const int n_pad = packed ? 0 : ((a.total_q - q_end) * a.H + kRows - 1) / kRows;
-  const int n_pre_tiles = packed ? (a.total_q * a.H + kRows - 1) / kRows : 0;
+  const int n_pre_tiles = packed ? a.row_blocks : 0;
   const int nreq = packed ? a.B : a.B + 1;
   const int n_tiles = static_cast<int>(min(n_pre_tiles + n_pad + own_tiles, static_cast<unsigned>(a.max_tiles)));
   if (tid == 0) {
@@ -461,6 +459,8 @@ __device__ __forceinline__ void load_q(const Args& a, uint8_t* smem, const Tile&
   }
 }
 
+// kProbe: with the test hook's waits (asked for in every call, they took up to 0.5 us of it).
+template <bool kProbe>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_mla_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r,
                       const Args a) {
@@ -484,10 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto spin = [&](uint64_t* bar, uint32_t parity, long long cycles = ptx::kWaitCycles) {
     return ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout, cycles);
   };
-  auto probed = [&](int site) { return a.probe_site == site + (rank != 0 ? kProbeOdd : 0); };
+  auto probed = [&](int site) { return kProbe && a.probe_site == site + (rank != 0 ? kProbeOdd : 0); };
   auto stop_at = [&](int site) { return probed(site) ? a.probe_at : ~0u; };
-  // (The copying warps ask before their first block only: asked in their loops, for every group, it took
-  // 64 x 64 heads behind 8192 keys from 74 to 82 us and 1781 prompt tokens from 0.91 to 1.09 ms.)
   auto run_out = [&]() { return __all_sync(0xffffffffu, spin(&bars->never, 0, a.probe_cycles)) != 0; };
 
   if (threadIdx.x == 0) {
@@ -558,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i <= nblk; ++i) {
           if (i < nblk) {
             const uint32_t d = tmem_base + (n1 & 1) * 64;
-            if (n1 == stop) ok = ok && spin(&bars->never, 0, a.probe_cycles);
+            if (kProbe && n1 == stop) ok = ok && spin(&bars->never, 0, a.probe_cycles);
             wait(&bars->sempty[n1 & 1], ((n1 >> 1) & 1) ^ 1);
 #pragma unroll
             for (int g = 0; g < 3; ++g) {
@@ -712,7 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t stop = stop_at(kProbeQueries);
     next_piece(a, p, u_hi, t);
     for (uint32_t seg = 1; next_piece(a, p, u_hi, t); ++seg) {
-      bool good = seg != stop || spin(&bars->never, 0, a.probe_cycles);
+      bool good = !kProbe || seg != stop || spin(&bars->never, 0, a.probe_cycles);
       good = good && spin(&bars->qempty, (seg & 1) ^ 1);
       if (!__all_sync(0xffffffffu, good)) {
         give_up();
@@ -978,7 +976,7 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
   }
   if (packed) {
     ta = blockIdx.x / per_tile;
-    if (ta * kRows >= a.total_q * a.H) return;
+    if (ta >= a.row_blocks) return;
     const int width = 128 / per_tile;
     by_piece = per_tile == 32;
     col0 = (blockIdx.x - ta * per_tile) * width;
@@ -1032,10 +1030,14 @@ __global__ void __launch_bounds__(512, 1) prefix_mla_join_kernel(const Args a, i
   const int k0 = by_piece ? y : 0, step = by_piece ? 4 : 1;
   const float2* part_ml = reinterpret_cast<const float2*>(a.part_ml);
   const float4* part_o = reinterpret_cast<const float4*>(a.part_o);
+  // the same places as the pieces were left in; a whole tile's by the rows of the batch (packed: row0 = 128 ta)
+  const int whole = 2 * a.G + ta, whole_b = whole + a.row_blocks;
+  if (b0 == b1) rb = r;
   auto place_of = [&](int k) -> Place {  // of piece k
     const bool in_a = k < na;
     const int kk = in_a ? k : k - na, first = in_a ? a0 : b0;
-    return place(a, first + kk, kk == 0, first == (in_a ? a1 : b1), !in_a, row, in_a ? r : rb);
+    if (first == (in_a ? a1 : b1)) return {in_a ? whole : whole_b, in_a ? r : rb};
+    return {2 * (first + kk) + (kk == 0 ? 1 : 0), in_a ? r : rb};
   };
 
   for (int q0 = 0; q0 < n_col; q0 += kAcc) {
@@ -1165,11 +1167,13 @@ int pair_count() {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(prefix_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(prefix_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(prefix_mla_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem)) != cudaSuccess ||
         cudaFuncSetAttribute(prefix_mla_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, prefix_mla_kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaOccupancyMaxActiveClusters(&n, prefix_mla_kernel<false>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       return 76;
     }
@@ -1278,8 +1282,11 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   k.max_tiles = p.max_tiles;
   k.G = p.G;
   k.past_row = static_cast<int>(slots);
-  const long long most = std::max(static_cast<long long>(a->max_pages_per_seq) * a->page_size,
-                                  static_cast<long long>(a->prefix_len)) / kKeys + 2 + kSetup;
+  const long long groups = (static_cast<long long>(a->total_q) * a->H + kRows - 1) / kRows;
+  k.row_blocks = static_cast<int>(groups);
+  k.room = static_cast<int>(std::min(std::max(static_cast<long long>(a->max_pages_per_seq) * a->page_size,
+                                              static_cast<long long>(a->prefix_len)), static_cast<long long>(kMaxKeys)));
+  const long long most = k.room / kKeys + 2 + kSetup;
   k.narrow = most * p.max_tiles < (1LL << 31) ? 1 : 0;
   k.scale_log2 = a->scale * 1.4426950408889634f;
   k.qn = static_cast<const __nv_bfloat16*>(a->q_nope);
@@ -1311,11 +1318,9 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* a, dsa_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(prefix_mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  e = launch_pdl(prefix_mla_kernel, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
+  e = launch_pdl(probe.site != 0 ? prefix_mla_kernel<true> : prefix_mla_kernel<false>, dim3(2 * p.G), dim3(kThreads), kSmem, s, tc, tr, k);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  const long long rows = static_cast<long long>(a->total_q) * a->H;
   // Few packed tiles have many pieces each: 32 CTAs a tile, which split them.
-  const long long groups = (rows + kRows - 1) / kRows;
   const int per_tile = groups * 32 <= 2LL * p.G ? 32 : (groups * 8 <= 2LL * p.G ? 8 : 4);
   const long long ctas = std::max(p.may_pack ? groups * per_tile : 0LL, p.G * 2LL);
   e = launch_pdl(prefix_mla_join_kernel, dim3(static_cast<unsigned>(ctas)), dim3(512), kJoinSmem, s, k, per_tile);
