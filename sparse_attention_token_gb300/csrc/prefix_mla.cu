@@ -37,8 +37,8 @@
 // Keys are staged twice, once for S and once for P . V (the MMAs of a pair read the same offsets in
 // both CTAs, so one copy cannot be split by keys and by columns), which fills shared memory with one
 // block; nine K and four V groups cost the two copying warps and the issuer more than they save.
-// 1781 x 64 rows behind 6000 keys take 0.98 ms, 1.60 PFLOP/s (0.87 to 0.93 ms, 1.70 to 1.80 PFLOP/s,
-// launch after launch in a graph), the tensor pipe active 76 % of its cycles under the profiler.
+// 1781 x 64 rows behind 6000 keys take 0.98 to 1.03 ms, 1.53 to 1.60 PFLOP/s (0.87 to 0.95 ms, 1.65 to
+// 1.80 PFLOP/s, launch after launch in a graph), the tensor pipe active 83 % of its cycles under the profiler.
 //
 // join: out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j over a row's pieces, in their order.
 //
@@ -459,7 +459,8 @@ __device__ __forceinline__ void load_q(const Args& a, uint8_t* smem, const Tile&
   }
 }
 
-// kProbe: with the test hook's waits (asked for in every call, they took up to 0.5 us of it).
+// kProbe: with the test hook's waits (asked for in every call, they took up to 0.6 us of it; asked for by
+// the copying warps before every group, 8 us of the 74 that 64 x 64 heads behind 8192 keys take).
 template <bool kProbe>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_mla_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r,
@@ -805,6 +806,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (m == -INFINITY || mb > m + 8.f) mn = mb;
         const float cr = (m == -INFINITY || mn == m) ? 1.f : ptx::ex2(m - mn);
         const float off = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every x is -inf, p = 0
+        // P goes into the product as bf16: an MMA's operands are of one type, and V is the cache.  That
+        // moves each p by at most 2^-9 of it, the output by about 0.0011 of its size; its own rounding
+        // to bf16 makes 0.0017, both together 0.0018 to 0.0020 (the mean error of the listed batches
+        // against 64 bits).  P as a sum of two bf16 would take P . V's 1024 of a block's 2284 cycles twice.
+        // The sum l takes p unrounded, so that lse has fp32 accuracy.
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[16];
 #pragma unroll
