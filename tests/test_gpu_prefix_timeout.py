@@ -8,8 +8,6 @@ host reads DSA_ERR_TIMEOUT, the context stays usable and the next call gives the
 Each drain gives up after 0.2 s (4e8 cycles at about 2 GHz) when it waits for something that does
 not come, so a call that ends sooner drained what was in flight and nothing else.
 """
-import time
-
 import pytest
 import torch
 
@@ -58,12 +56,15 @@ def test_a_wait_that_runs_out_ends_the_call_and_the_next_is_right(batch):
     args, kw = _batch(**BATCHES[batch])
     ref = dsa.dsa_prefix_mla(*args, **kw)
     assert dsa.dsa_check_device_status() == dsa.DSA_OK
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for site, at in SITES:
         dsa.dsa_test_arm_prefix_mla_timeout(site, at, LIMIT_NS)
-        t0 = time.monotonic()
+        begin.record()
         dsa.dsa_prefix_mla(*args, **kw)
+        end.record()
         status = dsa.dsa_check_device_status()
-        took = time.monotonic() - t0
+        torch.cuda.synchronize()
+        took = begin.elapsed_time(end) / 1e3
         assert status == dsa.DSA_ERR_TIMEOUT, (site, at)
         assert took < 0.15, (site, at, took)
         assert dsa.dsa_check_device_status() == dsa.DSA_OK        # the status word was cleared

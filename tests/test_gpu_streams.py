@@ -79,3 +79,28 @@ def test_scores_and_top_k_on_a_side_stream():
     torch.cuda.synchronize()
     assert dsa.dsa_check_device_status() == dsa.DSA_OK
     assert torch.equal(ref, got) and torch.equal(top, got_top)
+
+
+def test_a_side_stream_inside_a_captured_graph():
+    s, side = _step(3), torch.cuda.Stream()
+    bt = s["bt"].clone()
+    ref = _plan(s, bt=bt)
+    ref_out = _attend(s, ref[0], bt)
+    tables = s["bt"].clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = _plan(s, bt=tables, stream=side)
+        got_out = _attend(s, got[0], tables, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        doubled = got_out[1] * 2  # reads the result on the capturing stream
+    for _ in range(3):
+        for t in got + got_out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert dsa.dsa_check_device_status() == dsa.DSA_OK
+        for a, b in zip(ref + ref_out, got + got_out):
+            assert torch.equal(a, b)
+        assert torch.equal(doubled, ref_out[1] * 2)
