@@ -59,7 +59,7 @@ typedef enum {
     DSA_ERR_WORKSPACE = 6         /* workspace missing or smaller than required */
 } dsa_status;
 
-typedef enum { DSA_BF16 = 0, DSA_FP8_E4M3 = 1 } dsa_dtype;
+typedef enum { DSA_BF16 = 0, DSA_FP8_E4M3 = 1, DSA_FP4_E2M1 = 2 /* quantised latent cache only */ } dsa_dtype;
 
 typedef enum { DSA_LAYER_FULL = 0, DSA_LAYER_SHARED = 1 } dsa_layer_type;
 
@@ -507,6 +507,111 @@ typedef struct {
 } dsa_prefix_mla_args;
 dsa_status dsa_prefix_mla_workspace_size(const dsa_prefix_mla_args* args, size_t* bytes);
 dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* args, dsa_stream_t stream);
+
+/*
+ * A latent cache in 8 or 4 bits: quantised as it is written, attended over as it is, read back as
+ * bf16.  One array cache [num_pages, page_size, row] of bytes holds a token's 512 latent and 64
+ * rotary values; block tables, slots and positions are those of the calls above.
+ *   DSA_FP8_E4M3  656 bytes a row (bf16: 1152): 512 e4m3 codes, 64 bf16, one scale
+ *   DSA_FP4_E2M1  416 bytes a row: 512 e2m1 codes, 64 bf16, 32 scales of blocks of 16
+ * With c the latent row and a_max its largest magnitude:
+ *   E = the smallest integer with a_max <= 448 * 2^E (432 * 2^E in 4 bits), in [-60, 60], 0 for zeros
+ *   e4m3   code = the e4m3 value nearest to c / 2^E; it stands for 2^E * code
+ *   e2m1   per block of 16: s = the smallest value of 4 significant bits, at least 2^-5, with
+ *          6 * s >= the block's largest |c| / 2^E; code = the e2m1 value nearest to c / (2^E * s); it
+ *          stands for 2^E * e4m3(code * s), the product rounded to e4m3
+ * (nearest: ties to even; 2^-5 <= s <= 72).  The codes are those of c in exact arithmetic, not of a
+ * rounded c.  Every value that a row stands for is exact in bf16.  The rotary part is held as
+ * bf16(r) / 2^E.  A mean over 512 normal values is off by 2.7 % (e4m3) and 10 % (e2m1) of their size.
+ * Rows are the library's own: dsa_mla_quant_append writes and dsa_mla_quant_read reads them.  A page
+ * may be moved or copied as bytes.
+ */
+
+/* Bytes of a row of this format; 0 for one that there is not. */
+int dsa_mla_quant_row_bytes(int format);
+
+/*
+ * dsa_mla_quant_append -- dsa_mla_cache_append into a quantised cache: c = norm_weight * c_kv /
+ * sqrt(mean(c_kv^2) + norm_eps) (c_kv itself without norm_weight) and r = RoPE(k_rope) (k_rope itself
+ * without rope_cos), written to row slot of the cache in `format`.  Arguments, slots and reports are
+ * those of dsa_mla_cache_append; cache is 16-byte aligned.  Inputs must be finite.
+ */
+typedef struct {
+  int format, n, kv_rank, rope_dim, page_size, num_pages, rope_interleaved, rope_rows;
+  float norm_eps;
+  const void* c_kv;
+  const void* k_rope;
+  int64_t c_stride, r_stride;
+  const int64_t* slot_mapping;
+  const float* norm_weight;
+  const float* rope_cos;
+  const float* rope_sin;
+  const int32_t* positions;
+  void* cache;
+} dsa_mla_quant_append_args;
+dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* args, dsa_stream_t stream);
+
+/*
+ * dsa_mla_quant_read -- rows of a quantised cache as bf16: for request b and 0 <= i < cu_lens[b + 1] -
+ * cu_lens[b], row t = cu_lens[b] + i of c_kv and k_rope gets what position starts[b] + i of the request
+ * (i itself when starts is NULL) stands for, exactly.  The rows may be views of one [total, 576] array
+ * (c_stride, r_stride elements apart, multiples of 8; any when total = 1).  total is the outputs'
+ * length: rows past cu_lens[B] are left as they were, rows past total are dropped.  A position whose
+ * page is outside the cache, or that the table does not cover, leaves its row as it was and is
+ * reported through dsa_check_device_status.  c_kv, k_rope and cache 16-byte aligned.
+ * With pages of its own, the result is a bf16 cache that dsa_prefix_mla and dsa_sparse_mla take.
+ */
+typedef struct {
+  int format, B, total, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq;
+  const void* cache;
+  const int32_t* block_tables;
+  const int32_t* cu_lens;
+  const int32_t* starts;
+  void* c_kv;
+  void* k_rope;
+  int64_t c_stride, r_stride;
+} dsa_mla_quant_read_args;
+dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* args, dsa_stream_t stream);
+
+/*
+ * dsa_quant_mla -- absorbed multi-head latent attention over a quantised cache, each query over its
+ * selected keys or over all that it sees:
+ *     logit = scale * (q_nope[t, h] . c[s] + q_rope[t, h] . r[s])
+ *     out[t, h, :] = sum_s softmax_s(logit) * c[s]     (bf16, latent space)
+ *     lse[t, h]    = ln sum_s exp(logit)               (fp32; optional)
+ * with c, r what row s of the cache stands for.  topk_width > 0: over the positions s = topk[t, j] with
+ * 0 <= s < seq_lens[b], others are skipped (any order; one that is named twice counts twice).
+ * topk_width = 0: over all s <= p, p = seq_lens[b] - q_len(b) + i the position of the sequence's i-th
+ * query; the cache is then read once for every query, so a prompt of many tokens is better served by
+ * dsa_mla_quant_read and dsa_prefix_mla.  A query without keys and the rows t >= cu_q_lens[B]
+ * (padding) give zeros and lse = -inf.
+ *   q_nope [total_q, H, 512], q_rope [total_q, H, 64] bf16 with the given element strides (multiples of
+ *   8, any in a dimension of size 1; the last dimension dense); out [total_q, H, 512] bf16 dense;
+ *   lse [total_q, H]; topk [total_q, topk_width].
+ * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, scale > 0; total_q * H and num_pages * page_size below
+ * 2^31 - 128.  Rows of the cache that no query attends to may hold anything; the others are finite, and
+ * so are the queries.  A page outside the cache is skipped and reported through
+ * dsa_check_device_status, as are positions past the table (topk_width = 0).  Results do not depend
+ * on the run.  workspace: dsa_quant_mla_workspace_size bytes, 16-byte aligned like the other pointers.
+ */
+typedef struct {
+  int format, B, total_q, H, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq, topk_width;
+  float scale;
+  const void* q_nope;
+  const void* q_rope;
+  int64_t qn_stride_t, qn_stride_h, qr_stride_t, qr_stride_h;
+  const void* cache;
+  const int32_t* block_tables;
+  const int32_t* cu_q_lens;
+  const int32_t* seq_lens;
+  const int32_t* topk;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} dsa_quant_mla_args;
+dsa_status dsa_quant_mla_workspace_size(const dsa_quant_mla_args* args, size_t* bytes);
+dsa_status dsa_quant_mla(const dsa_quant_mla_args* args, dsa_stream_t stream);
 
 /*
  * dsa_indexer_static -- dsa_indexer for callers that cannot allocate device memory.

@@ -41,6 +41,7 @@ DSA_ERR_WORKSPACE = 6
 
 DSA_BF16 = 0
 DSA_FP8_E4M3 = 1
+DSA_FP4_E2M1 = 2  # the quantised latent cache only
 DSA_LAYER_FULL = 0
 DSA_LAYER_SHARED = 1
 DSA_ORDER_SCORE = 0
@@ -123,6 +124,35 @@ class dsa_prefix_mla_args(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class dsa_mla_quant_append_args(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("n", ctypes.c_int), ("kv_rank", ctypes.c_int), ("rope_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("rope_interleaved", ctypes.c_int),
+                ("rope_rows", ctypes.c_int), ("norm_eps", ctypes.c_float), ("c_kv", ctypes.c_void_p),
+                ("k_rope", ctypes.c_void_p), ("c_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("slot_mapping", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("rope_cos", ctypes.c_void_p),
+                ("rope_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("cache", ctypes.c_void_p)]
+
+
+class dsa_mla_quant_read_args(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("B", ctypes.c_int), ("total", ctypes.c_int), ("kv_rank", ctypes.c_int),
+                ("rope_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int), ("cache", ctypes.c_void_p), ("block_tables", ctypes.c_void_p),
+                ("cu_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("c_kv", ctypes.c_void_p),
+                ("k_rope", ctypes.c_void_p), ("c_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64)]
+
+
+class dsa_quant_mla_args(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("B", ctypes.c_int), ("total_q", ctypes.c_int), ("H", ctypes.c_int),
+                ("kv_rank", ctypes.c_int), ("rope_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages_per_seq", ctypes.c_int), ("topk_width", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_nope", ctypes.c_void_p), ("q_rope", ctypes.c_void_p),
+                ("qn_stride_t", ctypes.c_int64), ("qn_stride_h", ctypes.c_int64), ("qr_stride_t", ctypes.c_int64),
+                ("qr_stride_h", ctypes.c_int64), ("cache", ctypes.c_void_p), ("block_tables", ctypes.c_void_p),
+                ("cu_q_lens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("topk", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 _LIB = None
 
 
@@ -184,6 +214,16 @@ def lib():
         L.dsa_prefix_mla_workspace_size.argtypes = [P, ctypes.POINTER(S)]
         L.dsa_prefix_mla.restype = I
         L.dsa_prefix_mla.argtypes = [P, P]
+        L.dsa_mla_quant_row_bytes.restype = I
+        L.dsa_mla_quant_row_bytes.argtypes = [I]
+        L.dsa_mla_quant_append.restype = I
+        L.dsa_mla_quant_append.argtypes = [P, P]
+        L.dsa_mla_quant_read.restype = I
+        L.dsa_mla_quant_read.argtypes = [P, P]
+        L.dsa_quant_mla_workspace_size.restype = I
+        L.dsa_quant_mla_workspace_size.argtypes = [P, ctypes.POINTER(S)]
+        L.dsa_quant_mla.restype = I
+        L.dsa_quant_mla.argtypes = [P, P]
         L.dsa_test_arm_score_timeout.restype = I
         L.dsa_test_arm_score_timeout.argtypes = [ctypes.c_ulonglong]
         L.dsa_test_arm_prefix_mla_timeout.restype = I
@@ -938,6 +978,156 @@ def dsa_prefix_mla(q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, se
     if stream is not None:
         _hold(stream, (q_nope, q_rope, cache_c, cache_r, block_tables, cu_q_lens, seq_lens, prefix_pages, out, lse,
                        workspace), (out, lse))
+    return out, lse
+
+
+# ---- the latent cache in 8 or 4 bits: append, read-back, attention --------------------------
+
+_QUANT_APPEND_ARGS = struct.Struct("@8if2P2q6P")
+_QUANT_READ_ARGS = struct.Struct("@8i6P2q")
+_QUANT_MLA_ARGS = struct.Struct("@10if2P4q8PN")
+assert _QUANT_APPEND_ARGS.size == ctypes.sizeof(dsa_mla_quant_append_args)
+assert _QUANT_READ_ARGS.size == ctypes.sizeof(dsa_mla_quant_read_args)
+assert _QUANT_MLA_ARGS.size == ctypes.sizeof(dsa_quant_mla_args)
+
+_QUANT_FORMATS = {656: DSA_FP8_E4M3, 416: DSA_FP4_E2M1}  # by the bytes of a row
+
+
+def dsa_mla_quant_row_bytes(format: int) -> int:
+    """Bytes of a row of the quantised latent cache: 656 for DSA_FP8_E4M3, 416 for DSA_FP4_E2M1."""
+    n = int(lib().dsa_mla_quant_row_bytes(int(format)))
+    if n == 0:
+        raise ValueError(f"there is no quantised latent cache of format {format} (DSA_FP8_E4M3 or DSA_FP4_E2M1)")
+    return n
+
+
+def _quant_cache(cache: torch.Tensor, here: int):
+    """(format, pages, page size, device pointer) of a quantised latent cache."""
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] not in _QUANT_FORMATS:
+        raise ValueError("cache must have shape [num_pages, page_size, 656 (DSA_FP8_E4M3) or 416 (DSA_FP4_E2M1)], got "
+                         f"{tuple(shape)}")
+    return _QUANT_FORMATS[shape[2]], shape[0], shape[1], _ptr(cache, "cache", torch.uint8, here)
+
+
+def dsa_mla_quant_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor, cache: torch.Tensor, *,
+                         norm_weight: Optional[torch.Tensor] = None, norm_eps: float = 1e-6,
+                         rope_cos: Optional[torch.Tensor] = None, rope_sin: Optional[torch.Tensor] = None,
+                         positions: Optional[torch.Tensor] = None, rope_interleaved: bool = False,
+                         stream=None) -> None:
+    """dsa_mla_cache_append into a quantised cache [num_pages, page_size, row] uint8, in place: c_kv [n, 512]
+    (root-mean-square norm times norm_weight, when given) and k_rope [n, 64] (turned by row positions[t] of
+    rope_cos / rope_sin, when given) as one row of 656 bytes (e4m3) or 416 (e2m1), by the cache's row size,
+    at the slots slot_mapping [n] (int64; negative = skip)."""
+    if not (c_kv.dim() == k_rope.dim() == 2 and (rope_cos is None or rope_cos.dim() == 2)):
+        _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (rope_cos, "rope_cos", (None, None))])
+    n, R = c_kv.shape
+    rd = k_rope.shape[1]
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    rows = 0 if rope_cos is None else rope_cos.shape[0]
+    table = (rows, rd // 2)
+    if not (k_rope.shape[0] == n and slot_mapping.shape == (n,) and (norm_weight is None or norm_weight.shape == (R,))
+            and (rope_cos is None or rope_cos.shape == rope_sin.shape == table)
+            and (positions is None or positions.shape == (n,))):
+        _expect([(k_rope, "k_rope", (n, rd)), (slot_mapping, "slot_mapping", (n,)), (norm_weight, "norm_weight", (R,)),
+                 (rope_cos, "rope_cos", table), (rope_sin, "rope_sin", table), (positions, "positions", (n,))])
+    f32, here = torch.float32, _here(cache)
+    fmt, num_pages, page_size, at = _quant_cache(cache, here)
+    args = _QUANT_APPEND_ARGS.pack(
+        fmt, n, R, rd, page_size, num_pages, 1 if rope_interleaved else 0, rows, norm_eps, _rows(c_kv, "c_kv", here),
+        _rows(k_rope, "k_rope", here), c_kv.stride(0), k_rope.stride(0),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, here), _ptr(norm_weight, "norm_weight", f32, here),
+        _ptr(rope_cos, "rope_cos", f32, here), _ptr(rope_sin, "rope_sin", f32, here),
+        _ptr(positions, "positions", torch.int32, here), at)
+    status = lib().dsa_mla_quant_append(args, _stream_of(here, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_mla_quant_append")
+    if stream is not None:
+        _hold(stream, (c_kv, k_rope, slot_mapping, cache, norm_weight, rope_cos, rope_sin, positions))
+
+
+def dsa_mla_quant_read(cache: torch.Tensor, block_tables: torch.Tensor, cu_lens: torch.Tensor, *, total: int,
+                       starts: Optional[torch.Tensor] = None, c_kv: Optional[torch.Tensor] = None,
+                       k_rope: Optional[torch.Tensor] = None, stream=None):
+    """Rows of a quantised cache as bf16, exactly: (c_kv [total, 512], k_rope [total, 64]).  Rows cu_lens[b] ..
+    cu_lens[b + 1] - 1 get request b's positions from starts[b] (int32; 0 without starts) on, through
+    block_tables [B, max_pages].  Rows past cu_lens[B] are left as they were; c_kv and k_rope may be given,
+    also as views of one [total, 576] tensor."""
+    bs = block_tables.shape
+    B = bs[0] if len(bs) == 2 else -1
+    if B < 0 or cu_lens.shape != (B + 1,) or (starts is not None and starts.shape != (B,)):
+        _expect([(block_tables, "block_tables", (None, None)), (cu_lens, "cu_lens", (B + 1,)), (starts, "starts", (B,))])
+    i32, here, dev = torch.int32, _here(cache), cache.device
+    fmt, num_pages, page_size, at = _quant_cache(cache, here)
+    new = []
+    for t, name, width in ((c_kv, "c_kv", 512), (k_rope, "k_rope", 64)):
+        if t is None:
+            t = _new((total, width), torch.bfloat16, dev, stream)
+        elif t.shape != (total, width):
+            _expect([(t, name, (total, width))])
+        new.append(t)
+    c_kv, k_rope = new
+    args = _QUANT_READ_ARGS.pack(
+        fmt, B, total, 512, 64, page_size, num_pages, bs[1], at, _ptr(block_tables, "block_tables", i32, here),
+        _ptr(cu_lens, "cu_lens", i32, here), _ptr(starts, "starts", i32, here), _rows(c_kv, "c_kv", here),
+        _rows(k_rope, "k_rope", here), c_kv.stride(0), k_rope.stride(0))
+    status = lib().dsa_mla_quant_read(args, _stream_of(here, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_mla_quant_read")
+    if stream is not None:
+        _hold(stream, (cache, block_tables, cu_lens, starts, c_kv, k_rope), (c_kv, k_rope))
+    return c_kv, k_rope
+
+
+def dsa_quant_mla(q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk=None, *, scale: float, out=None,
+                  lse=None, workspace=None, stream=None):
+    """Latent attention over a quantised cache [num_pages, page_size, row] uint8: each query over its selected
+    keys topk [total_q, k] int32 (any order, -1 skipped), or without topk over every position up to its own.
+    Returns (out [total_q, H, 512] bf16, lse [total_q, H] fp32, the natural logarithm of the sum of
+    exponentials); a query without keys gets zeros and -inf.  q_nope [total_q, H, 512] and q_rope
+    [total_q, H, 64] bf16 may be views of one tensor.  out, lse and the workspace
+    (dsa_quant_mla_workspace_size bytes) are allocated when not given."""
+    qs, rs, bs = q_nope.shape, q_rope.shape, block_tables.shape
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if len(qs) != 3 or len(rs) != 3 or len(bs) != 2 or B < 0 or (topk is not None and topk.dim() != 2):
+        _expect([(q_nope, "q_nope", (None, None, None)), (q_rope, "q_rope", (None, None, None)),
+                 (seq_lens, "seq_lens", (None,)), (block_tables, "block_tables", (None, None)),
+                 (topk, "topk", (None, None))])
+    T, H, R = qs
+    rd = rs[2]
+    k = 0 if topk is None else topk.shape[1]
+    if rs != (T, H, rd) or bs[0] != B or cu_q_lens.shape != (B + 1,) or (topk is not None and topk.shape != (T, k)):
+        _expect([(q_rope, "q_rope", (T, H, rd)), (block_tables, "block_tables", (B, None)),
+                 (cu_q_lens, "cu_q_lens", (B + 1,)), (topk, "topk", (T, k))])
+    if topk is not None and k == 0:
+        raise ValueError("topk must have a column at least (without topk a query attends to every position up to its own)")
+    i32, bf16, dev, here = torch.int32, torch.bfloat16, cache.device, _here(cache)
+    fmt, num_pages, page_size, at = _quant_cache(cache, here)
+    sizes = (fmt, B, T, H, R, rd, page_size, num_pages, bs[1], k, scale)
+    qt, qh, _ = q_nope.stride()
+    rt, rh, _ = q_rope.stride()
+    tensors = (_rows(q_nope, "q_nope", here), _rows(q_rope, "q_rope", here), qt, qh, rt, rh, at,
+               _ptr(block_tables, "block_tables", i32, here), _ptr(cu_q_lens, "cu_q_lens", i32, here),
+               _ptr(seq_lens, "seq_lens", i32, here), _ptr(topk, "topk", i32, here))
+    out = _out(out, "out", (T, H, R), bf16, dev, here, stream)
+    lse = _out(lse, "lse", (T, H), torch.float32, dev, here, stream)
+    L = lib()
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        status = L.dsa_quant_mla_workspace_size(_QUANT_MLA_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need))
+        if status != DSA_OK:
+            raise DsaError(status, "dsa_quant_mla_workspace_size")
+        room = need.value or 16
+        workspace = _new(room, torch.uint8, dev, stream)
+    else:
+        room = workspace.numel() * workspace.element_size()
+    args = _QUANT_MLA_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"), room)
+    status = L.dsa_quant_mla(args, _stream_of(here, stream))
+    if status != DSA_OK:
+        raise DsaError(status, "dsa_quant_mla")
+    if stream is not None:
+        _hold(stream, (q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk, out, lse, workspace), (out, lse))
     return out, lse
 
 
