@@ -4,9 +4,33 @@
 //     out[t, h]      = sum_s softmax_s(logit[t, h, :]) c[s],   lse[t, h] = ln sum_s exp(logit[t, h, s])
 //
 // over the selected positions s = topk[t, j] of the query's sequence, or over every position up to its own.
-// One warp takes a (query, head) row: one pass over its keys with the running maximum and sum, lane i
-// holding 16 latent and 2 rotary values.
+//
+// Both formats are e4m3 numbers times a row's power of two, c[s] = 2^E c8[s], r[s] = 2^E r8[s], so the tensor
+// cores take the cache's codes as they are, and nothing is converted to bf16:
+//   q = 2^-a (hi + lo) in two e4m3 rows (exact for what lies within 2^9 of the row's largest value, and within
+//   2^-17 of that otherwise):      S = hi . c8 + lo . c8 + (2^a q_rope) . r8,   logit log2(e) = 2^-a 2^E S scale log2(e)
+//   x' = logit log2(e) + E,  m' its running maximum,  p = 2^(x' - m' + 5) in two e4m3 terms (2^-8 relative,
+//   2^-15 of the largest):         O = sum p c8,  L = sum p 2^-E (fp32),  out = O / L
+// Two e4m3 planes cost the tensor cores what one bf16 plane does and half the shared memory traffic.  Taking E
+// into the maximum keeps p in e4m3's range whatever the rows' scales are.
+//
+// Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64.  The blocks of all tiles stand
+// in one line, cut into equal parts, one per CTA: a part may start and end inside a tile.  A tile done in one
+// piece is normalised and written, the pieces of the others leave (O, m', L) in fp32 and a second kernel joins them.
+// Roles of a CTA:
+//   warps 0..3  softmax.  Rows of S alternate between 16 hi and 16 lo rows, so that a lane and the one 16 further
+//               hold a head's two planes; each adds the planes for half of the block's keys;
+//   warps 4..7  query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
+//               4-bit rows also: codes from the staged rows to e4m3 tiles;
+//   warp 8      rows of the cache: e4m3 tiles by gathering TMA (4 rows x 128 bytes), 4-bit rows by bulk copies;
+//   warp 9      TMEM, MMAs:  S [128 x 64 keys] = Q (TMEM) . K^T,  O^T [512 x heads] += V^T (the same tile,
+//               MN-major) . P^T;
+//   warp 10     e4m3: the rows' scales.
+// Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
+// (bounded) and TMEM is freed.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -17,92 +41,771 @@ namespace {
 
 using namespace quant;
 
-constexpr int kWarps = 4;
+constexpr int kHeads = 64;                                // heads per tile
+constexpr int kKeys = 64;                                 // keys per block
+constexpr int kThreads = 352;
+constexpr uint32_t kAtom = kKeys * 128;                   // 64 rows of 128 bytes
+constexpr uint32_t kTile = 5 * kAtom;                     // 4 columns of 128 codes, one of 64 bf16
+constexpr uint32_t kStaged = kKeys * kRow4;               // a block of 4-bit rows
+constexpr uint32_t kQRope = 128 * 128, kPBytes = kHeads * 128;
+constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // TMEM columns
+constexpr int kPShift = 5;                                // p = 2^5 at the reference maximum
+constexpr float kMove = 3.f;                              // the reference moves when passed by more: p <= 2^8
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxStages = 4;
+constexpr long long kMostKeys = 0x7FFFFF00ll;             // that a query sees: a block's last key fits 32 bits
+constexpr int kQRing = 4;                                 // scales of the queries of consecutive pieces
 
 template <bool FP4>
-__global__ void __launch_bounds__(kWarps * 32) quant_mla_kernel(const dsa_quant_mla_args a, unsigned* status) {
-  constexpr int kRow = FP4 ? kRow4 : kRow8;
-  const int lane = threadIdx.x & 31;
+struct Smem {
+  static constexpr int kStages = FP4 ? 3 : 4;             // tiles
+  static constexpr int kStagedBufs = FP4 ? 2 : 0;
+  static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
+  static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffMisc = kOffStaged + kStagedBufs * kStaged;
+  static constexpr uint32_t kBytes = kOffMisc + 6 * 1024;
+};
+
+struct Args {
+  int B, total_q, H, groups, page_size, num_pages, max_pages, topk_width;
+  int nb;                  // blocks of a tile (selected keys); 0: from the plan
+  int parts;               // CTAs
+  int past_row;            // a row past the cache: copies from there are zeros
+  float scale_log2;        // scale * log2(e)
+  const __nv_bfloat16 *qn, *qr;
+  long long qn_t, qn_h, qr_t, qr_h;
+  const uint8_t* cache;
+  const int32_t *block_tables, *cu, *lens, *topk;
+  const long long* cum;    // [total_q + 1] blocks before each query (every position)
+  __nv_bfloat16* out;
+  float* lse;
+  float *part_o, *part_ml; // pieces: [slot][4][16][128][4] (latent chunk, four heads, latent, head), [slot][64][2]
+  unsigned* status;
+};
+
+struct Bars {
+  uint64_t tfull[kMaxStages], tempty[kMaxStages], scfull[kMaxStages];
+  uint64_t gfull[2], gempty[2];           // staged 4-bit rows
+  uint64_t qfull[kQRing], qfree;
+  uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], done;
+};
+
+// Keys of query t (every position): those up to its own that the table covers.
+__device__ __forceinline__ long long keys_of(const Args& a, int t, int* b_out, unsigned* bad) {
+  if (t >= __ldg(a.cu + a.B)) {
+    *b_out = 0;
+    return 0;
+  }
+  const int b = sequence_of(a.cu, a.B, t);
+  *b_out = b;
+  long long n = static_cast<long long>(__ldg(a.lens + b)) - __ldg(a.cu + b + 1) + t + 1;
+  const long long room = min(static_cast<long long>(a.max_pages) * a.page_size, kMostKeys);
+  if (n > room) {
+    *bad = 1;
+    n = room;
+  }
+  return n < 0 ? 0 : n;
+}
+
+// The line of all blocks: tile w = (query w / groups, heads 64 (w % groups) ..) holds the places
+// tile_begin(w) .. tile_begin(w + 1) - 1, part c the places part_begin(c) .. part_begin(c + 1) - 1.
+struct Line {
+  long long total;
+  int parts;
+};
+__device__ __forceinline__ long long tile_begin(const Args& a, int w) {
+  if (a.nb) return static_cast<long long>(w) * a.nb;
+  const int t = w / a.groups, g = w - t * a.groups;
+  const long long c0 = __ldg(a.cum + t);
+  return c0 * a.groups + (g ? g * (__ldg(a.cum + t + 1) - c0) : 0);
+}
+__device__ __forceinline__ Line line_of(const Args& a) {
+  Line l;
+  l.total = tile_begin(a, a.total_q * a.groups);
+  l.parts = static_cast<int>(min(static_cast<long long>(a.parts), l.total));
+  return l;
+}
+__device__ __forceinline__ long long part_begin(const Line& l, int c) { return l.total * c / l.parts; }
+// The tile that holds place u.
+__device__ __forceinline__ int tile_at(const Args& a, long long u) {
+  if (a.nb) return static_cast<int>(u / a.nb);
+  int lo = 0, hi = a.total_q * a.groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile_begin(a, mid) <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The pieces of a part, in order; every role walks them by itself.
+struct Pieces {
+  long long u, end, t_end;  // the next piece's first place, the part's end, its tile's end
+  int w, t, g, k0, k1, blocks;  // the current piece: blocks k0 .. k1 - 1 of `blocks`
+  __device__ __forceinline__ Pieces(const Args& a, const Line& l, int c) {
+    u = c < l.parts ? part_begin(l, c) : 0;
+    end = c < l.parts ? part_begin(l, c + 1) : 0;
+    w = u < end ? tile_at(a, u) : 0;
+    --w;
+    t_end = u;
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (u >= end) return false;
+    ++w;
+    const long long b = tile_begin(a, w);
+    t_end = tile_begin(a, w + 1);
+    t = w / a.groups;
+    g = w - t * a.groups;
+    blocks = static_cast<int>(t_end - b);
+    k0 = static_cast<int>(u - b);
+    k1 = static_cast<int>(min(end, t_end) - b);
+    u = b + k1;
+    return true;
+  }
+};
+
+// The cache row of key `key` of a tile's query; a.past_row where there is none.
+struct Keys {
+  int b, len;
+  long long n;  // keys (every position)
+  const int32_t* sel;
+  const int32_t* table;
+  __device__ __forceinline__ Keys(const Args& a, int t, bool report) {
+    unsigned bad = 0;
+    if (a.nb) {
+      const bool live = t < __ldg(a.cu + a.B);
+      b = live ? sequence_of(a.cu, a.B, t) : 0;
+      len = live ? __ldg(a.lens + b) : 0;
+      n = a.topk_width;
+      sel = a.topk + static_cast<long long>(t) * a.topk_width;
+    } else {
+      n = keys_of(a, t, &b, &bad);
+      len = 0;
+      sel = nullptr;
+    }
+    if (bad && report) atomicOr(a.status, kStatusUncovered);
+    table = a.block_tables + static_cast<long long>(b) * a.max_pages;
+  }
+  __device__ __forceinline__ int position(const Args& a, int key) const {
+    if (key >= n) return -1;
+    if (!a.nb) return key;
+    const int s = __ldg(sel + key);
+    return s < len ? s : -1;
+  }
+  __device__ __forceinline__ int row(const Args& a, int pos, bool report) const {
+    if (pos < 0) return a.past_row;
+    const int lp = pos / a.page_size;
+    const int page = lp < a.max_pages ? __ldg(table + lp) : -1;
+    if (page < 0 || page >= a.num_pages) {
+      if (report) atomicOr(a.status, kStatusBadPage);
+      return a.past_row;
+    }
+    return page * a.page_size + (pos - lp * a.page_size);
+  }
+};
+
+// D[tmem] (+)= A[tmem] . B[smem]^T, e4m3.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+// Four rows of 128 bytes from column x on, into 512 bytes of a 128-byte swizzled tile.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int x, const int (&y)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+      : "memory");
+}
+
+template <bool FP4>
+__global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
+  using L = Smem<FP4>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((ptx::smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusSmemAlign);
+    return;
+  }
+  uint8_t* misc = smem + L::kOffMisc;
+  Bars* bars = reinterpret_cast<Bars*>(misc);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 512);
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 516);
+  uint64_t* gmask = reinterpret_cast<uint64_t*>(misc + 528);            // [2] rows that a staged block holds
+  uint2* levels = reinterpret_cast<uint2*>(misc + 576);                 // [8] magnitudes of the 4-bit codes
+  float* corr = reinterpret_cast<float*>(misc + 768);                   // [64]
+  float* qscale = reinterpret_cast<float*>(misc + 1024);                // [kQRing][64]
+  float2* sc = reinterpret_cast<float2*>(misc + 2048);                  // [kStages][64] (2^E, E) of the block's rows
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&bars->tfull[s], FP4 ? 4 : 1);
+      ptx::mbar_init(&bars->tempty[s], 1);
+      ptx::mbar_init(&bars->scfull[s], FP4 ? 4 : 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&bars->gfull[s], 1);
+      ptx::mbar_init(&bars->gempty[s], 4);
+      ptx::mbar_init(&bars->sfull[s], 1);
+      ptx::mbar_init(&bars->sempty[s], 4);
+      ptx::mbar_init(&bars->pfull[s], 4);
+      ptx::mbar_init(&bars->pvdone[s], 1);
+    }
+    for (int s = 0; s < kQRing; ++s) ptx::mbar_init(&bars->qfull[s], 4);
+    ptx::mbar_init(&bars->qfree, 1);
+    ptx::mbar_init(&bars->done, 1);
+    *abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (FP4 && threadIdx.x < 8) levels[threadIdx.x] = levels_base(threadIdx.x);
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_holder, 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) ptx::prefetch_tmap(&tmap);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const long long row_id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (row_id >= static_cast<long long>(a.total_q) * a.H) return;
-  const int t = static_cast<int>(row_id / a.H), h = static_cast<int>(row_id % a.H);
-  long long n = 0;  // keys to look at
-  int b = 0, len = 0;
-  if (t < __ldg(a.cu_q_lens + a.B)) {
-    b = sequence_of(a.cu_q_lens, a.B, t);
-    len = __ldg(a.seq_lens + b);
-    n = a.topk ? a.topk_width : static_cast<long long>(len) - __ldg(a.cu_q_lens + b + 1) + t + 1;
-    if (!a.topk) {
-      const long long room = static_cast<long long>(a.max_pages_per_seq) * a.page_size;
-      if (n > room) {
-        if (lane == 0) atomicOr(status, kStatusUncovered);
-        n = room;
+
+  const Line line = line_of(a);
+  const int part = blockIdx.x;
+  Pieces pc(a, line, part);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout); };
+  const uint32_t sbase = ptx::smem_u32(smem);
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ MMAs
+    const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
+    int it = 0, n = 0;  // blocks, pieces
+    bool ok = true;
+    auto qk = [&](int i, int piece) {
+      ok = ok && wait(&bars->qfull[piece % kQRing], (piece / kQRing) & 1) && wait(&bars->tfull[i % kStages], (i / kStages) & 1) &&
+           (i < 2 || wait(&bars->sempty[i & 1], ((i >> 1) & 1) ^ 1));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t d = tmem + kColS + (i & 1) * kKeys, tile = sbase + L::kOffTile + (i % kStages) * kTile;
+        for (int at = 0; at < 4; ++at) {
+          const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
+            mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
+        }
+        const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
+        ptx::mma_commit(&bars->sfull[i & 1]);
+      }
+      __syncwarp();
+    };
+    while (pc.next(a)) {
+      const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
+      const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
+      for (int i = 0; i <= cnt; ++i) {
+        if (i < cnt) {
+          qk(it + i, n);
+          if (i == cnt - 1 && ok && ptx::elect_one()) ptx::mma_commit(&bars->qfree);
+          __syncwarp();
+        }
+        if (i == 0) continue;
+        const int j = it + i - 1;
+        ok = ok && wait(&bars->pfull[j & 1], (j >> 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t tile = sbase + L::kOffTile + (j % kStages) * kTile;
+          const uint64_t bd = ptx::sw128_kmajor_desc(sbase + L::kOffP + (j & 1) * kPBytes);
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t d = tmem + kColO + c * kHeads;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {  // 32 keys per MMA
+              const uint64_t ad = ptx::sw128_mnmajor_desc(tile + c * kAtom + s * 4096, kAtom);
+              ptx::mma_f8(d, ad, bd + 2 * s, id_pv, (i > 1 || s > 0) ? 1u : 0u);
+              ptx::mma_f8(d, ad, bd + 4 + 2 * s, id_pv, 1u);
+            }
+          }
+          ptx::mma_commit(&bars->tempty[j % kStages]);
+          ptx::mma_commit(&bars->pvdone[j & 1]);
+        }
+        __syncwarp();
+      }
+      it += cnt;
+      ++n;
+    }
+    if (ptx::elect_one()) {
+      ptx::mma_commit(&bars->done);
+      ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, 400000000ll);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ rows of the cache
+    int it = 0;
+    bool ok = true;
+    while (ok && pc.next(a)) {
+      const Keys keys(a, pc.t, lane == 0);
+      for (int k = pc.k0; k < pc.k1 && ok; ++k, ++it) {
+        if (!FP4) {
+          int y[4];
+          const int g4 = lane & 15;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = keys.position(a, k * kKeys + 4 * g4 + j);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = keys.row(a, y[j], lane < 16);
+          const int st = it % kStages;
+          ok = it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->tfull[st], kTile);
+          __syncwarp();
+          uint8_t* dst = smem + L::kOffTile + st * kTile + g4 * 512;
+          const int c0 = lane < 16 ? 0 : 3, c1 = lane < 16 ? 3 : 5;
+          for (int c = c0; c < c1; ++c) tma_gather4(dst + c * kAtom, &tmap, &bars->tfull[st], c * 128, y);
+        } else {
+          int y[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) y[j] = keys.position(a, k * kKeys + 32 * j + lane);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) y[j] = keys.row(a, y[j], true);
+          const uint64_t mask = __ballot_sync(0xffffffffu, y[0] != a.past_row) |
+                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, y[1] != a.past_row)) << 32;
+          const int st = it & 1;
+          ok = it < 2 || wait(&bars->gempty[st], ((it >> 1) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            gmask[st] = mask;
+            ptx::mbar_arrive_expect_tx(&bars->gfull[st], __popcll(mask) * kRow4);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (y[j] != a.past_row)
+              ptx::bulk_load(smem + L::kOffStaged + st * kStaged + (32 * j + lane) * kRow4,
+                             a.cache + static_cast<long long>(y[j]) * kRow4, kRow4, &bars->gfull[st]);
+        }
       }
     }
+    // copies in flight land before the CTA can exit, whatever happened
+    constexpr int kBufs = FP4 ? 2 : kStages;
+    for (int i = max(0, it - kBufs); i < it; ++i)
+      ptx::mbar_spin_drain(FP4 ? &bars->gfull[i % kBufs] : &bars->tfull[i % kBufs], (i / kBufs) & 1, a.status, kStatusTimeout, 400000000ll);
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ scales of e4m3 rows
+    int it = 0;
+    bool ok = !FP4;
+    while (ok && pc.next(a)) {
+      const Keys keys(a, pc.t, false);
+      for (int k = pc.k0; k < pc.k1 && ok; ++k, ++it) {
+        int y[2];
+        float u[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) y[j] = keys.position(a, k * kKeys + 32 * j + lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) y[j] = keys.row(a, y[j], false);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          u[j] = y[j] != a.past_row ? __ldg(reinterpret_cast<const float*>(a.cache + static_cast<long long>(y[j]) * kRow8 + kScale8)) : 0.f;
+        const int st = it % kStages;
+        ok = it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          sc[st * kKeys + 32 * j + lane] =
+              make_float2(u[j], u[j] > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u[j]) >> 23) - 127) : -INFINITY);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->scfull[st]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ queries; tiles of 4-bit rows
+    const int row = threadIdx.x - 128, plane = lane >> 4, hl = (warp - 4) * 16 + (lane & 15);
+    const uint32_t lane_addr = static_cast<uint32_t>((warp - 4) * 32) << 16;
+    uint8_t* qrow = smem + L::kOffQr + row * 128;
+    if (plane) {  // the lo rows take no part in the rotary product
+#pragma unroll
+      for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(qrow)[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    int it = 0, n = 0;
+    bool ok = true;
+    while (ok && pc.next(a)) {
+      const int h = pc.g * kHeads + hl;
+      const bool live = h < a.H;
+      const uint4* src = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live ? h : 0) * a.qn_h) + plane * 32;
+      const uint4* srr = reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + (live ? h : 0) * a.qr_h);
+      // the power of two that takes the row's largest value to [128, 256)
+      float amax = 0.f;
+      uint4 rp[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) rp[c] = live ? __ldg(srr + plane * 4 + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 8
+      for (int c = 0; c < 32; ++c) {
+        float x[8];
+        unpack_bf16(live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x[8];
+        unpack_bf16(rp[c], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+      const int e = amax > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127))) : 0;
+      const float f = pow2f(e);
+      if (n > 0) {
+        ok = wait(&bars->qfree, (n - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      ptx::tc_fence_after();
+      {
+        // both planes' lanes write the rotary row of the hi plane, half each
+        uint8_t* dst = smem + L::kOffQr + (row - 16 * plane) * 128;
+        const int sw = (row - 16 * plane) & 7;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x[8];
+          unpack_bf16(rp[c], x);
+          *reinterpret_cast<uint4*>(dst + (((plane * 4 + c) ^ sw) << 4)) =
+              make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f), pack_bf16(x[4] * f, x[5] * f),
+                         pack_bf16(x[6] * f, x[7] * f));
+        }
+      }
+      // this lane's half of the row, 128 values at a time: its own plane's codes stay, the other's go to the
+      // lane of that plane
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        uint32_t lowc[32], highc[32];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x[8];
+          unpack_bf16(live ? __ldg(src + 16 * j + c) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float v0 = x[4 * i] * f, v1 = x[4 * i + 1] * f, v2 = x[4 * i + 2] * f, v3 = x[4 * i + 3] * f;
+            const uint32_t h01 = e4m3x2(v0, v1), h23 = e4m3x2(v2, v3);
+            const float2 b01 = from_e4m3x2(h01), b23 = from_e4m3x2(h23);
+            const uint32_t hi = h01 | (h23 << 16), lo = e4m3x2(v0 - b01.x, v1 - b01.y) | (e4m3x2(v2 - b23.x, v3 - b23.y) << 16);
+            const uint32_t keep = plane ? lo : hi, got = __shfl_xor_sync(0xffffffffu, plane ? hi : lo, 16);
+            lowc[2 * c + i] = plane ? got : keep;
+            highc[2 * c + i] = plane ? keep : got;
+          }
+        }
+        ptx::tmem_st_32x32b_x32(tmem + lane_addr + kColQ + 32 * j, lowc);
+        ptx::tmem_st_32x32b_x32(tmem + lane_addr + kColQ + 64 + 32 * j, highc);
+      }
+      ptx::tmem_st_wait();
+      if (!plane) qscale[(n % kQRing) * kHeads + hl] = a.scale_log2 * pow2f(-e);
+      ptx::tc_fence_before();
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars->qfull[n % kQRing]);
+      ++n;
+      if (!FP4) continue;
+      // 4-bit rows: a warp takes 16 rows of a block, a lane a block of 16 values
+      for (int k = pc.k0; k < pc.k1; ++k, ++it) {
+        const int st = it % kStages, gs = it & 1;
+        ok = wait(&bars->gfull[gs], (it >> 1) & 1) && (it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint64_t mask = gmask[gs];
+        const uint8_t* rows = smem + L::kOffStaged + gs * kStaged;
+        uint8_t* tile = smem + L::kOffTile + st * kTile;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int key = (warp - 4) * 16 + i;
+          const bool there = (mask >> key) & 1;
+          uint2 w = make_uint2(0u, 0u);
+          int byte = 0;
+          if (there) {
+            w = reinterpret_cast<const uint2*>(rows + key * kRow4)[lane];
+            byte = rows[key * kRow4 + kScale4 + lane];
+          }
+          const int E = static_cast<int>(__ballot_sync(0xffffffffu, byte >> 7) & 0xFFu) - 128;
+          const uint2 lv = levels_at(levels[byte & 7], byte & 127);
+          const uint2 c0 = codes4_to_e4m3(w.x, lv), c1 = codes4_to_e4m3(w.y, lv);
+          *reinterpret_cast<uint4*>(tile + (lane >> 3) * kAtom + key * 128 + (((lane & 7) ^ (key & 7)) << 4)) =
+              make_uint4(c0.x, c0.y, c1.x, c1.y);
+          if (lane == 0) sc[st * kKeys + key] = there ? make_float2(pow2f(E), static_cast<float>(E)) : make_float2(0.f, -INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (warp - 4) * 16 + 4 * i + (lane >> 3), c = lane & 7;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if ((mask >> key) & 1) v = reinterpret_cast<const uint4*>(rows + key * kRow4 + kRope4)[c];
+          *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((c ^ (key & 7)) << 4)) = v;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&bars->gempty[gs]);
+          ptx::mbar_arrive(&bars->scfull[st]);
+          ptx::mbar_arrive(&bars->tfull[st]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax, rescale, output (warps 0..3)
+    const int half = lane >> 4, hl = warp * 16 + (lane & 15);
+    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    int it = 0, n = 0;
+    bool ok = true;
+    // Every iteration runs its named barriers whatever happened, so that a wait that gave up leaves no warp
+    // behind at one.
+    while (pc.next(a)) {
+      const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
+      float m = -INFINITY, l = 0.f, qs = 0.f;
+      if (ok) ok = __all_sync(0xffffffffu, wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) != 0;
+      if (ok) qs = qscale[(n % kQRing) * kHeads + hl];
+      for (int i = 0; i < cnt; ++i, ++it) {
+        const int st = it % kStages;
+        float cr = 1.f;
+        float x[32];
+        if (ok) ok = __all_sync(0xffffffffu, wait(&bars->sfull[it & 1], (it >> 1) & 1) && wait(&bars->scfull[st], (it / kStages) & 1)) != 0;
+        if (ok) {
+          ptx::tc_fence_after();
+          uint32_t s0[32], s1[32];
+          ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + (it & 1) * kKeys, s0);
+          ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + (it & 1) * kKeys + 32, s1);
+          ptx::tmem_ld_wait_regs(s0);
+          ptx::tmem_ld_wait_regs(s1);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[it & 1]);
+          // the hi lane takes keys 0..31, the lo lane 32..63
+          const float4* scp = reinterpret_cast<const float4*>(sc + st * kKeys + half * 32);
+          float mb = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t mine = half ? s1[j] : s0[j], send = half ? s0[j] : s1[j];
+            x[j] = (__uint_as_float(mine) + __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16))) * qs;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 v = scp[j];
+            x[2 * j] = fmaf(x[2 * j], v.x, v.y);
+            x[2 * j + 1] = fmaf(x[2 * j + 1], v.z, v.w);
+            mb = fmaxf(mb, fmaxf(x[2 * j], x[2 * j + 1]));
+          }
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
+          // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
+          float mn = m;
+          if (m == -INFINITY || mb > m + kMove) mn = mb;
+          cr = m == -INFINITY ? 1.f : ptx::ex2(m - mn);
+          m = mn;
+          l *= cr;
+          if (!half) corr[hl] = cr;
+        }
+        // does any head's output need rescaling?
+        uint32_t any;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.f32 q, %1, 0f3F800000;\n\t"
+                     "bar.red.or.pred p, 2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(any) : "f"(hl < hg ? cr : 1.f) : "memory");
+        if (any) {
+          if (ok && i > 0) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1)) != 0;
+          if (ok && i > 0) {
+            ptx::tc_fence_after();
+            for (int c = 0; c < 4; ++c) {
+              for (int h0 = 0; h0 < hg; h0 += 32) {
+                const uint32_t col = tmem + lane_addr + kColO + c * kHeads + h0;
+                uint32_t r[32];
+                ptx::tmem_ld_32x32b_x32(col, r);
+                ptx::tmem_ld_wait_regs(r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * corr[h0 + j]);
+                ptx::tmem_st_32x32b_x32(col, r);
+              }
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+          }
+          ptx::named_bar_sync(2, 128);  // corr is read before the next block rewrites it
+        }
+        if (ok) {
+          const float ref = m == -INFINITY ? 0.f : m - kPShift;
+          const uint2* scu = reinterpret_cast<const uint2*>(sc + st * kKeys + half * 32);
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float p[4], r[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              p[q] = ptx::ex2(x[4 * j + q] - ref);
+              l = fmaf(p[q], __uint_as_float(0x7F000000u - scu[4 * j + q].x), l);  // p 2^-E
+              r[q] = __uint_as_float((__float_as_uint(p[q]) + 0x80000u) & 0xFFF00000u);  // 4 significant bits
+            }
+            hi[j] = e4m3x2(r[0], r[1]) | (e4m3x2(r[2], r[3]) << 16);
+            lo[j] = e4m3x2(p[0] - r[0], p[1] - r[1]) | (e4m3x2(p[2] - r[2], p[3] - r[3]) << 16);
+          }
+          // P's buffer is free once the products before the last have been done
+          if (it > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[it & 1], ((it >> 1) & 1) ^ 1)) != 0;
+          if (ok) {
+            uint8_t* prow = smem + L::kOffP + (it & 1) * kPBytes + hl * 128;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int ch = half * 2 + c;
+              *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+              *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->pfull[it & 1]);
+          }
+        }
+      }
+      ++n;
+      // the piece's output
+      if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1)) != 0;
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const bool whole = pc.k0 == 0 && pc.k1 == pc.blocks;
+      const int slot = 2 * part + (pc.k0 == 0 ? 1 : 0);
+      if (!half) {
+        corr[hl] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        if (hl < hg && ok) {
+          if (!whole) {
+            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = m;
+            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = l;
+          } else if (a.lse) {
+            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+          }
+        }
+      }
+      ptx::named_bar_sync(2, 128);
+      if (ok) {
+        ptx::tc_fence_after();
+        for (int c = 0; c < 4; ++c) {
+          const int lat = warp * 32 + lane;
+          for (int h0 = 0; h0 < hg; h0 += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColO + c * kHeads + h0, r);
+            ptx::tmem_ld_wait_regs(r);
+            if (whole) {
+              // pairs of lanes swap, so that each stores two latent values of one head
+              uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128) + (lat >> 1);
+              const bool odd = lane & 1;
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float v0 = __uint_as_float(r[j]) * corr[h0 + j], v1 = __uint_as_float(r[j + 1]) * corr[h0 + j + 1];
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                if (h0 + j + odd < hg) o[(j + odd) * (kRank / 2)] = odd ? pack_bf16(other, v1) : pack_bf16(v0, other);
+              }
+            } else {
+              float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (h0 + 4 * j < hg)
+                  o[j * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                           __uint_as_float(r[4 * j + 3]));
+            }
+          }
+        }
+        ptx::tc_fence_before();
+      }
+      ptx::named_bar_sync(2, 128);  // corr is read before the next piece rewrites it
+    }
   }
-  const __nv_bfloat16* qn = static_cast<const __nv_bfloat16*>(a.q_nope) + t * a.qn_stride_t + h * a.qn_stride_h + 16 * lane;
-  const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_stride_t + h * a.qr_stride_h + 2 * lane;
-  float q[18], o[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) q[i] = __bfloat162float(qn[i]), o[i] = 0.f;
-  q[16] = __bfloat162float(qr[0]), q[17] = __bfloat162float(qr[1]);
-  const uint8_t* cache = static_cast<const uint8_t*>(a.cache);
-  const float f = a.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.f;
-  for (long long j = 0; j < n; ++j) {
-    const long long s = a.topk ? __ldg(a.topk + static_cast<long long>(t) * a.topk_width + j) : j;
-    if (s < 0 || s >= len) continue;
-    const long long lp = s / a.page_size;
-    const int page = lp < a.max_pages_per_seq ? __ldg(a.block_tables + static_cast<long long>(b) * a.max_pages_per_seq + lp) : -1;
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) atomicOr(status, kStatusBadPage);
-      continue;
-    }
-    const uint8_t* row = cache + (static_cast<long long>(page) * a.page_size + s % a.page_size) * kRow;
-    uint2 c01, c23;
-    float scale;
-    if (FP4) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-      const int byte = __ldg(row + kScale4 + lane);
-      scale = pow2f(static_cast<int>(__ballot_sync(0xffffffffu, byte >> 7) & 0xFFu) - 128);
-      const uint2 lv = levels_at(levels_base(byte & 7), byte & 127);
-      c01 = codes4_to_e4m3(w.x, lv);
-      c23 = codes4_to_e4m3(w.y, lv);
-    } else {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(row) + lane);
-      c01 = make_uint2(w.x, w.y);
-      c23 = make_uint2(w.z, w.w);
-      scale = __ldg(reinterpret_cast<const float*>(row + kScale8));
-    }
-    float v[16];
-    const uint32_t cw[4] = {c01.x, c01.y, c23.x, c23.y};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 p = from_e4m3x2((cw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-      v[2 * i] = p.x, v[2 * i + 1] = p.y;
-    }
-    const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(row + (FP4 ? kRope4 : kRope8)) + lane);
-    float dot = q[16] * __uint_as_float(r << 16) + q[17] * __uint_as_float(r & 0xFFFF0000u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dot = fmaf(q[i], v[i], dot);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
-    const float x = dot * scale * f, mn = fmaxf(m, x);
-    const float old = exp2f(m - mn), p = exp2f(x - mn);
-    m = mn;
-    l = l * old + p;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = o[i] * old + p * scale * v[i];
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_id * kRank + 16 * lane);
+}
+
+// out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) L_j over the pieces of a tile, in their order.  Block (c - 1, y): the
+// tile that part c begins inside, if no earlier part does; y: four heads, a latent chunk.
+__global__ void __launch_bounds__(128) quant_join_kernel(const Args a) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const Line line = line_of(a);
+  const int c = blockIdx.x + 1, quad = blockIdx.y & 15, chunk = blockIdx.y >> 4;
+  if (c >= line.parts) return;
+  const long long u = part_begin(line, c);
+  const int w = tile_at(a, u);
+  const long long b = tile_begin(a, w), e = tile_begin(a, w + 1);
+  if (b == u || part_begin(line, c - 1) > b) return;
+  const int t = w / a.groups, g = w - t * a.groups, h0 = g * kHeads + quad * 4;
+  if (h0 >= a.H) return;
+  int last = c;
+  while (last + 1 < line.parts && part_begin(line, last + 1) < e) ++last;
+  float M[4], W[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    out[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                        pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-  if (lane == 0 && a.lse) a.lse[row_id] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  for (int i = 0; i < 4; ++i) M[i] = -INFINITY;
+  for (int j = c - 1; j <= last; ++j) {
+    const float* ml = a.part_ml + (static_cast<long long>(2 * j + (j == c - 1 ? 1 : 0)) * kHeads + quad * 4) * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h0 + i < a.H) M[i] = fmaxf(M[i], ml[2 * i]);
+  }
+  for (int j = c - 1; j <= last; ++j) {
+    const long long slot = 2 * j + (j == c - 1 ? 1 : 0);
+    const float* ml = a.part_ml + (slot * kHeads + quad * 4) * 2;
+    const float4 o = reinterpret_cast<const float4*>(a.part_o)[((slot * 4 + chunk) * 16 + quad) * 128 + threadIdx.x];
+    const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (h0 + i >= a.H) continue;
+      const float mj = ml[2 * i];
+      if (mj == -INFINITY) continue;
+      const float f = exp2f(mj - M[i]);
+      W[i] += f * ml[2 * i + 1];
+      acc[i] += f * v[i];
+    }
+  }
+  const long long row = static_cast<long long>(t) * a.H + h0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (h0 + i >= a.H) continue;
+    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : acc[i] / W[i]);
+    if (chunk == 0 && threadIdx.x == i && a.lse) a.lse[row + i] = W[i] == 0.f ? -INFINITY : (M[i] - kPShift + log2f(W[i])) * kLn2;
+  }
+}
+
+// Blocks before each query (every position): at least one a query, so that each has a tile that writes it.
+__global__ void __launch_bounds__(1024) quant_plan_kernel(const Args a, long long* cum) {
+  __shared__ long long sums[32];
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long before = 0;
+  for (int t0 = 0; t0 < a.total_q; t0 += 1024) {
+    const int t = t0 + threadIdx.x;
+    long long v = 0;
+    if (t < a.total_q) {
+      int b;
+      unsigned bad = 0;
+      v = max(1ll, (keys_of(a, t, &b, &bad) + kKeys - 1) / kKeys);
+    }
+    long long s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    long long w = sums[lane], add = 0;
+    for (int i = 0; i < 32; ++i) {
+      const long long x = __shfl_sync(0xffffffffu, w, i);
+      if (i < warp) add += x;
+    }
+    if (t < a.total_q) cum[t] = before + add + s - v;
+    long long total = 0;
+    for (int i = 0; i < 32; ++i) total += __shfl_sync(0xffffffffu, w, i);
+    before += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[a.total_q] = before;
 }
 
 dsa_status validate(const dsa_quant_mla_args* a) {
@@ -117,6 +820,37 @@ dsa_status validate(const dsa_quant_mla_args* a) {
   return DSA_OK;
 }
 
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return n > 0 ? n : 148;
+}
+
+struct Plan {
+  int groups, nb, parts;
+  size_t off_ml, off_cum, total;
+};
+Plan plan_of(const dsa_quant_mla_args* a) {
+  Plan p{};
+  p.groups = (a->H + kHeads - 1) / kHeads;
+  p.nb = (a->topk_width + kKeys - 1) / kKeys;
+  long long parts = sm_count();
+  if (p.nb) parts = std::min<long long>(parts, static_cast<long long>(a->total_q) * p.groups * p.nb);
+  p.parts = static_cast<int>(std::max<long long>(1, parts));
+  p.off_ml = static_cast<size_t>(2) * p.parts * kHeads * kRank * 4;
+  p.off_cum = p.off_ml + static_cast<size_t>(2) * p.parts * kHeads * 2 * 4;
+  p.total = p.off_cum + (p.nb ? 0 : (static_cast<size_t>(a->total_q) + 1) * 8);
+  return p;
+}
+
+template <bool FP4>
+cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(quant_mla_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(quant_mla_kernel<FP4>, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, s, map, k);
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -128,7 +862,7 @@ dsa_status dsa_quant_mla_workspace_size(const dsa_quant_mla_args* a, size_t* byt
   if (!bytes) return DSA_ERR_INVALID_ARGUMENT;
   const dsa_status st = validate(a);
   if (st != DSA_OK) return st;
-  *bytes = 16;
+  *bytes = plan_of(a).total;
   return DSA_OK;
 }
 
@@ -147,15 +881,57 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   if (!al(a->q_nope, 16) || !al(a->q_rope, 16) || !al(a->cache, 16) || !al(a->out, 16) || !al(a->lse, 4) ||
       !al(a->block_tables, 4) || !al(a->cu_q_lens, 4) || !al(a->seq_lens, 4) || !al(a->topk, 4))
     return DSA_ERR_INVALID_ARGUMENT;
-  size_t need = 0;
-  dsa_quant_mla_workspace_size(a, &need);
-  if (!a->workspace || a->workspace_bytes < need || !al(a->workspace, 16)) return DSA_ERR_WORKSPACE;
+  const Plan p = plan_of(a);
+  if (!a->workspace || a->workspace_bytes < p.total || !al(a->workspace, 16)) return DSA_ERR_WORKSPACE;
   unsigned* status = device_status_ptr();
   if (!status) return DSA_ERR_CUDA;
-  const long long rows = static_cast<long long>(a->total_q) * a->H;
-  const unsigned blocks = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  auto* kern = a->format == DSA_FP4_E2M1 ? quant_mla_kernel<true> : quant_mla_kernel<false>;
-  const cudaError_t e = launch_pdl(kern, dim3(blocks), dim3(kWarps * 32), 0, reinterpret_cast<cudaStream_t>(stream), *a, status);
+  Args k{};
+  k.B = a->B;
+  k.total_q = a->total_q;
+  k.H = a->H;
+  k.groups = p.groups;
+  k.page_size = a->page_size;
+  k.num_pages = a->num_pages;
+  k.max_pages = a->max_pages_per_seq;
+  k.topk_width = a->topk_width;
+  k.nb = p.nb;
+  k.parts = p.parts;
+  k.past_row = std::max(1, a->num_pages * a->page_size);
+  k.scale_log2 = a->scale * 1.4426950408889634f;
+  k.qn = static_cast<const __nv_bfloat16*>(a->q_nope);
+  k.qr = static_cast<const __nv_bfloat16*>(a->q_rope);
+  k.qn_t = a->qn_stride_t;
+  k.qn_h = a->qn_stride_h;
+  k.qr_t = a->qr_stride_t;
+  k.qr_h = a->qr_stride_h;
+  k.cache = static_cast<const uint8_t*>(a->cache);
+  k.block_tables = a->block_tables;
+  k.cu = a->cu_q_lens;
+  k.lens = a->seq_lens;
+  k.topk = a->topk;
+  k.out = static_cast<__nv_bfloat16*>(a->out);
+  k.lse = a->lse;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  k.part_o = reinterpret_cast<float*>(ws);
+  k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
+  k.status = status;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!p.nb) {
+    long long* cum = reinterpret_cast<long long*>(ws + p.off_cum);
+    e = launch_pdl(quant_plan_kernel, dim3(1), dim3(1024), 0, s, k, cum);
+    if (e != cudaSuccess) return DSA_ERR_CUDA;
+    k.cum = cum;
+  }
+  CUtensorMap map{};
+  if (a->format == DSA_FP8_E4M3) {
+    if (!make_gather_map(&map, a->cache ? a->cache : a->q_nope, quant::kRow8, k.past_row)) return DSA_ERR_CUDA;
+    e = launch_attend<false>(map, k, s);
+  } else {
+    e = launch_attend<true>(map, k, s);
+  }
+  if (e != cudaSuccess) return DSA_ERR_CUDA;
+  if (p.parts > 1) e = launch_pdl(quant_join_kernel, dim3(p.parts - 1, 64), dim3(128), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
