@@ -141,8 +141,9 @@ cudaError_t launch_topk(const TopkArgs& a, int max_row_len, cudaStream_t st);
 unsigned* device_status_ptr();  // address of the status word on the current device
 // Tensor map of a row-major [rows, D] bf16 or e4m3 operand, 128-byte swizzled boxes of {128 bytes, box_rows}.
 bool make_map_2d(CUtensorMap* m, const void* base, bool fp8, int D, long long rows, int box_rows);
-// Tensor map of rows of `row_bytes` bytes for gathering copies of 128 bytes of four rows (box one row high).
-bool make_gather_map(CUtensorMap* m, const void* base, int row_bytes, long long rows);
+// Tensor map of rows of `row_bytes` bytes for gathering copies of four rows (box one row high): whole rows one
+// behind the other, or 128 bytes of each, 128-byte swizzled.
+bool make_gather_map(CUtensorMap* m, const void* base, bool whole, int row_bytes, long long rows);
 
 // Sequence of query row t: the last b < B with cu[b] <= t.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {

@@ -18,14 +18,15 @@
 // in one line, cut into equal parts, one per CTA: a part may start and end inside a tile.  A tile done in one
 // piece is normalised and written, the pieces of the others leave (O, m', L) in fp32 and a second kernel joins them.
 // Roles of a CTA:
-//   warps 0..3  softmax.  Rows of S alternate between 16 hi and 16 lo rows, so that a lane and the one 16 further
-//               hold a head's two planes; each adds the planes for half of the block's keys;
-//   warps 4..7  query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
-//               4-bit rows also: codes from the staged rows to e4m3 tiles;
-//   warp 8      rows of the cache: e4m3 tiles by gathering TMA (4 rows x 128 bytes), 4-bit rows by bulk copies;
-//   warp 9      TMEM, MMAs:  S [128 x 64 keys] = Q (TMEM) . K^T,  O^T [512 x heads] += V^T (the same tile,
-//               MN-major) . P^T;
-//   warp 10     e4m3: the rows' scales.
+//   warps 0..7    softmax, two groups that take alternate blocks and hand the reference on.  Rows of S alternate
+//                 between 16 hi and 16 lo rows, so that a lane and the one 16 further hold a head's two planes;
+//                 each adds the planes for half of the block's keys;
+//   warps 8..11   query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
+//                 4-bit rows also: codes from the staged rows to e4m3 tiles;
+//   warps 12, 15  rows of the cache by gathering TMA: e4m3 tiles in 128-byte columns, 4-bit rows whole;
+//   warp 13       TMEM, MMAs:  S [128 x 64 keys] = Q (TMEM) . K^T,  O^T [512 x heads] += V^T (the same tile,
+//                 MN-major) . P^T;
+//   warp 14       where the rows lie, four blocks at a time; e4m3: their scales.
 // Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
 // (bounded) and TMEM is freed.
 #include <cuda_runtime.h>
@@ -43,30 +44,37 @@ using namespace quant;
 
 constexpr int kHeads = 64;                                // heads per tile
 constexpr int kKeys = 64;                                 // keys per block
-constexpr int kThreads = 352;
+constexpr int kThreads = 512;
 constexpr uint32_t kAtom = kKeys * 128;                   // 64 rows of 128 bytes
 constexpr uint32_t kTile = 5 * kAtom;                     // 4 columns of 128 codes, one of 64 bf16
 constexpr uint32_t kStaged = kKeys * kRow4;               // a block of 4-bit rows
 constexpr uint32_t kQRope = 128 * 128, kPBytes = kHeads * 128;
+constexpr uint32_t kQStride = 80, kQBuf = 4 * 32 * kQStride;  // 64 codes of 32 query rows a warp, 16 bytes apart further
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // TMEM columns
 constexpr int kPShift = 5;                                // p = 2^5 at the reference maximum
 constexpr float kMove = 3.f;                              // the reference moves when passed by more: p <= 2^8
+constexpr int kLoShift = 4;                               // lo = 2^4 (x - hi): below 2^4 of its step it is exact, and 2^7 at most
+constexpr int kExpRef = -7;                               // E of normalised rows: x' counts from there, so that it does not lose x's bits
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxStages = 4;
 constexpr long long kMostKeys = 0x7FFFFF00ll;             // that a query sees: a block's last key fits 32 bits
+constexpr int kMaxStages = 4;
 constexpr int kQRing = 4;                                 // scales of the queries of consecutive pieces
+constexpr int kBatch = 4, kBatches = 4, kRing = kBatch * kBatches;  // blocks whose rows are looked up together
 
 template <bool FP4>
 struct Smem {
   static constexpr int kStages = FP4 ? 3 : 4;             // tiles
   static constexpr int kStagedBufs = FP4 ? 2 : 0;
+  static constexpr int kScRing = FP4 ? kStages : kRing;   // blocks whose scales are held
   static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
-  static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffMisc = kOffStaged + kStagedBufs * kStaged;
-  static constexpr uint32_t kBytes = kOffMisc + 6 * 1024;
+  static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffQ = kOffStaged + kStagedBufs * kStaged;
+  static constexpr uint32_t kOffMisc = kOffQ + kQBuf, kOffRows = kOffMisc + 4096, kOffSc = kOffRows + kRing * kKeys * 4;
+  static constexpr uint32_t kBytes = kOffSc + kScRing * kKeys * 8;
 };
+static_assert(Smem<false>::kBytes <= 232448 && Smem<true>::kBytes <= 232448, "shared memory of a CTA");
 
 struct Args {
-  int B, total_q, H, groups, page_size, num_pages, max_pages, topk_width;
+  int B, total_q, H, groups, page_size, page_log2, num_pages, max_pages, topk_width;
   int nb;                  // blocks of a tile (selected keys); 0: from the plan
   int parts;               // CTAs
   int past_row;            // a row past the cache: copies from there are zeros
@@ -83,10 +91,12 @@ struct Args {
 };
 
 struct Bars {
-  uint64_t tfull[kMaxStages], tempty[kMaxStages], scfull[kMaxStages];
+  uint64_t tfull[kMaxStages], tempty[kMaxStages];
+  uint64_t rfull[kBatches], bempty[kBatches], scfull[kBatches];
   uint64_t gfull[2], gempty[2];           // staged 4-bit rows
   uint64_t qfull[kQRing], qfree;
-  uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], done;
+  uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], odrained, done;
+  uint64_t hand0[4], hand1[4];            // the reference after a block of group 0, 1, to the other group's warp
 };
 
 // Keys of query t (every position): those up to its own that the table covers.
@@ -162,7 +172,7 @@ struct Pieces {
   }
 };
 
-// The cache row of key `key` of a tile's query; a.past_row where there is none.
+// The keys of a query: the position of each, -1 where there is none.
 struct Keys {
   int b, len;
   long long n;  // keys (every position)
@@ -190,17 +200,18 @@ struct Keys {
     const int s = __ldg(sel + key);
     return s < len ? s : -1;
   }
-  __device__ __forceinline__ int row(const Args& a, int pos, bool report) const {
-    if (pos < 0) return a.past_row;
-    const int lp = pos / a.page_size;
-    const int page = lp < a.max_pages ? __ldg(table + lp) : -1;
-    if (page < 0 || page >= a.num_pages) {
-      if (report) atomicOr(a.status, kStatusBadPage);
-      return a.past_row;
-    }
-    return page * a.page_size + (pos - lp * a.page_size);
-  }
 };
+// The cache row of a position, through a request's table; a.past_row where there is none.
+__device__ __forceinline__ int row_of(const Args& a, const int32_t* table, int pos) {
+  if (pos < 0) return a.past_row;
+  const int lp = a.page_log2 >= 0 ? pos >> a.page_log2 : pos / a.page_size;
+  const int page = lp < a.max_pages ? __ldg(table + lp) : -1;
+  if (page < 0 || page >= a.num_pages) {
+    atomicOr(a.status, kStatusBadPage);
+    return a.past_row;
+  }
+  return page * a.page_size + (pos - lp * a.page_size);
+}
 
 // D[tmem] (+)= A[tmem] . B[smem]^T, e4m3.
 __device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -219,6 +230,15 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// 64 codes of 32 rows: thread i writes 16 columns of lane (base + i).
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 template <bool FP4>
 __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
   using L = Smem<FP4>;
@@ -233,37 +253,49 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   Bars* bars = reinterpret_cast<Bars*>(misc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 512);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 516);
-  uint64_t* gmask = reinterpret_cast<uint64_t*>(misc + 528);            // [2] rows that a staged block holds
   uint2* levels = reinterpret_cast<uint2*>(misc + 576);                 // [8] magnitudes of the 4-bit codes
-  float* corr = reinterpret_cast<float*>(misc + 768);                   // [64]
-  float* qscale = reinterpret_cast<float*>(misc + 1024);                // [kQRing][64]
-  float2* sc = reinterpret_cast<float2*>(misc + 2048);                  // [kStages][64] (2^E, E) of the block's rows
+  float* linv = reinterpret_cast<float*>(misc + 768);                   // [64] of the piece that is written
+  float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] each group's
+  float* refv = reinterpret_cast<float*>(misc + 1536);                  // [2][64] the reference after its last block
+  float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
+  float* qscale = reinterpret_cast<float*>(misc + 3072);                // [kQRing][64]
+  int* rows = reinterpret_cast<int*>(smem + L::kOffRows);               // [kRing][64] rows of a block's keys
+  float2* sc = reinterpret_cast<float2*>(smem + L::kOffSc);             // [kScRing][64] (2^E, E - kExpRef) of them
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&bars->tfull[s], FP4 ? 4 : 1);
+      ptx::mbar_init(&bars->tfull[s], FP4 ? 4 : 2);
       ptx::mbar_init(&bars->tempty[s], 1);
+    }
+    for (int s = 0; s < kBatches; ++s) {
+      ptx::mbar_init(&bars->rfull[s], 1);
+      ptx::mbar_init(&bars->bempty[s], FP4 ? 2 + 4 : 2 + 8);  // the copying warps; who reads validity or scales
       ptx::mbar_init(&bars->scfull[s], FP4 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&bars->gfull[s], 1);
+      ptx::mbar_init(&bars->gfull[s], 2);
       ptx::mbar_init(&bars->gempty[s], 4);
       ptx::mbar_init(&bars->sfull[s], 1);
       ptx::mbar_init(&bars->sempty[s], 4);
       ptx::mbar_init(&bars->pfull[s], 4);
       ptx::mbar_init(&bars->pvdone[s], 1);
     }
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(&bars->hand0[s], 1);
+      ptx::mbar_init(&bars->hand1[s], 1);
+    }
     for (int s = 0; s < kQRing; ++s) ptx::mbar_init(&bars->qfull[s], 4);
     ptx::mbar_init(&bars->qfree, 1);
+    ptx::mbar_init(&bars->odrained, 8);
     ptx::mbar_init(&bars->done, 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
   if (FP4 && threadIdx.x < 8) levels[threadIdx.x] = levels_base(threadIdx.x);
-  if (warp == 9) {
+  if (warp == 13) {
     ptx::tmem_alloc(tmem_holder, 512);
     ptx::tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) ptx::prefetch_tmap(&tmap);
+  if (warp == 12 && lane == 0) ptx::prefetch_tmap(&tmap);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -277,50 +309,50 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout); };
   const uint32_t sbase = ptx::smem_u32(smem);
 
-  if (warp == 9) {
+  if (warp == 13) {
     // ------------------------------------------------------------ MMAs
     const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
     int it = 0, n = 0;  // blocks, pieces
     bool ok = true;
-    auto qk = [&](int i, int piece) {
-      ok = ok && wait(&bars->qfull[piece % kQRing], (piece / kQRing) & 1) && wait(&bars->tfull[i % kStages], (i / kStages) & 1) &&
-           (i < 2 || wait(&bars->sempty[i & 1], ((i >> 1) & 1) ^ 1));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint32_t d = tmem + kColS + (i & 1) * kKeys, tile = sbase + L::kOffTile + (i % kStages) * kTile;
-        for (int at = 0; at < 4; ++at) {
-          const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
-#pragma unroll
-          for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
-            mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
-        }
-        const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
-        ptx::mma_commit(&bars->sfull[i & 1]);
-      }
-      __syncwarp();
-    };
     while (pc.next(a)) {
       const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
       const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
       for (int i = 0; i <= cnt; ++i) {
-        if (i < cnt) {
-          qk(it + i, n);
-          if (i == cnt - 1 && ok && ptx::elect_one()) ptx::mma_commit(&bars->qfree);
-          __syncwarp();
+        if (i < cnt) {  // S of block i
+          const int b = it + i;
+          ok = ok && (i > 0 || wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) && wait(&bars->tfull[b % kStages], (b / kStages) & 1) &&
+               (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              const uint32_t d = tmem + kColS + (b & 1) * kKeys, tile = sbase + L::kOffTile + (b % kStages) * kTile;
+#pragma unroll
+              for (int at = 0; at < 4; ++at) {
+                const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
+                  mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
+              }
+              const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
+#pragma unroll
+              for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
+              ptx::mma_commit(&bars->sfull[b & 1]);
+              if (i == cnt - 1) ptx::mma_commit(&bars->qfree);
+            }
+            __syncwarp();
+          }
         }
         if (i == 0) continue;
-        const int j = it + i - 1;
-        ok = ok && wait(&bars->pfull[j & 1], (j >> 1) & 1);
+        const int b = it + i - 1;  // P . V of the block before
+        ok = ok && wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 1 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint32_t tile = sbase + L::kOffTile + (j % kStages) * kTile;
-          const uint64_t bd = ptx::sw128_kmajor_desc(sbase + L::kOffP + (j & 1) * kPBytes);
+          const uint32_t tile = sbase + L::kOffTile + (b % kStages) * kTile;
+          const uint64_t bd = ptx::sw128_kmajor_desc(sbase + L::kOffP + (b & 1) * kPBytes);
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t d = tmem + kColO + c * kHeads;
 #pragma unroll
@@ -330,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               ptx::mma_f8(d, ad, bd + 4 + 2 * s, id_pv, 1u);
             }
           }
-          ptx::mma_commit(&bars->tempty[j % kStages]);
-          ptx::mma_commit(&bars->pvdone[j & 1]);
+          ptx::mma_commit(&bars->tempty[b % kStages]);
+          ptx::mma_commit(&bars->pvdone[b & 1]);
         }
         __syncwarp();
       }
@@ -343,313 +375,381 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, 400000000ll);
     }
     __syncwarp();
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ rows of the cache
+  } else if (warp == 12 || warp == 15) {
+    // ------------------------------------------------------------ rows of the cache, half of each block
+    const int first = warp == 12 ? 0 : 8;  // groups of four rows
+    constexpr int kBufs = FP4 ? 2 : kStages;
     int it = 0;
     bool ok = true;
     while (ok && pc.next(a)) {
-      const Keys keys(a, pc.t, lane == 0);
-      for (int k = pc.k0; k < pc.k1 && ok; ++k, ++it) {
-        if (!FP4) {
-          int y[4];
-          const int g4 = lane & 15;
+      for (int k = pc.k0; k < pc.k1; ++k, ++it) {
+        const int bt = (it / kBatch) % kBatches, st = it % kBufs;
+        uint64_t* full = FP4 ? &bars->gfull[st] : &bars->tfull[st];
+        ok = wait(&bars->rfull[bt], (it / kRing) & 1) &&
+             (it < kBufs || wait(FP4 ? &bars->gempty[st] : &bars->tempty[st], ((it / kBufs) & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(full, (FP4 ? kStaged : kTile) / 2);
+          const int4* y4 = reinterpret_cast<const int4*>(rows + (it % kRing) * kKeys) + first;
+#pragma unroll 4
+          for (int g = 0; g < 8; ++g) {
+            const int4 v = y4[g];
+            const int y[4] = {v.x, v.y, v.z, v.w};
+            if (FP4) {
+              tma_gather4(smem + L::kOffStaged + st * kStaged + (first + g) * 4 * kRow4, &tmap, full, 0, y);
+            } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = keys.position(a, k * kKeys + 4 * g4 + j);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = keys.row(a, y[j], lane < 16);
-          const int st = it % kStages;
-          ok = it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->tfull[st], kTile);
-          __syncwarp();
-          uint8_t* dst = smem + L::kOffTile + st * kTile + g4 * 512;
-          const int c0 = lane < 16 ? 0 : 3, c1 = lane < 16 ? 3 : 5;
-          for (int c = c0; c < c1; ++c) tma_gather4(dst + c * kAtom, &tmap, &bars->tfull[st], c * 128, y);
-        } else {
-          int y[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) y[j] = keys.position(a, k * kKeys + 32 * j + lane);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) y[j] = keys.row(a, y[j], true);
-          const uint64_t mask = __ballot_sync(0xffffffffu, y[0] != a.past_row) |
-                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, y[1] != a.past_row)) << 32;
-          const int st = it & 1;
-          ok = it < 2 || wait(&bars->gempty[st], ((it >> 1) & 1) ^ 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            gmask[st] = mask;
-            ptx::mbar_arrive_expect_tx(&bars->gfull[st], __popcll(mask) * kRow4);
+              for (int c = 0; c < 5; ++c)
+                tma_gather4(smem + L::kOffTile + st * kTile + c * kAtom + (first + g) * 512, &tmap, full, c * 64, y);
+            }
           }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (y[j] != a.past_row)
-              ptx::bulk_load(smem + L::kOffStaged + st * kStaged + (32 * j + lane) * kRow4,
-                             a.cache + static_cast<long long>(y[j]) * kRow4, kRow4, &bars->gfull[st]);
+          if (it % kBatch == kBatch - 1) ptx::mbar_arrive(&bars->bempty[bt]);
         }
+        __syncwarp();
       }
     }
     // copies in flight land before the CTA can exit, whatever happened
-    constexpr int kBufs = FP4 ? 2 : kStages;
     for (int i = max(0, it - kBufs); i < it; ++i)
       ptx::mbar_spin_drain(FP4 ? &bars->gfull[i % kBufs] : &bars->tfull[i % kBufs], (i / kBufs) & 1, a.status, kStatusTimeout, 400000000ll);
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ scales of e4m3 rows
-    int it = 0;
-    bool ok = !FP4;
-    while (ok && pc.next(a)) {
-      const Keys keys(a, pc.t, false);
-      for (int k = pc.k0; k < pc.k1 && ok; ++k, ++it) {
-        int y[2];
-        float u[2];
+  } else if (warp == 14) {
+    // ------------------------------------------------------------ where the rows lie; scales of e4m3 rows
+    bool more = pc.next(a);
+    Keys keys(a, more ? pc.t : 0, lane == 0 && more);
+    int k = pc.k0;
+    for (int it = 0; more; it += kBatch) {
+      int y[2 * kBatch];
+      const int32_t* table[kBatch];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) y[j] = keys.position(a, k * kKeys + 32 * j + lane);
+      for (int j = 0; j < kBatch; ++j) {
+        y[2 * j] = y[2 * j + 1] = -1;
+        table[j] = keys.table;
+        if (!more) continue;
+        y[2 * j] = keys.position(a, k * kKeys + lane);
+        y[2 * j + 1] = keys.position(a, k * kKeys + 32 + lane);
+        if (++k == pc.k1) {
+          more = pc.next(a);
+          if (more) keys = Keys(a, pc.t, lane == 0);
+          k = pc.k0;
+        }
+      }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) y[j] = keys.row(a, y[j], false);
+      for (int j = 0; j < 2 * kBatch; ++j) y[j] = row_of(a, table[j >> 1], y[j]);
+      const int bt = (it / kBatch) % kBatches;
+      bool ok = it < kRing || wait(&bars->bempty[bt], ((it / kRing) & 1) ^ 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 * kBatch; ++j) rows[(bt * kBatch + (j >> 1)) * kKeys + 32 * (j & 1) + lane] = y[j];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars->rfull[bt]);
+      if constexpr (!FP4) {
+        float u[2 * kBatch];
+  #pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j)
           u[j] = y[j] != a.past_row ? __ldg(reinterpret_cast<const float*>(a.cache + static_cast<long long>(y[j]) * kRow8 + kScale8)) : 0.f;
-        const int st = it % kStages;
-        ok = it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          sc[st * kKeys + 32 * j + lane] =
-              make_float2(u[j], u[j] > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u[j]) >> 23) - 127) : -INFINITY);
+  #pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j)
+          sc[(bt * kBatch + (j >> 1)) * kKeys + 32 * (j & 1) + lane] =
+              make_float2(u[j], u[j] > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u[j]) >> 23) - 127 - kExpRef) : -INFINITY);
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars->scfull[st]);
+        if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ queries; tiles of 4-bit rows
-    const int row = threadIdx.x - 128, plane = lane >> 4, hl = (warp - 4) * 16 + (lane & 15);
-    const uint32_t lane_addr = static_cast<uint32_t>((warp - 4) * 32) << 16;
-    uint8_t* qrow = smem + L::kOffQr + row * 128;
-    if (plane) {  // the lo rows take no part in the rotary product
+    const int w = warp - 8;
+    const uint32_t lane_addr = static_cast<uint32_t>(w * 32) << 16;
+    uint8_t* qbuf = smem + L::kOffQ + w * 32 * kQStride;
+    const int l8 = lane & 7, hr = lane >> 3;  // a lane takes 8 of 64 values of the heads 16 w + hr + 0, 4, 8, 12
+    {
+      // the lo rows take no part in the rotary product
+      uint4* qr = reinterpret_cast<uint4*>(smem + L::kOffQr + (w * 32 + 16) * 128);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(qrow)[c] = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < 4; ++c) qr[c * 32 + lane] = make_uint4(0u, 0u, 0u, 0u);
     }
     int it = 0, n = 0;
     bool ok = true;
     while (ok && pc.next(a)) {
-      const int h = pc.g * kHeads + hl;
-      const bool live = h < a.H;
-      const uint4* src = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live ? h : 0) * a.qn_h) + plane * 32;
-      const uint4* srr = reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + (live ? h : 0) * a.qr_h);
-      // the power of two that takes the row's largest value to [128, 256)
-      float amax = 0.f;
+      const uint4* src[4];
+      bool live[4];
       uint4 rp[4];
+      float am[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) rp[c] = live ? __ldg(srr + plane * 4 + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 8
-      for (int c = 0; c < 32; ++c) {
-        float x[8];
-        unpack_bf16(live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u), x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+      for (int i = 0; i < 4; ++i) {
+        const int h = pc.g * kHeads + w * 16 + 4 * i + hr;
+        live[i] = h < a.H;
+        src[i] = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live[i] ? h : 0) * a.qn_h) + l8;
+        rp[i] = live[i] ? __ldg(reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + h * a.qr_h) + l8) : make_uint4(0u, 0u, 0u, 0u);
+        am[i] = 0.f;
       }
+      auto load = [&](int c, uint4 (&v)[4]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[8];
-        unpack_bf16(rp[c], x);
+        for (int i = 0; i < 4; ++i) v[i] = live[i] ? __ldg(src[i] + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      auto most = [&](const uint4 (&v)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+        for (int i = 0; i < 4; ++i) {
+          float x[8];
+          unpack_bf16(v[i], x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) am[i] = fmaxf(am[i], fabsf(x[j]));
+        }
+      };
+      // (the chunks that the conversion begins with come last)
+      uint4 v[2][4];
+#pragma unroll 1
+      for (int c = 6; c >= 0; c -= 2) {
+        load(c, v[0]);
+        load(c + 1, v[1]);
+        most(v[0]);
+        most(v[1]);
       }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-      const int e = amax > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127))) : 0;
-      const float f = pow2f(e);
+      most(rp);
+      // the power of two that takes the row's largest value to [128, 256)
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) am[i] = fmaxf(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
+        const int e = am[i] > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(am[i]) >> 23) - 127))) : 0;
+        f[i] = pow2f(e);
+        if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = a.scale_log2 * pow2f(-e);
+      }
       if (n > 0) {
         ok = wait(&bars->qfree, (n - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
       ptx::tc_fence_after();
-      {
-        // both planes' lanes write the rotary row of the hi plane, half each
-        uint8_t* dst = smem + L::kOffQr + (row - 16 * plane) * 128;
-        const int sw = (row - 16 * plane) & 7;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[8];
-          unpack_bf16(rp[c], x);
-          *reinterpret_cast<uint4*>(dst + (((plane * 4 + c) ^ sw) << 4)) =
-              make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f), pack_bf16(x[4] * f, x[5] * f),
-                         pack_bf16(x[6] * f, x[7] * f));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int r = w * 32 + 4 * i + hr;
+        float x[8];
+        unpack_bf16(rp[i], x);
+        *reinterpret_cast<uint4*>(smem + L::kOffQr + r * 128 + ((l8 ^ (r & 7)) << 4)) =
+            make_uint4(pack_bf16(x[0] * f[i], x[1] * f[i]), pack_bf16(x[2] * f[i], x[3] * f[i]),
+                       pack_bf16(x[4] * f[i], x[5] * f[i]), pack_bf16(x[6] * f[i], x[7] * f[i]));
       }
-      // this lane's half of the row, 128 values at a time: its own plane's codes stay, the other's go to the
-      // lane of that plane
-#pragma unroll 1
-      for (int j = 0; j < 2; ++j) {
-        uint32_t lowc[32], highc[32];
+      // 64 values of every row at a time: codes to shared memory, from there by rows to TMEM
+      auto convert = [&](int c, const uint4 (&v)[4]) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int i = 0; i < 4; ++i) {
           float x[8];
-          unpack_bf16(live ? __ldg(src + 16 * j + c) : make_uint4(0u, 0u, 0u, 0u), x);
+          unpack_bf16(v[i], x);
+          uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float v0 = x[4 * i] * f, v1 = x[4 * i + 1] * f, v2 = x[4 * i + 2] * f, v3 = x[4 * i + 3] * f;
+          for (int j = 0; j < 2; ++j) {
+            const float v0 = x[4 * j] * f[i], v1 = x[4 * j + 1] * f[i], v2 = x[4 * j + 2] * f[i], v3 = x[4 * j + 3] * f[i];
             const uint32_t h01 = e4m3x2(v0, v1), h23 = e4m3x2(v2, v3);
             const float2 b01 = from_e4m3x2(h01), b23 = from_e4m3x2(h23);
-            const uint32_t hi = h01 | (h23 << 16), lo = e4m3x2(v0 - b01.x, v1 - b01.y) | (e4m3x2(v2 - b23.x, v3 - b23.y) << 16);
-            const uint32_t keep = plane ? lo : hi, got = __shfl_xor_sync(0xffffffffu, plane ? hi : lo, 16);
-            lowc[2 * c + i] = plane ? got : keep;
-            highc[2 * c + i] = plane ? keep : got;
+            constexpr float up = 1 << kLoShift;
+            hi[j] = h01 | (h23 << 16);
+            lo[j] = e4m3x2((v0 - b01.x) * up, (v1 - b01.y) * up) | (e4m3x2((v2 - b23.x) * up, (v3 - b23.y) * up) << 16);
           }
+          *reinterpret_cast<uint2*>(qbuf + (4 * i + hr) * kQStride + l8 * 8) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(qbuf + (16 + 4 * i + hr) * kQStride + l8 * 8) = make_uint2(lo[0], lo[1]);
         }
-        ptx::tmem_st_32x32b_x32(tmem + lane_addr + kColQ + 32 * j, lowc);
-        ptx::tmem_st_32x32b_x32(tmem + lane_addr + kColQ + 64 + 32 * j, highc);
+        __syncwarp();
+        uint32_t r[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 q = *reinterpret_cast<const uint4*>(qbuf + lane * kQStride + 16 * j);
+          r[4 * j] = q.x, r[4 * j + 1] = q.y, r[4 * j + 2] = q.z, r[4 * j + 3] = q.w;
+        }
+        tmem_st_32x32b_x16(tmem + lane_addr + kColQ + 16 * c, r);
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 2) {
+        convert(c, v[0]);
+        if (c < 6) load(c + 2, v[0]);
+        convert(c + 1, v[1]);
+        if (c < 6) load(c + 3, v[1]);
       }
       ptx::tmem_st_wait();
-      if (!plane) qscale[(n % kQRing) * kHeads + hl] = a.scale_log2 * pow2f(-e);
       ptx::tc_fence_before();
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars->qfull[n % kQRing]);
       ++n;
-      if (!FP4) continue;
-      // 4-bit rows: a warp takes 16 rows of a block, a lane a block of 16 values
-      for (int k = pc.k0; k < pc.k1; ++k, ++it) {
-        const int st = it % kStages, gs = it & 1;
-        ok = wait(&bars->gfull[gs], (it >> 1) & 1) && (it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint64_t mask = gmask[gs];
-        const uint8_t* rows = smem + L::kOffStaged + gs * kStaged;
-        uint8_t* tile = smem + L::kOffTile + st * kTile;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int key = (warp - 4) * 16 + i;
-          const bool there = (mask >> key) & 1;
-          uint2 w = make_uint2(0u, 0u);
-          int byte = 0;
-          if (there) {
-            w = reinterpret_cast<const uint2*>(rows + key * kRow4)[lane];
-            byte = rows[key * kRow4 + kScale4 + lane];
+      if constexpr (FP4) {
+        // 4-bit rows: a warp takes 16 rows of a block, a lane a block of 16 values
+        for (int k = pc.k0; k < pc.k1; ++k, ++it) {
+          const int st = it % kStages, gs = it & 1, bt = (it / kBatch) % kBatches;
+          ok = wait(&bars->gfull[gs], (it >> 1) & 1) && (it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const bool there = rows[(it % kRing) * kKeys + w * 16 + (lane & 15)] != a.past_row;  // of key 16 w + lane
+          const uint8_t* staged = smem + L::kOffStaged + gs * kStaged + w * 16 * kRow4;
+          uint8_t* tile = smem + L::kOffTile + st * kTile;
+          int E = 0;
+  #pragma unroll
+          for (int i0 = 0; i0 < 16; i0 += 8) {
+            uint2 q[8], lv[8];
+            int byte[8];
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              byte[i] = staged[(i0 + i) * kRow4 + kScale4 + lane];
+              q[i] = reinterpret_cast<const uint2*>(staged + (i0 + i) * kRow4)[lane];
+            }
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) lv[i] = levels[byte[i] & 7];
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = w * 16 + i0 + i;
+              const int e = static_cast<int>(__ballot_sync(0xffffffffu, byte[i] >> 7) & 0xFFu) - 128;
+              if (lane == i0 + i) E = e;
+              const uint2 l2 = levels_at(lv[i], byte[i] & 127);
+              const uint2 c0 = codes4_to_e4m3(q[i].x, l2), c1 = codes4_to_e4m3(q[i].y, l2);
+              *reinterpret_cast<uint4*>(tile + (lane >> 3) * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) =
+                  make_uint4(c0.x, c0.y, c1.x, c1.y);
+            }
           }
-          const int E = static_cast<int>(__ballot_sync(0xffffffffu, byte >> 7) & 0xFFu) - 128;
-          const uint2 lv = levels_at(levels[byte & 7], byte & 127);
-          const uint2 c0 = codes4_to_e4m3(w.x, lv), c1 = codes4_to_e4m3(w.y, lv);
-          *reinterpret_cast<uint4*>(tile + (lane >> 3) * kAtom + key * 128 + (((lane & 7) ^ (key & 7)) << 4)) =
-              make_uint4(c0.x, c0.y, c1.x, c1.y);
-          if (lane == 0) sc[st * kKeys + key] = there ? make_float2(pow2f(E), static_cast<float>(E)) : make_float2(0.f, -INFINITY);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = (warp - 4) * 16 + 4 * i + (lane >> 3), c = lane & 7;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if ((mask >> key) & 1) v = reinterpret_cast<const uint4*>(rows + key * kRow4 + kRope4)[c];
-          *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((c ^ (key & 7)) << 4)) = v;
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&bars->gempty[gs]);
-          ptx::mbar_arrive(&bars->scfull[st]);
-          ptx::mbar_arrive(&bars->tfull[st]);
+          uint4 rr[4];
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) rr[i] = reinterpret_cast<const uint4*>(staged + (4 * i + hr) * kRow4 + kRope4)[l8];
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = w * 16 + 4 * i + hr;
+            *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[i];
+          }
+          if (lane < 16)
+            sc[st * kKeys + w * 16 + lane] = there ? make_float2(pow2f(E), static_cast<float>(E - kExpRef)) : make_float2(0.f, -INFINITY);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&bars->gempty[gs]);
+            ptx::mbar_arrive(&bars->scfull[st]);
+            ptx::mbar_arrive(&bars->tfull[st]);
+            if (it % kBatch == kBatch - 1) ptx::mbar_arrive(&bars->bempty[bt]);
+          }
         }
       }
     }
   } else {
-    // ------------------------------------------------------------ softmax, rescale, output (warps 0..3)
-    const int half = lane >> 4, hl = warp * 16 + (lane & 15);
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    // ------------------------------------------------------------ softmax, rescale, output
+    const int grp = warp >> 2, w = warp & 3, half = lane >> 4, hl = w * 16 + (lane & 15);
+    const uint32_t lane_addr = static_cast<uint32_t>(w * 32) << 16;
+    uint64_t* mine = grp ? &bars->hand1[w] : &bars->hand0[w];
+    uint64_t* other = grp ? &bars->hand0[w] : &bars->hand1[w];
     int it = 0, n = 0;
     bool ok = true;
-    // Every iteration runs its named barriers whatever happened, so that a wait that gave up leaves no warp
-    // behind at one.
+    // Every piece and block runs its named barriers whatever happened, so that a wait that gave up leaves no
+    // warp behind at one.
     while (pc.next(a)) {
-      const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
-      float m = -INFINITY, l = 0.f, qs = 0.f;
+      const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads), end = it + cnt;
+      float m = -INFINITY, l = 0.f, qm = 0.f, qo = 0.f;  // the group's reference at its last block, its sum
       if (ok) ok = __all_sync(0xffffffffu, wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) != 0;
-      if (ok) qs = qscale[(n % kQRing) * kHeads + hl];
-      for (int i = 0; i < cnt; ++i, ++it) {
-        const int st = it % kStages;
+      if (ok) {
+        const float qs = qscale[(n % kQRing) * kHeads + hl];
+        qm = half ? qs * (1.f / (1 << kLoShift)) : qs;  // of this lane's plane, and of the other's
+        qo = half ? qs : qs * (1.f / (1 << kLoShift));
+      }
+      for (int b = it + ((it ^ grp) & 1); b < end; b += 2) {
+        const int ss = FP4 ? b % kStages : b % kRing;
         float cr = 1.f;
         float x[32];
-        if (ok) ok = __all_sync(0xffffffffu, wait(&bars->sfull[it & 1], (it >> 1) & 1) && wait(&bars->scfull[st], (it / kStages) & 1)) != 0;
+        if (ok)
+          ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
+                                           (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
+                                                : wait(&bars->scfull[(b / kBatch) % kBatches], (b / kRing) & 1))) != 0;
         if (ok) {
           ptx::tc_fence_after();
-          uint32_t s0[32], s1[32];
-          ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + (it & 1) * kKeys, s0);
-          ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + (it & 1) * kKeys + 32, s1);
-          ptx::tmem_ld_wait_regs(s0);
-          ptx::tmem_ld_wait_regs(s1);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->sempty[it & 1]);
-          // the hi lane takes keys 0..31, the lo lane 32..63
-          const float4* scp = reinterpret_cast<const float4*>(sc + st * kKeys + half * 32);
           float mb = -INFINITY;
+          {
+            uint32_t s0[32], s1[32];
+            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + grp * kKeys, s0);
+            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + grp * kKeys + 32, s1);
+            ptx::tmem_ld_wait_regs(s0);
+            ptx::tmem_ld_wait_regs(s1);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
+            // the hi lane takes keys 0..31, the lo lane 32..63
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t mine = half ? s1[j] : s0[j], send = half ? s0[j] : s1[j];
-            x[j] = (__uint_as_float(mine) + __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16))) * qs;
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t keep = half ? s1[j] : s0[j], send = half ? s0[j] : s1[j];
+              x[j] = fmaf(__uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16)), qo, __uint_as_float(keep) * qm);
+            }
           }
+          const float4* scp = reinterpret_cast<const float4*>(sc + ss * kKeys + half * 32);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float4 v = scp[j];
             x[2 * j] = fmaf(x[2 * j], v.x, v.y);
             x[2 * j + 1] = fmaf(x[2 * j + 1], v.z, v.w);
-            mb = fmaxf(mb, fmaxf(x[2 * j], x[2 * j + 1]));
+            mx[j & 3] = fmaxf(mx[j & 3], fmaxf(x[2 * j], x[2 * j + 1]));
           }
+          mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
-          // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
-          float mn = m;
-          if (m == -INFINITY || mb > m + kMove) mn = mb;
-          cr = m == -INFINITY ? 1.f : ptx::ex2(m - mn);
-          m = mn;
-          l *= cr;
-          if (!half) corr[hl] = cr;
+          if (b > 0) ok = __all_sync(0xffffffffu, wait(other, ((b - 1) >> 1) & 1)) != 0;
+          if (ok) {
+            const float before = b == end - cnt ? -INFINITY : refv[(grp ^ 1) * kHeads + hl];
+            // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
+            float mn = before;
+            if (before == -INFINITY || mb > before + kMove) mn = mb;
+            cr = before == -INFINITY ? 1.f : ptx::ex2(before - mn);
+            l = m == -INFINITY ? 0.f : l * ptx::ex2(m - mn);
+            m = mn;
+            if (!half) {
+              refv[grp * kHeads + hl] = mn;
+              corr[grp * kHeads + hl] = cr;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(mine);
+          }
         }
         // does any head's output need rescaling?
         uint32_t any;
         asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.f32 q, %1, 0f3F800000;\n\t"
-                     "bar.red.or.pred p, 2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(any) : "f"(hl < hg ? cr : 1.f) : "memory");
+                     "bar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(any) : "f"(hl < hg ? cr : 1.f), "r"(2 + grp) : "memory");
         if (any) {
-          if (ok && i > 0) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1)) != 0;
-          if (ok && i > 0) {
+          if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp ^ 1], ((b - 1) >> 1) & 1)) != 0;
+          if (ok) {
             ptx::tc_fence_after();
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
               for (int h0 = 0; h0 < hg; h0 += 32) {
                 const uint32_t col = tmem + lane_addr + kColO + c * kHeads + h0;
                 uint32_t r[32];
                 ptx::tmem_ld_32x32b_x32(col, r);
                 ptx::tmem_ld_wait_regs(r);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * corr[h0 + j]);
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * corr[grp * kHeads + h0 + j]);
                 ptx::tmem_st_32x32b_x32(col, r);
               }
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
           }
-          ptx::named_bar_sync(2, 128);  // corr is read before the next block rewrites it
+          ptx::named_bar_sync(2 + grp, 128);  // corr is read before the group's next block rewrites it
         }
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : m - kPShift;
-          const uint2* scu = reinterpret_cast<const uint2*>(sc + st * kKeys + half * 32);
+          const uint4* scu = reinterpret_cast<const uint4*>(sc + ss * kKeys + half * 32);
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
+            const uint4 u0 = scu[2 * j], u1 = scu[2 * j + 1];
+            const uint32_t u[4] = {u0.x, u0.z, u1.x, u1.z};
             float p[4], r[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               p[q] = ptx::ex2(x[4 * j + q] - ref);
-              l = fmaf(p[q], __uint_as_float(0x7F000000u - scu[4 * j + q].x), l);  // p 2^-E
+              l = fmaf(p[q], __uint_as_float((static_cast<uint32_t>(254 + kExpRef) << 23) - u[q]), l);  // p 2^(kExpRef - E)
               r[q] = __uint_as_float((__float_as_uint(p[q]) + 0x80000u) & 0xFFF00000u);  // 4 significant bits
             }
             hi[j] = e4m3x2(r[0], r[1]) | (e4m3x2(r[2], r[3]) << 16);
             lo[j] = e4m3x2(p[0] - r[0], p[1] - r[1]) | (e4m3x2(p[2] - r[2], p[3] - r[3]) << 16);
           }
-          // P's buffer is free once the products before the last have been done
-          if (it > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[it & 1], ((it >> 1) & 1) ^ 1)) != 0;
+          // the group's P is free once the products of its block before have been done
+          if (b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp], ((b >> 1) & 1) ^ 1)) != 0;
           if (ok) {
-            uint8_t* prow = smem + L::kOffP + (it & 1) * kPBytes + hl * 128;
+            uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int ch = half * 2 + c;
@@ -659,32 +759,46 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->pfull[it & 1]);
+            if (lane == 0) {
+              ptx::mbar_arrive(&bars->pfull[grp]);
+              if (!FP4 && (b % kBatch) >> 1 == kBatch / 2 - 1) ptx::mbar_arrive(&bars->bempty[(b / kBatch) % kBatches]);
+            }
           }
         }
       }
+      it = end;
       ++n;
-      // the piece's output
-      if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1)) != 0;
+      // the piece's output: the sums of both groups against the last reference
+      const int last = (end - 1) & 1;
+      if (ok)
+        ok = __all_sync(0xffffffffu, (last == grp || wait(other, ((end - 1) >> 1) & 1)) &&
+                                         wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
+      const float fin = refv[last * kHeads + hl];
+      l = m == -INFINITY ? 0.f : l * ptx::ex2(m - fin);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (!half) lsum[grp * kHeads + hl] = l;
+      ptx::named_bar_sync(4, 256);
       const bool whole = pc.k0 == 0 && pc.k1 == pc.blocks;
       const int slot = 2 * part + (pc.k0 == 0 ? 1 : 0);
-      if (!half) {
-        corr[hl] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      if (grp == 0 && !half) {
+        l = lsum[hl] + lsum[kHeads + hl];
+        linv[hl] = l == 0.f ? 0.f : pow2f(kExpRef) / l;
         if (hl < hg && ok) {
           if (!whole) {
-            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = m;
+            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin;
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = l;
           } else if (a.lse) {
-            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = l == 0.f ? -INFINITY : (fin - kPShift + log2f(l)) * kLn2;
           }
         }
       }
-      ptx::named_bar_sync(2, 128);
+      ptx::named_bar_sync(4, 256);
       if (ok) {
         ptx::tc_fence_after();
-        for (int c = 0; c < 4; ++c) {
-          const int lat = warp * 32 + lane;
+        const int lat = w * 32 + lane;
+#pragma unroll 1
+        for (int c = 2 * grp; c < 2 * grp + 2; ++c) {
+#pragma unroll 1
           for (int h0 = 0; h0 < hg; h0 += 32) {
             uint32_t r[32];
             ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColO + c * kHeads + h0, r);
@@ -695,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               const bool odd = lane & 1;
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
-                const float v0 = __uint_as_float(r[j]) * corr[h0 + j], v1 = __uint_as_float(r[j + 1]) * corr[h0 + j + 1];
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                if (h0 + j + odd < hg) o[(j + odd) * (kRank / 2)] = odd ? pack_bf16(other, v1) : pack_bf16(v0, other);
+                const float v0 = __uint_as_float(r[j]) * linv[h0 + j], v1 = __uint_as_float(r[j + 1]) * linv[h0 + j + 1];
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                if (h0 + j + odd < hg) o[(j + odd) * (kRank / 2)] = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
               }
             } else {
               float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
@@ -710,13 +824,14 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           }
         }
         ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->odrained);
       }
-      ptx::named_bar_sync(2, 128);  // corr is read before the next piece rewrites it
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -766,7 +881,7 @@ __global__ void __launch_bounds__(128) quant_join_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (h0 + i >= a.H) continue;
-    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : acc[i] / W[i]);
+    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : ldexpf(acc[i] / W[i], kExpRef));
     if (chunk == 0 && threadIdx.x == i && a.lse) a.lse[row + i] = W[i] == 0.f ? -INFINITY : (M[i] - kPShift + log2f(W[i])) * kLn2;
   }
 }
@@ -891,6 +1006,9 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.H = a->H;
   k.groups = p.groups;
   k.page_size = a->page_size;
+  k.page_log2 = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a->page_size == 1 << i) k.page_log2 = i;
   k.num_pages = a->num_pages;
   k.max_pages = a->max_pages_per_seq;
   k.topk_width = a->topk_width;
@@ -923,13 +1041,11 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     k.cum = cum;
   }
-  CUtensorMap map{};
-  if (a->format == DSA_FP8_E4M3) {
-    if (!make_gather_map(&map, a->cache ? a->cache : a->q_nope, quant::kRow8, k.past_row)) return DSA_ERR_CUDA;
-    e = launch_attend<false>(map, k, s);
-  } else {
-    e = launch_attend<true>(map, k, s);
-  }
+  // (a cache without pages: a map of one row, past which every copy lies)
+  CUtensorMap map;
+  const bool fp4 = a->format == DSA_FP4_E2M1;
+  if (!make_gather_map(&map, a->cache ? a->cache : a->q_nope, fp4, quant::row_bytes(a->format), k.past_row)) return DSA_ERR_CUDA;
+  e = fp4 ? launch_attend<true>(map, k, s) : launch_attend<false>(map, k, s);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (p.parts > 1) e = launch_pdl(quant_join_kernel, dim3(p.parts - 1, 64), dim3(128), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
