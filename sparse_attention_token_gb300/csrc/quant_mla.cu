@@ -311,45 +311,41 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
 
   if (warp == 13) {
     // ------------------------------------------------------------ MMAs
-    const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
-    int it = 0, n = 0;  // blocks, pieces
-    bool ok = true;
-    while (pc.next(a)) {
-      const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
-      const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
-      for (int i = 0; i <= cnt; ++i) {
-        if (i < cnt) {  // S of block i
-          const int b = it + i;
-          ok = ok && (i > 0 || wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) && wait(&bars->tfull[b % kStages], (b / kStages) & 1) &&
-               (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
+    // One elected lane runs the whole loop, its waits too: under any condition that the compiler cannot see to be
+    // the same for the warp, an MMA takes some 90 cycles to issue.
+    if (ptx::elect_one()) {
+      const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
+      int it = 0, n = 0;  // blocks, pieces
+      bool ok = true;
+      while (ok && pc.next(a)) {
+        const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
+        const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
+        ok = wait(&bars->qfull[n % kQRing], (n / kQRing) & 1);
+        for (int i = 0; i <= cnt && ok; ++i) {
+          if (i < cnt) {  // S of block i
+            const int b = it + i;
+            ok = wait(&bars->tfull[b % kStages], (b / kStages) & 1) && (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
+            if (!ok) break;
             ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint32_t d = tmem + kColS + (b & 1) * kKeys, tile = sbase + L::kOffTile + (b % kStages) * kTile;
+            const uint32_t d = tmem + kColS + (b & 1) * kKeys, tile = sbase + L::kOffTile + (b % kStages) * kTile;
 #pragma unroll
-              for (int at = 0; at < 4; ++at) {
-                const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
+            for (int at = 0; at < 4; ++at) {
+              const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
-                  mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
-              }
-              const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
-#pragma unroll
-              for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
-              ptx::mma_commit(&bars->sfull[b & 1]);
-              if (i == cnt - 1) ptx::mma_commit(&bars->qfree);
+              for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
+                mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
             }
-            __syncwarp();
+            const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
+            ptx::mma_commit(&bars->sfull[b & 1]);
+            if (i == cnt - 1) ptx::mma_commit(&bars->qfree);
           }
-        }
-        if (i == 0) continue;
-        const int b = it + i - 1;  // P . V of the block before
-        ok = ok && wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 1 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
+          if (i == 0) continue;
+          const int b = it + i - 1;  // P . V of the block before
+          ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 1 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
+          if (!ok) break;
+          ptx::tc_fence_after();
           const uint32_t tile = sbase + L::kOffTile + (b % kStages) * kTile;
           const uint64_t bd = ptx::sw128_kmajor_desc(sbase + L::kOffP + (b & 1) * kPBytes);
 #pragma unroll
@@ -365,12 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           ptx::mma_commit(&bars->tempty[b % kStages]);
           ptx::mma_commit(&bars->pvdone[b & 1]);
         }
-        __syncwarp();
+        it += cnt;
+        ++n;
       }
-      it += cnt;
-      ++n;
-    }
-    if (ptx::elect_one()) {
       ptx::mma_commit(&bars->done);
       ptx::mbar_spin_drain(&bars->done, 0, a.status, kStatusTimeout, 400000000ll);
     }
