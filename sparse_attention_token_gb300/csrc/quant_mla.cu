@@ -50,9 +50,11 @@ constexpr uint32_t kTile = 5 * kAtom;                     // 4 columns of 128 co
 constexpr uint32_t kStaged = kKeys * kRow4;               // a block of 4-bit rows
 constexpr uint32_t kQRope = 128 * 128, kPBytes = kHeads * 128;
 constexpr uint32_t kQStride = 80, kQBuf = 4 * 32 * kQStride;  // 64 codes of 32 query rows a warp, 16 bytes apart further
+constexpr uint32_t kBe5m2 = 1u << 10;                     // instruction descriptor: B holds e5m2
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // TMEM columns
 constexpr int kPShift = 5;                                // p = 2^5 at the reference maximum
 constexpr float kMove = 3.f;                              // the reference moves when passed by more: p <= 2^8
+constexpr int kFewHeads = 12;                             // rescaled one by one (130 cycles each; all at once 2000)
 constexpr int kLoShift = 4;                               // lo = 2^4 (x - hi): below 2^4 of its step it is exact, and 2^7 at most
 constexpr int kExpRef = -7;                               // E of normalised rows: x' counts from there, so that it does not lose x's bits
 constexpr float kLn2 = 0.6931471805599453f;
@@ -213,12 +215,27 @@ __device__ __forceinline__ int row_of(const Args& a, const int32_t* table, int p
   return page * a.page_size + (pos - lp * a.page_size);
 }
 
-// D[tmem] (+)= A[tmem] . B[smem]^T, e4m3.
-__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A . B[smem]^T: A e4m3 in TMEM, e4m3 or bf16 in shared memory.  Operands in shared memory are given by the
+// low words of their descriptors; the high word is the same for all (128-byte swizzle, K-major or MN-major).
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(idesc),
+      "r"(accumulate), "n"(ptx::kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a_lo),
+      "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a_lo),
+      "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kDescHi)
       : "memory");
 }
 // Four rows of 128 bytes from column x on, into 512 bytes of a 128-byte swizzled tile.
@@ -230,6 +247,34 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// Whether v is non-zero in any of the 128 threads at named barrier `id`.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t v) {
+  uint32_t any;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(any) : "r"(v), "r"(id) : "memory");
+  return any != 0;
+}
+// One column of 32 lanes.
+__device__ __forceinline__ float tmem_ld_x1(uint32_t taddr) {
+  float r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(r) : "r"(taddr));
+  return r;
+}
+__device__ __forceinline__ void tmem_st_x1(uint32_t taddr, float r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(r) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait4(float (&r)[4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : : "memory");
+}
+// Two values 0 <= p <= 2^8 as e4m3 codes (x) and the e5m2 codes of what they leave (y), through fp16 (2^-11 of p,
+// 2^-25 below 2^-14): both differences are exact.
+__device__ __forceinline__ uint2 two_terms(float p0, float p1) {
+  const __half2 h = __floats2half2_rn(p0, p1);
+  const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+  const __half2 rest = __hsub2(h, __half2(back));
+  return make_uint2(hi, __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2));
+}
 // 64 codes of 32 rows: thread i writes 16 columns of lane (base + i).
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -257,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   float* linv = reinterpret_cast<float*>(misc + 768);                   // [64] of the piece that is written
   float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] each group's
   float* refv = reinterpret_cast<float*>(misc + 1536);                  // [2][64] the reference after its last block
+  uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] moved heads of each group's warps
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
   float* qscale = reinterpret_cast<float*>(misc + 3072);                // [kQRing][64]
   int* rows = reinterpret_cast<int*>(smem + L::kOffRows);               // [kRing][64] rows of a block's keys
@@ -315,47 +361,46 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     // the same for the warp, an MMA takes some 90 cycles to issue.
     if (ptx::elect_one()) {
       const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
+      const uint32_t tile0 = ptx::desc_lo(sbase + L::kOffTile, kAtom), rope0 = ptx::desc_lo(sbase + L::kOffQr, 16);
+      const uint32_t p0 = ptx::desc_lo(sbase + L::kOffP, 16);
       int it = 0, n = 0;  // blocks, pieces
       bool ok = true;
       while (ok && pc.next(a)) {
         const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
         const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
         ok = wait(&bars->qfull[n % kQRing], (n / kQRing) & 1);
-        for (int i = 0; i <= cnt && ok; ++i) {
+        // S runs two blocks ahead: both groups of softmax warps have their next block when they are done with one.
+        for (int i = 0; i < cnt + 2 && ok; ++i) {
           if (i < cnt) {  // S of block i
             const int b = it + i;
             ok = wait(&bars->tfull[b % kStages], (b / kStages) & 1) && (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t d = tmem + kColS + (b & 1) * kKeys, tile = sbase + L::kOffTile + (b % kStages) * kTile;
+            const uint32_t d = tmem + kColS + (b & 1) * kKeys;
+            uint32_t kd = tile0 + (b % kStages) * (kTile >> 4), qd = rope0;
+            asm volatile("" : "+r"(kd), "+r"(qd));  // descriptors are added up here, not kept over the loop
 #pragma unroll
-            for (int at = 0; at < 4; ++at) {
-              const uint64_t bd = ptx::sw128_kmajor_desc(tile + at * kAtom);
+            for (int s = 0; s < 16; ++s)  // 32 codes of K per MMA, four in a column
+              mma_f8_ts(d, tmem + kColQ + s * 8, kd + (((s >> 2) * kAtom + (s & 3) * 32) >> 4), id_qk, s > 0 ? 1u : 0u);
 #pragma unroll
-              for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA
-                mma_f8_ts(d, tmem + kColQ + at * 32 + s * 8, bd + 2 * s, id_qk, (at > 0 || s > 0) ? 1u : 0u);
-            }
-            const uint64_t ad = ptx::sw128_kmajor_desc(sbase + L::kOffQr), bd = ptx::sw128_kmajor_desc(tile + 4 * kAtom);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) ptx::mma_bf16(d, ad + 2 * s, bd + 2 * s, id_qr, 1u);
+            for (int s = 0; s < 4; ++s) mma_bf16_ss(d, qd + 2 * s, kd + ((4 * kAtom) >> 4) + 2 * s, id_qr, 1u);
             ptx::mma_commit(&bars->sfull[b & 1]);
             if (i == cnt - 1) ptx::mma_commit(&bars->qfree);
           }
-          if (i == 0) continue;
-          const int b = it + i - 1;  // P . V of the block before
-          ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 1 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
+          if (i < 2) continue;
+          const int b = it + i - 2;  // P . V of the block before the last
+          ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 2 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t tile = sbase + L::kOffTile + (b % kStages) * kTile;
-          const uint64_t bd = ptx::sw128_kmajor_desc(sbase + L::kOffP + (b & 1) * kPBytes);
+          uint32_t vd = tile0 + (b % kStages) * (kTile >> 4), pd = p0 + (b & 1) * (kPBytes >> 4);
+          asm volatile("" : "+r"(vd), "+r"(pd));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t d = tmem + kColO + c * kHeads;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 32 keys per MMA
-              const uint64_t ad = ptx::sw128_mnmajor_desc(tile + c * kAtom + s * 4096, kAtom);
-              ptx::mma_f8(d, ad, bd + 2 * s, id_pv, (i > 1 || s > 0) ? 1u : 0u);
-              ptx::mma_f8(d, ad, bd + 4 + 2 * s, id_pv, 1u);
+              const uint32_t ad = vd + ((c * kAtom + s * 4096) >> 4);
+              mma_f8_ss(tmem + kColO + c * kHeads, ad, pd + 2 * s, id_pv, (i > 2 || s > 0) ? 1u : 0u);
+              mma_f8_ss(tmem + kColO + c * kHeads, ad, pd + 4 + 2 * s, id_pv | kBe5m2, 1u);
             }
           }
           ptx::mma_commit(&bars->tempty[b % kStages]);
@@ -694,33 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             if (lane == 0) ptx::mbar_arrive(mine);
           }
         }
-        // does any head's output need rescaling?
-        uint32_t any;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.f32 q, %1, 0f3F800000;\n\t"
-                     "bar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(any) : "f"(hl < hg ? cr : 1.f), "r"(2 + grp) : "memory");
-        if (any) {
-          if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp ^ 1], ((b - 1) >> 1) & 1)) != 0;
-          if (ok) {
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll 1
-              for (int h0 = 0; h0 < hg; h0 += 32) {
-                const uint32_t col = tmem + lane_addr + kColO + c * kHeads + h0;
-                uint32_t r[32];
-                ptx::tmem_ld_32x32b_x32(col, r);
-                ptx::tmem_ld_wait_regs(r);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * corr[grp * kHeads + h0 + j]);
-                ptx::tmem_st_32x32b_x32(col, r);
-              }
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-          }
-          ptx::named_bar_sync(2 + grp, 128);  // corr is read before the group's next block rewrites it
-        }
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : m - kPShift;
           const uint4* scu = reinterpret_cast<const uint4*>(sc + ss * kKeys + half * 32);
@@ -729,15 +747,15 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           for (int j = 0; j < 8; ++j) {
             const uint4 u0 = scu[2 * j], u1 = scu[2 * j + 1];
             const uint32_t u[4] = {u0.x, u0.z, u1.x, u1.z};
-            float p[4], r[4];
+            float p[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               p[q] = ptx::ex2(x[4 * j + q] - ref);
               l = fmaf(p[q], __uint_as_float((static_cast<uint32_t>(254 + kExpRef) << 23) - u[q]), l);  // p 2^(kExpRef - E)
-              r[q] = __uint_as_float((__float_as_uint(p[q]) + 0x80000u) & 0xFFF00000u);  // 4 significant bits
             }
-            hi[j] = e4m3x2(r[0], r[1]) | (e4m3x2(r[2], r[3]) << 16);
-            lo[j] = e4m3x2(p[0] - r[0], p[1] - r[1]) | (e4m3x2(p[2] - r[2], p[3] - r[3]) << 16);
+            const uint2 p01 = two_terms(p[0], p[1]), p23 = two_terms(p[2], p[3]);
+            hi[j] = p01.x | (p23.x << 16);
+            lo[j] = p01.y | (p23.y << 16);
           }
           // the group's P is free once the products of its block before have been done
           if (b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp], ((b >> 1) & 1) ^ 1)) != 0;
@@ -750,12 +768,52 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
             }
             ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::mbar_arrive(&bars->pfull[grp]);
-              if (!FP4 && (b % kBatch) >> 1 == kBatch / 2 - 1) ptx::mbar_arrive(&bars->bempty[(b / kBatch) % kBatches]);
+          }
+        }
+        // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
+        // done and before those of this one begin (which wait for them in any case).
+        const unsigned moved = __ballot_sync(0xffffffffu, !half && hl < hg && cr != 1.f);
+        if (lane == 0) movedv[grp * 4 + w] = moved;
+        if (bar_any(2 + grp, moved)) {
+          if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp ^ 1], ((b - 1) >> 1) & 1)) != 0;
+          if (ok) {
+            ptx::tc_fence_after();
+            const uint2 m01 = *reinterpret_cast<const uint2*>(movedv + grp * 4), m23 = *reinterpret_cast<const uint2*>(movedv + grp * 4 + 2);
+            uint64_t todo = (m01.x | m01.y << 16) | static_cast<uint64_t>(m23.x | m23.y << 16) << 32;
+            const uint32_t o = tmem + lane_addr + kColO;
+            const float* f = corr + grp * kHeads;
+            if (__popcll(todo) <= kFewHeads) {
+              for (; todo; todo &= todo - 1) {
+                const int h = __ffsll(static_cast<long long>(todo)) - 1;
+                float r[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) r[c] = tmem_ld_x1(o + c * kHeads + h);
+                tmem_ld_wait4(r);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_st_x1(o + c * kHeads + h, r[c] * f[h]);
+              }
+            } else {
+#pragma unroll 1
+              for (int q = 0; q < 8; ++q) {
+                const uint32_t col = o + q * 32;
+                uint32_t r[32];
+                ptx::tmem_ld_32x32b_x32(col, r);
+                ptx::tmem_ld_wait_regs(r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f[(q & 1) * 32 + j]);
+                ptx::tmem_st_32x32b_x32(col, r);
+              }
             }
+            ptx::tmem_st_wait();
+          }
+          ptx::named_bar_sync(2 + grp, 128);  // corr is read before the group's next block rewrites it
+        }
+        if (ok) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&bars->pfull[grp]);
+            if (!FP4 && (b % kBatch) >> 1 == kBatch / 2 - 1) ptx::mbar_arrive(&bars->bempty[(b / kBatch) % kBatches]);
           }
         }
       }
