@@ -247,6 +247,10 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// A wait that did not succeed at once (one copy of its code for all of them).
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  return ptx::mbar_spin(bar, parity, abort, status, kStatusTimeout);
+}
 // Whether v is non-zero in any of the 128 threads at named barrier `id`.
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t v) {
   uint32_t any;
@@ -266,14 +270,57 @@ __device__ __forceinline__ void tmem_st_x1(uint32_t taddr, float r) {
 __device__ __forceinline__ void tmem_ld_wait4(float (&r)[4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : : "memory");
 }
-// Two values 0 <= p <= 2^8 as e4m3 codes (x) and the e5m2 codes of what they leave (y), through fp16 (2^-11 of p,
-// 2^-25 below 2^-14): both differences are exact.
-__device__ __forceinline__ uint2 two_terms(float p0, float p1) {
-  const __half2 h = __floats2half2_rn(p0, p1);
-  const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
-  const __half2 rest = __hsub2(h, __half2(back));
-  return make_uint2(hi, __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2));
+// Four values 0 <= p <= 2^8, given as 2^-8 p in fp16, as e4m3 codes (x) and the e5m2 codes of what they leave (y).
+// 2^-8 p has e4m3's exponents as its low four and its subnormals where e4m3 has them, so rounding its bits to three
+// of the mantissa is the code; e5m2 is the upper half of fp16.  (Conversions take the slow pipe, integers do not.)
+__device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b) {
+  const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a), ub = *reinterpret_cast<const uint32_t*>(&b);
+  const uint32_t ra = (ua + 0x00400040u) & 0x7F807F80u, rb = (ub + 0x00400040u) & 0x7F807F80u;
+  const __half2 up = __float2half2_rn(256.f);
+  const __half2 la = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ra)), up);
+  const __half2 lb = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&rb)), up);
+  return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531),
+                    __byte_perm(*reinterpret_cast<const uint32_t*>(&la) + 0x00800080u,
+                                *reinterpret_cast<const uint32_t*>(&lb) + 0x00800080u, 0x7531));
+}
+// Scale u = 2^E of a block's row `key` (0: no row, which takes no weight).
+__device__ __forceinline__ void put_scale(float4* block, int key, float u) {
+  float* pair = reinterpret_cast<float*>(block + (key >> 1)) + (key & 1);
+  pair[0] = u;
+  pair[2] = u > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u) >> 23) - 127 - kExpRef) : -INFINITY;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b));
+  return d;
+}
+// 16 columns of 32 lanes, and the wait for earlier loads (the registers tied to it).
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16], uint32_t (&q)[16]) {
+  tmem_ld_wait16(r);
+  tmem_ld_wait16(q);
 }
 // 64 codes of 32 rows: thread i writes 16 columns of lane (base + i).
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -306,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
   float* qscale = reinterpret_cast<float*>(misc + 3072);                // [kQRing][64]
   int* rows = reinterpret_cast<int*>(smem + L::kOffRows);               // [kRing][64] rows of a block's keys
-  float2* sc = reinterpret_cast<float2*>(smem + L::kOffSc);             // [kScRing][64] (2^E, E - kExpRef) of them
+  float4* sc = reinterpret_cast<float4*>(smem + L::kOffSc);             // [kScRing][32] two rows' 2^E, then their E - kExpRef
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&bars->tfull[s], FP4 ? 4 : 2);
@@ -352,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   const Line line = line_of(a);
   const int part = blockIdx.x;
   Pieces pc(a, line, part);
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_spin(bar, parity, abort, a.status, kStatusTimeout); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, a.status); };
   const uint32_t sbase = ptx::smem_u32(smem);
 
   if (warp == 13) {
@@ -488,8 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           u[j] = y[j] != a.past_row ? __ldg(reinterpret_cast<const float*>(a.cache + static_cast<long long>(y[j]) * kRow8 + kScale8)) : 0.f;
   #pragma unroll
         for (int j = 0; j < 2 * kBatch; ++j)
-          sc[(bt * kBatch + (j >> 1)) * kKeys + 32 * (j & 1) + lane] =
-              make_float2(u[j], u[j] > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u[j]) >> 23) - 127 - kExpRef) : -INFINITY);
+          put_scale(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane, u[j]);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
       }
@@ -652,8 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             const int key = w * 16 + 4 * i + hr;
             *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[i];
           }
-          if (lane < 16)
-            sc[st * kKeys + w * 16 + lane] = there ? make_float2(pow2f(E), static_cast<float>(E - kExpRef)) : make_float2(0.f, -INFINITY);
+          if (lane < 16) put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(E) : 0.f);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -677,50 +722,56 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     // warp behind at one.
     while (pc.next(a)) {
       const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads), end = it + cnt;
-      float m = -INFINITY, l = 0.f, qm = 0.f, qo = 0.f;  // the group's reference at its last block, its sum
+      float m = -INFINITY;  // the group's reference at its last block
+      float2 l = make_float2(0.f, 0.f), qm = l, qo = l;  // its sum, in two parts; the planes' scales
       if (ok) ok = __all_sync(0xffffffffu, wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) != 0;
       if (ok) {
         const float qs = qscale[(n % kQRing) * kHeads + hl];
-        qm = half ? qs * (1.f / (1 << kLoShift)) : qs;  // of this lane's plane, and of the other's
-        qo = half ? qs : qs * (1.f / (1 << kLoShift));
+        qm.x = qm.y = half ? qs * (1.f / (1 << kLoShift)) : qs;  // of this lane's plane, and of the other's
+        qo.x = qo.y = half ? qs : qs * (1.f / (1 << kLoShift));
       }
       for (int b = it + ((it ^ grp) & 1); b < end; b += 2) {
         const int ss = FP4 ? b % kStages : b % kRing;
+        const uint32_t col = tmem + lane_addr + kColS + grp * kKeys;
+        const float4* scp = sc + ss * (kKeys / 2) + half * 16;
         float cr = 1.f;
-        float x[32];
         if (ok)
           ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
                                            (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
                                                 : wait(&bars->scfull[(b / kBatch) % kBatches], (b / kRing) & 1))) != 0;
         if (ok) {
+          // x' of the block, 16 keys at a time (the hi lane takes keys 0..31, the lo lane 32..63), back over S.
+          // Both passes are loops: as straight code the two groups' block is more than an SM's schedulers hold of
+          // instructions (a third of the cycles went by waiting for them).
           ptx::tc_fence_after();
-          float mb = -INFINITY;
-          {
-            uint32_t s0[32], s1[32];
-            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + grp * kKeys, s0);
-            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColS + grp * kKeys + 32, s1);
-            ptx::tmem_ld_wait_regs(s0);
-            ptx::tmem_ld_wait_regs(s1);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
-            // the hi lane takes keys 0..31, the lo lane 32..63
+          float2 mx = make_float2(-INFINITY, -INFINITY);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s0[16], s1[16], x[16];
+            tmem_ld_x16(col + 16 * c, s0);
+            tmem_ld_x16(col + 32 + 16 * c, s1);
+            tmem_ld_wait16(s0, s1);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const uint32_t keep = half ? s1[j] : s0[j], send = half ? s0[j] : s1[j];
-              x[j] = fmaf(__uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16)), qo, __uint_as_float(keep) * qm);
+            for (int j = 0; j < 16; j += 2) {
+              float2 keep, got;
+              keep.x = __uint_as_float(half ? s1[j] : s0[j]);
+              keep.y = __uint_as_float(half ? s1[j + 1] : s0[j + 1]);
+              got.x = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j] : s1[j], 16));
+              got.y = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j + 1] : s1[j + 1], 16));
+              const float4 v = scp[8 * c + (j >> 1)];
+              float2 y = mul2(keep, qm);
+              ptx::ffma2(y, got, qo);
+              float2 z = make_float2(v.z, v.w);
+              ptx::ffma2(z, y, make_float2(v.x, v.y));
+              mx.x = fmaxf(mx.x, z.x);
+              mx.y = fmaxf(mx.y, z.y);
+              x[j] = __float_as_uint(z.x);
+              x[j + 1] = __float_as_uint(z.y);
             }
+            tmem_st_32x32b_x16(col + 16 * c, x);
           }
-          const float4* scp = reinterpret_cast<const float4*>(sc + ss * kKeys + half * 32);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 v = scp[j];
-            x[2 * j] = fmaf(x[2 * j], v.x, v.y);
-            x[2 * j + 1] = fmaf(x[2 * j + 1], v.z, v.w);
-            mx[j & 3] = fmaxf(mx[j & 3], fmaxf(x[2 * j], x[2 * j + 1]));
-          }
-          mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          ptx::tmem_st_wait();
+          float mb = fmaxf(mx.x, mx.y);
           mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
           if (b > 0) ok = __all_sync(0xffffffffu, wait(other, ((b - 1) >> 1) & 1)) != 0;
           if (ok) {
@@ -729,7 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             float mn = before;
             if (before == -INFINITY || mb > before + kMove) mn = mb;
             cr = before == -INFINITY ? 1.f : ptx::ex2(before - mn);
-            l = m == -INFINITY ? 0.f : l * ptx::ex2(m - mn);
+            const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
+            l.x *= f;
+            l.y *= f;
             m = mn;
             if (!half) {
               refv[grp * kHeads + hl] = mn;
@@ -738,37 +791,40 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(mine);
           }
+          // the group's P is free once the products of its block before have been done
+          if (ok && b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp], ((b >> 1) & 1) ^ 1)) != 0;
         }
         if (ok) {
-          const float ref = m == -INFINITY ? 0.f : m - kPShift;
-          const uint4* scu = reinterpret_cast<const uint4*>(sc + ss * kKeys + half * 32);
-          uint32_t hi[8], lo[8];
+          const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
+          uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[16], hi[4], lo[4];
+            tmem_ld_x16(col + 16 * c, x);
+            tmem_ld_wait16(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 u0 = scu[2 * j], u1 = scu[2 * j + 1];
-            const uint32_t u[4] = {u0.x, u0.z, u1.x, u1.z};
-            float p[4];
+            for (int j = 0; j < 4; ++j) {
+              float2 p[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              p[q] = ptx::ex2(x[4 * j + q] - ref);
-              l = fmaf(p[q], __uint_as_float((static_cast<uint32_t>(254 + kExpRef) << 23) - u[q]), l);  // p 2^(kExpRef - E)
+              for (int q = 0; q < 2; ++q) {
+                const uint2 u = *reinterpret_cast<const uint2*>(scp + 8 * c + 2 * j + q);
+                constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
+                p[q] = add2(make_float2(__uint_as_float(x[4 * j + 2 * q]), __uint_as_float(x[4 * j + 2 * q + 1])), ref);
+                p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
+                ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
+              }
+              const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y));
+              hi[j] = t.x;
+              lo[j] = t.y;
             }
-            const uint2 p01 = two_terms(p[0], p[1]), p23 = two_terms(p[2], p[3]);
-            hi[j] = p01.x | (p23.x << 16);
-            lo[j] = p01.y | (p23.y << 16);
+            const int ch = half * 2 + c;
+            *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          // the group's P is free once the products of its block before have been done
-          if (b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp], ((b >> 1) & 1) ^ 1)) != 0;
-          if (ok) {
-            uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int ch = half * 2 + c;
-              *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-            }
-            ptx::fence_proxy_async_smem();
-          }
+          ptx::tc_fence_before();
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
         }
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
         // done and before those of this one begin (which wait for them in any case).
@@ -794,14 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               }
             } else {
 #pragma unroll 1
-              for (int q = 0; q < 8; ++q) {
-                const uint32_t col = o + q * 32;
-                uint32_t r[32];
-                ptx::tmem_ld_32x32b_x32(col, r);
-                ptx::tmem_ld_wait_regs(r);
+              for (int q = 0; q < 16; ++q) {
+                uint32_t r[16];
+                tmem_ld_x16(o + q * 16, r);
+                tmem_ld_wait16(r);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f[(q & 1) * 32 + j]);
-                ptx::tmem_st_32x32b_x32(col, r);
+                for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f[(q & 3) * 16 + j]);
+                tmem_st_32x32b_x16(o + q * 16, r);
               }
             }
             ptx::tmem_st_wait();
@@ -825,21 +880,21 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         ok = __all_sync(0xffffffffu, (last == grp || wait(other, ((end - 1) >> 1) & 1)) &&
                                          wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
       const float fin = refv[last * kHeads + hl];
-      l = m == -INFINITY ? 0.f : l * ptx::ex2(m - fin);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (!half) lsum[grp * kHeads + hl] = l;
+      float sum = m == -INFINITY ? 0.f : (l.x + l.y) * ptx::ex2(m - fin);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (!half) lsum[grp * kHeads + hl] = sum;
       ptx::named_bar_sync(4, 256);
       const bool whole = pc.k0 == 0 && pc.k1 == pc.blocks;
       const int slot = 2 * part + (pc.k0 == 0 ? 1 : 0);
       if (grp == 0 && !half) {
-        l = lsum[hl] + lsum[kHeads + hl];
-        linv[hl] = l == 0.f ? 0.f : pow2f(kExpRef) / l;
+        sum = lsum[hl] + lsum[kHeads + hl];
+        linv[hl] = sum == 0.f ? 0.f : pow2f(kExpRef - 8) / sum;
         if (hl < hg && ok) {
           if (!whole) {
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin;
-            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = l;
+            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = sum;
           } else if (a.lse) {
-            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = l == 0.f ? -INFINITY : (fin - kPShift + log2f(l)) * kLn2;
+            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = sum == 0.f ? -INFINITY : (fin - (kPShift - 8) + log2f(sum)) * kLn2;
           }
         }
       }
@@ -847,31 +902,31 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       if (ok) {
         ptx::tc_fence_after();
         const int lat = w * 32 + lane;
+        const bool odd = lane & 1;
 #pragma unroll 1
-        for (int c = 2 * grp; c < 2 * grp + 2; ++c) {
-#pragma unroll 1
-          for (int h0 = 0; h0 < hg; h0 += 32) {
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(tmem + lane_addr + kColO + c * kHeads + h0, r);
-            ptx::tmem_ld_wait_regs(r);
-            if (whole) {
-              // pairs of lanes swap, so that each stores two latent values of one head
-              uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128) + (lat >> 1);
-              const bool odd = lane & 1;
+        for (int q = 0; q < 8; ++q) {  // this group's two latent chunks, 16 heads at a time
+          const int c = 2 * grp + (q >> 2), h0 = (q & 3) * 16;
+          if (h0 >= hg) continue;
+          uint32_t r[16];
+          tmem_ld_x16(tmem + lane_addr + kColO + c * kHeads + h0, r);
+          tmem_ld_wait16(r);
+          if (whole) {
+            // pairs of lanes swap, so that each stores two latent values of one head
+            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0 + odd) * kRank + c * 128) + (lat >> 1);
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float v0 = __uint_as_float(r[j]) * linv[h0 + j], v1 = __uint_as_float(r[j + 1]) * linv[h0 + j + 1];
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                if (h0 + j + odd < hg) o[(j + odd) * (kRank / 2)] = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
-              }
-            } else {
-              float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (h0 + 4 * j < hg)
-                  o[j * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
-                                           __uint_as_float(r[4 * j + 3]));
+            for (int j = 0; j < 16; j += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(linv + h0 + j);
+              const float v0 = __uint_as_float(r[j]) * f.x, v1 = __uint_as_float(r[j + 1]) * f.y;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+              if (h0 + j + odd < hg) o[j * (kRank / 2)] = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
             }
+          } else {
+            float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (h0 + 4 * j < hg)
+                o[j * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                         __uint_as_float(r[4 * j + 3]));
           }
         }
         ptx::tc_fence_before();
@@ -932,8 +987,8 @@ __global__ void __launch_bounds__(128) quant_join_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (h0 + i >= a.H) continue;
-    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : ldexpf(acc[i] / W[i], kExpRef));
-    if (chunk == 0 && threadIdx.x == i && a.lse) a.lse[row + i] = W[i] == 0.f ? -INFINITY : (M[i] - kPShift + log2f(W[i])) * kLn2;
+    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : ldexpf(acc[i] / W[i], kExpRef - 8));
+    if (chunk == 0 && threadIdx.x == i && a.lse) a.lse[row + i] = W[i] == 0.f ? -INFINITY : (M[i] - (kPShift - 8) + log2f(W[i])) * kLn2;
   }
 }
 
