@@ -61,11 +61,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr long long kMostKeys = 0x7FFFFF00ll;             // that a query sees: a block's last key fits 32 bits
 constexpr int kMaxStages = 4;
 constexpr int kQRing = 4;                                 // scales of the queries of consecutive pieces
-constexpr int kBatch = 4, kBatches = 4, kRing = kBatch * kBatches;  // blocks whose rows are looked up together
+constexpr int kBatch = 4, kBatches = 4, kRing = kBatch * kBatches;  // blocks of a piece whose rows are looked up together
 
 template <bool FP4>
 struct Smem {
   static constexpr int kStages = FP4 ? 3 : 4;             // tiles
+  static constexpr int kAhead = kStages - 2;              // blocks that S runs ahead of P . V: a tile is always left to fill
   static constexpr int kStagedBufs = FP4 ? 2 : 0;
   static constexpr int kScRing = FP4 ? kStages : kRing;   // blocks whose scales are held
   static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
@@ -76,10 +77,12 @@ struct Smem {
 static_assert(Smem<false>::kBytes <= 232448 && Smem<true>::kBytes <= 232448, "shared memory of a CTA");
 
 struct Args {
-  int B, total_q, H, groups, page_size, page_log2, num_pages, max_pages, topk_width;
+  int B, total_q, H, groups, page_size, num_pages, max_pages, topk_width;
   int nb;                  // blocks of a tile (selected keys); 0: from the plan
   int parts;               // CTAs
   int past_row;            // a row past the cache: copies from there are zeros
+  unsigned long long page_mul;  // position / page_size = position * page_mul >> page_shift
+  int page_shift;
   float scale_log2;        // scale * log2(e)
   const __nv_bfloat16 *qn, *qr;
   long long qn_t, qn_h, qr_t, qr_h;
@@ -89,6 +92,7 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   float *part_o, *part_ml; // pieces: [slot][4][16][128][4] (latent chunk, four heads, latent, head), [slot][64][2]
+  int2* joins;             // [parts] the tile that a part begins inside, if no earlier one does (-1: none), its last part
   unsigned* status;
 };
 
@@ -101,28 +105,24 @@ struct Bars {
   uint64_t hand0[4], hand1[4];            // the reference after a block of group 0, 1, to the other group's warp
 };
 
-// Keys of query t (every position): those up to its own that the table covers.
-__device__ __forceinline__ long long keys_of(const Args& a, int t, int* b_out, unsigned* bad) {
-  if (t >= __ldg(a.cu + a.B)) {
-    *b_out = 0;
-    return 0;
-  }
-  const int b = sequence_of(a.cu, a.B, t);
-  *b_out = b;
-  long long n = static_cast<long long>(__ldg(a.lens + b)) - __ldg(a.cu + b + 1) + t + 1;
-  const long long room = min(static_cast<long long>(a.max_pages) * a.page_size, kMostKeys);
-  if (n > room) {
-    *bad = 1;
-    n = room;
-  }
-  return n < 0 ? 0 : n;
+// Keys that a query at place i of the last q of n tokens sees (every position): those up to its own that the table
+// covers.
+__device__ __forceinline__ long long keys_seen(const Args& a, long long pos, bool report) {
+  const long long n = pos + 1, room = min(static_cast<long long>(a.max_pages) * a.page_size, kMostKeys);
+  if (n > room && report) atomicOr(a.status, kStatusUncovered);
+  return max(0ll, min(n, room));
 }
 
 // The line of all blocks: tile w = (query w / groups, heads 64 (w % groups) ..) holds the places
-// tile_begin(w) .. tile_begin(w + 1) - 1, part c the places part_begin(c) .. part_begin(c + 1) - 1.
+// tile_begin(w) .. tile_begin(w + 1) - 1; the parts are of `size` places, the first `more` of them of one more.
 struct Line {
-  long long total;
-  int parts;
+  long long size;
+  int more, parts;
+  __device__ __forceinline__ long long begin(int c) const { return size * c + min(c, more); }
+  __device__ __forceinline__ int part_at(long long u) const {
+    const long long first = (size + 1) * more;
+    return static_cast<int>(u < first ? u / (size + 1) : more + (u - first) / size);
+  }
 };
 __device__ __forceinline__ long long tile_begin(const Args& a, int w) {
   if (a.nb) return static_cast<long long>(w) * a.nb;
@@ -131,12 +131,13 @@ __device__ __forceinline__ long long tile_begin(const Args& a, int w) {
   return c0 * a.groups + (g ? g * (__ldg(a.cum + t + 1) - c0) : 0);
 }
 __device__ __forceinline__ Line line_of(const Args& a) {
+  const long long total = tile_begin(a, a.total_q * a.groups);
   Line l;
-  l.total = tile_begin(a, a.total_q * a.groups);
-  l.parts = static_cast<int>(min(static_cast<long long>(a.parts), l.total));
+  l.parts = static_cast<int>(min(static_cast<long long>(a.parts), total));
+  l.size = total / l.parts;
+  l.more = static_cast<int>(total - l.size * l.parts);
   return l;
 }
-__device__ __forceinline__ long long part_begin(const Line& l, int c) { return l.total * c / l.parts; }
 // The tile that holds place u.
 __device__ __forceinline__ int tile_at(const Args& a, long long u) {
   if (a.nb) return static_cast<int>(u / a.nb);
@@ -153,8 +154,8 @@ struct Pieces {
   long long u, end, t_end;  // the next piece's first place, the part's end, its tile's end
   int w, t, g, k0, k1, blocks;  // the current piece: blocks k0 .. k1 - 1 of `blocks`
   __device__ __forceinline__ Pieces(const Args& a, const Line& l, int c) {
-    u = c < l.parts ? part_begin(l, c) : 0;
-    end = c < l.parts ? part_begin(l, c + 1) : 0;
+    u = c < l.parts ? l.begin(c) : 0;
+    end = c < l.parts ? l.begin(c + 1) : 0;
     w = u < end ? tile_at(a, u) : 0;
     --w;
     t_end = u;
@@ -174,27 +175,33 @@ struct Pieces {
   }
 };
 
-// The keys of a query: the position of each, -1 where there is none.
+// A piece's blocks are looked up in batches: how many, and whether block i (from the piece's first) ends one.
+__device__ __forceinline__ int batches(const Pieces& p) { return (p.k1 - p.k0 + kBatch - 1) / kBatch; }
+__device__ __forceinline__ bool last_of_batch(const Pieces& p, int i) { return i % kBatch == kBatch - 1 || i == p.k1 - p.k0 - 1; }
+// The keys of a query: the position of each, -1 where there is none.  Queries come in ascending order, so the request is
+// searched for once and then walked to.
 struct Keys {
-  int b, len;
-  long long n;  // keys (every position)
-  const int32_t* sel;
-  const int32_t* table;
-  __device__ __forceinline__ Keys(const Args& a, int t, bool report) {
-    unsigned bad = 0;
-    if (a.nb) {
-      const bool live = t < __ldg(a.cu + a.B);
-      b = live ? sequence_of(a.cu, a.B, t) : 0;
-      len = live ? __ldg(a.lens + b) : 0;
-      n = a.topk_width;
-      sel = a.topk + static_cast<long long>(t) * a.topk_width;
+  int t = -1, b = -1, lo = 0, hi = 0, len = 0, live = 0;
+  long long n = 0;  // keys (every position)
+  const int32_t* sel = nullptr;
+  const int32_t* table = nullptr;
+  __device__ __forceinline__ void move(const Args& a, int query, bool report) {
+    if (query == t) return;
+    t = query;
+    if (b < 0) {
+      live = __ldg(a.cu + a.B);  // rows of queries; the others are padding
+      b = t < live ? sequence_of(a.cu, a.B, t) : 0;
+      hi = t;
     } else {
-      n = keys_of(a, t, &b, &bad);
-      len = 0;
-      sel = nullptr;
+      while (t < live && t >= hi && b + 1 < a.B && __ldg(a.cu + b + 1) <= t) ++b;
     }
-    if (bad && report) atomicOr(a.status, kStatusUncovered);
+    if (t < live && t >= hi) {
+      hi = __ldg(a.cu + b + 1);
+      len = __ldg(a.lens + b);
+    }
     table = a.block_tables + static_cast<long long>(b) * a.max_pages;
+    sel = a.topk + static_cast<long long>(t) * a.topk_width;
+    n = t >= live ? 0 : a.nb ? a.topk_width : keys_seen(a, static_cast<long long>(len) - hi + t, report);
   }
   __device__ __forceinline__ int position(const Args& a, int key) const {
     if (key >= n) return -1;
@@ -203,16 +210,13 @@ struct Keys {
     return s < len ? s : -1;
   }
 };
-// The cache row of a position, through a request's table; a.past_row where there is none.
-__device__ __forceinline__ int row_of(const Args& a, const int32_t* table, int pos) {
-  if (pos < 0) return a.past_row;
-  const int lp = a.page_log2 >= 0 ? pos >> a.page_log2 : pos / a.page_size;
-  const int page = lp < a.max_pages ? __ldg(table + lp) : -1;
-  if (page < 0 || page >= a.num_pages) {
-    atomicOr(a.status, kStatusBadPage);
-    return a.past_row;
-  }
-  return page * a.page_size + (pos - lp * a.page_size);
+// The cache row of a position, through a request's table; a.past_row where there is none (*bad: its page is not there).
+__device__ __forceinline__ int row_of(const Args& a, const int32_t* table, int pos, bool* bad) {
+  const int lp = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(pos)) * a.page_mul >> a.page_shift);
+  const int page = pos >= 0 && lp < a.max_pages ? __ldg(table + lp) : -1;
+  const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);
+  *bad |= pos >= 0 && !there;
+  return there ? page * a.page_size + (pos - lp * a.page_size) : a.past_row;
 }
 
 // D[tmem] (+)= A . B[smem]^T: A e4m3 in TMEM, e4m3 or bf16 in shared memory.  Operands in shared memory are given by the
@@ -282,6 +286,24 @@ __device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b) {
   return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531),
                     __byte_perm(*reinterpret_cast<const uint32_t*>(&la) + 0x00800080u,
                                 *reinterpret_cast<const uint32_t*>(&lb) + 0x00800080u, 0x7531));
+}
+// Four values |x| < 2^8, given as 2^-8 x in fp16, as e4m3 codes (x) and as those of 2^kLoShift times what they leave (y).
+__device__ __forceinline__ uint32_t e4m3_bytes(uint32_t a, uint32_t b) {  // fp16 bits, rounded to three of the mantissa
+  return __byte_perm(a << 1, b << 1, 0x7531) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+}
+__device__ __forceinline__ uint32_t round_e4m3(__half2 v) {
+  return (*reinterpret_cast<const uint32_t*>(&v) + 0x00400040u) & 0xFF80FF80u;
+}
+__device__ __forceinline__ uint2 two_planes(__half2 a, __half2 b) {
+  const uint32_t ra = round_e4m3(a), rb = round_e4m3(b);
+  const __half2 up = __float2half2_rn(1 << kLoShift);
+  return make_uint2(e4m3_bytes(ra, rb), e4m3_bytes(round_e4m3(__hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ra)), up)),
+                                                   round_e4m3(__hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&rb)), up))));
+}
+// The largest magnitudes among 8 bf16 values, in two halves.
+__device__ __forceinline__ __nv_bfloat162 most(const uint4& v) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+  return __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
 }
 // Scale u = 2^E of a block's row `key` (0: no row, which takes no weight).
 __device__ __forceinline__ void put_scale(float4* block, int key, float u) {
@@ -416,8 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads);
         const uint32_t id_pv = ptx::idesc_f32acc(128, (hg + 15) & ~15, false) | (1u << 15);
         ok = wait(&bars->qfull[n % kQRing], (n / kQRing) & 1);
-        // S runs two blocks ahead: both groups of softmax warps have their next block when they are done with one.
-        for (int i = 0; i < cnt + 2 && ok; ++i) {
+        for (int i = 0; i < cnt + L::kAhead && ok; ++i) {
           if (i < cnt) {  // S of block i
             const int b = it + i;
             ok = wait(&bars->tfull[b % kStages], (b / kStages) & 1) && (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
@@ -434,9 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             ptx::mma_commit(&bars->sfull[b & 1]);
             if (i == cnt - 1) ptx::mma_commit(&bars->qfree);
           }
-          if (i < 2) continue;
-          const int b = it + i - 2;  // P . V of the block before the last
-          ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (i > 2 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
+          const int j = i - L::kAhead;  // P . V of an earlier block
+          if (j < 0) continue;
+          const int b = it + j;
+          ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (j > 0 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
           if (!ok) break;
           ptx::tc_fence_after();
           uint32_t vd = tile0 + (b % kStages) * (kTile >> 4), pd = p0 + (b & 1) * (kPBytes >> 4);
@@ -446,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 32 keys per MMA
               const uint32_t ad = vd + ((c * kAtom + s * 4096) >> 4);
-              mma_f8_ss(tmem + kColO + c * kHeads, ad, pd + 2 * s, id_pv, (i > 2 || s > 0) ? 1u : 0u);
+              mma_f8_ss(tmem + kColO + c * kHeads, ad, pd + 2 * s, id_pv, (j > 0 || s > 0) ? 1u : 0u);
               mma_f8_ss(tmem + kColO + c * kHeads, ad, pd + 4 + 2 * s, id_pv | kBe5m2, 1u);
             }
           }
@@ -464,19 +486,19 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     // ------------------------------------------------------------ rows of the cache, half of each block
     const int first = warp == 12 ? 0 : 8;  // groups of four rows
     constexpr int kBufs = FP4 ? 2 : kStages;
-    int it = 0;
+    int it = 0, bn = 0;  // blocks, batches before this piece
     bool ok = true;
-    while (ok && pc.next(a)) {
-      for (int k = pc.k0; k < pc.k1; ++k, ++it) {
-        const int bt = (it / kBatch) % kBatches, st = it % kBufs;
+    for (; ok && pc.next(a); bn += batches(pc)) {
+      for (int i = 0; i < pc.k1 - pc.k0; ++i, ++it) {
+        const int bi = bn + i / kBatch, bt = bi % kBatches, st = it % kBufs;
         uint64_t* full = FP4 ? &bars->gfull[st] : &bars->tfull[st];
-        ok = wait(&bars->rfull[bt], (it / kRing) & 1) &&
+        ok = (i % kBatch || wait(&bars->rfull[bt], (bi / kBatches) & 1)) &&
              (it < kBufs || wait(FP4 ? &bars->gempty[st] : &bars->tempty[st], ((it / kBufs) & 1) ^ 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(full, (FP4 ? kStaged : kTile) / 2);
-          const int4* y4 = reinterpret_cast<const int4*>(rows + (it % kRing) * kKeys) + first;
+          const int4* y4 = reinterpret_cast<const int4*>(rows + (bt * kBatch + i % kBatch) * kKeys) + first;
 #pragma unroll 4
           for (int g = 0; g < 8; ++g) {
             const int4 v = y4[g];
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
                 tma_gather4(smem + L::kOffTile + st * kTile + c * kAtom + (first + g) * 512, &tmap, full, c * 64, y);
             }
           }
-          if (it % kBatch == kBatch - 1) ptx::mbar_arrive(&bars->bempty[bt]);
+          if (last_of_batch(pc, i)) ptx::mbar_arrive(&bars->bempty[bt]);
         }
         __syncwarp();
       }
@@ -499,47 +521,69 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       ptx::mbar_spin_drain(FP4 ? &bars->gfull[i % kBufs] : &bars->tfull[i % kBufs], (i / kBufs) & 1, a.status, kStatusTimeout, 400000000ll);
   } else if (warp == 14) {
     // ------------------------------------------------------------ where the rows lie; scales of e4m3 rows
-    bool more = pc.next(a);
-    Keys keys(a, more ? pc.t : 0, lane == 0 && more);
-    int k = pc.k0;
-    for (int it = 0; more; it += kBatch) {
-      int y[2 * kBatch];
-      const int32_t* table[kBatch];
+    // A batch's loads pass behind each other: positions of the next batch and pages of this one together, then the
+    // scales of this one behind the next one's.
+    Keys keys;
+    int k = 0, bi = 0;
+    int pos[2 * kBatch];
+    float u[2 * kBatch];
+    const int32_t* table = nullptr;
+    auto scales = [&](int bt) {
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        y[2 * j] = y[2 * j + 1] = -1;
-        table[j] = keys.table;
-        if (!more) continue;
-        y[2 * j] = keys.position(a, k * kKeys + lane);
-        y[2 * j + 1] = keys.position(a, k * kKeys + 32 + lane);
-        if (++k == pc.k1) {
-          more = pc.next(a);
-          if (more) keys = Keys(a, pc.t, lane == 0);
+      for (int j = 0; j < 2 * kBatch; ++j) put_scale(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane, u[j]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
+    };
+    bool have = false, ok = true, bad = false;
+    pc.k1 = 0;
+    for (;;) {
+      int y[2 * kBatch];
+#pragma unroll
+      for (int j = 0; j < 2 * kBatch; ++j) y[j] = pos[j];
+      const int32_t* rows_of = table;
+      bool more = true;  // the next batch's positions
+      if (k >= pc.k1) {
+        more = pc.next(a);
+        if (more) {
+          keys.move(a, pc.t, lane == 0);
           k = pc.k0;
+          if (!have && part > 0 && lane == 0) {  // the join's part of the plan
+            const bool inside = k > 0 && line.begin(part - 1) <= pc.t_end - pc.blocks;
+            a.joins[part] = inside ? make_int2(pc.w, line.part_at(pc.t_end - 1)) : make_int2(-1, 0);
+          }
         }
       }
+      if (more) {
+        table = keys.table;
 #pragma unroll
-      for (int j = 0; j < 2 * kBatch; ++j) y[j] = row_of(a, table[j >> 1], y[j]);
-      const int bt = (it / kBatch) % kBatches;
-      bool ok = it < kRing || wait(&bars->bempty[bt], ((it / kRing) & 1) ^ 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-#pragma unroll
-      for (int j = 0; j < 2 * kBatch; ++j) rows[(bt * kBatch + (j >> 1)) * kKeys + 32 * (j & 1) + lane] = y[j];
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bars->rfull[bt]);
-      if constexpr (!FP4) {
-        float u[2 * kBatch];
-  #pragma unroll
         for (int j = 0; j < 2 * kBatch; ++j)
-          u[j] = y[j] != a.past_row ? __ldg(reinterpret_cast<const float*>(a.cache + static_cast<long long>(y[j]) * kRow8 + kScale8)) : 0.f;
-  #pragma unroll
-        for (int j = 0; j < 2 * kBatch; ++j)
-          put_scale(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane, u[j]);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
+          pos[j] = k + (j >> 1) < pc.k1 ? keys.position(a, (k + (j >> 1)) * kKeys + 32 * (j & 1) + lane) : -1;
+        k += kBatch;
       }
+      if (have) {
+#pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j) y[j] = row_of(a, rows_of, y[j], &bad);
+        const int bt = bi % kBatches;
+        if (!FP4 && bi) scales((bt + kBatches - 1) % kBatches);
+        ok = bi < kBatches || wait(&bars->bempty[bt], ((bi / kBatches) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j) rows[(bt * kBatch + (j >> 1)) * kKeys + 32 * (j & 1) + lane] = y[j];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->rfull[bt]);
+        if constexpr (!FP4) {
+#pragma unroll
+          for (int j = 0; j < 2 * kBatch; ++j)
+            u[j] = y[j] != a.past_row ? __ldg(reinterpret_cast<const float*>(a.cache + static_cast<long long>(y[j]) * kRow8 + kScale8)) : 0.f;
+        }
+        ++bi;
+      }
+      have = more;
+      if (!more) break;
     }
+    if (!FP4 && ok && bi) scales((bi + kBatches - 1) % kBatches);
+    if (bad) atomicOr(a.status, kStatusBadPage);
   } else if (warp >= 8) {
     // ------------------------------------------------------------ queries; tiles of 4-bit rows
     const int w = warp - 8;
@@ -552,51 +596,42 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
 #pragma unroll
       for (int c = 0; c < 4; ++c) qr[c * 32 + lane] = make_uint4(0u, 0u, 0u, 0u);
     }
-    int it = 0, n = 0;
+    int it = 0, n = 0, bn = 0;
     bool ok = true;
-    while (ok && pc.next(a)) {
+    for (; ok && pc.next(a); bn += batches(pc)) {
       const uint4* src[4];
       bool live[4];
-      uint4 rp[4];
-      float am[4];
+      uint4 rp[4], r[4][4];
+      __nv_bfloat162 am[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int h = pc.g * kHeads + w * 16 + 4 * i + hr;
         live[i] = h < a.H;
         src[i] = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live[i] ? h : 0) * a.qn_h) + l8;
         rp[i] = live[i] ? __ldg(reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + h * a.qr_h) + l8) : make_uint4(0u, 0u, 0u, 0u);
-        am[i] = 0.f;
+        am[i] = most(rp[i]);
       }
       auto load = [&](int c, uint4 (&v)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = live[i] ? __ldg(src[i] + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
       };
-      auto most = [&](const uint4 (&v)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[8];
-          unpack_bf16(v[i], x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) am[i] = fmaxf(am[i], fabsf(x[j]));
-        }
-      };
-      // (the chunks that the conversion begins with come last)
-      uint4 v[2][4];
 #pragma unroll 1
-      for (int c = 6; c >= 0; c -= 2) {
-        load(c, v[0]);
-        load(c + 1, v[1]);
-        most(v[0]);
-        most(v[1]);
+      for (int c = 4; c >= 0; c -= 4) {  // (the chunks that the conversion begins with come last, and stay)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load(c + q, r[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) am[i] = __hmax2(am[i], most(r[q][i]));
       }
-      most(rp);
       // the power of two that takes the row's largest value to [128, 256)
       float f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        float m = fmaxf(__low2float(am[i]), __high2float(am[i]));
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) am[i] = fmaxf(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
-        const int e = am[i] > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(am[i]) >> 23) - 127))) : 0;
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = m > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127))) : 0;
         f[i] = pow2f(e);
         if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = a.scale_log2 * pow2f(-e);
       }
@@ -616,40 +651,35 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
                        pack_bf16(x[4] * f[i], x[5] * f[i]), pack_bf16(x[6] * f[i], x[7] * f[i]));
       }
       // 64 values of every row at a time: codes to shared memory, from there by rows to TMEM
-      auto convert = [&](int c, const uint4 (&v)[4]) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[8];
-          unpack_bf16(v[i], x);
+          unpack_bf16(r[0][i], x);
+          const float g = f[i] * (1.f / 256.f);
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float v0 = x[4 * j] * f[i], v1 = x[4 * j + 1] * f[i], v2 = x[4 * j + 2] * f[i], v3 = x[4 * j + 3] * f[i];
-            const uint32_t h01 = e4m3x2(v0, v1), h23 = e4m3x2(v2, v3);
-            const float2 b01 = from_e4m3x2(h01), b23 = from_e4m3x2(h23);
-            constexpr float up = 1 << kLoShift;
-            hi[j] = h01 | (h23 << 16);
-            lo[j] = e4m3x2((v0 - b01.x) * up, (v1 - b01.y) * up) | (e4m3x2((v2 - b23.x) * up, (v3 - b23.y) * up) << 16);
+            const uint2 p = two_planes(__floats2half2_rn(x[4 * j] * g, x[4 * j + 1] * g), __floats2half2_rn(x[4 * j + 2] * g, x[4 * j + 3] * g));
+            hi[j] = p.x;
+            lo[j] = p.y;
           }
           *reinterpret_cast<uint2*>(qbuf + (4 * i + hr) * kQStride + l8 * 8) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(qbuf + (16 + 4 * i + hr) * kQStride + l8 * 8) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) r[q][i] = r[q + 1][i];
         }
+        if (c < 4) load(4 + c, r[3]);
         __syncwarp();
-        uint32_t r[16];
+        uint32_t t[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 q = *reinterpret_cast<const uint4*>(qbuf + lane * kQStride + 16 * j);
-          r[4 * j] = q.x, r[4 * j + 1] = q.y, r[4 * j + 2] = q.z, r[4 * j + 3] = q.w;
+          t[4 * j] = q.x, t[4 * j + 1] = q.y, t[4 * j + 2] = q.z, t[4 * j + 3] = q.w;
         }
-        tmem_st_32x32b_x16(tmem + lane_addr + kColQ + 16 * c, r);
+        tmem_st_32x32b_x16(tmem + lane_addr + kColQ + 16 * c, t);
         __syncwarp();
-      };
-#pragma unroll 1
-      for (int c = 0; c < 8; c += 2) {
-        convert(c, v[0]);
-        if (c < 6) load(c + 2, v[0]);
-        convert(c + 1, v[1]);
-        if (c < 6) load(c + 3, v[1]);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
@@ -659,16 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       ++n;
       if constexpr (FP4) {
         // 4-bit rows: a warp takes 16 rows of a block, a lane a block of 16 values
-        for (int k = pc.k0; k < pc.k1; ++k, ++it) {
-          const int st = it % kStages, gs = it & 1, bt = (it / kBatch) % kBatches;
+        for (int i = 0; i < pc.k1 - pc.k0; ++i, ++it) {
+          const int st = it % kStages, gs = it & 1, bt = (bn + i / kBatch) % kBatches;
           ok = wait(&bars->gfull[gs], (it >> 1) & 1) && (it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const bool there = rows[(it % kRing) * kKeys + w * 16 + (lane & 15)] != a.past_row;  // of key 16 w + lane
+          const bool there = rows[(bt * kBatch + i % kBatch) * kKeys + w * 16 + (lane & 15)] != a.past_row;  // of key 16 w + lane
           const uint8_t* staged = smem + L::kOffStaged + gs * kStaged + w * 16 * kRow4;
           uint8_t* tile = smem + L::kOffTile + st * kTile;
           int E = 0;
-  #pragma unroll
+  #pragma unroll 1
           for (int i0 = 0; i0 < 16; i0 += 8) {
             uint2 q[8], lv[8];
             int byte[8];
@@ -705,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             ptx::mbar_arrive(&bars->gempty[gs]);
             ptx::mbar_arrive(&bars->scfull[st]);
             ptx::mbar_arrive(&bars->tfull[st]);
-            if (it % kBatch == kBatch - 1) ptx::mbar_arrive(&bars->bempty[bt]);
+            if (last_of_batch(pc, i)) ptx::mbar_arrive(&bars->bempty[bt]);
           }
         }
       }
@@ -716,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     const uint32_t lane_addr = static_cast<uint32_t>(w * 32) << 16;
     uint64_t* mine = grp ? &bars->hand1[w] : &bars->hand0[w];
     uint64_t* other = grp ? &bars->hand0[w] : &bars->hand1[w];
-    int it = 0, n = 0;
+    int it = 0, n = 0, bn = 0;
     bool ok = true;
     // Every piece and block runs its named barriers whatever happened, so that a wait that gave up leaves no
     // warp behind at one.
@@ -731,14 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         qo.x = qo.y = half ? qs : qs * (1.f / (1 << kLoShift));
       }
       for (int b = it + ((it ^ grp) & 1); b < end; b += 2) {
-        const int ss = FP4 ? b % kStages : b % kRing;
+        const int bi = bn + (b - it) / kBatch, bt = bi % kBatches;
+        const int ss = FP4 ? b % kStages : bt * kBatch + (b - it) % kBatch;
         const uint32_t col = tmem + lane_addr + kColS + grp * kKeys;
         const float4* scp = sc + ss * (kKeys / 2) + half * 16;
         float cr = 1.f;
         if (ok)
           ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
                                            (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
-                                                : wait(&bars->scfull[(b / kBatch) % kBatches], (b / kRing) & 1))) != 0;
+                                                : wait(&bars->scfull[bt], (bi / kBatches) & 1))) != 0;
         if (ok) {
           // x' of the block, 16 keys at a time (the hi lane takes keys 0..31, the lo lane 32..63), back over S.
           // Both passes are loops: as straight code the two groups' block is more than an SM's schedulers hold of
@@ -868,14 +899,17 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) {
             ptx::mbar_arrive(&bars->pfull[grp]);
-            if (!FP4 && (b % kBatch) >> 1 == kBatch / 2 - 1) ptx::mbar_arrive(&bars->bempty[(b / kBatch) % kBatches]);
+            if (!FP4 && ((b - it) % kBatch >= kBatch - 2 || b + 2 >= end)) ptx::mbar_arrive(&bars->bempty[bt]);
           }
         }
       }
       it = end;
       ++n;
+      bn += batches(pc);
       // the piece's output: the sums of both groups against the last reference
       const int last = (end - 1) & 1;
+      // (a batch of one block is one group's)
+      if (!FP4 && cnt % kBatch == 1 && last != grp && lane == 0) ptx::mbar_arrive(&bars->bempty[(bn - 1) % kBatches]);
       if (ok)
         ok = __all_sync(0xffffffffu, (last == grp || wait(other, ((end - 1) >> 1) & 1)) &&
                                          wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
@@ -902,7 +936,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       if (ok) {
         ptx::tc_fence_after();
         const int lat = w * 32 + lane;
-        const bool odd = lane & 1;
 #pragma unroll 1
         for (int q = 0; q < 8; ++q) {  // this group's two latent chunks, 16 heads at a time
           const int c = 2 * grp + (q >> 2), h0 = (q & 3) * 16;
@@ -911,15 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           tmem_ld_x16(tmem + lane_addr + kColO + c * kHeads + h0, r);
           tmem_ld_wait16(r);
           if (whole) {
-            // pairs of lanes swap, so that each stores two latent values of one head
-            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0 + odd) * kRank + c * 128) + (lat >> 1);
+            __nv_bfloat16* o = a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128 + lat;
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(linv + h0 + j);
-              const float v0 = __uint_as_float(r[j]) * f.x, v1 = __uint_as_float(r[j + 1]) * f.y;
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-              if (h0 + j + odd < hg) o[j * (kRank / 2)] = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
-            }
+            for (int j = 0; j < 16; ++j)
+              if (h0 + j < hg) o[j * kRank] = __float2bfloat16_rn(__uint_as_float(r[j]) * linv[h0 + j]);
           } else {
             float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
 #pragma unroll
@@ -943,69 +971,186 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   }
 }
 
-// out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) L_j over the pieces of a tile, in their order.  Block (c - 1, y): the
-// tile that part c begins inside, if no earlier part does; y: four heads, a latent chunk.
-__global__ void __launch_bounds__(128) quant_join_kernel(const Args a) {
+// out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) L_j over the pieces of a tile, in their order.  The tiles are listed by
+// the parts that begin inside them.  Of a tile of few pieces a warp takes four heads of a latent chunk, a lane four
+// latent values of each; of many, a CTA, its warps four chunks of every fourth piece.
+constexpr int kJoinThreads = 512, kFewPieces = 16, kMaxParts = 512;
+__device__ __forceinline__ void add_piece(float4& acc, float4 f, float4 v) {  // (a piece without keys may hold anything)
+  acc.x = fmaf(f.x, f.x == 0.f ? 0.f : v.x, acc.x);
+  acc.y = fmaf(f.y, f.y == 0.f ? 0.f : v.y, acc.y);
+  acc.z = fmaf(f.z, f.z == 0.f ? 0.f : v.z, acc.z);
+  acc.w = fmaf(f.w, f.w == 0.f ? 0.f : v.w, acc.w);
+}
+__device__ __forceinline__ float4 warp_sum4(float4 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  return v;
+}
+__device__ __forceinline__ float4 warp_max4(float4 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+    v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+    v.z = fmaxf(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+    v.w = fmaxf(v.w, __shfl_xor_sync(0xffffffffu, v.w, o));
+  }
+  return v;
+}
+__global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) {
+  __shared__ int2 joins[kMaxParts];
+  __shared__ int4 few[kMaxParts], many[kMaxParts];  // tile, first part, pieces
+  __shared__ float4 weights[kMaxParts], sums[4][128];
+  __shared__ int n_few, n_many;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const Line line = line_of(a);
-  const int c = blockIdx.x + 1, quad = blockIdx.y & 15, chunk = blockIdx.y >> 4;
-  if (c >= line.parts) return;
-  const long long u = part_begin(line, c);
-  const int w = tile_at(a, u);
-  const long long b = tile_begin(a, w), e = tile_begin(a, w + 1);
-  if (b == u || part_begin(line, c - 1) > b) return;
-  const int t = w / a.groups, g = w - t * a.groups, h0 = g * kHeads + quad * 4;
-  if (h0 >= a.H) return;
-  int last = c;
-  while (last + 1 < line.parts && part_begin(line, last + 1) < e) ++last;
-  float M[4], W[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) M[i] = -INFINITY;
-  for (int j = c - 1; j <= last; ++j) {
-    const float* ml = a.part_ml + (static_cast<long long>(2 * j + (j == c - 1 ? 1 : 0)) * kHeads + quad * 4) * 2;
+  if (tid < line.parts) joins[tid] = tid ? a.joins[tid] : make_int2(-1, 0);
+  __syncthreads();
+  if (warp == 0) {
+    int nf = 0, nm = 0;
+    for (int c0 = 0; c0 < line.parts; c0 += 32) {
+      const int c = c0 + lane;
+      const int2 r = c < line.parts ? joins[c] : make_int2(-1, 0);
+      const int n = r.y - c + 2;
+      const unsigned f = __ballot_sync(0xffffffffu, r.x >= 0 && n <= kFewPieces), m = __ballot_sync(0xffffffffu, r.x >= 0 && n > kFewPieces);
+      const unsigned below = (1u << lane) - 1;
+      if (f >> lane & 1) few[nf + __popc(f & below)] = make_int4(r.x, c - 1, n, 0);
+      if (m >> lane & 1) many[nm + __popc(m & below)] = make_int4(r.x, c - 1, n, 0);
+      nf += __popc(f);
+      nm += __popc(m);
+    }
+    if (lane == 0) n_few = nf, n_many = nm;
+  }
+  __syncthreads();
+  auto slot = [](int c0, int j) { return static_cast<long long>(2 * (c0 + j) + (j == 0 ? 1 : 0)); };
+  auto stats = [&](int c0, int j, int quad, float4* m, float4* l) {
+    const float4* ml = reinterpret_cast<const float4*>(a.part_ml + (slot(c0, j) * kHeads + quad * 4) * 2);
+    const float4 x = ml[0], y = ml[1];
+    *m = make_float4(x.x, x.z, y.x, y.z);
+    *l = make_float4(x.y, x.w, y.y, y.w);
+  };
+  // weight of a piece against the tile's maximum, and its part of the sum
+  auto weigh = [](float4 m, float4 M, float4 l, float4* f) {
+    *f = make_float4(m.x == -INFINITY ? 0.f : exp2f(m.x - M.x), m.y == -INFINITY ? 0.f : exp2f(m.y - M.y),
+                     m.z == -INFINITY ? 0.f : exp2f(m.z - M.z), m.w == -INFINITY ? 0.f : exp2f(m.w - M.w));
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    add_piece(s, *f, l);
+    return s;
+  };
+  auto store = [&](int t, int h0, int lat, float4 acc, float4 total) {
+    const float v[4] = {acc.x, acc.y, acc.z, acc.w}, s[4] = {total.x, total.y, total.z, total.w};
+    __nv_bfloat16* dst = a.out + (static_cast<long long>(t) * a.H + h0) * kRank + lat;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (h0 + i < a.H) M[i] = fmaxf(M[i], ml[2 * i]);
-  }
-  for (int j = c - 1; j <= last; ++j) {
-    const long long slot = 2 * j + (j == c - 1 ? 1 : 0);
-    const float* ml = a.part_ml + (slot * kHeads + quad * 4) * 2;
-    const float4 o = reinterpret_cast<const float4*>(a.part_o)[((slot * 4 + chunk) * 16 + quad) * 128 + threadIdx.x];
-    const float v[4] = {o.x, o.y, o.z, o.w};
+      if (h0 + i < a.H) dst[i * kRank] = __float2bfloat16_rn(s[i] == 0.f ? 0.f : v[i] / s[i] * pow2f(kExpRef - 8));
+  };
+  auto store_lse = [&](int t, int h0, float4 M, float4 total) {
+    const float m[4] = {M.x, M.y, M.z, M.w}, s[4] = {total.x, total.y, total.z, total.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (h0 + i >= a.H) continue;
-      const float mj = ml[2 * i];
-      if (mj == -INFINITY) continue;
-      const float f = exp2f(mj - M[i]);
-      W[i] += f * ml[2 * i + 1];
-      acc[i] += f * v[i];
+    for (int i = 0; i < 4; ++i)
+      if (a.lse && h0 + i < a.H)
+        a.lse[static_cast<long long>(t) * a.H + h0 + i] = s[i] == 0.f ? -INFINITY : (m[i] - (kPShift - 8) + log2f(s[i])) * kLn2;
+  };
+  const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < n_few * 64; item += gridDim.x * (kJoinThreads / 32)) {
+    const int4 tile = few[item >> 6];
+    const int quad = item & 15, chunk = (item >> 4) & 3, n = tile.z;
+    const int t = tile.x / a.groups, h0 = (tile.x - t * a.groups) * kHeads + quad * 4;
+    if (h0 >= a.H) continue;
+    float4 m = none, l = zero, f;  // lane j: piece j
+    if (lane < n) stats(tile.y, lane, quad, &m, &l);
+    const float4* o = reinterpret_cast<const float4*>(a.part_o) + (static_cast<long long>(chunk) * 16 + quad) * 128 + lane;
+    const float4 M = warp_max4(m);
+    const float4 total = warp_sum4(weigh(m, M, l, &f));
+    float4 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 2
+    for (int j = 0; j < n; ++j) {
+      const float4 fj = make_float4(__shfl_sync(0xffffffffu, f.x, j), __shfl_sync(0xffffffffu, f.y, j),
+                                    __shfl_sync(0xffffffffu, f.z, j), __shfl_sync(0xffffffffu, f.w, j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_piece(acc[i], fj, o[slot(tile.y, j) * (4 * 16 * 128) + 32 * i]);
     }
-  }
-  const long long row = static_cast<long long>(t) * a.H + h0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (h0 + i >= a.H) continue;
-    a.out[(row + i) * kRank + chunk * 128 + threadIdx.x] = __float2bfloat16_rn(W[i] == 0.f ? 0.f : ldexpf(acc[i] / W[i], kExpRef - 8));
-    if (chunk == 0 && threadIdx.x == i && a.lse) a.lse[row + i] = W[i] == 0.f ? -INFINITY : (M[i] - (kPShift - 8) + log2f(W[i])) * kLn2;
+    for (int i = 0; i < 4; ++i) store(t, h0, chunk * 128 + 32 * i + lane, acc[i], total);
+    if (chunk == 0 && lane == 0) store_lse(t, h0, M, total);
+  }
+
+  for (int item = blockIdx.x; item < n_many * 64; item += gridDim.x) {
+    const int4 tile = many[item >> 6];
+    const int quad = item & 15, chunk = (item >> 4) & 3, n = tile.z, grp = tid >> 7, lat = tid & 127;
+    const int t = tile.x / a.groups, h0 = (tile.x - t * a.groups) * kHeads + quad * 4;
+    if (h0 >= a.H) continue;  // the same in the whole CTA
+    __syncthreads();
+    if (warp == 0) {
+      float4 M = none, total = zero, m, l, f;
+      for (int j = lane; j < n; j += 32) {
+        stats(tile.y, j, quad, &m, &l);
+        M = make_float4(fmaxf(M.x, m.x), fmaxf(M.y, m.y), fmaxf(M.z, m.z), fmaxf(M.w, m.w));
+      }
+      M = warp_max4(M);
+      for (int j = lane; j < n; j += 32) {
+        stats(tile.y, j, quad, &m, &l);
+        const float4 s = weigh(m, M, l, &f);
+        total = make_float4(total.x + s.x, total.y + s.y, total.z + s.z, total.w + s.w);
+        weights[j] = f;
+      }
+      total = warp_sum4(total);
+      if (lane == 0) {
+        sums[3][0] = total;
+        if (chunk == 0) store_lse(t, h0, M, total);
+      }
+    }
+    __syncthreads();
+    const float4 total = sums[3][0];
+    const float4* o = reinterpret_cast<const float4*>(a.part_o) + (static_cast<long long>(chunk) * 16 + quad) * 128 + lat;
+    float4 acc = zero;
+#pragma unroll 4
+    for (int j = grp; j < n; j += 4) add_piece(acc, weights[j], o[slot(tile.y, j) * (4 * 16 * 128)]);
+    if (grp) sums[grp - 1][lat] = acc;
+    __syncthreads();
+    if (!grp) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const float4 x = sums[q][lat];
+        acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+      }
+      store(t, h0, chunk * 128 + lat, acc, total);
+    }
   }
 }
 
 // Blocks before each query (every position): at least one a query, so that each has a tile that writes it.
+constexpr int kPlanRequests = 4096;
 __global__ void __launch_bounds__(1024) quant_plan_kernel(const Args a, long long* cum) {
   __shared__ long long sums[32];
+  __shared__ int32_t first[kPlanRequests + 1];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool held = a.B <= kPlanRequests;  // else from memory
+  if (held)
+    for (int b = threadIdx.x; b <= a.B; b += 1024) first[b] = __ldg(a.cu + b);
+  __syncthreads();
+  auto cu = [&](int b) { return held ? first[b] : __ldg(a.cu + b); };
+  const int rows = cu(a.B);
   long long before = 0;
   for (int t0 = 0; t0 < a.total_q; t0 += 1024) {
     const int t = t0 + threadIdx.x;
-    long long v = 0;
-    if (t < a.total_q) {
-      int b;
-      unsigned bad = 0;
-      v = max(1ll, (keys_of(a, t, &b, &bad) + kKeys - 1) / kKeys);
+    long long v = t < a.total_q ? 1 : 0;
+    if (t < a.total_q && t < rows) {
+      int lo = 0, hi = a.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu(mid) <= t) lo = mid; else hi = mid;
+      }
+      v = max(1ll, (keys_seen(a, static_cast<long long>(__ldg(a.lens + lo)) - cu(lo + 1) + t, false) + kKeys - 1) / kKeys);
     }
     long long s = v;
 #pragma unroll
@@ -1015,15 +1160,15 @@ __global__ void __launch_bounds__(1024) quant_plan_kernel(const Args a, long lon
     }
     if (lane == 31) sums[warp] = s;
     __syncthreads();
-    long long w = sums[lane], add = 0;
-    for (int i = 0; i < 32; ++i) {
-      const long long x = __shfl_sync(0xffffffffu, w, i);
-      if (i < warp) add += x;
+    long long w = sums[lane];  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
     }
+    const long long add = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
     if (t < a.total_q) cum[t] = before + add + s - v;
-    long long total = 0;
-    for (int i = 0; i < 32; ++i) total += __shfl_sync(0xffffffffu, w, i);
-    before += total;
+    before += __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
   }
   if (threadIdx.x == 0) cum[a.total_q] = before;
@@ -1050,17 +1195,18 @@ int sm_count() {
 
 struct Plan {
   int groups, nb, parts;
-  size_t off_ml, off_cum, total;
+  size_t off_ml, off_joins, off_cum, total;
 };
 Plan plan_of(const dsa_quant_mla_args* a) {
   Plan p{};
   p.groups = (a->H + kHeads - 1) / kHeads;
   p.nb = (a->topk_width + kKeys - 1) / kKeys;
-  long long parts = sm_count();
+  long long parts = std::min(sm_count(), kMaxParts);
   if (p.nb) parts = std::min<long long>(parts, static_cast<long long>(a->total_q) * p.groups * p.nb);
   p.parts = static_cast<int>(std::max<long long>(1, parts));
   p.off_ml = static_cast<size_t>(2) * p.parts * kHeads * kRank * 4;
-  p.off_cum = p.off_ml + static_cast<size_t>(2) * p.parts * kHeads * 2 * 4;
+  p.off_joins = p.off_ml + static_cast<size_t>(2) * p.parts * kHeads * 2 * 4;
+  p.off_cum = p.off_joins + static_cast<size_t>(p.parts) * 8;
   p.total = p.off_cum + (p.nb ? 0 : (static_cast<size_t>(a->total_q) + 1) * 8);
   return p;
 }
@@ -1112,9 +1258,11 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.H = a->H;
   k.groups = p.groups;
   k.page_size = a->page_size;
-  k.page_log2 = -1;
-  for (int i = 0; i < 31; ++i)
-    if (a->page_size == 1 << i) k.page_log2 = i;
+  // d <= 2^s: m = ceil(2^(32 + s) / d) exceeds 2^(32 + s) / d by less than 2^s / d, too little to matter below 2^32
+  int s2 = 0;
+  while (1ll << s2 < a->page_size) ++s2;
+  k.page_mul = ((1ull << (32 + s2)) + a->page_size - 1) / a->page_size;
+  k.page_shift = 32 + s2;
   k.num_pages = a->num_pages;
   k.max_pages = a->max_pages_per_seq;
   k.topk_width = a->topk_width;
@@ -1138,6 +1286,7 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   k.part_o = reinterpret_cast<float*>(ws);
   k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
+  k.joins = reinterpret_cast<int2*>(ws + p.off_joins);
   k.status = status;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
@@ -1153,7 +1302,8 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   if (!make_gather_map(&map, a->cache ? a->cache : a->q_nope, fp4, quant::row_bytes(a->format), k.past_row)) return DSA_ERR_CUDA;
   e = fp4 ? launch_attend<true>(map, k, s) : launch_attend<false>(map, k, s);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  if (p.parts > 1) e = launch_pdl(quant_join_kernel, dim3(p.parts - 1, 64), dim3(128), 0, s, k);
+  if (p.parts > 1)
+    e = launch_pdl(quant_join_kernel, dim3(2 * sm_count()), dim3(kJoinThreads), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
