@@ -2,11 +2,11 @@
 //
 //     c = w * x / sqrt(mean(x^2) + eps),   r = RoPE(r, position),   row = codes of c / 2^E, r / 2^E, scales
 //
-// A code is that of c in exact arithmetic.  In fp32, c is off by up to 2^-19 (the sum of 512 squares, the
-// root, two products), which moves a value next to a border between two codes over it: once in some
-// 10^5 values, by a whole step of the code.  So each decision (the row's exponent, a block's scale, every
-// code) is taken for c (1 - 2^-18) and for c (1 + 2^-18); where the two differ, one row in some 100, the
-// warp takes the row again in fp64.  Without norm c is the input and fp32 is exact.
+// A code is that of c in exact arithmetic.  In fp32, c is off by up to 13 * 2^-24 (12 roundings of the sum of squares
+// and eps count half through the root, which is 2 * 2^-24 off itself; then two products and the three of its scaling),
+// which moves a value next to a border between two codes over it: once in some 10^5 values, by a whole step of the code.  So each decision (the row's exponent, a
+// block's scale, every code) is taken for c (1 - 2^-20) and for c (1 + 2^-20); where the two differ, one row in some
+// 100, the warp takes the row again in fp64.  Without norm c is the input and fp32 is exact.
 //
 // One warp takes a token: lane i holds the values 16 i .. 16 i + 15, which are one block of the 4-bit format.
 #include <cuda_runtime.h>
@@ -21,7 +21,7 @@ namespace {
 using namespace quant;
 
 constexpr int kWarps = 4;
-constexpr float kSlack = 1.f / 262144.f;  // 2^-18
+constexpr float kSlack = 1.f / 1048576.f;  // 2^-20
 
 // The smallest E with amax <= TOP 2^E, within +-kMaxExp; 0 for a row of zeros.
 template <bool FP4>
@@ -69,53 +69,58 @@ __device__ __forceinline__ float amax16(const float (&v)[16]) {
   return a;
 }
 
-// Codes of v, exact fp32 values (NORM off); with NORM, v is off by up to kSlack / 2 and *near is set where that
-// may have changed a decision.
+// Codes of v, exact fp32 values (NORM off); with NORM, v is off by up to kSlack and *near is set where that may have
+// changed a decision.
 template <bool FP4, bool NORM>
 __device__ __forceinline__ Codes encode(const float (&v)[16], bool* near) {
   Codes r;
   const float block = amax16<FP4>(v), amax = warp_max(block);
   const float lo = 1.f - kSlack, hi = 1.f + kSlack;
-  r.E = row_exponent<FP4>(amax);
-  bool off = false;
-  if (NORM) off = row_exponent<FP4>(amax * lo) != r.E || row_exponent<FP4>(amax * hi) != r.E;
-  float f = pow2f(-r.E);
+  r.E = row_exponent<FP4>(NORM ? amax * hi : amax);
+  // the scales are chosen for the larger value; would the smaller one take less?
+  bool off = NORM && amax > 0.f && amax * lo <= (FP4 ? kTop4 : kTop8) * pow2f(r.E - 1) && r.E > -kMaxExp;
+  const float f = pow2f(-r.E);
   if (FP4) {
     const float a = block * f;
-    const float s = block_scale(a);
-    if (NORM) off |= block_scale(a * lo) != s || block_scale(a * hi) != s;
+    const float s = block_scale(NORM ? a * hi : a);
+    if (NORM) off |= a * lo <= 6.f * __uint_as_float(__float_as_uint(s) - 0x100000u) && s > 0.03125f;
     r.scale = static_cast<int>(__float_as_uint(s) >> 20) - (122 << 3);
-    const float inv = NORM ? __frcp_rn(s) : 1.f;  // 2^-24 off, within the slack
+    const float g = NORM ? f * __frcp_rn(s) : f;
+    const float2 gl = make_float2(g * lo, g * lo), gh = make_float2(g * hi, g * hi);
+    uint32_t differ = 0u;
     r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float x = v[2 * i] * f, y = v[2 * i + 1] * f;
+      const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
       uint32_t c;
       if (NORM) {
-        x *= inv, y *= inv;
-        c = e2m1x2(x * lo, y * lo);
-        off |= c != e2m1x2(x * hi, y * hi);
+        const float2 l = mul2(x, gl), h = mul2(x, gh);
+        c = e2m1x2(l.x, l.y);
+        differ |= c ^ e2m1x2(h.x, h.y);
       } else {
-        c = e2m1x2(__fdiv_rn(x, s), __fdiv_rn(y, s));  // a tie divides exactly, and nothing else rounds to one
+        c = e2m1x2(__fdiv_rn(x.x * g, s), __fdiv_rn(x.y * g, s));  // a tie divides exactly, and nothing else rounds to one
       }
       r.w[i >> 2] |= c << (8 * (i & 3));
     }
+    if (NORM) off |= differ != 0u;
     r.w[0] = place_signs(r.w[0]);
     r.w[1] = place_signs(r.w[1]);
   } else {
     r.scale = 0;
+    const float2 fl = make_float2(f * lo, f * lo), fh = make_float2(f * hi, f * hi);
+    uint32_t differ = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = v[4 * i + j] * f;
+      const float2 x = make_float2(v[4 * i], v[4 * i + 1]), y = make_float2(v[4 * i + 2], v[4 * i + 3]);
       if (NORM) {
-        r.w[i] = e4m3x2(x[0] * lo, x[1] * lo) | (e4m3x2(x[2] * lo, x[3] * lo) << 16);
-        off |= r.w[i] != (e4m3x2(x[0] * hi, x[1] * hi) | (e4m3x2(x[2] * hi, x[3] * hi) << 16));
+        const float2 xl = mul2(x, fl), yl = mul2(y, fl), xh = mul2(x, fh), yh = mul2(y, fh);
+        r.w[i] = e4m3x2(xl.x, xl.y) | (e4m3x2(yl.x, yl.y) << 16);
+        differ |= r.w[i] ^ (e4m3x2(xh.x, xh.y) | (e4m3x2(yh.x, yh.y) << 16));
       } else {
-        r.w[i] = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+        r.w[i] = e4m3x2(x.x * f, x.y * f) | (e4m3x2(y.x * f, y.y * f) << 16);
       }
     }
+    if (NORM) off |= differ != 0u;
   }
   if (NORM) *near = off;
   return r;
@@ -129,10 +134,10 @@ __device__ __noinline__ Codes encode_exact(const float (&x)[16], const float (&w
   for (int i = 0; i < 16; ++i) ss += static_cast<double>(x[i]) * x[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double root = sqrt(ss / kRank + static_cast<double>(eps));
+  const double inv = 1.0 / sqrt(ss * (1.0 / kRank) + static_cast<double>(eps));
   float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = to_odd(static_cast<double>(w[i]) * x[i] / root);
+  for (int i = 0; i < 16; ++i) v[i] = to_odd(static_cast<double>(w[i]) * x[i] * inv);
   // amax and the scales from the odd-rounded values: a value just above a border stays above it
   Codes r;
   const float block = amax16<FP4>(v), amax = warp_max(block);
@@ -147,12 +152,11 @@ __device__ __noinline__ Codes encode_exact(const float (&x)[16], const float (&w
   }
   const float s = block_scale(block * f);
   r.scale = static_cast<int>(__float_as_uint(s) >> 20) - (122 << 3);
+  const double fs = inv * f / s;
   r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const double fs = static_cast<double>(f) / root;
-    const uint32_t c = e2m1x2(to_odd(static_cast<double>(w[2 * i]) * x[2 * i] * fs / s),
-                              to_odd(static_cast<double>(w[2 * i + 1]) * x[2 * i + 1] * fs / s));
+    const uint32_t c = e2m1x2(to_odd(static_cast<double>(w[2 * i]) * x[2 * i] * fs), to_odd(static_cast<double>(w[2 * i + 1]) * x[2 * i + 1] * fs));
     r.w[i >> 2] |= c << (8 * (i & 3));
   }
   r.w[0] = place_signs(r.w[0]);
@@ -233,15 +237,20 @@ __global__ void __launch_bounds__(kWarps * 32) quant_append_kernel(const dsa_mla
     }
     Codes c;
     if (NORM) {
-      float ss = 0.f;
+      float part[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < 4; ++i) part[i] = x[i] * x[i];
+#pragma unroll
+      for (int i = 4; i < 16; ++i) part[i & 3] = fmaf(x[i], x[i], part[i & 3]);
+      float ss = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float inv = rsqrtf(ss * (1.f / kRank) + a.norm_eps);
+      const float mean = ss * (1.f / kRank) + a.norm_eps;
+      float inv = rsqrtf(mean);
+      if (inv < INFINITY) inv = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = x[i] * inv * w[i];
+      for (int i = 0; i < 16; ++i) v[i] = x[i] * (inv * w[i]);
       bool near;
       c = encode<FP4, true>(v, &near);
       if (__any_sync(0xffffffffu, near)) c = encode_exact<FP4>(x, w, a.norm_eps);

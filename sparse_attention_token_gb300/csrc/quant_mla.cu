@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -49,6 +50,7 @@ constexpr uint32_t kAtom = kKeys * 128;                   // 64 rows of 128 byte
 constexpr uint32_t kTile = 5 * kAtom;                     // 4 columns of 128 codes, one of 64 bf16
 constexpr uint32_t kStaged = kKeys * kRow4;               // a block of 4-bit rows
 constexpr uint32_t kQRope = 128 * 128, kPBytes = kHeads * 128;
+constexpr uint32_t kOutStride = 80;                       // 32 bf16 of an output row, 16 bytes apart further
 constexpr uint32_t kQStride = 80, kQBuf = 4 * 32 * kQStride;  // 64 codes of 32 query rows a warp, 16 bytes apart further
 constexpr uint32_t kBe5m2 = 1u << 10;                     // instruction descriptor: B holds e5m2
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // TMEM columns
@@ -310,13 +312,6 @@ __device__ __forceinline__ void put_scale(float4* block, int key, float u) {
   float* pair = reinterpret_cast<float*>(block + (key >> 1)) + (key & 1);
   pair[0] = u;
   pair[2] = u > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u) >> 23) - 127 - kExpRef) : -INFINITY;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float b) {
   float2 d;
@@ -766,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const uint32_t col = tmem + lane_addr + kColS + grp * kKeys;
         const float4* scp = sc + ss * (kKeys / 2) + half * 16;
         float cr = 1.f;
+        float2 x[16];
         if (ok)
           ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
                                            (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
@@ -776,9 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           // instructions (a third of the cycles went by waiting for them).
           ptx::tc_fence_after();
           float2 mx = make_float2(-INFINITY, -INFINITY);
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t s0[16], s1[16], x[16];
+            uint32_t s0[16], s1[16];
             tmem_ld_x16(col + 16 * c, s0);
             tmem_ld_x16(col + 32 + 16 * c, s1);
             tmem_ld_wait16(s0, s1);
@@ -796,12 +792,12 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               ptx::ffma2(z, y, make_float2(v.x, v.y));
               mx.x = fmaxf(mx.x, z.x);
               mx.y = fmaxf(mx.y, z.y);
-              x[j] = __float_as_uint(z.x);
-              x[j + 1] = __float_as_uint(z.y);
+              x[8 * c + (j >> 1)] = z;
             }
-            tmem_st_32x32b_x16(col + 16 * c, x);
           }
-          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
           float mb = fmaxf(mx.x, mx.y);
           mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
           if (b > 0) ok = __all_sync(0xffffffffu, wait(other, ((b - 1) >> 1) & 1)) != 0;
@@ -828,11 +824,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
           uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t x[16], hi[4], lo[4];
-            tmem_ld_x16(col + 16 * c, x);
-            tmem_ld_wait16(x);
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float2 p[2];
@@ -840,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               for (int q = 0; q < 2; ++q) {
                 const uint2 u = *reinterpret_cast<const uint2*>(scp + 8 * c + 2 * j + q);
                 constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
-                p[q] = add2(make_float2(__uint_as_float(x[4 * j + 2 * q]), __uint_as_float(x[4 * j + 2 * q + 1])), ref);
+                p[q] = add2(x[8 * c + 2 * j + q], ref);
                 p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
                 ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
               }
@@ -852,10 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          ptx::tc_fence_before();
           ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
         }
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
         // done and before those of this one begin (which wait for them in any case).
@@ -944,10 +935,20 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           tmem_ld_x16(tmem + lane_addr + kColO + c * kHeads + h0, r);
           tmem_ld_wait16(r);
           if (whole) {
-            __nv_bfloat16* o = a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128 + lat;
+            // 16 heads x 32 latent values through the warp's part of P, so that a store takes 16 bytes
+            uint8_t* buf = smem + L::kOffP + grp * kPBytes + w * 16 * kOutStride;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              if (h0 + j < hg) o[j * kRank] = __float2bfloat16_rn(__uint_as_float(r[j]) * linv[h0 + j]);
+              *reinterpret_cast<__nv_bfloat16*>(buf + j * kOutStride + lane * 2) = __float2bfloat16_rn(__uint_as_float(r[j]) * linv[h0 + j]);
+            __syncwarp();
+            __nv_bfloat16* o = a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128 + w * 32;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int h = 8 * k + (lane >> 2);
+              const uint4 v = *reinterpret_cast<const uint4*>(buf + h * kOutStride + (lane & 3) * 16);
+              if (h0 + h < hg) reinterpret_cast<uint4*>(o + h * kRank)[lane & 3] = v;
+            }
+            __syncwarp();
           } else {
             float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
 #pragma unroll
@@ -1186,11 +1187,15 @@ dsa_status validate(const dsa_quant_mla_args* a) {
   return DSA_OK;
 }
 
+// SMs of the current device, asked for once (148 where there is no device to ask: a workspace size).
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
-  return n > 0 ? n : 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 struct Plan {
@@ -1213,8 +1218,15 @@ Plan plan_of(const dsa_quant_mla_args* a) {
 
 template <bool FP4>
 cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(quant_mla_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
+  static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory size
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(quant_mla_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   return launch_pdl(quant_mla_kernel<FP4>, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, s, map, k);
 }
 
