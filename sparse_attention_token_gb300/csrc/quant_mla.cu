@@ -80,8 +80,9 @@ static_assert(Smem<false>::kBytes <= 232448 && Smem<true>::kBytes <= 232448, "sh
 
 struct Args {
   int B, total_q, H, groups, page_size, num_pages, max_pages, topk_width;
-  int nb;                  // blocks of a tile (selected keys); 0: from the plan
+  int nb;                  // blocks of a tile (selected keys)
   int parts;               // CTAs
+  int whole, rest, split;  // selected keys: whole tiles a CTA, tiles behind them, pieces of each
   int past_row;            // a row past the cache: copies from there are zeros
   unsigned long long page_mul;  // position / page_size = position * page_mul >> page_shift
   int page_shift;
@@ -115,8 +116,14 @@ __device__ __forceinline__ long long keys_seen(const Args& a, long long pos, boo
   return max(0ll, min(n, room));
 }
 
-// The line of all blocks: tile w = (query w / groups, heads 64 (w % groups) ..) holds the places
-// tile_begin(w) .. tile_begin(w + 1) - 1; the parts are of `size` places, the first `more` of them of one more.
+// Tile w: query w / groups, its heads 64 (w % groups) ..  How the tiles come to the CTAs:
+//
+// Selected keys (every tile of nb blocks): CTA c takes the whole tiles c * whole .. and then, of the `rest` tiles that
+// do not fill a round of all CTAs, piece c % split of tile c / split.  Cutting no more tiles than that: a piece costs
+// some six blocks beside its own (its queries, its output), and a cut one is read again by the join.
+//
+// Every position (blocks by the queries' lengths): the blocks of all tiles stand in one line, tile w at the places
+// tile_begin(w) .. tile_begin(w + 1) - 1, cut into parts of `size` places, the first `more` of them of one more.
 struct Line {
   long long size;
   int more, parts;
@@ -127,7 +134,6 @@ struct Line {
   }
 };
 __device__ __forceinline__ long long tile_begin(const Args& a, int w) {
-  if (a.nb) return static_cast<long long>(w) * a.nb;
   const int t = w / a.groups, g = w - t * a.groups;
   const long long c0 = __ldg(a.cum + t);
   return c0 * a.groups + (g ? g * (__ldg(a.cum + t + 1) - c0) : 0);
@@ -142,7 +148,6 @@ __device__ __forceinline__ Line line_of(const Args& a) {
 }
 // The tile that holds place u.
 __device__ __forceinline__ int tile_at(const Args& a, long long u) {
-  if (a.nb) return static_cast<int>(u / a.nb);
   int lo = 0, hi = a.total_q * a.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -151,16 +156,42 @@ __device__ __forceinline__ int tile_at(const Args& a, long long u) {
   return lo;
 }
 
-// The pieces of a part, in order; every role walks them by itself.
-struct Pieces {
+// The pieces of a CTA, in order; every role walks them by itself.
+template <bool ALL>
+struct Pieces;
+template <>
+struct Pieces<false> {
+  int w, t, g, k0, k1 = 0, blocks;  // the current piece: blocks k0 .. k1 - 1 of `blocks`
+  int c, q = 0;
+  __device__ __forceinline__ Pieces(const Args& a, int part) : blocks(a.nb), c(part) {}
+  __device__ __forceinline__ bool next(const Args& a) {
+    k0 = 0;
+    k1 = blocks;
+    if (q < a.whole) {
+      w = c * a.whole + q;
+    } else {
+      if (q > a.whole || c >= a.rest * a.split) return false;
+      const int r = c / a.split, j = c - r * a.split;
+      w = a.parts * a.whole + r;
+      k0 = static_cast<int>(static_cast<long long>(blocks) * j / a.split);
+      k1 = static_cast<int>(static_cast<long long>(blocks) * (j + 1) / a.split);
+    }
+    ++q;
+    t = w / a.groups;
+    g = w - t * a.groups;
+    return true;
+  }
+};
+template <>
+struct Pieces<true> {
   long long u, end, t_end;  // the next piece's first place, the part's end, its tile's end
-  int w, t, g, k0, k1, blocks;  // the current piece: blocks k0 .. k1 - 1 of `blocks`
-  __device__ __forceinline__ Pieces(const Args& a, const Line& l, int c) {
-    u = c < l.parts ? l.begin(c) : 0;
-    end = c < l.parts ? l.begin(c + 1) : 0;
+  int w, t, g, k0, k1 = 0, blocks;
+  __device__ __forceinline__ Pieces(const Args& a, int part) {
+    const Line l = line_of(a);
+    u = part < l.parts ? l.begin(part) : 0;
+    end = part < l.parts ? l.begin(part + 1) : 0;
     w = u < end ? tile_at(a, u) : 0;
     --w;
-    t_end = u;
   }
   __device__ __forceinline__ bool next(const Args& a) {
     if (u >= end) return false;
@@ -178,21 +209,32 @@ struct Pieces {
 };
 
 // A piece's blocks are looked up in batches: how many, and whether block i (from the piece's first) ends one.
-__device__ __forceinline__ int batches(const Pieces& p) { return (p.k1 - p.k0 + kBatch - 1) / kBatch; }
-__device__ __forceinline__ bool last_of_batch(const Pieces& p, int i) { return i % kBatch == kBatch - 1 || i == p.k1 - p.k0 - 1; }
-// The keys of a query: the position of each, -1 where there is none.  Queries come in ascending order, so the request is
-// searched for once and then walked to.
+template <typename P>
+__device__ __forceinline__ int batches(const P& p) { return (p.k1 - p.k0 + kBatch - 1) / kBatch; }
+template <typename P>
+__device__ __forceinline__ bool last_of_batch(const P& p, int i) { return i % kBatch == kBatch - 1 || i == p.k1 - p.k0 - 1; }
+// The request of query t: the last b < B with cu[b] <= t, by a whole warp, 32 places a look.
+__device__ __forceinline__ int request_of(const int32_t* cu, int B, int t, int lane) {
+  int lo = 0, n = B;  // among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, at < n && __ldg(cu + lo + at) <= t);
+    const int last = below ? 31 - __clz(below) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+// The keys of a query.  Queries come in ascending order, so the request is searched for once and then walked to.
 struct Keys {
-  int t = -1, b = -1, lo = 0, hi = 0, len = 0, live = 0;
-  long long n = 0;  // keys (every position)
-  const int32_t* sel = nullptr;
-  const int32_t* table = nullptr;
-  __device__ __forceinline__ void move(const Args& a, int query, bool report) {
+  int t = -1, b = -1, hi = 0, len = 0, live = 0;
+  long long n = 0;  // keys
+  __device__ __forceinline__ void move(const Args& a, bool all, int query, int lane) {
     if (query == t) return;
     t = query;
     if (b < 0) {
       live = __ldg(a.cu + a.B);  // rows of queries; the others are padding
-      b = t < live ? sequence_of(a.cu, a.B, t) : 0;
+      b = t < live ? request_of(a.cu, a.B, t, lane) : 0;
       hi = t;
     } else {
       while (t < live && t >= hi && b + 1 < a.B && __ldg(a.cu + b + 1) <= t) ++b;
@@ -201,15 +243,7 @@ struct Keys {
       hi = __ldg(a.cu + b + 1);
       len = __ldg(a.lens + b);
     }
-    table = a.block_tables + static_cast<long long>(b) * a.max_pages;
-    sel = a.topk + static_cast<long long>(t) * a.topk_width;
-    n = t >= live ? 0 : a.nb ? a.topk_width : keys_seen(a, static_cast<long long>(len) - hi + t, report);
-  }
-  __device__ __forceinline__ int position(const Args& a, int key) const {
-    if (key >= n) return -1;
-    if (!a.nb) return key;
-    const int s = __ldg(sel + key);
-    return s < len ? s : -1;
+    n = t >= live ? 0 : all ? keys_seen(a, static_cast<long long>(len) - hi + t, lane == 0) : a.topk_width;
   }
 };
 // The cache row of a position, through a request's table; a.past_row where there is none (*bad: its page is not there).
@@ -348,7 +382,7 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
-template <bool FP4>
+template <bool FP4, bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
   using L = Smem<FP4>;
   constexpr int kStages = L::kStages;
@@ -413,9 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
-  const Line line = line_of(a);
   const int part = blockIdx.x;
-  Pieces pc(a, line, part);
+  Pieces<ALL> pc(a, part);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, a.status); };
   const uint32_t sbase = ptx::smem_u32(smem);
 
@@ -442,9 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             const uint32_t d = tmem + kColS + (b & 1) * kKeys;
             uint32_t kd = tile0 + (b % kStages) * (kTile >> 4), qd = rope0;
             asm volatile("" : "+r"(kd), "+r"(qd));  // descriptors are added up here, not kept over the loop
+#pragma unroll 1
+            for (int at = 0; at < 4; ++at) {
 #pragma unroll
-            for (int s = 0; s < 16; ++s)  // 32 codes of K per MMA, four in a column
-              mma_f8_ts(d, tmem + kColQ + s * 8, kd + (((s >> 2) * kAtom + (s & 3) * 32) >> 4), id_qk, s > 0 ? 1u : 0u);
+              for (int s = 0; s < 4; ++s)  // 32 codes of K per MMA, four in a column
+                mma_f8_ts(d, tmem + kColQ + (4 * at + s) * 8, kd + ((at * kAtom + s * 32) >> 4), id_qk, at + s);
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_bf16_ss(d, qd + 2 * s, kd + ((4 * kAtom) >> 4) + 2 * s, id_qr, 1u);
             ptx::mma_commit(&bars->sfull[b & 1]);
@@ -458,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           ptx::tc_fence_after();
           uint32_t vd = tile0 + (b % kStages) * (kTile >> 4), pd = p0 + (b & 1) * (kPBytes >> 4);
           asm volatile("" : "+r"(vd), "+r"(pd));
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 32 keys per MMA
@@ -494,10 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         if (ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(full, (FP4 ? kStaged : kTile) / 2);
           const int4* y4 = reinterpret_cast<const int4*>(rows + (bt * kBatch + i % kBatch) * kKeys) + first;
-#pragma unroll 4
+          int4 v = y4[0];
+#pragma unroll 1
           for (int g = 0; g < 8; ++g) {
-            const int4 v = y4[g];
             const int y[4] = {v.x, v.y, v.z, v.w};
+            if (g < 7) v = y4[g + 1];  // (ahead of the copies, which nothing is moved across)
             if (FP4) {
               tma_gather4(smem + L::kOffStaged + st * kStaged + (first + g) * 4 * kRow4, &tmap, full, 0, y);
             } else {
@@ -530,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
     };
     bool have = false, ok = true, bad = false;
-    pc.k1 = 0;
     for (;;) {
       int y[2 * kBatch];
 #pragma unroll
@@ -539,20 +575,32 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       bool more = true;  // the next batch's positions
       if (k >= pc.k1) {
         more = pc.next(a);
-        if (more) {
-          keys.move(a, pc.t, lane == 0);
-          k = pc.k0;
-          if (!have && part > 0 && lane == 0) {  // the join's part of the plan
+        k = pc.k0;
+        if constexpr (ALL) {
+          if (more && !have && part > 0 && lane == 0) {  // the join's part of the plan
+            const Line line = line_of(a);
             const bool inside = k > 0 && line.begin(part - 1) <= pc.t_end - pc.blocks;
             a.joins[part] = inside ? make_int2(pc.w, line.part_at(pc.t_end - 1)) : make_int2(-1, 0);
           }
         }
       }
       if (more) {
-        table = keys.table;
+        if (!ALL) {  // (read before it is known what the query sees: one trip to memory less)
+          const int32_t* sel = a.topk + static_cast<long long>(pc.t) * a.topk_width;
 #pragma unroll
-        for (int j = 0; j < 2 * kBatch; ++j)
-          pos[j] = k + (j >> 1) < pc.k1 ? keys.position(a, (k + (j >> 1)) * kKeys + 32 * (j & 1) + lane) : -1;
+          for (int j = 0; j < 2 * kBatch; ++j) {
+            const int key = (k + (j >> 1)) * kKeys + 32 * (j & 1) + lane;
+            pos[j] = k + (j >> 1) < pc.k1 && key < a.topk_width ? __ldg(sel + key) : -1;
+          }
+        }
+        keys.move(a, ALL, pc.t, lane);
+        table = a.block_tables + static_cast<long long>(keys.b) * a.max_pages;
+#pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j) {
+          const int key = (k + (j >> 1)) * kKeys + 32 * (j & 1) + lane;
+          if (ALL) pos[j] = k + (j >> 1) < pc.k1 && key < keys.n ? key : -1;
+          else if (keys.n == 0 || pos[j] >= keys.len) pos[j] = -1;
+        }
         k += kBatch;
       }
       if (have) {
@@ -761,7 +809,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const uint32_t col = tmem + lane_addr + kColS + grp * kKeys;
         const float4* scp = sc + ss * (kKeys / 2) + half * 16;
         float cr = 1.f;
-        float2 x[16];
         if (ok)
           ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
                                            (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
@@ -772,9 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           // instructions (a third of the cycles went by waiting for them).
           ptx::tc_fence_after();
           float2 mx = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
-            uint32_t s0[16], s1[16];
+            uint32_t s0[16], s1[16], x[16];
             tmem_ld_x16(col + 16 * c, s0);
             tmem_ld_x16(col + 32 + 16 * c, s1);
             tmem_ld_wait16(s0, s1);
@@ -792,12 +839,12 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               ptx::ffma2(z, y, make_float2(v.x, v.y));
               mx.x = fmaxf(mx.x, z.x);
               mx.y = fmaxf(mx.y, z.y);
-              x[8 * c + (j >> 1)] = z;
+              x[j] = __float_as_uint(z.x);
+              x[j + 1] = __float_as_uint(z.y);
             }
+            tmem_st_32x32b_x16(col + 16 * c, x);
           }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
+          ptx::tmem_st_wait();
           float mb = fmaxf(mx.x, mx.y);
           mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
           if (b > 0) ok = __all_sync(0xffffffffu, wait(other, ((b - 1) >> 1) & 1)) != 0;
@@ -824,9 +871,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
           uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
-            uint32_t hi[4], lo[4];
+            uint32_t x[16], hi[4], lo[4];
+            tmem_ld_x16(col + 16 * c, x);
+            tmem_ld_wait16(x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float2 p[2];
@@ -834,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               for (int q = 0; q < 2; ++q) {
                 const uint2 u = *reinterpret_cast<const uint2*>(scp + 8 * c + 2 * j + q);
                 constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
-                p[q] = add2(x[8 * c + 2 * j + q], ref);
+                p[q] = add2(make_float2(__uint_as_float(x[4 * j + 2 * q]), __uint_as_float(x[4 * j + 2 * q + 1])), ref);
                 p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
                 ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
               }
@@ -846,7 +895,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
+          ptx::tc_fence_before();
           ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
         }
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
         // done and before those of this one begin (which wait for them in any case).
@@ -1002,6 +1054,7 @@ __device__ __forceinline__ float4 warp_max4(float4 v) {
   }
   return v;
 }
+template <bool ALL>
 __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) {
   __shared__ int2 joins[kMaxParts];
   __shared__ int4 few[kMaxParts], many[kMaxParts];  // tile, first part, pieces
@@ -1010,25 +1063,29 @@ __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const Line line = line_of(a);
-  if (tid < line.parts) joins[tid] = tid ? a.joins[tid] : make_int2(-1, 0);
-  __syncthreads();
-  if (warp == 0) {
-    int nf = 0, nm = 0;
-    for (int c0 = 0; c0 < line.parts; c0 += 32) {
-      const int c = c0 + lane;
-      const int2 r = c < line.parts ? joins[c] : make_int2(-1, 0);
-      const int n = r.y - c + 2;
-      const unsigned f = __ballot_sync(0xffffffffu, r.x >= 0 && n <= kFewPieces), m = __ballot_sync(0xffffffffu, r.x >= 0 && n > kFewPieces);
-      const unsigned below = (1u << lane) - 1;
-      if (f >> lane & 1) few[nf + __popc(f & below)] = make_int4(r.x, c - 1, n, 0);
-      if (m >> lane & 1) many[nm + __popc(m & below)] = make_int4(r.x, c - 1, n, 0);
-      nf += __popc(f);
-      nm += __popc(m);
+  if constexpr (ALL) {
+    const int parts = line_of(a).parts;
+    if (tid < parts) joins[tid] = tid ? a.joins[tid] : make_int2(-1, 0);
+    __syncthreads();
+    if (warp == 0) {
+      int nf = 0, nm = 0;
+      for (int c0 = 0; c0 < parts; c0 += 32) {
+        const int c = c0 + lane;
+        const int2 r = c < parts ? joins[c] : make_int2(-1, 0);
+        const int n = r.y - c + 2;
+        const unsigned f = __ballot_sync(0xffffffffu, r.x >= 0 && n <= kFewPieces), m = __ballot_sync(0xffffffffu, r.x >= 0 && n > kFewPieces);
+        const unsigned below = (1u << lane) - 1;
+        if (f >> lane & 1) few[nf + __popc(f & below)] = make_int4(r.x, c - 1, n, 0);
+        if (m >> lane & 1) many[nm + __popc(m & below)] = make_int4(r.x, c - 1, n, 0);
+        nf += __popc(f);
+        nm += __popc(m);
+      }
+      if (lane == 0) n_few = nf, n_many = nm;
     }
-    if (lane == 0) n_few = nf, n_many = nm;
+    __syncthreads();
   }
-  __syncthreads();
+  const int tiles_few = ALL ? n_few : a.split <= kFewPieces ? a.rest : 0, tiles_many = ALL ? n_many : a.rest - tiles_few;
+  auto tile_of = [&](const int4* list, int i) { return ALL ? list[i] : make_int4(a.parts * a.whole + i, i * a.split, a.split, 0); };
   auto slot = [](int c0, int j) { return static_cast<long long>(2 * (c0 + j) + (j == 0 ? 1 : 0)); };
   auto stats = [&](int c0, int j, int quad, float4* m, float4* l) {
     const float4* ml = reinterpret_cast<const float4*>(a.part_ml + (slot(c0, j) * kHeads + quad * 4) * 2);
@@ -1060,8 +1117,8 @@ __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) 
   };
   const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), zero = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < n_few * 64; item += gridDim.x * (kJoinThreads / 32)) {
-    const int4 tile = few[item >> 6];
+  for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < tiles_few * 64; item += gridDim.x * (kJoinThreads / 32)) {
+    const int4 tile = tile_of(few, item >> 6);
     const int quad = item & 15, chunk = (item >> 4) & 3, n = tile.z;
     const int t = tile.x / a.groups, h0 = (tile.x - t * a.groups) * kHeads + quad * 4;
     if (h0 >= a.H) continue;
@@ -1071,7 +1128,7 @@ __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) 
     const float4 M = warp_max4(m);
     const float4 total = warp_sum4(weigh(m, M, l, &f));
     float4 acc[4] = {zero, zero, zero, zero};
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const float4 fj = make_float4(__shfl_sync(0xffffffffu, f.x, j), __shfl_sync(0xffffffffu, f.y, j),
                                     __shfl_sync(0xffffffffu, f.z, j), __shfl_sync(0xffffffffu, f.w, j));
@@ -1083,8 +1140,8 @@ __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) 
     if (chunk == 0 && lane == 0) store_lse(t, h0, M, total);
   }
 
-  for (int item = blockIdx.x; item < n_many * 64; item += gridDim.x) {
-    const int4 tile = many[item >> 6];
+  for (int item = blockIdx.x; item < tiles_many * 64; item += gridDim.x) {
+    const int4 tile = tile_of(many, item >> 6);
     const int quad = item & 15, chunk = (item >> 4) & 3, n = tile.z, grp = tid >> 7, lat = tid & 127;
     const int t = tile.x / a.groups, h0 = (tile.x - t * a.groups) * kHeads + quad * 4;
     if (h0 >= a.H) continue;  // the same in the whole CTA
@@ -1199,16 +1256,22 @@ int sm_count() {
 }
 
 struct Plan {
-  int groups, nb, parts;
+  int groups, nb, parts, whole, rest, split;
   size_t off_ml, off_joins, off_cum, total;
 };
 Plan plan_of(const dsa_quant_mla_args* a) {
   Plan p{};
   p.groups = (a->H + kHeads - 1) / kHeads;
   p.nb = (a->topk_width + kKeys - 1) / kKeys;
-  long long parts = std::min(sm_count(), kMaxParts);
-  if (p.nb) parts = std::min<long long>(parts, static_cast<long long>(a->total_q) * p.groups * p.nb);
-  p.parts = static_cast<int>(std::max<long long>(1, parts));
+  p.parts = std::min(sm_count(), kMaxParts);
+  if (p.nb) {
+    const int tiles = static_cast<int>(static_cast<long long>(a->total_q) * p.groups);
+    p.whole = tiles / p.parts;
+    p.rest = tiles - p.whole * p.parts;
+    // pieces of two blocks at least: of one, 4 tiles of 32 blocks take as long, and the join longer
+    p.split = p.rest ? std::max(1, std::min(p.parts / p.rest, p.nb / 2)) : 1;
+    if (!p.whole) p.parts = p.rest * p.split;
+  }
   p.off_ml = static_cast<size_t>(2) * p.parts * kHeads * kRank * 4;
   p.off_joins = p.off_ml + static_cast<size_t>(2) * p.parts * kHeads * 2 * 4;
   p.off_cum = p.off_joins + static_cast<size_t>(p.parts) * 8;
@@ -1216,18 +1279,19 @@ Plan plan_of(const dsa_quant_mla_args* a) {
   return p;
 }
 
-template <bool FP4>
+template <bool FP4, bool ALL>
 cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s) {
   static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory size
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  auto* kern = quant_mla_kernel<FP4, ALL>;
   if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(quant_mla_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_pdl(quant_mla_kernel<FP4>, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, s, map, k);
+  return launch_pdl(kern, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, s, map, k);
 }
 
 }  // namespace
@@ -1280,6 +1344,9 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.topk_width = a->topk_width;
   k.nb = p.nb;
   k.parts = p.parts;
+  k.whole = p.whole;
+  k.rest = p.rest;
+  k.split = p.split;
   k.past_row = std::max(1, a->num_pages * a->page_size);
   k.scale_log2 = a->scale * 1.4426950408889634f;
   k.qn = static_cast<const __nv_bfloat16*>(a->q_nope);
@@ -1312,10 +1379,14 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   CUtensorMap map;
   const bool fp4 = a->format == DSA_FP4_E2M1;
   if (!make_gather_map(&map, a->cache ? a->cache : a->q_nope, fp4, quant::row_bytes(a->format), k.past_row)) return DSA_ERR_CUDA;
-  e = fp4 ? launch_attend<true>(map, k, s) : launch_attend<false>(map, k, s);
+  const bool all = p.nb == 0;
+  e = fp4 ? (all ? launch_attend<true, true>(map, k, s) : launch_attend<true, false>(map, k, s))
+          : (all ? launch_attend<false, true>(map, k, s) : launch_attend<false, false>(map, k, s));
   if (e != cudaSuccess) return DSA_ERR_CUDA;
-  if (p.parts > 1)
-    e = launch_pdl(quant_join_kernel, dim3(2 * sm_count()), dim3(kJoinThreads), 0, s, k);
+  // two CTAs of the join fill an SM; of selected keys it is known how many it takes, and whether any
+  const int per = p.split <= kFewPieces ? kJoinThreads / 32 : 1;
+  const int blocks = all ? 2 * sm_count() : p.split > 1 ? std::min(2 * sm_count(), (p.rest * 64 + per - 1) / per) : 0;
+  if (blocks) e = launch_pdl(all ? quant_join_kernel<true> : quant_join_kernel<false>, dim3(blocks), dim3(kJoinThreads), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
