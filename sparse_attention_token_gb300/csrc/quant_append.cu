@@ -6,7 +6,7 @@
 // and eps count half through the root, which is 2 * 2^-24 off itself; then two products and the three of its scaling),
 // which moves a value next to a border between two codes over it: once in some 10^5 values, by a whole step of the code.  So each decision (the row's exponent, a
 // block's scale, every code) is taken for c (1 - 2^-20) and for c (1 + 2^-20); where the two differ, one row in some
-// 100, the warp takes the row again in fp64.  Without norm c is the input and fp32 is exact.
+// 100, the warp takes the row again with two floats a value.  Without norm c is the input and fp32 is exact.
 //
 // One warp takes a token: lane i holds the values 16 i .. 16 i + 15, which are one block of the 4-bit format.
 #include <cuda_runtime.h>
@@ -38,10 +38,29 @@ __device__ __forceinline__ float block_scale(float a) {
   if (6.f * __uint_as_float(s) < a) s += 0x100000u;
   return fminf(__uint_as_float(s), 72.f);
 }
-// A double as fp32 with the last bit set where it was cut: rounding this to fewer bits rounds the double.
-__device__ __forceinline__ float to_odd(double v) {
-  const float f = __double2float_rz(v);
-  return static_cast<double>(f) == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+// Sums and products of two floats that carry what one loses.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // exact
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {  // exact
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  const float e = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), h = __fadd_rn(s.hi, e);
+  return {h, __fsub_rn(e, __fsub_rn(h, s.hi))};
+}
+// hi + lo as one float whose last bit is set where it was cut: rounding this to fewer bits rounds the sum.
+__device__ __forceinline__ float to_odd(float hi, float lo) {
+  const float s = __fadd_rn(hi, lo), e = __fsub_rn(lo, __fsub_rn(s, hi));
+  if (e == 0.f) return s;
+  const uint32_t b = __float_as_uint(s);
+  return __uint_as_float(((e > 0.f) == (s > 0.f) ? b : b - 1u) | 1u);
 }
 // Standard nibbles (sign on top of each) to the row's order of signs.
 __device__ __forceinline__ uint32_t place_signs(uint32_t w) {
@@ -126,39 +145,56 @@ __device__ __forceinline__ Codes encode(const float (&v)[16], bool* near) {
   return r;
 }
 
-// The same row in fp64: x the inputs, w the weights.
+// The same row with every value in two floats, 2^-44 of it off: x the inputs, w the weights.  (fp64 itself took 8 us for
+// 64 rows, some of which always come here.)
 template <bool FP4>
-__device__ __noinline__ Codes encode_exact(const float (&x)[16], const float (&w)[16], float eps) {
-  double ss = 0.0;
+__device__ __noinline__ Codes encode_close(const float (&x)[16], const float (&w)[16], float eps) {
+  Two ss{0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss += static_cast<double>(x[i]) * x[i];
+  for (int i = 0; i < 16; ++i) ss = add(ss, Two{x[i] * x[i], 0.f});  // (a square of 8 bits is exact)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double inv = 1.0 / sqrt(ss * (1.0 / kRank) + static_cast<double>(eps));
-  float v[16];
+  for (int o = 16; o > 0; o >>= 1) {
+    const Two other{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)};
+    ss = add(ss, other);
+  }
+  const Two mean = add(Two{ss.hi * (1.f / kRank), ss.lo * (1.f / kRank)}, Two{eps, 0.f});
+  // 1 / sqrt(mean) = y + y r / 2, r = 1 - mean y^2
+  const float y = rsqrtf(mean.hi);
+  const Two yy = two_prod(y, y), my = two_prod(mean.hi, yy.hi);
+  const float r0 = (1.f - my.hi) - (my.lo + (mean.hi * yy.lo + mean.lo * yy.hi));
+  const float dy = y < INFINITY ? 0.5f * y * r0 : 0.f;
+  float v[16], rest[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = to_odd(static_cast<double>(w[i]) * x[i] * inv);
-  // amax and the scales from the odd-rounded values: a value just above a border stays above it
+  for (int i = 0; i < 16; ++i) {
+    const Two wx = two_prod(w[i], x[i]), p = two_prod(wx.hi, y);
+    v[i] = p.hi;
+    rest[i] = p.lo + (wx.hi * dy + wx.lo * y);
+  }
+  float odd[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) odd[i] = to_odd(v[i], rest[i]);
+  // exponent and scales from the values cut to odd: one just above a border stays above it
   Codes r;
-  const float block = amax16<FP4>(v), amax = warp_max(block);
+  const float block = amax16<FP4>(odd), amax = warp_max(block);
   r.E = row_exponent<FP4>(amax);
   const float f = pow2f(-r.E);
   if (!FP4) {
     r.scale = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      r.w[i] = e4m3x2(v[4 * i] * f, v[4 * i + 1] * f) | (e4m3x2(v[4 * i + 2] * f, v[4 * i + 3] * f) << 16);
+      r.w[i] = e4m3x2(odd[4 * i] * f, odd[4 * i + 1] * f) | (e4m3x2(odd[4 * i + 2] * f, odd[4 * i + 3] * f) << 16);
     return r;
   }
   const float s = block_scale(block * f);
   r.scale = static_cast<int>(__float_as_uint(s) >> 20) - (122 << 3);
-  const double fs = inv * f / s;
   r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = e2m1x2(to_odd(static_cast<double>(w[2 * i]) * x[2 * i] * fs), to_odd(static_cast<double>(w[2 * i + 1]) * x[2 * i + 1] * fs));
-    r.w[i >> 2] |= c << (8 * (i & 3));
+  for (int i = 0; i < 16; ++i) {
+    const float t = v[i] * f, q = __fdiv_rn(t, s);
+    odd[i] = to_odd(q, __fdiv_rn(__fmaf_rn(-q, s, t) + rest[i] * f, s));
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.w[i >> 2] |= e2m1x2(odd[2 * i], odd[2 * i + 1]) << (8 * (i & 3));
   r.w[0] = place_signs(r.w[0]);
   r.w[1] = place_signs(r.w[1]);
   return r;
@@ -253,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32) quant_append_kernel(const dsa_mla
       for (int i = 0; i < 16; ++i) v[i] = x[i] * (inv * w[i]);
       bool near;
       c = encode<FP4, true>(v, &near);
-      if (__any_sync(0xffffffffu, near)) c = encode_exact<FP4>(x, w, a.norm_eps);
+      if (__any_sync(0xffffffffu, near)) c = encode_close<FP4>(x, w, a.norm_eps);
     } else {
       c = encode<FP4, false>(x, nullptr);
     }
@@ -356,7 +392,10 @@ dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* a, dsa_stream_t
     return DSA_ERR_INVALID_ARGUMENT;
   unsigned* status = device_status_ptr();
   if (!status) return DSA_ERR_CUDA;
-  const cudaError_t e = launch_append<1>(*a, status, reinterpret_cast<cudaStream_t>(stream));
+  // Tokens a warp: more of them share the weights' loads, as long as the warps fill the SMs.  With the read-back of the
+  // same rows, 1, 2, 4 tokens a warp: 64 rows 11.0, 11.0, 12.3 us; 8195 20.1, 18.8, 20.4; 74967 in 4 bits 101.9, 90.9, 85.4.
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->n >= 16384 ? launch_append<4>(*a, status, s) : a->n >= 4096 ? launch_append<2>(*a, status, s) : launch_append<1>(*a, status, s);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
