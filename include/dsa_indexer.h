@@ -520,9 +520,9 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* args, dsa_stream_t stream);
  *   e2m1   per block of 16: s = the smallest value of 4 significant bits, at least 2^-5, with
  *          6 * s >= the block's largest |c| / 2^E; code = the e2m1 value nearest to c / (2^E * s); it
  *          stands for 2^E * e4m3(code * s), the product rounded to e4m3
- * (nearest: ties to even; 2^-5 <= s <= 72).  The codes are those of c in exact arithmetic, not of a
- * rounded c.  Every value that a row stands for is exact in bf16.  The rotary part is held as
- * bf16(r) / 2^E.  A mean over 512 normal values is off by 2.7 % (e4m3) and 10 % (e2m1) of their size.
+ * (nearest: ties to even; 2^-5 <= s <= 72).  The codes are those of c itself, not of a rounded c: with
+ * a norm, of c to within 2^-40.  Every value that a row stands for is exact in bf16.  The rotary part is
+ * held as bf16(r) / 2^E (exact for 2^-66 <= |r| < 2^67).  A mean over 512 normal values is off by 2.7 % (e4m3) and 10 % (e2m1) of their size.
  * Rows are the library's own: dsa_mla_quant_append writes and dsa_mla_quant_read reads them.  A page
  * may be moved or copied as bytes.
  */
@@ -534,7 +534,8 @@ int dsa_mla_quant_row_bytes(int format);
  * dsa_mla_quant_append -- dsa_mla_cache_append into a quantised cache: c = norm_weight * c_kv /
  * sqrt(mean(c_kv^2) + norm_eps) (c_kv itself without norm_weight) and r = RoPE(k_rope) (k_rope itself
  * without rope_cos), written to row slot of the cache in `format`.  Arguments, slots and reports are
- * those of dsa_mla_cache_append; cache is 16-byte aligned.  Inputs must be finite.
+ * those of dsa_mla_cache_append; cache is 16-byte aligned.  Inputs of rows that are written must be
+ * finite, the sum of squares of a row too.  Two rows for one slot: one of them, or a mixture.
  */
 typedef struct {
   int format, n, kv_rank, rope_dim, page_size, num_pages, rope_interleaved, rope_rows;

@@ -57,7 +57,7 @@ def encode_row(c, r, row) -> np.ndarray:
         return out
     for b in range(32):
         v = y[16 * b: 16 * b + 16]
-        code = int(np.searchsorted(6 * SCALES, np.abs(v).max()))
+        code = min(int(np.searchsorted(6 * SCALES, np.abs(v).max())), len(SCALES) - 1)  # (rows above 2^60 saturate)
         q = nearest(v / SCALES[code], E2M1)
         out[384 + b] = code
         for j in range(16):
@@ -117,7 +117,9 @@ def latent(c_kv, k_rope, *, norm_weight=None, norm_eps=1e-6, rope_cos=None, rope
 
 def quant_mla(q_nope, q_rope, rows, block_tables, cu_q_lens, seq_lens, topk=None, *, scale, page_size, num_pages):
     """dict of out [T, H, 512], lse [T, H] and what their error bounds are made of: cond [T, H, 512] = sum_s p_s |c_s|,
-    tail [T, H, 512] = max_s(p_s S_s) sum_s |c_s| / S_s (S the rows' scales), reach [T, H] = max_s scale sum_d |q_d k_d|,
+    square [T, H, 512] = sum_s p_s^2 c_s^2,
+    tail [T, H, 512] = max_s(p_s S_s) sum_s |c_s| / S_s (S the rows' scales), tail2 = max_s(p_s S_s)^2 sum_s (c_s / S_s)^2,
+    reach [T, H] = max_s scale sum_d |q_d k_d|,
     small [T, H] = max_s scale max_d |q_d| sum_d |k_d|, n [T] keys.  rows: (c, r, S) of every row of the cache.  A
     position that the table does not cover, or whose page is not in the cache, is left out."""
     qn, qr = f64(q_nope), f64(q_rope)
@@ -126,7 +128,8 @@ def quant_mla(q_nope, q_rope, rows, block_tables, cu_q_lens, seq_lens, topk=None
     tk = None if topk is None else topk.cpu().numpy()
     T, H, R = qn.shape
     res = {"out": np.zeros((T, H, R)), "lse": np.full((T, H), -np.inf), "cond": np.zeros((T, H, R)), "tail": np.zeros((T, H, R)),
-           "reach": np.zeros((T, H)), "small": np.zeros((T, H)), "n": np.zeros(T, dtype=np.int64)}
+           "reach": np.zeros((T, H)), "small": np.zeros((T, H)), "square": np.zeros((T, H, R)),
+           "tail2": np.zeros((T, H, R)), "n": np.zeros(T, dtype=np.int64)}
     for b in range(len(lens)):
         q = int(cu[b + 1] - cu[b])
         for i in range(q):
@@ -144,7 +147,9 @@ def quant_mla(q_nope, q_rope, rows, block_tables, cu_q_lens, seq_lens, topk=None
             e = np.exp(x - m)
             p = e / e.sum(1, keepdims=True)
             res["out"][t], res["cond"][t] = p @ c, p @ np.abs(c)
+            res["square"][t] = (p * p) @ (c * c)
             res["tail"][t] = (p * S).max(1, keepdims=True) * (np.abs(c) / S[:, None]).sum(0)
+            res["tail2"][t] = (p * S).max(1, keepdims=True) ** 2 * ((c / S[:, None]) ** 2).sum(0)
             res["lse"][t] = (m + np.log(e.sum(1, keepdims=True)))[:, 0]
             ka = np.abs(c).sum(1) + np.abs(r).sum(1)
             res["reach"][t] = (scale * (np.abs(qn[t]) @ np.abs(c).T + np.abs(qr[t]) @ np.abs(r).T)).max(1)

@@ -1080,6 +1080,14 @@ def dsa_mla_quant_read(cache: torch.Tensor, block_tables: torch.Tensor, cu_lens:
     return c_kv, k_rope
 
 
+def dsa_quant_mla_workspace_size(total_q: int, H: int, *, k: int = 0) -> int:
+    """Bytes of workspace that dsa_quant_mla takes on the current device for k selected keys a query (0: every position)."""
+    need = ctypes.c_size_t(0)
+    args = _QUANT_MLA_ARGS.pack(DSA_FP8_E4M3, 0, total_q, H, 512, 64, 64, 0, 0, k, 1.0, *[0] * 15)
+    _check(lib().dsa_quant_mla_workspace_size(args, ctypes.byref(need)), "dsa_quant_mla_workspace_size")
+    return int(need.value)
+
+
 def dsa_quant_mla(q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk=None, *, scale: float, out=None,
                   lse=None, workspace=None, stream=None):
     """Latent attention over a quantised cache [num_pages, page_size, row] uint8: each query over its selected

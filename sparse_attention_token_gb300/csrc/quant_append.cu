@@ -159,10 +159,10 @@ __device__ __noinline__ Codes encode_close(const float (&x)[16], const float (&w
   }
   const Two mean = add(Two{ss.hi * (1.f / kRank), ss.lo * (1.f / kRank)}, Two{eps, 0.f});
   // 1 / sqrt(mean) = y + y r / 2, r = 1 - mean y^2
-  const float y = rsqrtf(mean.hi);
+  const float y = mean.hi > 0.f ? rsqrtf(mean.hi) : 0.f;
   const Two yy = two_prod(y, y), my = two_prod(mean.hi, yy.hi);
   const float r0 = (1.f - my.hi) - (my.lo + (mean.hi * yy.lo + mean.lo * yy.hi));
-  const float dy = y < INFINITY ? 0.5f * y * r0 : 0.f;
+  const float dy = 0.5f * y * r0;
   float v[16], rest[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32) quant_append_kernel(const dsa_mla
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float mean = ss * (1.f / kRank) + a.norm_eps;
       float inv = rsqrtf(mean);
-      if (inv < INFINITY) inv = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);
+      inv = inv < INFINITY ? fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv) : 0.f;  // (zeros without norm_eps stay zeros)
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = x[i] * (inv * w[i]);
@@ -379,7 +379,7 @@ dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* a, dsa_stream_t
   if (a->kv_rank != quant::kRank || a->rope_dim != quant::kRope || quant::row_bytes(a->format) == 0)
     return DSA_ERR_UNSUPPORTED;
   if (a->n == 0) return DSA_OK;
-  if (!a->c_kv || !a->k_rope || !a->slot_mapping || !a->cache) return DSA_ERR_INVALID_ARGUMENT;
+  if (!a->c_kv || !a->k_rope || !a->slot_mapping || (!a->cache && a->num_pages > 0)) return DSA_ERR_INVALID_ARGUMENT;
   if ((a->rope_cos == nullptr) != (a->rope_sin == nullptr)) return DSA_ERR_INVALID_ARGUMENT;
   if (a->rope_cos && (a->rope_rows < 1 || (!a->positions && a->rope_rows < a->n))) return DSA_ERR_INVALID_ARGUMENT;
   if (a->norm_weight && !(a->norm_eps >= 0.f)) return DSA_ERR_INVALID_ARGUMENT;

@@ -313,15 +313,23 @@ __device__ __forceinline__ void tmem_ld_wait4(float (&r)[4]) {
 // Four values 0 <= p <= 2^8, given as 2^-8 p in fp16, as e4m3 codes (x) and the e5m2 codes of what they leave (y).
 // 2^-8 p has e4m3's exponents as its low four and its subnormals where e4m3 has them, so rounding its bits to three
 // of the mantissa is the code; e5m2 is the upper half of fp16.  (Conversions take the slow pipe, integers do not.)
-__device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b) {
+// Together they are within 2^-7 of p.  Below e4m3's normal numbers, p < 2^-6, the second term's two bits are all that
+// counts, 2^-13 at most off; thousands of such keys behind a large one may be alike, and their errors with them (a tenth
+// of their share of the output), so there the rounding goes up for as many of 16 neighbouring keys as it should: `at` is
+// the place among them of the first of the four.
+__device__ __forceinline__ constexpr uint32_t round_at(int i) {  // 16 thresholds of a step, in bit-reversed order
+  return 8u + 16u * ((i & 1) << 3 | (i & 2) << 1 | (i & 4) >> 1 | (i & 8) >> 3);
+}
+__device__ __forceinline__ uint32_t second_term(__half2 v, uint32_t first, int at) {
+  const __half2 left = __hmul2(__hsub2(v, *reinterpret_cast<const __half2*>(&first)), __float2half2_rn(256.f));
+  const uint32_t small = __hlt2_mask(v, __float2half2_rn(6.103515625e-05f));  // p < 2^-6
+  const uint32_t spread = (round_at(at) | round_at(at + 1) << 16) ^ 0x00800080u;
+  return *reinterpret_cast<const uint32_t*>(&left) + ((small & spread) ^ 0x00800080u);
+}
+__device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b, int at) {
   const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a), ub = *reinterpret_cast<const uint32_t*>(&b);
   const uint32_t ra = (ua + 0x00400040u) & 0x7F807F80u, rb = (ub + 0x00400040u) & 0x7F807F80u;
-  const __half2 up = __float2half2_rn(256.f);
-  const __half2 la = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ra)), up);
-  const __half2 lb = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&rb)), up);
-  return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531),
-                    __byte_perm(*reinterpret_cast<const uint32_t*>(&la) + 0x00800080u,
-                                *reinterpret_cast<const uint32_t*>(&lb) + 0x00800080u, 0x7531));
+  return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531), __byte_perm(second_term(a, ra, at), second_term(b, rb, at + 2), 0x7531));
 }
 // Four values |x| < 2^8, given as 2^-8 x in fp16, as e4m3 codes (x) and as those of 2^kLoShift times what they leave (y).
 __device__ __forceinline__ uint32_t e4m3_bytes(uint32_t a, uint32_t b) {  // fp16 bits, rounded to three of the mantissa
@@ -646,10 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       bool live[4];
       uint4 rp[4], r[4][4];
       __nv_bfloat162 am[4];
+      const int heads = pc.t < __ldg(a.cu + a.B) ? a.H : 0;  // (rows of padding may hold anything: taken as zeros)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int h = pc.g * kHeads + w * 16 + 4 * i + hr;
-        live[i] = h < a.H;
+        live[i] = h < heads;
         src[i] = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live[i] ? h : 0) * a.qn_h) + l8;
         rp[i] = live[i] ? __ldg(reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + h * a.qr_h) + l8) : make_uint4(0u, 0u, 0u, 0u);
         am[i] = most(rp[i]);
@@ -674,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         float m = fmaxf(__low2float(am[i]), __high2float(am[i]));
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = m > 0.f ? max(-60, min(60, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127))) : 0;
+        const int e = m > 0.f ? min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127)) : 0;
         f[i] = pow2f(e);
         if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = a.scale_log2 * pow2f(-e);
       }
@@ -741,35 +750,35 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           const uint8_t* staged = smem + L::kOffStaged + gs * kStaged + w * 16 * kRow4;
           uint8_t* tile = smem + L::kOffTile + st * kTile;
           int E = 0;
-  #pragma unroll 1
+#pragma unroll 1
           for (int i0 = 0; i0 < 16; i0 += 8) {
             uint2 q[8], lv[8];
             int byte[8];
-  #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              byte[i] = staged[(i0 + i) * kRow4 + kScale4 + lane];
-              q[i] = reinterpret_cast<const uint2*>(staged + (i0 + i) * kRow4)[lane];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              byte[j] = staged[(i0 + j) * kRow4 + kScale4 + lane];
+              q[j] = reinterpret_cast<const uint2*>(staged + (i0 + j) * kRow4)[lane];
             }
-  #pragma unroll
-            for (int i = 0; i < 8; ++i) lv[i] = levels[byte[i] & 7];
-  #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int key = w * 16 + i0 + i;
-              const int e = static_cast<int>(__ballot_sync(0xffffffffu, byte[i] >> 7) & 0xFFu) - 128;
-              if (lane == i0 + i) E = e;
-              const uint2 l2 = levels_at(lv[i], byte[i] & 127);
-              const uint2 c0 = codes4_to_e4m3(q[i].x, l2), c1 = codes4_to_e4m3(q[i].y, l2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lv[j] = levels[byte[j] & 7];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int key = w * 16 + i0 + j;
+              const int e = static_cast<int>(__ballot_sync(0xffffffffu, byte[j] >> 7) & 0xFFu) - 128;
+              if (lane == i0 + j) E = e;
+              const uint2 l2 = levels_at(lv[j], byte[j] & 127);
+              const uint2 c0 = codes4_to_e4m3(q[j].x, l2), c1 = codes4_to_e4m3(q[j].y, l2);
               *reinterpret_cast<uint4*>(tile + (lane >> 3) * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) =
                   make_uint4(c0.x, c0.y, c1.x, c1.y);
             }
           }
           uint4 rr[4];
-  #pragma unroll
-          for (int i = 0; i < 4; ++i) rr[i] = reinterpret_cast<const uint4*>(staged + (4 * i + hr) * kRow4 + kRope4)[l8];
-  #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = w * 16 + 4 * i + hr;
-            *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rr[j] = reinterpret_cast<const uint4*>(staged + (4 * j + hr) * kRow4 + kRope4)[l8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = w * 16 + 4 * j + hr;
+            *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[j];
           }
           if (lane < 16) put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(E) : 0.f);
           ptx::fence_proxy_async_smem();
@@ -887,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
                 p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
                 ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
               }
-              const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y));
+              const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y), 4 * j);
               hi[j] = t.x;
               lo[j] = t.y;
             }

@@ -79,7 +79,7 @@ extern "C" dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* a, dsa_s
   if (a->kv_rank != quant::kRank || a->rope_dim != quant::kRope || quant::row_bytes(a->format) == 0)
     return DSA_ERR_UNSUPPORTED;
   if (a->total == 0 || a->B == 0) return DSA_OK;
-  if (!a->cache || !a->cu_lens || !a->c_kv || !a->k_rope || (!a->block_tables && a->max_pages_per_seq > 0))
+  if ((!a->cache && a->num_pages > 0) || !a->cu_lens || !a->c_kv || !a->k_rope || (!a->block_tables && a->max_pages_per_seq > 0))
     return DSA_ERR_INVALID_ARGUMENT;
   if (a->total > 1 && (a->c_stride < 0 || a->r_stride < 0 || a->c_stride % 8 != 0 || a->r_stride % 8 != 0))
     return DSA_ERR_INVALID_ARGUMENT;
