@@ -654,11 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       bool live[4];
       uint4 rp[4], r[4][4];
       __nv_bfloat162 am[4];
-      const int heads = pc.t < __ldg(a.cu + a.B) ? a.H : 0;  // (rows of padding may hold anything: taken as zeros)
+      const uint32_t keep = pc.t < __ldg(a.cu + a.B) ? 0xffffffffu : 0u;  // rows of padding may hold anything: taken as zeros
+      auto kept = [&](const uint4& v) { return make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep); };
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int h = pc.g * kHeads + w * 16 + 4 * i + hr;
-        live[i] = h < heads;
+        live[i] = h < a.H;
         src[i] = reinterpret_cast<const uint4*>(a.qn + pc.t * a.qn_t + (live[i] ? h : 0) * a.qn_h) + l8;
         rp[i] = live[i] ? __ldg(reinterpret_cast<const uint4*>(a.qr + pc.t * a.qr_t + h * a.qr_h) + l8) : make_uint4(0u, 0u, 0u, 0u);
         am[i] = most(rp[i]);
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         float m = fmaxf(__low2float(am[i]), __high2float(am[i]));
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = m > 0.f ? min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127)) : 0;
+        const int e = keep && m > 0.f ? min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127)) : 0;
         f[i] = pow2f(e);
         if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = a.scale_log2 * pow2f(-e);
       }
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       for (int i = 0; i < 4; ++i) {
         const int r = w * 32 + 4 * i + hr;
         float x[8];
-        unpack_bf16(rp[i], x);
+        unpack_bf16(kept(rp[i]), x);
         *reinterpret_cast<uint4*>(smem + L::kOffQr + r * 128 + ((l8 ^ (r & 7)) << 4)) =
             make_uint4(pack_bf16(x[0] * f[i], x[1] * f[i]), pack_bf16(x[2] * f[i], x[3] * f[i]),
                        pack_bf16(x[4] * f[i], x[5] * f[i]), pack_bf16(x[6] * f[i], x[7] * f[i]));
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[8];
-          unpack_bf16(r[0][i], x);
+          unpack_bf16(kept(r[0][i]), x);
           const float g = f[i] * (1.f / 256.f);
           uint32_t hi[2], lo[2];
 #pragma unroll
