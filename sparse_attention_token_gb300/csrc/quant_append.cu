@@ -9,6 +9,9 @@
 // 100, the warp takes the row again with two floats a value.  Without norm c is the input and fp32 is exact.
 //
 // One warp takes a token: lane i holds the values 16 i .. 16 i + 15, which are one block of the 4-bit format.
+// In a graph with the read-back of the same rows: 64 tokens 6.2 us (latency: launch, slot, row, reductions, store; rows
+// that are taken again 1 us of it), 8195 tokens in 8 bits 14.3 (4.7 at the copy bandwidth), 74967 in 4 bits 77 (38): there
+// the arithmetic of the decisions, some 90 instructions a value pair, takes longer than the bytes.
 #include <cuda_runtime.h>
 
 #include "internal.h"

@@ -7,17 +7,18 @@
 //
 // Both formats are e4m3 numbers times a row's power of two, c[s] = 2^E c8[s], r[s] = 2^E r8[s], so the tensor
 // cores take the cache's codes as they are, and nothing is converted to bf16:
-//   q = 2^-a (hi + lo) in two e4m3 rows (exact for what lies within 2^9 of the row's largest value, and within
-//   2^-17 of that otherwise):      S = hi . c8 + lo . c8 + (2^a q_rope) . r8,   logit log2(e) = 2^-a 2^E S scale log2(e)
-//   x' = logit log2(e) + E,  m' its running maximum,  p = 2^(x' - m' + 5) in two e4m3 terms (2^-8 relative,
-//   2^-15 of the largest):         O = sum p c8,  L = sum p 2^-E (fp32),  out = O / L
-// Two e4m3 planes cost the tensor cores what one bf16 plane does and half the shared memory traffic.  Taking E
-// into the maximum keeps p in e4m3's range whatever the rows' scales are.
+//   q = 2^-a (hi + 2^-4 lo) in two e4m3 rows, the largest value of a row in [128, 256): exact for what lies within 2^13
+//   of that, 2^-21 of it off otherwise:
+//       S = hi . c8 + 2^-4 lo . c8 + (2^a q_rope) . r8,   x = S 2^(E - a) scale log2(e)
+//   x' = x + E - kExpRef,  m' its running maximum,  p = 2^(x' - m' + kPShift) in an e4m3 and an e5m2 term (two_terms):
+//       O = sum p c8,  L = sum p 2^(kExpRef - E) (fp32, of the unrounded p),  out = 2^kExpRef O / L
+// Two 8-bit planes cost the tensor cores what one bf16 plane does and half the shared memory traffic.  Taking E
+// into the maximum keeps p in range whatever the rows' scales are.  Against 64 bits the output's mean error is 0.0020 of
+// its size, 0.0017 of which is its own rounding to bf16; lse is within 6e-8.
 //
-// Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64.  The blocks of all tiles stand
-// in one line, cut into equal parts, one per CTA: a part may start and end inside a tile.  A tile done in one
-// piece is normalised and written, the pieces of the others leave (O, m', L) in fp32 and a second kernel joins them.
-// Roles of a CTA:
+// Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64; how tiles come to CTAs stands at Pieces.
+// A tile done in one piece is normalised and written, the pieces of the others leave (O, m', L) in fp32 and a second
+// kernel joins them.  Roles of a CTA:
 //   warps 0..7    softmax, two groups that take alternate blocks and hand the reference on.  Rows of S alternate
 //                 between 16 hi and 16 lo rows, so that a lane and the one 16 further hold a head's two planes;
 //                 each adds the planes for half of the block's keys;
@@ -27,6 +28,18 @@
 //   warp 13       TMEM, MMAs:  S [128 x 64 keys] = Q (TMEM) . K^T,  O^T [512 x heads] += V^T (the same tile,
 //                 MN-major) . P^T;
 //   warp 14       where the rows lie, four blocks at a time; e4m3: their scales.
+// A tile in shared memory serves both products, so a key is fetched once for 64 heads: at 64 heads an e4m3 row of 656
+// bytes meets 128 x 576 + 2 x 64 x 512 multiplications.
+//
+// What bounds it (GB300, 1.9 GHz, captured in a graph):
+//   block     the MMAs of a block take 1470 cycles.  e4m3: 2100 to 2200 a block, by the four tiles that are in flight:
+//             a tile is gathered (950 cycles from L2, 1430 with one issuing warp less), waits its turn, is multiplied
+//             twice and freed, 8500 to 9000 cycles round, 11000 when its rows come from DRAM.  1100 queries x 64 heads
+//             x 2048 keys: 334 us, 166 at the tensor cores' rate.  4 bits: the decoding warps, 3000 a block.
+//   piece     some 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 17000 from a piece's
+//             last block to the next one's first (output 12000, the next queries beside it).  64 queries x 64 heads x
+//             2048 keys: 47 us (e4m3 and 4 bits alike), 14 at the copy bandwidth.
+//   join      7 to 17 us, after 2 us in which its CTAs wait for room.
 // Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
 // (bounded) and TMEM is freed.
 #include <cuda_runtime.h>
@@ -50,7 +63,6 @@ constexpr uint32_t kAtom = kKeys * 128;                   // 64 rows of 128 byte
 constexpr uint32_t kTile = 5 * kAtom;                     // 4 columns of 128 codes, one of 64 bf16
 constexpr uint32_t kStaged = kKeys * kRow4;               // a block of 4-bit rows
 constexpr uint32_t kQRope = 128 * 128, kPBytes = kHeads * 128;
-constexpr uint32_t kOutStride = 80;                       // 32 bf16 of an output row, 16 bytes apart further
 constexpr uint32_t kQStride = 80, kQBuf = 4 * 32 * kQStride;  // 64 codes of 32 query rows a warp, 16 bytes apart further
 constexpr uint32_t kBe5m2 = 1u << 10;                     // instruction descriptor: B holds e5m2
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // TMEM columns
@@ -331,23 +343,28 @@ __device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b, int at) {
   const uint32_t ra = (ua + 0x00400040u) & 0x7F807F80u, rb = (ub + 0x00400040u) & 0x7F807F80u;
   return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531), __byte_perm(second_term(a, ra, at), second_term(b, rb, at + 2), 0x7531));
 }
-// Four values |x| < 2^8, given as 2^-8 x in fp16, as e4m3 codes (x) and as those of 2^kLoShift times what they leave (y).
-__device__ __forceinline__ uint32_t e4m3_bytes(uint32_t a, uint32_t b) {  // fp16 bits, rounded to three of the mantissa
-  return __byte_perm(a << 1, b << 1, 0x7531) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+// Four values |x| < 2^8 as e4m3 codes (x) and as those of 2^kLoShift times what they leave (y).  (By conversions, which are
+// fewer instructions: the warps that do this have a scheduler each, and the softmax is not at work beside them.)
+__device__ __forceinline__ uint32_t to_e4m3x2(__half2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
 }
-__device__ __forceinline__ uint32_t round_e4m3(__half2 v) {
-  return (*reinterpret_cast<const uint32_t*>(&v) + 0x00400040u) & 0xFF80FF80u;
+__device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return *reinterpret_cast<const __half2*>(&r);
 }
 __device__ __forceinline__ uint2 two_planes(__half2 a, __half2 b) {
-  const uint32_t ra = round_e4m3(a), rb = round_e4m3(b);
+  const uint32_t ha = to_e4m3x2(a), hb = to_e4m3x2(b);
   const __half2 up = __float2half2_rn(1 << kLoShift);
-  return make_uint2(e4m3_bytes(ra, rb), e4m3_bytes(round_e4m3(__hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ra)), up)),
-                                                   round_e4m3(__hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&rb)), up))));
+  return make_uint2(ha | hb << 16, to_e4m3x2(__hmul2(__hsub2(a, half2_of_e4m3x2(ha)), up)) |
+                                       to_e4m3x2(__hmul2(__hsub2(b, half2_of_e4m3x2(hb)), up)) << 16);
 }
 // The largest magnitudes among 8 bf16 values, in two halves.
 __device__ __forceinline__ __nv_bfloat162 most(const uint4& v) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-  return __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
 }
 // Scale u = 2^E of a block's row `key` (0: no row, which takes no weight).
 __device__ __forceinline__ void put_scale(float4* block, int key, float u) {
@@ -675,18 +692,18 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) am[i] = __hmax2(am[i], most(r[q][i]));
+          for (int i = 0; i < 4; ++i) am[i] = __hmax2_nan(am[i], most(r[q][i]));
       }
       // the power of two that takes the row's largest value to [128, 256)
       float f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float m = fmaxf(__low2float(am[i]), __high2float(am[i]));
+        uint32_t m = max(__float_as_uint(__low2float(am[i])), __float_as_uint(__high2float(am[i]))) & keep;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = keep && m > 0.f ? min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127)) : 0;
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = m > 0u ? min(126, 7 - (static_cast<int>(m >> 23) - 127)) : 0;
         f[i] = pow2f(e);
-        if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = a.scale_log2 * pow2f(-e);
+        if (l8 == 0) qscale[(n % kQRing) * kHeads + w * 16 + 4 * i + hr] = m < 0x7F800000u ? a.scale_log2 * pow2f(-e) : NAN;  // (its codes would hide it)
       }
       if (n > 0) {
         ok = wait(&bars->qfree, (n - 1) & 1);
@@ -710,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         for (int i = 0; i < 4; ++i) {
           float x[8];
           unpack_bf16(kept(r[0][i]), x);
-          const float g = f[i] * (1.f / 256.f);
+          const float g = f[i];
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -967,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         ok = __all_sync(0xffffffffu, (last == grp || wait(other, ((end - 1) >> 1) & 1)) &&
                                          wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
       const float fin = refv[last * kHeads + hl];
-      float sum = m == -INFINITY ? 0.f : (l.x + l.y) * ptx::ex2(m - fin);
+      float sum = (l.x + l.y) * (m == -INFINITY ? 1.f : ptx::ex2(m - fin));  // (without keys 0, or not a number)
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (!half) lsum[grp * kHeads + hl] = sum;
       ptx::named_bar_sync(4, 256);
@@ -978,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         linv[hl] = sum == 0.f ? 0.f : pow2f(kExpRef - 8) / sum;
         if (hl < hg && ok) {
           if (!whole) {
-            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin;
+            a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin + 0.f * sum;  // (not a number if the sum is not)
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = sum;
           } else if (a.lse) {
             a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = sum == 0.f ? -INFINITY : (fin - (kPShift - 8) + log2f(sum)) * kLn2;
@@ -997,20 +1014,18 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           tmem_ld_x16(tmem + lane_addr + kColO + c * kHeads + h0, r);
           tmem_ld_wait16(r);
           if (whole) {
-            // 16 heads x 32 latent values through the warp's part of P, so that a store takes 16 bytes
-            uint8_t* buf = smem + L::kOffP + grp * kPBytes + w * 16 * kOutStride;
+            // neighbouring lanes exchange heads, so that a store takes two latent values: the even lane head j, the odd one j + 1
+            const bool odd = lane & 1;
+            __nv_bfloat16* o = a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0 + odd) * kRank + c * 128 + w * 32 + (lane & 30);
+            const int heads = hg - h0 - odd;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              *reinterpret_cast<__nv_bfloat16*>(buf + j * kOutStride + lane * 2) = __float2bfloat16_rn(__uint_as_float(r[j]) * linv[h0 + j]);
-            __syncwarp();
-            __nv_bfloat16* o = a.out + (static_cast<long long>(pc.t) * a.H + pc.g * kHeads + h0) * kRank + c * 128 + w * 32;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int h = 8 * k + (lane >> 2);
-              const uint4 v = *reinterpret_cast<const uint4*>(buf + h * kOutStride + (lane & 3) * 16);
-              if (h0 + h < hg) reinterpret_cast<uint4*>(o + h * kRank)[lane & 3] = v;
+            for (int j = 0; j < 16; j += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(linv + h0 + j);
+              const float x = __uint_as_float(r[j]) * f.x, y = __uint_as_float(r[j + 1]) * f.y;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+              const uint32_t v = odd ? pack_bf16(got, y) : pack_bf16(x, got);
+              if (j < heads) *reinterpret_cast<uint32_t*>(o + j * kRank) = v;
             }
-            __syncwarp();
           } else {
             float4* o = reinterpret_cast<float4*>(a.part_o) + ((static_cast<long long>(slot) * 4 + c) * 16 + h0 / 4) * 128 + lat;
 #pragma unroll

@@ -456,3 +456,29 @@ def test_a_serving_run(row):
             _ok()
             # the roundings of P and of the output: 2^-7 + 2^-11 + 2^-8 here and 2^-7 there, of max |c| at most
             assert (out.float() - want.float()).abs().max() <= (2.0 ** -6 + 2.0 ** -8 + 2.0 ** -11 + 4 * E) * rows.abs().max().float()
+
+
+@pytest.mark.parametrize("row", FORMATS)
+@pytest.mark.parametrize("k", [None, 90])
+def test_nan_in_a_query_stays_in_its_row(row, k):
+    case = Case(row, 70, 16, [(2, 200), (1, 77)], k=k, seed=3)
+    want = case.run()
+    case.q[1, 66, 100] = float("nan")
+    case.q[2, 3, 530] = float("nan")
+    out, lse = case.run()
+    _ok()
+    for t, h in ((1, 66), (2, 3)):
+        assert torch.isnan(lse[t, h]) and torch.isnan(out[t, h]).all()
+        out[t, h], lse[t, h] = want[0][t, h], want[1][t, h]
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("args", [[], ["--bits", "4", "--requests", "3", "--heads", "20", "--prompt", "150", "--topk", "64", "--steps", "3"]])
+def test_the_example_runs(args):
+    import os
+    import subprocess
+    import sys
+    script = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "quantised_cache_step.py")
+    got = subprocess.run([sys.executable, script] + args, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0, got.stderr[-2000:]
+    assert "decode:" in got.stdout and "nan" not in got.stdout
