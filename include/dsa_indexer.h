@@ -594,7 +594,7 @@ dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* args, dsa_stream_t 
  * so are the queries of rows that are not padding (what is not finite makes its own query and head
  * NaN).  A page outside the cache is skipped and reported through dsa_check_device_status, as are
  * positions past the table (topk_width = 0).  Results do not depend on the run.  workspace:
- * dsa_quant_mla_workspace_size bytes, 16-byte aligned like the other pointers.
+ * dsa_quant_mla_workspace_size bytes (0: none is taken), 16-byte aligned like the other pointers.
  */
 typedef struct {
   int format, B, total_q, H, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq, topk_width;

@@ -1095,7 +1095,7 @@ def dsa_quant_mla(q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk
     Returns (out [total_q, H, 512] bf16, lse [total_q, H] fp32, the natural logarithm of the sum of
     exponentials); a query without keys gets zeros and -inf.  q_nope [total_q, H, 512] and q_rope
     [total_q, H, 64] bf16 may be views of one tensor.  out, lse and the workspace
-    (dsa_quant_mla_workspace_size bytes) are allocated when not given."""
+    (dsa_quant_mla_workspace_size bytes, which may be none) are allocated when not given."""
     qs, rs, bs = q_nope.shape, q_rope.shape, block_tables.shape
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     if len(qs) != 3 or len(rs) != 3 or len(bs) != 2 or B < 0 or (topk is not None and topk.dim() != 2):
@@ -1126,11 +1126,15 @@ def dsa_quant_mla(q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk
         status = L.dsa_quant_mla_workspace_size(_QUANT_MLA_ARGS.pack(*sizes, *tensors, 0, 0, 0, 0), ctypes.byref(need))
         if status != DSA_OK:
             raise DsaError(status, "dsa_quant_mla_workspace_size")
-        room = need.value or 16
-        workspace = _new(room, torch.uint8, dev, stream)
+        room = need.value
+        ws = 0
+        if room:
+            workspace = _new(room, torch.uint8, dev, stream)
+            ws = workspace.data_ptr()
     else:
         room = workspace.numel() * workspace.element_size()
-    args = _QUANT_MLA_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), _dev(workspace, "workspace"), room)
+        ws = _dev(workspace, "workspace")
+    args = _QUANT_MLA_ARGS.pack(*sizes, *tensors, out.data_ptr(), lse.data_ptr(), ws, room)
     status = L.dsa_quant_mla(args, _stream_of(here, stream))
     if status != DSA_OK:
         raise DsaError(status, "dsa_quant_mla")

@@ -95,6 +95,7 @@ struct Args {
   int nb;                  // blocks of a tile (selected keys)
   int parts;               // CTAs
   int whole, rest, split;  // selected keys: whole tiles a CTA, tiles behind them, pieces of each
+  int cluster;             // CTAs that hold the pieces of a tile and join them among themselves (1: the pieces go through memory)
   int past_row;            // a row past the cache: copies from there are zeros
   unsigned long long page_mul;  // position / page_size = position * page_mul >> page_shift
   int page_shift;
@@ -407,6 +408,87 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) L_j over the pieces j of a tile, in their order, which the CTAs of a cluster
+// hold: each takes a part of the heads and gets the others' O for it through distributed shared memory (their tiles are
+// free by then), so that the pieces are neither written to memory nor joined by another launch.  All threads.
+struct Held {
+  float m, sum;
+};
+__device__ __noinline__ void join_in_cluster(const Args& a, uint8_t* tiles, uint8_t* room, uint32_t* to, const Held* held, uint32_t tmem) {
+  const int C = a.cluster, rank = static_cast<int>(ptx::cluster_ctarank()), tid = threadIdx.x;
+  const int tile = a.parts * a.whole + static_cast<int>(blockIdx.x) / C;
+  const int t = tile / a.groups, g = tile - t * a.groups, hg = min(kHeads, a.H - g * kHeads), per = (hg + C - 1) / C;
+  float* got = reinterpret_cast<float*>(tiles);                 // [C - 1][per][512], the others' in their order
+  Held* stats = reinterpret_cast<Held*>(room);                  // [C][64]
+  float* weights = reinterpret_cast<float*>(stats + C * kHeads);  // [C][64]
+  ptx::cluster_sync();  // every CTA is done with its tiles
+  if (tid < C * kHeads) {
+    const int h = tid & (kHeads - 1), dst = tid / kHeads;
+    const uint32_t at = ptx::mapa_shared(ptx::smem_u32(stats + rank * kHeads + h), dst);
+    ptx::st_shared_cluster(at, __float_as_uint(held[h].m));
+    ptx::st_shared_cluster(at + 4, __float_as_uint(held[h].sum));
+  }
+  if (tid < kHeads) {
+    const int dst = tid / per, slot = rank < dst ? rank : rank - 1;
+    to[tid] = tid < hg && dst != rank ? ptx::mapa_shared(ptx::smem_u32(got + (slot * per + tid - dst * per) * kRank), dst) : 0u;
+  }
+  __syncthreads();
+  const int lane = tid & 31, quarter = (tid >> 5) & 3, chunk = tid >> 7, lat = chunk * 128 + quarter * 32 + lane;
+  const uint32_t o = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kColO + chunk * kHeads;
+#pragma unroll 1
+  for (int h0 = 0; h0 < hg; h0 += 16) {
+    uint32_t r[16];
+    tmem_ld_x16(o + h0, r);
+    tmem_ld_wait16(r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t at = to[h0 + j];
+      if (at) ptx::st_shared_cluster(at + lat * 4, r[j]);
+    }
+  }
+  ptx::cluster_sync();  // (nothing is written to another CTA from here on)
+  const int first = rank * per, mine = min(per, hg - first);
+  if (tid < mine) {
+    const int h = first + tid;
+    float M = -INFINITY, total = 0.f;
+    for (int j = 0; j < C; ++j) M = fmaxf(M, stats[j * kHeads + h].m);
+    for (int j = 0; j < C; ++j) {
+      const Held s = stats[j * kHeads + h];
+      const float f = s.m == -INFINITY ? 0.f : exp2f(s.m - M);
+      total += f == 0.f ? 0.f : f * s.sum;
+      weights[j * kHeads + tid] = f;
+    }
+    for (int j = 0; j < C; ++j) weights[j * kHeads + tid] = total == 0.f ? 0.f : weights[j * kHeads + tid] * (pow2f(kExpRef - 8) / total);
+    if (a.lse) a.lse[static_cast<long long>(t) * a.H + g * kHeads + h] = total == 0.f ? -INFINITY : (M - (kPShift - 8) + log2f(total)) * kLn2;
+  }
+  __syncthreads();
+  const bool odd = lane & 1;
+  __nv_bfloat16* out = a.out + (static_cast<long long>(t) * a.H + g * kHeads + first + odd) * kRank + (lat & ~1);
+#pragma unroll 1
+  for (int i0 = 0; i0 < mine; i0 += 4) {
+    float own[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) own[i] = tmem_ld_x1(o + min(first + i0 + i, kHeads - 1));
+    tmem_ld_wait4(own);
+#pragma unroll 1
+    for (int j = 0; j < C; ++j) {
+      const float* v = got + (j < rank ? j : j - 1) * per * kRank + lat;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = min(i0 + i, mine - 1);
+        const float f = weights[j * kHeads + h];
+        acc[i] = fmaf(f, f == 0.f ? 0.f : j == rank ? own[i] : v[h * kRank], acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float x = __shfl_xor_sync(0xffffffffu, odd ? acc[i] : acc[i + 1], 1);
+      const uint32_t v = odd ? pack_bf16(x, acc[i + 1]) : pack_bf16(acc[i], x);
+      if (i0 + i + odd < mine) *reinterpret_cast<uint32_t*>(out + (i0 + i) * kRank) = v;
+    }
+  }
+}
+
 template <bool FP4, bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
   using L = Smem<FP4>;
@@ -427,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   float* refv = reinterpret_cast<float*>(misc + 1536);                  // [2][64] the reference after its last block
   uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] moved heads of each group's warps
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
+  Held* held = reinterpret_cast<Held*>(misc + 2560);                    // [64] of the piece that the cluster joins
   float* qscale = reinterpret_cast<float*>(misc + 3072);                // [kQRing][64]
   int* rows = reinterpret_cast<int*>(smem + L::kOffRows);               // [kRing][64] rows of a block's keys
   float4* sc = reinterpret_cast<float4*>(smem + L::kOffSc);             // [kScRing][32] two rows' 2^E, then their E - kExpRef
@@ -994,7 +1077,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         sum = lsum[hl] + lsum[kHeads + hl];
         linv[hl] = sum == 0.f ? 0.f : pow2f(kExpRef - 8) / sum;
         if (hl < hg && ok) {
-          if (!whole) {
+          if (!ALL && !whole && a.cluster > 1) {
+            held[hl] = {fin + 0.f * sum, sum};
+          } else if (!whole) {
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin + 0.f * sum;  // (not a number if the sum is not)
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = sum;
           } else if (a.lse) {
@@ -1003,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         }
       }
       ptx::named_bar_sync(4, 256);
-      if (ok) {
+      if (ok && (ALL || whole || a.cluster == 1)) {
         ptx::tc_fence_after();
         const int lat = w * 32 + lane;
 #pragma unroll 1
@@ -1043,13 +1128,21 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if constexpr (!ALL) {
+    if (a.cluster > 1 && static_cast<int>(blockIdx.x) < a.rest * a.cluster) {  // (the same in all CTAs of a cluster)
+      ptx::tc_fence_after();
+      join_in_cluster(a, smem + L::kOffTile, smem + L::kOffP, reinterpret_cast<uint32_t*>(smem + L::kOffQ), held, tmem);
+      ptx::tc_fence_before();
+      __syncthreads();
+    }
+  }
   if (warp == 13) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
 }
 
-// out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) L_j over the pieces of a tile, in their order.  The tiles are listed by
+// The same of pieces that went through memory.  The tiles are listed by
 // the parts that begin inside them.  Of a tile of few pieces a warp takes four heads of a latent chunk, a lane four
 // latent values of each; of many, a CTA, its warps four chunks of every fourth piece.
 constexpr int kJoinThreads = 512, kFewPieces = 16, kMaxParts = 512;
@@ -1281,11 +1374,12 @@ int sm_count() {
 }
 
 struct Plan {
-  int groups, nb, parts, whole, rest, split;
+  int groups, nb, parts, whole, rest, split, cluster;
   size_t off_ml, off_joins, off_cum, total;
 };
 Plan plan_of(const dsa_quant_mla_args* a) {
   Plan p{};
+  p.cluster = 1;
   p.groups = (a->H + kHeads - 1) / kHeads;
   p.nb = (a->topk_width + kKeys - 1) / kKeys;
   p.parts = std::min(sm_count(), kMaxParts);
@@ -1295,7 +1389,13 @@ Plan plan_of(const dsa_quant_mla_args* a) {
     p.rest = tiles - p.whole * p.parts;
     // pieces of two blocks at least: of one, 4 tiles of 32 blocks take as long, and the join longer
     p.split = p.rest ? std::max(1, std::min(p.parts / p.rest, p.nb / 2)) : 1;
+    // Pieces of a tile in a cluster of 2, 4 or 8 where its size is near the number of pieces and all clusters find room at
+    // once: a GPC holds two of 8 or four of 4, and with whole tiles every SM is taken.
+    if (p.split > 1 && !p.whole) p.cluster = p.split >= 8 && p.rest <= 16 ? 8 : p.split >= 4 && p.rest <= 32 ? 4 : 2;
+    if (p.whole && (p.split == 2 || p.split == 3) && p.parts % 2 == 0) p.cluster = 2;
+    if (p.cluster > 1) p.split = p.cluster;
     if (!p.whole) p.parts = p.rest * p.split;
+    if (p.split == 1 || p.cluster > 1) return p;  // no workspace
   }
   p.off_ml = static_cast<size_t>(2) * p.parts * kHeads * kRank * 4;
   p.off_joins = p.off_ml + static_cast<size_t>(2) * p.parts * kHeads * 2 * 4;
@@ -1316,7 +1416,7 @@ cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_pdl(kern, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, s, map, k);
+  return launch_pdl_cluster(kern, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, ALL ? 1 : k.cluster, s, map, k);
 }
 
 }  // namespace
@@ -1350,7 +1450,7 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
       !al(a->block_tables, 4) || !al(a->cu_q_lens, 4) || !al(a->seq_lens, 4) || !al(a->topk, 4))
     return DSA_ERR_INVALID_ARGUMENT;
   const Plan p = plan_of(a);
-  if (!a->workspace || a->workspace_bytes < p.total || !al(a->workspace, 16)) return DSA_ERR_WORKSPACE;
+  if (p.total && (!a->workspace || a->workspace_bytes < p.total || !al(a->workspace, 16))) return DSA_ERR_WORKSPACE;
   unsigned* status = device_status_ptr();
   if (!status) return DSA_ERR_CUDA;
   Args k{};
@@ -1372,6 +1472,7 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.whole = p.whole;
   k.rest = p.rest;
   k.split = p.split;
+  k.cluster = p.cluster;
   k.past_row = std::max(1, a->num_pages * a->page_size);
   k.scale_log2 = a->scale * 1.4426950408889634f;
   k.qn = static_cast<const __nv_bfloat16*>(a->q_nope);
@@ -1410,7 +1511,7 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   // two CTAs of the join fill an SM; of selected keys it is known how many it takes, and whether any
   const int per = p.split <= kFewPieces ? kJoinThreads / 32 : 1;
-  const int blocks = all ? 2 * sm_count() : p.split > 1 ? std::min(2 * sm_count(), (p.rest * 64 + per - 1) / per) : 0;
+  const int blocks = all ? 2 * sm_count() : p.split > 1 && p.cluster == 1 ? std::min(2 * sm_count(), (p.rest * 64 + per - 1) / per) : 0;
   if (blocks) e = launch_pdl(all ? quant_join_kernel<true> : quant_join_kernel<false>, dim3(blocks), dim3(kJoinThreads), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

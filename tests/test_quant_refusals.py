@@ -94,11 +94,15 @@ def _size(dsa, **kw):
     return n.value
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(topk_width=0, topk=None), dict(total_q=1, H=128, topk_width=4096), dict(total_q=900)])
+@pytest.mark.parametrize("kw", [dict(topk_width=0, topk=None), dict(topk_width=0, topk=None, total_q=900), dict(total_q=151, H=64, topk_width=1000),
+                                dict(total_q=160, H=64, topk_width=1000), dict(topk_width=64)])
 def test_workspace(dsa, kw):
     need = _size(dsa, **kw)
     t, h = kw.get("total_q", 5), kw.get("H", 20)
     assert dsa.dsa_quant_mla_workspace_size(t, h, k=kw.get("topk_width", 100)) == need
+    if need == 0:  # tiles that are not cut, or whose pieces stay in a cluster
+        assert kw["topk_width"] > 0
+        return
     for bad in (dict(workspace_bytes=need - 1), dict(workspace=None), dict(workspace=FAKE + 8)):
         assert _call(dsa, "dsa_quant_mla", MLA, {**kw, "workspace_bytes": need, **bad}) == dsa.DSA_ERR_WORKSPACE
     # two pieces of 64 x 512 fp32 and their sums for each SM, and 8 bytes a query: not by the cache or the keys
@@ -111,7 +115,7 @@ def test_workspace(dsa, kw):
 
 
 def test_strides_of_dimensions_of_size_one_do_not_count(dsa):
-    call = lambda **kw: _call(dsa, "dsa_quant_mla", MLA, dict(workspace_bytes=0, **kw))
+    call = lambda **kw: _call(dsa, "dsa_quant_mla", MLA, dict(workspace_bytes=0, topk_width=0, **kw))
     odd = dict(qn_stride_t=577, qr_stride_t=-3)
     assert call(total_q=1, **odd) == dsa.DSA_ERR_WORKSPACE and call(**odd) == dsa.DSA_ERR_INVALID_ARGUMENT
     odd = dict(qn_stride_h=577, qr_stride_h=65)
