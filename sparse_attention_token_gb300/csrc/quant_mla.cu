@@ -17,8 +17,8 @@
 // its size, 0.0017 of which is its own rounding to bf16; lse is within 6e-8.
 //
 // Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64; how tiles come to CTAs stands at Pieces.
-// A tile done in one piece is normalised and written, the pieces of the others leave (O, m', L) in fp32 and a second
-// kernel joins them.  Roles of a CTA:
+// A tile done in one piece is normalised and written; the pieces of the others, (O, m', L) in fp32, are joined by the CTAs of
+// a cluster that hold them, or else go through memory to a second kernel.  Roles of a CTA:
 //   warps 0..7    softmax, two groups that take alternate blocks and hand the reference on.  Rows of S alternate
 //                 between 16 hi and 16 lo rows, so that a lane and the one 16 further hold a head's two planes;
 //                 each adds the planes for half of the block's keys;
@@ -32,14 +32,15 @@
 // bytes meets 128 x 576 + 2 x 64 x 512 multiplications.
 //
 // What bounds it (GB300, 1.9 GHz, captured in a graph):
-//   block     the MMAs of a block take 1470 cycles.  e4m3: 2100 to 2200 a block, by the four tiles that are in flight:
+//   block     the MMAs of a block take 1470 cycles.  e4m3: 2000 to 2200 a block, by the four tiles that are in flight:
 //             a tile is gathered (950 cycles from L2, 1430 with one issuing warp less), waits its turn, is multiplied
-//             twice and freed, 8500 to 9000 cycles round, 11000 when its rows come from DRAM.  1100 queries x 64 heads
-//             x 2048 keys: 334 us, 166 at the tensor cores' rate.  4 bits: the decoding warps, 3000 a block.
-//   piece     some 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 17000 from a piece's
-//             last block to the next one's first (output 12000, the next queries beside it).  64 queries x 64 heads x
-//             2048 keys: 47 us (e4m3 and 4 bits alike), 14 at the copy bandwidth.
-//   join      7 to 17 us, after 2 us in which its CTAs wait for room.
+//             twice and freed, 8500 to 9000 cycles round, 11000 when its rows come from DRAM.  1127 queries x 64 heads
+//             x 2048 keys: 311 us, 166 at the tensor cores' rate.  4 bits: the decoding warps, 3000 a block.
+//   piece     some 8000 to 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 11000 from a
+//             piece's last product to the next one's first (next queries 6000, then their first block's softmax; the
+//             output, 6000, beside them).  64 queries x 64 heads x 2048 keys: 45 us (e4m3 and 4 bits alike), 14 and 9 at
+//             the copy bandwidth.
+//   join      in a cluster 3 us; through memory 7 to 14, 2 of which its CTAs wait for room.
 // Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
 // (bounded) and TMEM is freed.
 #include <cuda_runtime.h>
