@@ -87,7 +87,8 @@ struct Smem {
   static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
   static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffQ = kOffStaged + kStagedBufs * kStaged;
   static constexpr uint32_t kOffMisc = kOffQ + kQBuf, kOffRows = kOffMisc + 4096, kOffSc = kOffRows + kRing * kKeys * 4;
-  static constexpr uint32_t kBytes = kOffSc + kScRing * kKeys * 8;
+  static constexpr uint32_t kOffLevels = kOffSc + kScRing * kKeys * 8;  // 4 bits: magnitudes by the scale's byte
+  static constexpr uint32_t kBytes = kOffLevels + (FP4 ? 256 * 8 : 0);
 };
 static_assert(Smem<false>::kBytes <= 232448 && Smem<true>::kBytes <= 232448, "shared memory of a CTA");
 
@@ -368,6 +369,8 @@ __device__ __forceinline__ __nv_bfloat162 most(const uint4& v) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
   return __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
 }
+// The top bits of four bytes, the first byte's lowest.
+__device__ __forceinline__ int top_bits(uint32_t x) { return static_cast<int>((x >> 7 & 0x01010101u) * 0x01020408u >> 24 & 15u); }
 // Scale u = 2^E of a block's row `key` (0: no row, which takes no weight).
 __device__ __forceinline__ void put_scale(float4* block, int key, float u) {
   float* pair = reinterpret_cast<float*>(block + (key >> 1)) + (key & 1);
@@ -504,14 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   Bars* bars = reinterpret_cast<Bars*>(misc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 512);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 516);
-  uint2* levels = reinterpret_cast<uint2*>(misc + 576);                 // [8] magnitudes of the 4-bit codes
+  uint2* levels = reinterpret_cast<uint2*>(smem + L::kOffLevels);       // [256] the eight magnitudes that codes stand for
   float* linv = reinterpret_cast<float*>(misc + 768);                   // [64] of the piece that is written
   float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] each group's
   float* refv = reinterpret_cast<float*>(misc + 1536);                  // [2][64] the reference after its last block
   uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] moved heads of each group's warps
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
   Held* held = reinterpret_cast<Held*>(misc + 2560);                    // [64] of the piece that the cluster joins
-  float* qscale = reinterpret_cast<float*>(misc + 3072);                // [kQRing][64]
+  float* qscale = reinterpret_cast<float*>(held + kHeads);             // [kQRing][64]
   int* rows = reinterpret_cast<int*>(smem + L::kOffRows);               // [kRing][64] rows of a block's keys
   float4* sc = reinterpret_cast<float4*>(smem + L::kOffSc);             // [kScRing][32] two rows' 2^E, then their E - kExpRef
   if (threadIdx.x == 0) {
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  if (FP4 && threadIdx.x < 8) levels[threadIdx.x] = levels_base(threadIdx.x);
+  if (FP4 && threadIdx.x < 256) levels[threadIdx.x] = levels_at(levels_base(threadIdx.x & 7), threadIdx.x & 127);
   if (warp == 13) {
     ptx::tmem_alloc(tmem_holder, 512);
     ptx::tmem_relinquish();
@@ -851,7 +854,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           const bool there = rows[(bt * kBatch + i % kBatch) * kKeys + w * 16 + (lane & 15)] != a.past_row;  // of key 16 w + lane
           const uint8_t* staged = smem + L::kOffStaged + gs * kStaged + w * 16 * kRow4;
           uint8_t* tile = smem + L::kOffTile + st * kTile;
-          int E = 0;
 #pragma unroll 1
           for (int i0 = 0; i0 < 16; i0 += 8) {
             uint2 q[8], lv[8];
@@ -862,14 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               q[j] = reinterpret_cast<const uint2*>(staged + (i0 + j) * kRow4)[lane];
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lv[j] = levels[byte[j] & 7];
+            for (int j = 0; j < 8; ++j) lv[j] = levels[byte[j]];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int key = w * 16 + i0 + j;
-              const int e = static_cast<int>(__ballot_sync(0xffffffffu, byte[j] >> 7) & 0xFFu) - 128;
-              if (lane == i0 + j) E = e;
-              const uint2 l2 = levels_at(lv[j], byte[j] & 127);
-              const uint2 c0 = codes4_to_e4m3(q[j].x, l2), c1 = codes4_to_e4m3(q[j].y, l2);
+              const uint2 c0 = codes4_to_e4m3(q[j].x, lv[j]), c1 = codes4_to_e4m3(q[j].y, lv[j]);
               *reinterpret_cast<uint4*>(tile + (lane >> 3) * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) =
                   make_uint4(c0.x, c0.y, c1.x, c1.y);
             }
@@ -882,7 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             const int key = w * 16 + 4 * j + hr;
             *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[j];
           }
-          if (lane < 16) put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(E) : 0.f);
+          if (lane < 16) {  // (the row's exponent from the top bits of its first eight scales)
+            const uint2 top = *reinterpret_cast<const uint2*>(staged + lane * kRow4 + kScale4);
+            put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(top_bits(top.x) + 16 * top_bits(top.y) - 128) : 0.f);
+          }
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {

@@ -151,7 +151,7 @@ def test_every_position(row, H, page, reqs):
 
 
 @pytest.mark.parametrize("row", FORMATS)
-@pytest.mark.parametrize("k", [None, 96])
+@pytest.mark.parametrize("k", [None, 96, 900])
 @pytest.mark.parametrize("pad", [1, 40])
 def test_padded_batches(row, k, pad):
     """Padding rows hold NaN queries and selections of their own: zeros and -inf all the same."""
@@ -160,9 +160,11 @@ def test_padded_batches(row, k, pad):
 
 
 @pytest.mark.parametrize("row", FORMATS)
-@pytest.mark.parametrize("H,k,queries", [(16, 2048, 1), (128, 2048, 3), (64, 1001, 80), (64, 130, 200), (20, 64, 310), (128, 640, 90)])
+@pytest.mark.parametrize("H,k,queries", [(16, 2048, 1), (128, 2048, 3), (64, 1001, 80), (64, 130, 200), (20, 64, 310), (128, 640, 90),
+                                         (64, 640, 215), (64, 1001, 30), (20, 2048, 10), (1, 2048, 2), (33, 700, 5), (128, 1500, 60)])
 def test_schedules(row, H, k, queries):
-    """One tile in many pieces, rounds of whole tiles with a rest in pieces, rests that are not cut."""
+    """One tile in many pieces, rounds of whole tiles with a rest in pieces, rests that are not cut; pieces that go through
+    memory and those of clusters of 2, 4 and 8."""
     Case(row, H, 64, [(queries, 2500)], k=k, seed=k).check()
 
 
@@ -459,9 +461,9 @@ def test_a_serving_run(row):
 
 
 @pytest.mark.parametrize("row", FORMATS)
-@pytest.mark.parametrize("k", [None, 90])
+@pytest.mark.parametrize("k", [None, 90, 700])
 def test_nan_in_a_query_stays_in_its_row(row, k):
-    case = Case(row, 70, 16, [(2, 200), (1, 77)], k=k, seed=3)
+    case = Case(row, 70, 16, [(2, 800), (1, 77)], k=k, seed=3)
     want = case.run()
     case.q[1, 66, 100] = float("nan")
     case.q[2, 3, 530] = float("nan")
