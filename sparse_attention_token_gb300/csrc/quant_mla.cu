@@ -19,9 +19,11 @@
 // Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64; how tiles come to CTAs stands at Pieces.
 // A tile done in one piece is normalised and written; the pieces of the others, (O, m', L) in fp32, are joined by the CTAs of
 // a cluster that hold them, or else go through memory to a second kernel.  Roles of a CTA:
-//   warps 0..7    softmax, two groups that take alternate blocks and hand the reference on.  Rows of S alternate
-//                 between 16 hi and 16 lo rows, so that a lane and the one 16 further hold a head's two planes;
-//                 each adds the planes for half of the block's keys;
+//   warps 0..7    softmax, two groups that take 32 keys each of every block.  Rows of S alternate between 16 hi and
+//                 16 lo rows, so that a lane and the one 16 further hold a head's two planes; each adds the planes
+//                 for half of its group's keys.  (Alternate blocks to the groups: 312 us instead of 327 for the first
+//                 figure below, but 37.1 instead of 35.5 for 62 x 128 heads x 1001 keys in 4 bits, and 3 % more for
+//                 the other 4-bit cases: there the time from S to P is what counts);
 //   warps 8..11   query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
 //                 4-bit rows also: codes from the staged rows to e4m3 tiles;
 //   warps 12, 15  rows of the cache by gathering TMA: e4m3 tiles in 128-byte columns, 4-bit rows whole;
@@ -32,13 +34,14 @@
 // bytes meets 128 x 576 + 2 x 64 x 512 multiplications.
 //
 // What bounds it (GB300, 1.9 GHz, captured in a graph):
-//   block     the MMAs of a block take 1470 cycles.  e4m3: 2000 to 2200 a block, by the four tiles that are in flight:
-//             a tile is gathered (950 cycles from L2, 1430 with one issuing warp less), waits its turn, is multiplied
-//             twice and freed, 8500 to 9000 cycles round, 11000 when its rows come from DRAM.  1127 queries x 64 heads
-//             x 2048 keys: 311 us, 166 at the tensor cores' rate.  4 bits: the decoding warps, 3000 a block.
-//   piece     some 8000 to 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 11000 from a
+//   block     the MMAs of a block take 1470 cycles.  e4m3: 2100 to 2200 a block, by the softmax (some 400 instructions a
+//             warp, each waiting for the one before) and the four tiles in flight: a tile is gathered (950 cycles from
+//             L2, 1430 with one issuing warp less), waits its turn, is multiplied twice and freed; 2800 a block when rows
+//             come from DRAM.  1127 queries x 64 heads x 2048 keys: 327 us, 166 at the tensor cores' rate.  4 bits: three
+//             tiles, and decoding stands in the round: 2700 a block.
+//   piece     some 8000 to 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 10000 from a
 //             piece's last product to the next one's first (next queries 6000, then their first block's softmax; the
-//             output, 6000, beside them).  64 queries x 64 heads x 2048 keys: 45 us (e4m3 and 4 bits alike), 14 and 9 at
+//             output, 6000, beside them).  64 queries x 64 heads x 2048 keys: 45 us (e4m3) and 43 (4 bits), 14 and 9 at
 //             the copy bandwidth.
 //   join      in a cluster 3 us; through memory 7 to 14, 2 of which its CTAs wait for room.
 // Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
@@ -86,7 +89,7 @@ struct Smem {
   static constexpr int kScRing = FP4 ? kStages : kRing;   // blocks whose scales are held
   static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
   static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffQ = kOffStaged + kStagedBufs * kStaged;
-  static constexpr uint32_t kOffMisc = kOffQ + kQBuf, kOffRows = kOffMisc + 4096, kOffSc = kOffRows + kRing * kKeys * 4;
+  static constexpr uint32_t kOffMisc = kOffQ + kQBuf, kOffRows = kOffMisc + 5120, kOffSc = kOffRows + kRing * kKeys * 4;
   static constexpr uint32_t kOffLevels = kOffSc + kScRing * kKeys * 8;  // 4 bits: magnitudes by the scale's byte
   static constexpr uint32_t kBytes = kOffLevels + (FP4 ? 256 * 8 : 0);
 };
@@ -120,7 +123,6 @@ struct Bars {
   uint64_t gfull[2], gempty[2];           // staged 4-bit rows
   uint64_t qfull[kQRing], qfree;
   uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], odrained, done;
-  uint64_t hand0[4], hand1[4];            // the reference after a block of group 0, 1, to the other group's warp
 };
 
 // Keys that a query at place i of the last q of n tokens sees (every position): those up to its own that the table
@@ -306,10 +308,10 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uin
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
   return ptx::mbar_spin(bar, parity, abort, status, kStatusTimeout);
 }
-// Whether v is non-zero in any of the 128 threads at named barrier `id`.
+// Whether v is non-zero in any of the 256 threads at named barrier `id`.
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t v) {
   uint32_t any;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(any) : "r"(v), "r"(id) : "memory");
   return any != 0;
 }
@@ -509,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 516);
   uint2* levels = reinterpret_cast<uint2*>(smem + L::kOffLevels);       // [256] the eight magnitudes that codes stand for
   float* linv = reinterpret_cast<float*>(misc + 768);                   // [64] of the piece that is written
-  float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] each group's
-  float* refv = reinterpret_cast<float*>(misc + 1536);                  // [2][64] the reference after its last block
-  uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] moved heads of each group's warps
+  float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] factors of a block's heads
+  float* top = reinterpret_cast<float*>(misc + 4096);                   // [2][2][64] a block's maxima over each group's keys
+  uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] a block's moved heads, by 16
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
   Held* held = reinterpret_cast<Held*>(misc + 2560);                    // [64] of the piece that the cluster joins
   float* qscale = reinterpret_cast<float*>(held + kHeads);             // [kQRing][64]
@@ -531,13 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       ptx::mbar_init(&bars->gfull[s], 2);
       ptx::mbar_init(&bars->gempty[s], 4);
       ptx::mbar_init(&bars->sfull[s], 1);
-      ptx::mbar_init(&bars->sempty[s], 4);
-      ptx::mbar_init(&bars->pfull[s], 4);
+      ptx::mbar_init(&bars->sempty[s], 8);
+      ptx::mbar_init(&bars->pfull[s], 8);
       ptx::mbar_init(&bars->pvdone[s], 1);
-    }
-    for (int s = 0; s < 4; ++s) {
-      ptx::mbar_init(&bars->hand0[s], 1);
-      ptx::mbar_init(&bars->hand1[s], 1);
     }
     for (int s = 0; s < kQRing; ++s) ptx::mbar_init(&bars->qfull[s], 4);
     ptx::mbar_init(&bars->qfree, 1);
@@ -898,146 +896,126 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     }
   } else {
     // ------------------------------------------------------------ softmax, rescale, output
+    // Group g takes the keys 32 g .. of every block, of which the hi lane has the first 16 and the lo lane the others.
     const int grp = warp >> 2, w = warp & 3, half = lane >> 4, hl = w * 16 + (lane & 15);
     const uint32_t lane_addr = static_cast<uint32_t>(w * 32) << 16;
-    uint64_t* mine = grp ? &bars->hand1[w] : &bars->hand0[w];
-    uint64_t* other = grp ? &bars->hand0[w] : &bars->hand1[w];
     int it = 0, n = 0, bn = 0;
     bool ok = true;
     // Every piece and block runs its named barriers whatever happened, so that a wait that gave up leaves no
     // warp behind at one.
     while (pc.next(a)) {
       const int cnt = pc.k1 - pc.k0, hg = min(kHeads, a.H - pc.g * kHeads), end = it + cnt;
-      float m = -INFINITY;  // the group's reference at its last block
-      float2 l = make_float2(0.f, 0.f), qm = l, qo = l;  // its sum, in two parts; the planes' scales
+      float m = -INFINITY;  // the reference, the same in both groups
+      float2 l = make_float2(0.f, 0.f), qm = l, qo = l;  // the sum, in two parts; the planes' scales
       if (ok) ok = __all_sync(0xffffffffu, wait(&bars->qfull[n % kQRing], (n / kQRing) & 1)) != 0;
       if (ok) {
         const float qs = qscale[(n % kQRing) * kHeads + hl];
         qm.x = qm.y = half ? qs * (1.f / (1 << kLoShift)) : qs;  // of this lane's plane, and of the other's
         qo.x = qo.y = half ? qs : qs * (1.f / (1 << kLoShift));
       }
-      for (int b = it + ((it ^ grp) & 1); b < end; b += 2) {
-        const int bi = bn + (b - it) / kBatch, bt = bi % kBatches;
+      for (int b = it; b < end; ++b) {
+        const int bi = bn + (b - it) / kBatch, bt = bi % kBatches, s2 = b & 1;
         const int ss = FP4 ? b % kStages : bt * kBatch + (b - it) % kBatch;
-        const uint32_t col = tmem + lane_addr + kColS + grp * kKeys;
-        const float4* scp = sc + ss * (kKeys / 2) + half * 16;
-        float cr = 1.f;
+        const float4* scp = sc + ss * (kKeys / 2) + grp * 16 + half * 8;
+        float x[16];
+        float mb = -INFINITY;
         if (ok)
-          ok = __all_sync(0xffffffffu, wait(&bars->sfull[grp], (b >> 1) & 1) &&
+          ok = __all_sync(0xffffffffu, wait(&bars->sfull[s2], (b >> 1) & 1) &&
                                            (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
                                                 : wait(&bars->scfull[bt], (bi / kBatches) & 1))) != 0;
         if (ok) {
-          // x' of the block, 16 keys at a time (the hi lane takes keys 0..31, the lo lane 32..63), back over S.
-          // Both passes are loops: as straight code the two groups' block is more than an SM's schedulers hold of
-          // instructions (a third of the cycles went by waiting for them).
           ptx::tc_fence_after();
+          const uint32_t col = tmem + lane_addr + kColS + s2 * kKeys + grp * 32;
+          uint32_t s0[16], s1[16];
+          tmem_ld_x16(col, s0);
+          tmem_ld_x16(col + 16, s1);
+          tmem_ld_wait16(s0, s1);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[s2]);
           float2 mx = make_float2(-INFINITY, -INFINITY);
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t s0[16], s1[16], x[16];
-            tmem_ld_x16(col + 16 * c, s0);
-            tmem_ld_x16(col + 32 + 16 * c, s1);
-            tmem_ld_wait16(s0, s1);
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float2 keep, got;
-              keep.x = __uint_as_float(half ? s1[j] : s0[j]);
-              keep.y = __uint_as_float(half ? s1[j + 1] : s0[j + 1]);
-              got.x = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j] : s1[j], 16));
-              got.y = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j + 1] : s1[j + 1], 16));
-              const float4 v = scp[8 * c + (j >> 1)];
-              float2 y = mul2(keep, qm);
-              ptx::ffma2(y, got, qo);
-              float2 z = make_float2(v.z, v.w);
-              ptx::ffma2(z, y, make_float2(v.x, v.y));
-              mx.x = fmaxf(mx.x, z.x);
-              mx.y = fmaxf(mx.y, z.y);
-              x[j] = __float_as_uint(z.x);
-              x[j + 1] = __float_as_uint(z.y);
-            }
-            tmem_st_32x32b_x16(col + 16 * c, x);
+          for (int j = 0; j < 16; j += 2) {
+            float2 keep, got;
+            keep.x = __uint_as_float(half ? s1[j] : s0[j]);
+            keep.y = __uint_as_float(half ? s1[j + 1] : s0[j + 1]);
+            got.x = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j] : s1[j], 16));
+            got.y = __uint_as_float(__shfl_xor_sync(0xffffffffu, half ? s0[j + 1] : s1[j + 1], 16));
+            const float4 v = scp[j >> 1];
+            float2 y = mul2(keep, qm);
+            ptx::ffma2(y, got, qo);
+            float2 z = make_float2(v.z, v.w);
+            ptx::ffma2(z, y, make_float2(v.x, v.y));
+            mx.x = fmaxf(mx.x, z.x);
+            mx.y = fmaxf(mx.y, z.y);
+            x[j] = z.x;
+            x[j + 1] = z.y;
           }
-          ptx::tmem_st_wait();
-          float mb = fmaxf(mx.x, mx.y);
-          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
-          if (b > 0) ok = __all_sync(0xffffffffu, wait(other, ((b - 1) >> 1) & 1)) != 0;
-          if (ok) {
-            const float before = b == end - cnt ? -INFINITY : refv[(grp ^ 1) * kHeads + hl];
-            // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
-            float mn = before;
-            if (before == -INFINITY || mb > before + kMove) mn = mb;
-            cr = before == -INFINITY ? 1.f : ptx::ex2(before - mn);
-            const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
-            l.x *= f;
-            l.y *= f;
-            m = mn;
-            if (!half) {
-              refv[grp * kHeads + hl] = mn;
-              corr[grp * kHeads + hl] = cr;
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(mine);
-          }
-          // the group's P is free once the products of its block before have been done
-          if (ok && b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp], ((b >> 1) & 1) ^ 1)) != 0;
+          mb = fmaxf(mx.x, mx.y);
         }
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
+        if (!half) top[(s2 * 2 + grp) * kHeads + hl] = mb;
+        ptx::named_bar_sync(5 + w, 64);  // the two groups' warps of these heads
+        mb = fmaxf(mb, top[(s2 * 2 + (grp ^ 1)) * kHeads + hl]);
+        // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
+        const float before = m;
+        if (m == -INFINITY || mb > m + kMove) m = mb;
+        const float cr = before == -INFINITY ? 1.f : ptx::ex2(before - m);
+        l.x *= cr;
+        l.y *= cr;
+        const unsigned moved = __ballot_sync(0xffffffffu, !half && hl < hg && cr != 1.f);
+        if (grp == 0) {
+          if (!half) corr[s2 * kHeads + hl] = cr;
+          if (lane == 0) movedv[s2 * 4 + w] = moved;
+        }
+        // P's buffer is free once the products of the block that had it before have been done
+        if (ok && b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2], ((b >> 1) & 1) ^ 1)) != 0;
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
-          uint8_t* prow = smem + L::kOffP + grp * kPBytes + hl * 128;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[16], hi[4], lo[4];
-            tmem_ld_x16(col + 16 * c, x);
-            tmem_ld_wait16(x);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2 p[2];
+          for (int j = 0; j < 4; ++j) {
+            float2 p[2];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint2 u = *reinterpret_cast<const uint2*>(scp + 8 * c + 2 * j + q);
-                constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
-                p[q] = add2(make_float2(__uint_as_float(x[4 * j + 2 * q]), __uint_as_float(x[4 * j + 2 * q + 1])), ref);
-                p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
-                ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
-              }
-              const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y), 4 * j);
-              hi[j] = t.x;
-              lo[j] = t.y;
+            for (int q = 0; q < 2; ++q) {
+              const uint2 u = *reinterpret_cast<const uint2*>(scp + 2 * j + q);
+              constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
+              p[q] = add2(make_float2(x[4 * j + 2 * q], x[4 * j + 2 * q + 1]), ref);
+              p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
+              ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
             }
-            const int ch = half * 2 + c;
-            *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y), 4 * j);
+            hi[j] = t.x;
+            lo[j] = t.y;
           }
-          ptx::tc_fence_before();
+          const int ch = grp * 2 + half;
+          uint8_t* prow = smem + L::kOffP + s2 * kPBytes + hl * 128;
+          *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->sempty[grp]);
         }
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
-        // done and before those of this one begin (which wait for them in any case).
-        const unsigned moved = __ballot_sync(0xffffffffu, !half && hl < hg && cr != 1.f);
-        if (lane == 0) movedv[grp * 4 + w] = moved;
-        if (bar_any(2 + grp, moved)) {
-          if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[grp ^ 1], ((b - 1) >> 1) & 1)) != 0;
+        // done and before those of this one begin (which wait for them in any case), each group's two latent chunks.
+        // (corr and movedv are read before the barrier of the next block, and rewritten behind it.)
+        if (bar_any(2, moved)) {
+          if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2 ^ 1], ((b - 1) >> 1) & 1)) != 0;
           if (ok) {
             ptx::tc_fence_after();
-            const uint2 m01 = *reinterpret_cast<const uint2*>(movedv + grp * 4), m23 = *reinterpret_cast<const uint2*>(movedv + grp * 4 + 2);
+            const uint2 m01 = *reinterpret_cast<const uint2*>(movedv + s2 * 4), m23 = *reinterpret_cast<const uint2*>(movedv + s2 * 4 + 2);
             uint64_t todo = (m01.x | m01.y << 16) | static_cast<uint64_t>(m23.x | m23.y << 16) << 32;
-            const uint32_t o = tmem + lane_addr + kColO;
-            const float* f = corr + grp * kHeads;
+            const uint32_t o = tmem + lane_addr + kColO + grp * 2 * kHeads;
+            const float* f = corr + s2 * kHeads;
             if (__popcll(todo) <= kFewHeads) {
               for (; todo; todo &= todo - 1) {
                 const int h = __ffsll(static_cast<long long>(todo)) - 1;
-                float r[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) r[c] = tmem_ld_x1(o + c * kHeads + h);
-                tmem_ld_wait4(r);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_st_x1(o + c * kHeads + h, r[c] * f[h]);
+                float r0 = tmem_ld_x1(o + h), r1 = tmem_ld_x1(o + kHeads + h);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r0), "+f"(r1) : : "memory");
+                tmem_st_x1(o + h, r0 * f[h]);
+                tmem_st_x1(o + kHeads + h, r1 * f[h]);
               }
             } else {
 #pragma unroll 1
-              for (int q = 0; q < 16; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 uint32_t r[16];
                 tmem_ld_x16(o + q * 16, r);
                 tmem_ld_wait16(r);
@@ -1048,29 +1026,24 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             }
             ptx::tmem_st_wait();
           }
-          ptx::named_bar_sync(2 + grp, 128);  // corr is read before the group's next block rewrites it
         }
         if (ok) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            ptx::mbar_arrive(&bars->pfull[grp]);
-            if (!FP4 && ((b - it) % kBatch >= kBatch - 2 || b + 2 >= end)) ptx::mbar_arrive(&bars->bempty[bt]);
+            ptx::mbar_arrive(&bars->pfull[s2]);
+            if (!FP4 && last_of_batch(pc, b - it)) ptx::mbar_arrive(&bars->bempty[bt]);
           }
         }
       }
       it = end;
       ++n;
       bn += batches(pc);
-      // the piece's output: the sums of both groups against the last reference
+      // the piece's output: the sums of both groups
       const int last = (end - 1) & 1;
-      // (a batch of one block is one group's)
-      if (!FP4 && cnt % kBatch == 1 && last != grp && lane == 0) ptx::mbar_arrive(&bars->bempty[(bn - 1) % kBatches]);
-      if (ok)
-        ok = __all_sync(0xffffffffu, (last == grp || wait(other, ((end - 1) >> 1) & 1)) &&
-                                         wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
-      const float fin = refv[last * kHeads + hl];
-      float sum = (l.x + l.y) * (m == -INFINITY ? 1.f : ptx::ex2(m - fin));  // (without keys 0, or not a number)
+      if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[last], ((end - 1) >> 1) & 1)) != 0;
+      const float fin = m;
+      float sum = l.x + l.y;
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (!half) lsum[grp * kHeads + hl] = sum;
       ptx::named_bar_sync(4, 256);
