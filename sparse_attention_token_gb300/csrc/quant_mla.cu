@@ -560,6 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   const int part = blockIdx.x;
   Pieces<ALL> pc(a, part);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, a.status); };
+  // Two at once: a try takes some 100 cycles even when it succeeds.
+  auto wait2 = [&](uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1) {
+    const bool r0 = ptx::mbar_try_wait(bar0, parity0), r1 = ptx::mbar_try_wait(bar1, parity1);
+    return (r0 || wait_on(bar0, parity0, abort, a.status)) && (r1 || wait_on(bar1, parity1, abort, a.status));
+  };
   const uint32_t sbase = ptx::smem_u32(smem);
 
   if (warp == 13) {
@@ -579,7 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         for (int i = 0; i < cnt + L::kAhead && ok; ++i) {
           if (i < cnt) {  // S of block i
             const int b = it + i;
-            ok = wait(&bars->tfull[b % kStages], (b / kStages) & 1) && (b < 2 || wait(&bars->sempty[b & 1], ((b >> 1) & 1) ^ 1));
+            // (one block ahead, P of the block that S's place was last for has been waited for already)
+            ok = b < 2 || L::kAhead == 1 ? wait(&bars->tfull[b % kStages], (b / kStages) & 1)
+                                         : wait2(&bars->tfull[b % kStages], (b / kStages) & 1, &bars->sempty[b & 1], ((b >> 1) & 1) ^ 1);
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t d = tmem + kColS + (b & 1) * kKeys;
@@ -920,9 +927,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         float x[16];
         float mb = -INFINITY;
         if (ok)
-          ok = __all_sync(0xffffffffu, wait(&bars->sfull[s2], (b >> 1) & 1) &&
-                                           (FP4 ? wait(&bars->scfull[ss], (b / kStages) & 1)
-                                                : wait(&bars->scfull[bt], (bi / kBatches) & 1))) != 0;
+          ok = __all_sync(0xffffffffu, FP4 ? wait2(&bars->sfull[s2], (b >> 1) & 1, &bars->scfull[ss], (b / kStages) & 1)
+                                       : (b - it) % kBatch ? wait(&bars->sfull[s2], (b >> 1) & 1)
+                                       : wait2(&bars->sfull[s2], (b >> 1) & 1, &bars->scfull[bt], (bi / kBatches) & 1)) != 0;
         if (ok) {
           ptx::tc_fence_after();
           const uint32_t col = tmem + lane_addr + kColS + s2 * kKeys + grp * 32;
@@ -955,21 +962,17 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         }
         mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
         if (!half) top[(s2 * 2 + grp) * kHeads + hl] = mb;
-        ptx::named_bar_sync(5 + w, 64);  // the two groups' warps of these heads
-        mb = fmaxf(mb, top[(s2 * 2 + (grp ^ 1)) * kHeads + hl]);
         // The reference moves only when it is passed by more than kMove, so that most blocks leave O as it is.
+        const bool any = bar_any(2, m != -INFINITY && mb > m + kMove && hl < hg);
+        mb = fmaxf(mb, top[(s2 * 2 + (grp ^ 1)) * kHeads + hl]);
         const float before = m;
         if (m == -INFINITY || mb > m + kMove) m = mb;
         const float cr = before == -INFINITY ? 1.f : ptx::ex2(before - m);
         l.x *= cr;
         l.y *= cr;
-        const unsigned moved = __ballot_sync(0xffffffffu, !half && hl < hg && cr != 1.f);
-        if (grp == 0) {
-          if (!half) corr[s2 * kHeads + hl] = cr;
-          if (lane == 0) movedv[s2 * 4 + w] = moved;
-        }
         // P's buffer is free once the products of the block that had it before have been done
-        if (ok && b > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2], ((b >> 1) & 1) ^ 1)) != 0;
+        // (one block ahead, this block's S was behind them)
+        if (ok && b > 1 && L::kAhead > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2], ((b >> 1) & 1) ^ 1)) != 0;
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
           uint32_t hi[4], lo[4];
@@ -997,7 +1000,13 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
         // done and before those of this one begin (which wait for them in any case), each group's two latent chunks.
         // (corr and movedv are read before the barrier of the next block, and rewritten behind it.)
-        if (bar_any(2, moved)) {
+        if (any) {
+          const unsigned moved = __ballot_sync(0xffffffffu, !half && hl < hg && cr != 1.f);
+          if (grp == 0) {
+            if (!half) corr[s2 * kHeads + hl] = cr;
+            if (lane == 0) movedv[s2 * 4 + w] = moved;
+          }
+          ptx::named_bar_sync(3, 256);
           if (ok) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2 ^ 1], ((b - 1) >> 1) & 1)) != 0;
           if (ok) {
             ptx::tc_fence_after();
