@@ -21,8 +21,8 @@
 // a cluster that hold them, or else go through memory to a second kernel.  Roles of a CTA:
 //   warps 0..7    softmax, two groups that take 32 keys each of every block.  Rows of S alternate between 16 hi and
 //                 16 lo rows, so that a lane and the one 16 further hold a head's two planes; each adds the planes
-//                 for half of its group's keys.  (Alternate blocks to the groups: 312 us instead of 327 for the first
-//                 figure below, but 37.1 instead of 35.5 for 62 x 128 heads x 1001 keys in 4 bits, and 3 % more for
+//                 for half of its group's keys.  (Alternate blocks to the groups: 312 us instead of 315 for the first
+//                 figure below, but 37.0 instead of 34.9 for 62 x 128 heads x 1001 keys in 4 bits, and 4 % more for
 //                 the other 4-bit cases: there the time from S to P is what counts);
 //   warps 8..11   query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
 //                 4-bit rows also: codes from the staged rows to e4m3 tiles;
@@ -34,10 +34,10 @@
 // bytes meets 128 x 576 + 2 x 64 x 512 multiplications.
 //
 // What bounds it (GB300, 1.9 GHz, captured in a graph):
-//   block     the MMAs of a block take 1470 cycles.  e4m3: 2100 to 2200 a block, by the softmax (some 400 instructions a
-//             warp, each waiting for the one before) and the four tiles in flight: a tile is gathered (950 cycles from
+//   block     the MMAs of a block take 1470 cycles.  e4m3: 2000 to 2100 a block, by the softmax (some 350 instructions a
+//             warp, each waiting for the one before, and a barrier) and the four tiles in flight: a tile is gathered (950 cycles from
 //             L2, 1430 with one issuing warp less), waits its turn, is multiplied twice and freed; 2800 a block when rows
-//             come from DRAM.  1127 queries x 64 heads x 2048 keys: 327 us, 166 at the tensor cores' rate.  4 bits: three
+//             come from DRAM.  1127 queries x 64 heads x 2048 keys: 315 us, 166 at the tensor cores' rate.  4 bits: three
 //             tiles, and decoding stands in the round: 2700 a block.
 //   piece     some 8000 to 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 10000 from a
 //             piece's last product to the next one's first (next queries 6000, then their first block's softmax; the
@@ -85,10 +85,11 @@ template <bool FP4>
 struct Smem {
   static constexpr int kStages = FP4 ? 3 : 4;             // tiles
   static constexpr int kAhead = kStages - 2;              // blocks that S runs ahead of P . V: a tile is always left to fill
+  static constexpr int kPBufs = kAhead + 1;               // S of block b is issued behind P . V of b - kPBufs, whose P it then replaces
   static constexpr int kStagedBufs = FP4 ? 2 : 0;
   static constexpr int kScRing = FP4 ? kStages : kRing;   // blocks whose scales are held
   static constexpr uint32_t kOffTile = 0, kOffQr = kOffTile + kStages * kTile, kOffP = kOffQr + kQRope;
-  static constexpr uint32_t kOffStaged = kOffP + 2 * kPBytes, kOffQ = kOffStaged + kStagedBufs * kStaged;
+  static constexpr uint32_t kOffStaged = kOffP + kPBufs * kPBytes, kOffQ = kOffStaged + kStagedBufs * kStaged;
   static constexpr uint32_t kOffMisc = kOffQ + kQBuf, kOffRows = kOffMisc + 5120, kOffSc = kOffRows + kRing * kKeys * 4;
   static constexpr uint32_t kOffLevels = kOffSc + kScRing * kKeys * 8;  // 4 bits: magnitudes by the scale's byte
   static constexpr uint32_t kBytes = kOffLevels + (FP4 ? 256 * 8 : 0);
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           ok = wait(&bars->pfull[b & 1], (b >> 1) & 1) && (j > 0 || n == 0 || wait(&bars->odrained, (n - 1) & 1));
           if (!ok) break;
           ptx::tc_fence_after();
-          uint32_t vd = tile0 + (b % kStages) * (kTile >> 4), pd = p0 + (b & 1) * (kPBytes >> 4);
+          uint32_t vd = tile0 + (b % kStages) * (kTile >> 4), pd = p0 + (b % L::kPBufs) * (kPBytes >> 4);
           asm volatile("" : "+r"(vd), "+r"(pd));
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -970,9 +971,6 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const float cr = before == -INFINITY ? 1.f : ptx::ex2(before - m);
         l.x *= cr;
         l.y *= cr;
-        // P's buffer is free once the products of the block that had it before have been done
-        // (one block ahead, this block's S was behind them)
-        if (ok && b > 1 && L::kAhead > 1) ok = __all_sync(0xffffffffu, wait(&bars->pvdone[s2], ((b >> 1) & 1) ^ 1)) != 0;
         if (ok) {
           const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
           uint32_t hi[4], lo[4];
@@ -992,7 +990,8 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             lo[j] = t.y;
           }
           const int ch = grp * 2 + half;
-          uint8_t* prow = smem + L::kOffP + s2 * kPBytes + hl * 128;
+          // (its buffer is free: this block's S was issued behind the products that read it, and has been done)
+          uint8_t* prow = smem + L::kOffP + (b % L::kPBufs) * kPBytes + hl * 128;
           *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           ptx::fence_proxy_async_smem();
