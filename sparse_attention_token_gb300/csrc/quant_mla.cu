@@ -1375,6 +1375,8 @@ Plan plan_of(const dsa_quant_mla_args* a) {
     p.split = p.rest ? std::max(1, std::min(p.parts / p.rest, p.nb / 2)) : 1;
     // Pieces of a tile in a cluster of 2, 4 or 8 where its size is near the number of pieces and all clusters find room at
     // once: a GPC holds two of 8 or four of 4, and with whole tiles every SM is taken.
+    // (64 tiles in two pieces each 47.2 us through memory, 44.7 in clusters; 4 tiles 18.5 in 16 pieces through memory, 17.8 in
+    // clusters of 8.)
     if (p.split > 1 && !p.whole) p.cluster = p.split >= 8 && p.rest <= 16 ? 8 : p.split >= 4 && p.rest <= 32 ? 4 : 2;
     if (p.whole && (p.split == 2 || p.split == 3) && p.parts % 2 == 0) p.cluster = 2;
     if (p.cluster > 1) p.split = p.cluster;
