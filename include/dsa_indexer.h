@@ -522,7 +522,8 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* args, dsa_stream_t stream);
  *          stands for 2^E * e4m3(code * s), the product rounded to e4m3
  * (nearest: ties to even; 2^-5 <= s <= 72).  The codes are those of c itself, not of a rounded c: with
  * a norm, of c to within 2^-40.  Every value that a row stands for is exact in bf16.  The rotary part is
- * held as bf16(r) / 2^E (exact for 2^-66 <= |r| < 2^67).  A mean over 512 normal values is off by 2.7 % (e4m3) and 10 % (e2m1) of their size.
+ * held as bf16(r) / 2^E (exact for 2^-66 <= |r| < 2^67).  A mean over 512 normal values is off by
+ * 2.7 % (e4m3) and 10 % (e2m1) of their size.
  * Rows are the library's own: dsa_mla_quant_append writes and dsa_mla_quant_read reads them.  A page
  * may be moved or copied as bytes.
  */
