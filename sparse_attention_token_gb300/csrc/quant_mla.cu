@@ -380,6 +380,30 @@ __device__ __forceinline__ void put_scale(float4* block, int key, float u) {
   pair[0] = u;
   pair[2] = u > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(u) >> 23) - 127 - kExpRef) : -INFINITY;
 }
+// The same of a row of zeros.  Its own E is 0, which stays in u (its rotary part is in these units), marked by the last bit;
+// in x' it takes kZeroExp: it adds nothing to O, and with E = 0, seven octaves above normalised rows, one that is ahead would
+// push the others' p below the smallest that the product takes.
+constexpr int kZeroExp = -kMaxExp;
+__device__ __forceinline__ void put_scale_of_zeros(float4* block, int key) {
+  float* pair = reinterpret_cast<float*>(block + (key >> 1)) + (key & 1);
+  pair[0] = __uint_as_float(0x3F800001u);
+  pair[2] = static_cast<float>(kZeroExp - kExpRef);
+}
+// Of the rows `rows[32 j]` (e4m3) whose bits j are set in `of`, those whose codes are all zeros.  (Only rows of E = 0 are
+// asked about; another row of that scale has a code of 224 or more, found in its first bytes as a rule.)
+__device__ __noinline__ unsigned rows_of_zeros(const uint8_t* cache, const int* rows, unsigned of) {
+#pragma unroll 1
+  for (int i = 0; i < kRank / 16 && of; ++i) {
+    uint4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = of >> j & 1 ? __ldg(reinterpret_cast<const uint4*>(cache + static_cast<long long>(rows[32 * j]) * kRow8) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((v[j].x | v[j].y | v[j].z | v[j].w) & 0x7F7F7F7Fu) of &= ~(1u << j);
+  }
+  return of;
+}
 __device__ __forceinline__ float2 add2(float2 a, float b) {
   float2 d;
   asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
@@ -496,6 +520,19 @@ __device__ __noinline__ void join_in_cluster(const Args& a, uint8_t* tiles, uint
   }
 }
 
+// What the rows of zeros among a lane's 16 keys add to L: p 2^(kExpRef - kZeroExp) each.  (The loop over all keys takes E from u:
+// 2^kExpRef of these p, 2^-60 of what is added here.  Beside that loop, not in it: few blocks have such rows.)
+__device__ __noinline__ float sum_of_zeros(const float4* scp, float ref, float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                           float x7, float x8, float x9, float x10, float x11, float x12, float x13, float x14, float x15) {
+  const float x[16] = {x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (__float_as_uint(reinterpret_cast<const float*>(scp + (j >> 1))[j & 1]) & 1u) s += ptx::ex2(x[j] + ref);
+  static_assert(kExpRef - kZeroExp == 53, "the factor");
+  return s * 0x1p53f;
+}
+
 template <bool FP4, bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
   using L = Smem<FP4>;
@@ -515,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] factors of a block's heads
   float* top = reinterpret_cast<float*>(misc + 4096);                   // [2][2][64] a block's maxima over each group's keys
   uint32_t* movedv = reinterpret_cast<uint32_t*>(misc + 640);           // [2][4] a block's moved heads, by 16
+  uint32_t* zeros = reinterpret_cast<uint32_t*>(misc + 672);            // [kScRing] whether a block has rows of zeros (4 bits: by 16 rows)
   float* lsum = reinterpret_cast<float*>(misc + 2048);                  // [2][64]
   Held* held = reinterpret_cast<Held*>(misc + 2560);                    // [64] of the piece that the cluster joins
   float* qscale = reinterpret_cast<float*>(held + kHeads);             // [kQRing][64]
@@ -679,8 +717,22 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     float u[2 * kBatch];
     const int32_t* table = nullptr;
     auto scales = [&](int bt) {
+      unsigned z = 0u, some = 0u;
 #pragma unroll
-      for (int j = 0; j < 2 * kBatch; ++j) put_scale(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane, u[j]);
+      for (int j = 0; j < 2 * kBatch; ++j) {
+        put_scale(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane, u[j]);
+        z |= (u[j] == 1.f ? 1u : 0u) << j;
+      }
+      if (__builtin_expect(__any_sync(0xffffffffu, z != 0u), 0)) {
+        z = rows_of_zeros(a.cache, rows + bt * kBatch * kKeys + lane, z);
+        __syncwarp();
+        some = __reduce_or_sync(0xffffffffu, z);
+        for (; z; z &= z - 1) {
+          const int j = __ffs(z) - 1;
+          put_scale_of_zeros(sc + (bt * kBatch + (j >> 1)) * (kKeys / 2), 32 * (j & 1) + lane);
+        }
+      }
+      if (lane < kBatch) zeros[bt * kBatch + lane] = some >> (2 * lane) & 3u;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars->scfull[bt]);
     };
@@ -887,10 +939,16 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             const int key = w * 16 + 4 * j + hr;
             *reinterpret_cast<uint4*>(tile + 4 * kAtom + key * 128 + ((l8 ^ (key & 7)) << 4)) = rr[j];
           }
-          if (lane < 16) {  // (the row's exponent from the top bits of its first eight scales)
-            const uint2 top = *reinterpret_cast<const uint2*>(staged + lane * kRow4 + kScale4);
-            put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(top_bits(top.x) + 16 * top_bits(top.y) - 128) : 0.f);
+          bool none = false;
+          if (lane < 16) {  // (the row's exponent from the top bits of its first eight scales; of zeros: E = 0, the smallest scales)
+            const uint4 lo = *reinterpret_cast<const uint4*>(staged + lane * kRow4 + kScale4);
+            const uint4 hi = *reinterpret_cast<const uint4*>(staged + lane * kRow4 + kScale4 + 16);
+            none = there && ((lo.x | (lo.y ^ 0x80000000u)) | (lo.z | lo.w) | (hi.x | hi.y) | (hi.z | hi.w)) == 0u;
+            put_scale(sc + st * (kKeys / 2), w * 16 + lane, there ? pow2f(top_bits(lo.x) + 16 * top_bits(lo.y) - 128) : 0.f);
+            if (none) put_scale_of_zeros(sc + st * (kKeys / 2), w * 16 + lane);
           }
+          none = __any_sync(0xffffffffu, none);
+          if (lane == 0) reinterpret_cast<uint8_t*>(zeros + st)[w] = none;
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -927,6 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const float4* scp = sc + ss * (kKeys / 2) + grp * 16 + half * 8;
         float x[16];
         float mb = -INFINITY;
+        uint32_t none = 0u;  // rows of zeros in the block
         if (ok)
           ok = __all_sync(0xffffffffu, FP4 ? wait2(&bars->sfull[s2], (b >> 1) & 1, &bars->scfull[ss], (b / kStages) & 1)
                                        : (b - it) % kBatch ? wait(&bars->sfull[s2], (b >> 1) & 1)
@@ -941,6 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars->sempty[s2]);
+          none = zeros[ss];
           float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
@@ -994,6 +1054,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
           uint8_t* prow = smem + L::kOffP + (b % L::kPBufs) * kPBytes + hl * 128;
           *reinterpret_cast<uint4*>(prow + ((ch ^ (hl & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (hl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (__builtin_expect(none != 0u, 0))
+            l.x += sum_of_zeros(scp, ref, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8], x[9], x[10], x[11], x[12], x[13], x[14],
+                                x[15]);
           ptx::fence_proxy_async_smem();
         }
         // Heads whose reference moved: their columns of O are rescaled when the products of the block before are
