@@ -596,6 +596,10 @@ dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* args, dsa_stream_t 
  * NaN).  A page outside the cache is skipped and reported through dsa_check_device_status, as are
  * positions past the table (topk_width = 0).  Results do not depend on the run.  workspace:
  * dsa_quant_mla_workspace_size bytes (0: none is taken), 16-byte aligned like the other pointers.
+ * Weights enter out to 2^-7 each.  Small ones, of which many may count together, are rounded up for some keys and down for
+ * others: a key whose weight times its row's 2^E is below 2^-11 of the largest such product is off by up to 2^-17 of that,
+ * and the mean of many that weigh alike by 2^-7 of itself and 2^-30 of that product.  Below 2^-30 of it a key adds nothing to
+ * out (to lse all do); the product of a row of zeros, which adds nothing to out, counts with E = -60.
  */
 typedef struct {
   int format, B, total_q, H, kv_rank, rope_dim, page_size, num_pages, max_pages_per_seq, topk_width;

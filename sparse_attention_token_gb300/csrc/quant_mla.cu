@@ -328,26 +328,35 @@ __device__ __forceinline__ void tmem_st_x1(uint32_t taddr, float r) {
 __device__ __forceinline__ void tmem_ld_wait4(float (&r)[4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : : "memory");
 }
-// Four values 0 <= p <= 2^8, given as 2^-8 p in fp16, as e4m3 codes (x) and the e5m2 codes of what they leave (y).
+// Four values 0 <= p <= 2^8 in fp16 as e4m3 codes (x) and the e5m2 codes of what they leave (y).
 // 2^-8 p has e4m3's exponents as its low four and its subnormals where e4m3 has them, so rounding its bits to three
 // of the mantissa is the code; e5m2 is the upper half of fp16.  (Conversions take the slow pipe, integers do not.)
 // Together they are within 2^-7 of p.  Below e4m3's normal numbers, p < 2^-6, the second term's two bits are all that
-// counts, 2^-13 at most off; thousands of such keys behind a large one may be alike, and their errors with them (a tenth
-// of their share of the output), so there the rounding goes up for as many of 16 neighbouring keys as it should: `at` is
-// the place among them of the first of the four.
+// counts, and its step is 2^-12 to 2^-16.  Thousands of such keys behind a large one may be alike, and their errors with them, or
+// all less than half a step, so there the rounding goes up for as many keys as it should: a key's threshold among the 256 that
+// fp16 has in a step is 16 times its place among 16 in bit-reversed order (`at`: of the first of the four), its bits changed by
+// the hash of the sixteen (`change`), so that keys at a regular distance are not rounded alike.  What is lost is fp16's: p
+// below 2^-25, 2^-30 of the largest, and up to 2^-25 of others.
 __device__ __forceinline__ constexpr uint32_t round_at(int i) {  // 16 thresholds of a step, in bit-reversed order
-  return 8u + 16u * ((i & 1) << 3 | (i & 2) << 1 | (i & 4) >> 1 | (i & 8) >> 3);
+  return 16u * ((i & 1) << 3 | (i & 2) << 1 | (i & 4) >> 1 | (i & 8) >> 3);
 }
-__device__ __forceinline__ uint32_t second_term(__half2 v, uint32_t first, int at) {
-  const __half2 left = __hmul2(__hsub2(v, *reinterpret_cast<const __half2*>(&first)), __float2half2_rn(256.f));
-  const uint32_t small = __hlt2_mask(v, __float2half2_rn(6.103515625e-05f));  // p < 2^-6
+__device__ __forceinline__ uint32_t threshold_change(int sixteen) {
+  return __byte_perm(static_cast<uint32_t>(sixteen) * 0x9E3779B9u, 0u, 0x4242);  // (2^32 over the golden ratio)
+}
+__device__ __forceinline__ uint32_t first_term(__half2 p) {  // in 2^-8
+  const __half2 v = __hmul2(p, __float2half2_rn(0.00390625f));
+  return (*reinterpret_cast<const uint32_t*>(&v) + 0x00400040u) & 0x7F807F80u;
+}
+__device__ __forceinline__ uint32_t second_term(__half2 p, uint32_t first, int at, uint32_t change) {
+  const __half2 left = __hfma2(*reinterpret_cast<const __half2*>(&first), __float2half2_rn(-256.f), p);  // (exact)
+  const uint32_t small = __hlt2_mask(p, __float2half2_rn(0.015625f));  // p < 2^-6
   const uint32_t spread = (round_at(at) | round_at(at + 1) << 16) ^ 0x00800080u;
-  return *reinterpret_cast<const uint32_t*>(&left) + ((small & spread) ^ 0x00800080u);
+  return *reinterpret_cast<const uint32_t*>(&left) + ((small & (spread ^ change)) ^ 0x00800080u);
 }
-__device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b, int at) {
-  const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a), ub = *reinterpret_cast<const uint32_t*>(&b);
-  const uint32_t ra = (ua + 0x00400040u) & 0x7F807F80u, rb = (ub + 0x00400040u) & 0x7F807F80u;
-  return make_uint2(__byte_perm(ra << 1, rb << 1, 0x7531), __byte_perm(second_term(a, ra, at), second_term(b, rb, at + 2), 0x7531));
+__device__ __forceinline__ uint2 two_terms(__half2 a, __half2 b, int at, uint32_t change) {
+  const uint32_t fa = first_term(a), fb = first_term(b);
+  return make_uint2(__byte_perm(fa << 1, fb << 1, 0x7531),
+                    __byte_perm(second_term(a, fa, at, change), second_term(b, fb, at + 2, change), 0x7531));
 }
 // Four values |x| < 2^8 as e4m3 codes (x) and as those of 2^kLoShift times what they leave (y).  (By conversions, which are
 // fewer instructions: the warps that do this have a scheduler each, and the softmax is not at work beside them.)
@@ -489,8 +498,8 @@ __device__ __noinline__ void join_in_cluster(const Args& a, uint8_t* tiles, uint
       total += f == 0.f ? 0.f : f * s.sum;
       weights[j * kHeads + tid] = f;
     }
-    for (int j = 0; j < C; ++j) weights[j * kHeads + tid] = total == 0.f ? 0.f : weights[j * kHeads + tid] * (pow2f(kExpRef - 8) / total);
-    if (a.lse) a.lse[static_cast<long long>(t) * a.H + g * kHeads + h] = total == 0.f ? -INFINITY : (M - (kPShift - 8) + log2f(total)) * kLn2;
+    for (int j = 0; j < C; ++j) weights[j * kHeads + tid] = total == 0.f ? 0.f : weights[j * kHeads + tid] * (pow2f(kExpRef) / total);
+    if (a.lse) a.lse[static_cast<long long>(t) * a.H + g * kHeads + h] = total == 0.f ? -INFINITY : (M - kPShift + log2f(total)) * kLn2;
   }
   __syncthreads();
   const bool odd = lane & 1;
@@ -1029,10 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const float before = m;
         if (m == -INFINITY || mb > m + kMove) m = mb;
         const float cr = before == -INFINITY ? 1.f : ptx::ex2(before - m);
-        l.x *= cr;
-        l.y *= cr;
+        float2 lb = make_float2(0.f, 0.f);  // the block's sum, by itself first: a long row's has 16 times fewer terms
         if (ok) {
-          const float ref = m == -INFINITY ? 0.f : (kPShift - 8) - m;
+          const float ref = m == -INFINITY ? 0.f : kPShift - m;
+          const uint32_t change = threshold_change((pc.k0 + b - it) * 4 + grp * 2 + half);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1042,13 +1051,15 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
               const uint2 u = *reinterpret_cast<const uint2*>(scp + 2 * j + q);
               constexpr uint32_t kInv = static_cast<uint32_t>(254 + kExpRef) << 23;
               p[q] = add2(make_float2(x[4 * j + 2 * q], x[4 * j + 2 * q + 1]), ref);
-              p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));  // 2^-8 p
-              ptx::ffma2(l, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // 2^-8 p 2^(kExpRef - E)
+              p[q] = make_float2(ptx::ex2(p[q].x), ptx::ex2(p[q].y));
+              ptx::ffma2(lb, p[q], make_float2(__uint_as_float(kInv - u.x), __uint_as_float(kInv - u.y)));  // p 2^(kExpRef - E)
             }
-            const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y), 4 * j);
+            const uint2 t = two_terms(__floats2half2_rn(p[0].x, p[0].y), __floats2half2_rn(p[1].x, p[1].y), 4 * j, change);
             hi[j] = t.x;
             lo[j] = t.y;
           }
+          ptx::ffma2(lb, l, make_float2(cr, cr));
+          l = lb;
           const int ch = grp * 2 + half;
           // (its buffer is free: this block's S was issued behind the products that read it, and has been done)
           uint8_t* prow = smem + L::kOffP + (b % L::kPBufs) * kPBytes + hl * 128;
@@ -1122,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       const int slot = 2 * part + (pc.k0 == 0 ? 1 : 0);
       if (grp == 0 && !half) {
         sum = lsum[hl] + lsum[kHeads + hl];
-        linv[hl] = sum == 0.f ? 0.f : pow2f(kExpRef - 8) / sum;
+        linv[hl] = sum == 0.f ? 0.f : pow2f(kExpRef) / sum;
         if (hl < hg && ok) {
           if (!ALL && !whole && a.cluster > 1) {
             held[hl] = {fin + 0.f * sum, sum};
@@ -1130,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2] = fin + 0.f * sum;  // (not a number if the sum is not)
             a.part_ml[(static_cast<long long>(slot) * kHeads + hl) * 2 + 1] = sum;
           } else if (a.lse) {
-            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = sum == 0.f ? -INFINITY : (fin - (kPShift - 8) + log2f(sum)) * kLn2;
+            a.lse[static_cast<long long>(pc.t) * a.H + pc.g * kHeads + hl] = sum == 0.f ? -INFINITY : (fin - kPShift + log2f(sum)) * kLn2;
           }
         }
       }
@@ -1271,14 +1282,14 @@ __global__ void __launch_bounds__(kJoinThreads) quant_join_kernel(const Args a) 
     __nv_bfloat16* dst = a.out + (static_cast<long long>(t) * a.H + h0) * kRank + lat;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (h0 + i < a.H) dst[i * kRank] = __float2bfloat16_rn(s[i] == 0.f ? 0.f : v[i] / s[i] * pow2f(kExpRef - 8));
+      if (h0 + i < a.H) dst[i * kRank] = __float2bfloat16_rn(s[i] == 0.f ? 0.f : v[i] / s[i] * pow2f(kExpRef));
   };
   auto store_lse = [&](int t, int h0, float4 M, float4 total) {
     const float m[4] = {M.x, M.y, M.z, M.w}, s[4] = {total.x, total.y, total.z, total.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (a.lse && h0 + i < a.H)
-        a.lse[static_cast<long long>(t) * a.H + h0 + i] = s[i] == 0.f ? -INFINITY : (m[i] - (kPShift - 8) + log2f(s[i])) * kLn2;
+        a.lse[static_cast<long long>(t) * a.H + h0 + i] = s[i] == 0.f ? -INFINITY : (m[i] - kPShift + log2f(s[i])) * kLn2;
   };
   const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), zero = make_float4(0.f, 0.f, 0.f, 0.f);
 
