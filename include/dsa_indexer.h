@@ -591,7 +591,7 @@ dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* args, dsa_stream_t 
  *   8, any in a dimension of size 1; the last dimension dense); out [total_q, H, 512] bf16 dense;
  *   lse [total_q, H]; topk [total_q, topk_width].
  * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, scale > 0; total_q * H and num_pages * page_size below
- * 2^31 - 128.  Rows of the cache that no query attends to may hold anything; the others are finite, and
+ * 2^31 - 128; topk_width at most 2^31 - 256.  Rows of the cache that no query attends to may hold anything; the others are finite, and
  * so are the queries of rows that are not padding (what is not finite makes its own query and head
  * NaN).  A page outside the cache is skipped and reported through dsa_check_device_status, as are
  * positions past the table (topk_width = 0).  Results do not depend on the run.  workspace:

@@ -76,7 +76,7 @@ constexpr int kFewHeads = 12;                             // rescaled one by one
 constexpr int kLoShift = 4;                               // lo = 2^4 (x - hi): below 2^4 of its step it is exact, and 2^7 at most
 constexpr int kExpRef = -7;                               // E of normalised rows: x' counts from there, so that it does not lose x's bits
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr long long kMostKeys = 0x7FFFFF00ll;             // that a query sees: a block's last key fits 32 bits
+constexpr long long kMostKeys = 0x7FFFFF00ll;             // that a query sees: a key of its last blocks fits 32 bits, and of three behind them
 constexpr int kMaxStages = 4;
 constexpr int kQRing = 4;                                 // scales of the queries of consecutive pieces
 constexpr int kBatch = 4, kBatches = 4, kRing = kBatch * kBatches;  // blocks of a piece whose rows are looked up together
@@ -1415,6 +1415,7 @@ dsa_status validate(const dsa_quant_mla_args* a) {
     return DSA_ERR_INVALID_ARGUMENT;
   if (a->kv_rank != quant::kRank || a->rope_dim != quant::kRope || quant::row_bytes(a->format) == 0 || a->H > 128)
     return DSA_ERR_UNSUPPORTED;
+  if (a->topk_width > kMostKeys) return DSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(a->total_q) * a->H >= 0x7FFFFF80LL || static_cast<long long>(a->num_pages) * a->page_size >= 0x7FFFFF80LL)
     return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
