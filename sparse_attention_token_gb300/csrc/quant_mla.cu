@@ -99,6 +99,7 @@ static_assert(Smem<false>::kBytes <= 232448 && Smem<true>::kBytes <= 232448, "sh
 struct Args {
   int B, total_q, H, groups, page_size, num_pages, max_pages, topk_width;
   int nb;                  // blocks of a tile (selected keys)
+  int most_live;           // total_q; 0 without requests, where there are no lengths to look at
   int parts;               // CTAs
   int whole, rest, split;  // selected keys: whole tiles a CTA, tiles behind them, pieces of each
   int cluster;             // CTAs that hold the pieces of a tile and join them among themselves (1: the pieces go through memory)
@@ -125,6 +126,9 @@ struct Bars {
   uint64_t qfull[kQRing], qfree;
   uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], odrained, done;
 };
+
+// Rows of queries; the others are padding.
+__device__ __forceinline__ int live_rows(const Args& a) { return min(__ldg(a.cu + a.B), a.most_live); }
 
 // Keys that a query at place i of the last q of n tokens sees (every position): those up to its own that the table
 // covers.
@@ -251,7 +255,7 @@ struct Keys {
     if (query == t) return;
     t = query;
     if (b < 0) {
-      live = __ldg(a.cu + a.B);  // rows of queries; the others are padding
+      live = live_rows(a);
       b = t < live ? request_of(a.cu, a.B, t, lane) : 0;
       hi = t;
     } else {
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       bool live[4];
       uint4 rp[4], r[4][4];
       __nv_bfloat162 am[4];
-      const uint32_t keep = pc.t < __ldg(a.cu + a.B) ? 0xffffffffu : 0u;  // rows of padding may hold anything: taken as zeros
+      const uint32_t keep = pc.t < live_rows(a) ? 0xffffffffu : 0u;  // rows of padding may hold anything: taken as zeros
       auto kept = [&](const uint4& v) { return make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep); };
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1373,7 +1377,7 @@ __global__ void __launch_bounds__(1024) quant_plan_kernel(const Args a, long lon
     for (int b = threadIdx.x; b <= a.B; b += 1024) first[b] = __ldg(a.cu + b);
   __syncthreads();
   auto cu = [&](int b) { return held ? first[b] : __ldg(a.cu + b); };
-  const int rows = cu(a.B);
+  const int rows = min(cu(a.B), a.most_live);
   long long before = 0;
   for (int t0 = 0; t0 < a.total_q; t0 += 1024) {
     const int t = t0 + threadIdx.x;
@@ -1529,6 +1533,7 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.max_pages = a->max_pages_per_seq;
   k.topk_width = a->topk_width;
   k.nb = p.nb;
+  k.most_live = a->B > 0 ? a->total_q : 0;
   k.parts = p.parts;
   k.whole = p.whole;
   k.rest = p.rest;
