@@ -1415,7 +1415,7 @@ __global__ void __launch_bounds__(1024) quant_plan_kernel(const Args a, long lon
 dsa_status validate(const dsa_quant_mla_args* a) {
   if (!a) return DSA_ERR_INVALID_ARGUMENT;
   if (a->B < 0 || a->total_q < 0 || a->H <= 0 || a->topk_width < 0 || a->page_size <= 0 || a->num_pages < 0 ||
-      a->max_pages_per_seq < 0 || !(a->scale > 0.f))
+      a->max_pages_per_seq < 0 || !(a->scale > 0.f) || !(a->scale < INFINITY))
     return DSA_ERR_INVALID_ARGUMENT;
   if (a->kv_rank != quant::kRank || a->rope_dim != quant::kRope || quant::row_bytes(a->format) == 0 || a->H > 128)
     return DSA_ERR_UNSUPPORTED;

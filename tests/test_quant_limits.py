@@ -12,3 +12,8 @@ def test_selections_whose_blocks_pass_32_bits(dsa, width):  # noqa: F811
 def test_the_widest_selection_is_cut_like_others(dsa):  # noqa: F811
     sizes = [_size(dsa, topk_width=k, total_q=1, H=64) for k in (1 << 20, 0x7FFFFF00)]
     assert sizes[0] == sizes[1]
+
+
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf")])
+def test_a_scale_that_is_not_finite(dsa, scale):  # noqa: F811
+    assert _call(dsa, "dsa_quant_mla", MLA, dict(scale=scale)) == dsa.DSA_ERR_INVALID_ARGUMENT
