@@ -557,7 +557,7 @@ dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* args, dsa_strea
  * dsa_mla_quant_read -- rows of a quantised cache as bf16: for request b and 0 <= i < cu_lens[b + 1] -
  * cu_lens[b], row t = cu_lens[b] + i of c_kv and k_rope gets what position starts[b] + i of the request
  * (i itself when starts is NULL) stands for, exactly.  The rows may be views of one [total, 576] array
- * (c_stride, r_stride elements apart, multiples of 8; any when total = 1).  total is the outputs'
+ * (c_stride, r_stride elements apart, 512 and 64 or more, multiples of 8; any when total = 1).  total is the outputs'
  * length: rows past cu_lens[B] are left as they were, rows past total are dropped.  A position whose
  * page is outside the cache, or that the table does not cover, leaves its row as it was and is
  * reported through dsa_check_device_status.  c_kv, k_rope and cache 16-byte aligned.

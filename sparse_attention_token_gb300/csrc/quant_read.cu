@@ -82,7 +82,8 @@ extern "C" dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* a, dsa_s
   if (a->total == 0 || a->B == 0) return DSA_OK;
   if ((!a->cache && a->num_pages > 0) || !a->cu_lens || !a->c_kv || !a->k_rope || (!a->block_tables && a->max_pages_per_seq > 0))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (a->total > 1 && (a->c_stride < 0 || a->r_stride < 0 || a->c_stride % 8 != 0 || a->r_stride % 8 != 0))
+  // (rows that lie over one another would be written by two warps)
+  if (a->total > 1 && (a->c_stride < quant::kRank || a->r_stride < quant::kRope || a->c_stride % 8 != 0 || a->r_stride % 8 != 0))
     return DSA_ERR_INVALID_ARGUMENT;
   auto al = [](const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
   if (!al(a->cache, 16) || !al(a->c_kv, 16) || !al(a->k_rope, 16) || !al(a->block_tables, 4) || !al(a->cu_lens, 4) ||
