@@ -1452,12 +1452,21 @@ Plan plan_of(const dsa_quant_mla_args* a) {
     p.rest = tiles - p.whole * p.parts;
     // pieces of two blocks at least: of one, 4 tiles of 32 blocks take as long, and the join longer
     p.split = p.rest ? std::max(1, std::min(p.parts / p.rest, p.nb / 2)) : 1;
-    // Pieces of a tile in a cluster of 2, 4 or 8 where its size is near the number of pieces and all clusters find room at
-    // once: a GPC holds two of 8 or four of 4, and with whole tiles every SM is taken.
-    // (64 tiles in two pieces each 47.2 us through memory, 44.7 in clusters; 4 tiles 18.5 in 16 pieces through memory, 17.8 in
-    // clusters of 8.)
-    if (p.split > 1 && !p.whole) p.cluster = p.split >= 8 && p.rest <= 16 ? 8 : p.split >= 4 && p.rest <= 32 ? 4 : 2;
-    if (p.whole && (p.split == 2 || p.split == 3) && p.parts % 2 == 0) p.cluster = 2;
+    // Pieces of a tile in a cluster (as many as it has CTAs) where that is faster than more pieces, joined through memory, and
+    // all clusters find room at once: 15 of 8, 32 of 4, 76 of 2 (16 of 8: 46.0 us instead of 23.6; with whole tiles every SM is
+    // taken).  The cluster's join saves a launch, some 3 us; it adds blocks to a CTA, 1.0 to 1.4 us each; and with many heads it
+    // takes longer than a join through memory of few pieces.  us in a cluster, through memory; 2048 keys in 8 bits (4 bits alike):
+    //   4 tiles of 16 heads    8 or 16 pieces  17.0, 18.0      of 64 heads           23.4, 21.6
+    //   24 tiles of 16 heads   4 or 6          21.1, 21.1      17 tiles, 4 or 8      20.5, 19.6 (four blocks more)
+    //   32 tiles of 32 heads   4               23.7, 23.4      of 48 heads           26.3, 24.6
+    //   64 tiles of 8 heads    2               28.4, 32.3      of 64 heads           35.8, 37.6
+    //   48 tiles of 64 heads   2 or 3          35.5, 32.8 (five blocks more)
+    //   64 tiles behind 152    2               76.4, 81.1      40 tiles, 2 or 3      75.5, 74.4
+    //   33 tiles of 64 heads, 256 keys, 2  19.5, 17.9      1 tile of 64, 65536 keys, 8 or 152  164, 28.8
+    const int most = !p.whole && p.split >= 8 && p.rest <= 15 ? 8 : !p.whole && p.split >= 4 && p.rest <= 32 ? 4 : 2;
+    const int added = (p.nb + most - 1) / most - (p.nb + p.split - 1) / p.split;
+    if (p.split >= 2 && added <= 2 && (a->H <= 32 || (most == 2 && 3 * p.rest > p.parts)) && p.rest * most <= p.parts && p.parts % (p.whole ? most : 1) == 0)
+      p.cluster = most;
     if (p.cluster > 1) p.split = p.cluster;
     if (!p.whole) p.parts = p.rest * p.split;
     if (p.split == 1 || p.cluster > 1) return p;  // no workspace

@@ -20,3 +20,11 @@ def test_without_requests_all_rows_are_padding(row, k):
         out, lse = case.run()
         _ok()
         assert not out.any() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("row", FORMATS)
+@pytest.mark.parametrize("H,k,queries", [(64, 2048, 16), (16, 2048, 16), (16, 2048, 15), (64, 2048, 17), (20, 2048, 33), (32, 2048, 24),
+                                         (64, 20000, 1), (128, 9000, 2), (8, 700, 45), (64, 384, 192)])
+def test_cuts_of_few_tiles(row, H, k, queries):
+    """On both sides of the rule that takes a cluster or memory for the pieces of a tile."""
+    Case(row, H, 64, [(queries, max(k, 2500))], k=k, seed=k + queries).check()

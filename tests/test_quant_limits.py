@@ -24,3 +24,21 @@ def test_rows_that_lie_over_one_another_are_not_written(dsa, strides):  # noqa: 
     """Two rows of an output would be written to the same place by two warps; one row's stride leads nowhere."""
     assert _call(dsa, "dsa_mla_quant_read", READ, strides) == dsa.DSA_ERR_INVALID_ARGUMENT
     assert _call(dsa, "dsa_mla_quant_read", READ, dict(strides, total=0)) == dsa.DSA_OK
+
+
+@pytest.mark.parametrize("kw", [dict(total_q=1, H=64, topk_width=65536), dict(total_q=16, H=64, topk_width=2048),
+                                dict(total_q=17, H=64, topk_width=2048), dict(total_q=33, H=16, topk_width=2048),
+                                dict(total_q=4, H=128, topk_width=8192), dict(total_q=33, H=64, topk_width=256)], ids=str)
+def test_tiles_are_not_cut_less_for_the_sake_of_a_cluster(dsa, kw):  # noqa: F811
+    """Few tiles of many keys are cut for all SMs: their pieces go through memory, so the call takes a workspace of their size
+    (148 SMs where there is none to ask, two pieces of 64 x 512 fp32 a CTA)."""
+    tiles = kw["total_q"] * -(-kw["H"] // 64)
+    blocks = -(-kw["topk_width"] // 64)
+    pieces = tiles * min(148 // tiles, blocks // 2)
+    assert _size(dsa, **kw) >= 2 * pieces * 64 * 512 * 4
+
+
+@pytest.mark.parametrize("kw", [dict(total_q=4, H=16, topk_width=2048), dict(total_q=64, H=64, topk_width=2048),
+                                dict(total_q=30, H=32, topk_width=512)], ids=str)
+def test_pieces_of_a_cluster_take_no_workspace(dsa, kw):  # noqa: F811
+    assert _size(dsa, **kw) == 0
