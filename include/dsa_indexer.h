@@ -714,6 +714,16 @@ dsa_status dsa_test_arm_score_timeout(unsigned long long limit_ns);
  */
 dsa_status dsa_test_arm_prefix_mla_timeout(int site, unsigned at, unsigned long long limit_ns);
 
+/*
+ * dsa_test_arm_quant_mla_timeout -- the same for the attention kernel of dsa_quant_mla, in its CTAs of
+ * even number.  site, each before its number `at` of a CTA:
+ *   1 MMA issuer, block of 64 keys; 2, 3 either warp that copies rows, block; 4 the warp that looks
+ *   them up, batch of 4 blocks; 5 one warp of the queries, query and 64 heads; 6 one warp that decodes
+ *   4-bit rows, block; 7 one warp of the softmax, block; 9 .. 15 are 1 .. 7 in the CTAs of odd number.
+ * A site that the call does not come to changes nothing.
+ */
+dsa_status dsa_test_arm_quant_mla_timeout(int site, unsigned at, unsigned long long limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

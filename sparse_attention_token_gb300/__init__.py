@@ -228,6 +228,8 @@ def lib():
         L.dsa_test_arm_score_timeout.argtypes = [ctypes.c_ulonglong]
         L.dsa_test_arm_prefix_mla_timeout.restype = I
         L.dsa_test_arm_prefix_mla_timeout.argtypes = [I, ctypes.c_uint, ctypes.c_ulonglong]
+        L.dsa_test_arm_quant_mla_timeout.restype = I
+        L.dsa_test_arm_quant_mla_timeout.argtypes = [I, ctypes.c_uint, ctypes.c_ulonglong]
         _LIB = L
     return _LIB
 
@@ -1155,6 +1157,13 @@ def dsa_test_arm_prefix_mla_timeout(site: int, at: int, limit_ns: int) -> None:
     before block `at`, 2 keys, 3 values, 4 queries before piece `at`, 5 softmax; + 8 in the odd CTAs)."""
     _check(lib().dsa_test_arm_prefix_mla_timeout(int(site), int(at), int(limit_ns)),
            "dsa_test_arm_prefix_mla_timeout")
+
+
+def dsa_test_arm_quant_mla_timeout(site: int, at: int, limit_ns: int) -> None:
+    """The same for the attention kernel of the next dsa_quant_mla: a wait of one role runs out (before block `at`: 1 MMAs,
+    2 and 3 the copying warps, 6 decoding, 7 softmax; 4 look-ups before batch `at`, 5 queries before tile `at`; + 8 in
+    the CTAs of odd number)."""
+    _check(lib().dsa_test_arm_quant_mla_timeout(int(site), int(at), int(limit_ns)), "dsa_test_arm_quant_mla_timeout")
 
 
 def dsa_check_device_status(stream=None) -> int:

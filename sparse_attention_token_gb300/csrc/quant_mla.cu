@@ -117,7 +117,24 @@ struct Args {
   float *part_o, *part_ml; // pieces: [slot][4][16][128][4] (latent chunk, four heads, latent, head), [slot][64][2]
   int2* joins;             // [parts] the tile that a part begins inside, if no earlier one does (-1: none), its last part
   unsigned* status;
+  // failure-path test hook: a role waits, at probe_at, for what never comes
+  int probe_site;
+  uint32_t probe_at;
+  long long probe_cycles;
 };
+
+// Roles whose waits the test hook can let run out: before a block (MMAs; either copying warp; decoding; softmax), a batch of
+// look-ups or a piece's queries, in the CTAs of even number; + kProbeOdd: in the others.
+enum : int { kProbeMma = 1, kProbeCopy = 2, kProbeCopy2 = 3, kProbeRows = 4, kProbeQueries = 5, kProbeDecode = 6, kProbeSoftmax = 7, kProbeOdd = 8 };
+struct Probe {
+  int site;
+  uint32_t at;
+  unsigned long long limit_ns;
+};
+Probe& armed_probe() {
+  static thread_local Probe p{0, 0, 0};
+  return p;
+}
 
 struct Bars {
   uint64_t tfull[kMaxStages], tempty[kMaxStages];
@@ -125,6 +142,7 @@ struct Bars {
   uint64_t gfull[2], gempty[2];           // staged 4-bit rows
   uint64_t qfull[kQRing], qfree;
   uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], odrained, done;
+  uint64_t never;                         // test hook: nothing arrives
 };
 
 // Rows of queries; the others are padding.
@@ -546,7 +564,8 @@ __device__ __noinline__ float sum_of_zeros(const float4* scp, float ref, float x
   return s * 0x1p53f;
 }
 
-template <bool FP4, bool ALL>
+// kProbe: with the test hook's waits.
+template <bool FP4, bool ALL, bool kProbe>
 __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_constant__ CUtensorMap tmap, const Args a) {
   using L = Smem<FP4>;
   constexpr int kStages = L::kStages;
@@ -560,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
   Bars* bars = reinterpret_cast<Bars*>(misc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 512);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 516);
+  volatile int* stopped = reinterpret_cast<volatile int*>(misc + 520);  // [2] blocks that either copying warp came to
   uint2* levels = reinterpret_cast<uint2*>(smem + L::kOffLevels);       // [256] the eight magnitudes that codes stand for
   float* linv = reinterpret_cast<float*>(misc + 768);                   // [64] of the piece that is written
   float* corr = reinterpret_cast<float*>(misc + 1024);                  // [2][64] factors of a block's heads
@@ -593,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     ptx::mbar_init(&bars->qfree, 1);
     ptx::mbar_init(&bars->odrained, 8);
     ptx::mbar_init(&bars->done, 1);
+    if (kProbe) ptx::mbar_init(&bars->never, 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
@@ -618,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     return (r0 || wait_on(bar0, parity0, abort, a.status)) && (r1 || wait_on(bar1, parity1, abort, a.status));
   };
   const uint32_t sbase = ptx::smem_u32(smem);
+  auto stop_at = [&](int site) { return kProbe && a.probe_site == site + (blockIdx.x & 1 ? kProbeOdd : 0) ? a.probe_at : ~0u; };
+  auto run_out = [&]() { return ptx::mbar_spin(&bars->never, 0, abort, a.status, kStatusTimeout, a.probe_cycles); };
 
   if (warp == 13) {
     // ------------------------------------------------------------ MMAs
@@ -627,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
       const uint32_t id_qk = ptx::idesc_f32acc(128, kKeys, false), id_qr = ptx::idesc_f32acc(128, kKeys, true);
       const uint32_t tile0 = ptx::desc_lo(sbase + L::kOffTile, kAtom), rope0 = ptx::desc_lo(sbase + L::kOffQr, 16);
       const uint32_t p0 = ptx::desc_lo(sbase + L::kOffP, 16);
+      const uint32_t stop = stop_at(kProbeMma);
       int it = 0, n = 0;  // blocks, pieces
       bool ok = true;
       while (ok && pc.next(a)) {
@@ -636,6 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         for (int i = 0; i < cnt + L::kAhead && ok; ++i) {
           if (i < cnt) {  // S of block i
             const int b = it + i;
+            if (kProbe && static_cast<uint32_t>(b) == stop && !run_out()) {
+              ok = false;
+              break;
+            }
             // (one block ahead, P of the block that S's place was last for has been waited for already)
             ok = b < 2 || L::kAhead == 1 ? wait(&bars->tfull[b % kStages], (b / kStages) & 1)
                                          : wait2(&bars->tfull[b % kStages], (b / kStages) & 1, &bars->sempty[b & 1], ((b >> 1) & 1) ^ 1);
@@ -686,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     // ------------------------------------------------------------ rows of the cache, half of each block
     const int first = warp == 12 ? 0 : 8;  // groups of four rows
     constexpr int kBufs = FP4 ? 2 : kStages;
+    const uint32_t stop = stop_at(warp == 12 ? kProbeCopy : kProbeCopy2);
     int it = 0, bn = 0;  // blocks, batches before this piece
     bool ok = true;
     for (; ok && pc.next(a); bn += batches(pc)) {
@@ -694,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         uint64_t* full = FP4 ? &bars->gfull[st] : &bars->tfull[st];
         ok = (i % kBatch || wait(&bars->rfull[bt], (bi / kBatches) & 1)) &&
              (it < kBufs || wait(FP4 ? &bars->gempty[st] : &bars->tempty[st], ((it / kBufs) & 1) ^ 1));
+        if (kProbe && static_cast<uint32_t>(it) == stop) ok = ok && run_out();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (ptx::elect_one()) {
@@ -717,9 +747,17 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         __syncwarp();
       }
     }
-    // copies in flight land before the CTA can exit, whatever happened
-    for (int i = max(0, it - kBufs); i < it; ++i)
-      ptx::mbar_spin_drain(FP4 ? &bars->gfull[i % kBufs] : &bars->tfull[i % kBufs], (i / kBufs) & 1, a.status, kStatusTimeout, 400000000ll);
+    // Copies in flight land before the CTA can exit, whatever happened.  A block's barrier counts both warps; where one gave up,
+    // the other may have gone up to kBufs blocks further, and arrives in its place for those once both have stopped, so that
+    // their drain ends when they have landed, not at its limit.  (A block that was issued kBufs after another shows that one done.)
+    if (lane == 0) stopped[warp == 12 ? 0 : 1] = it;
+    ptx::named_bar_sync(5, 64);
+    const int other = stopped[warp == 12 ? 1 : 0];
+    auto full = [&](int i) { return FP4 ? &bars->gfull[i % kBufs] : &bars->tfull[i % kBufs]; };
+    if (lane == 0)
+      for (int i = other; i < it; ++i) ptx::mbar_arrive(full(i));
+    for (int i = max(0, max(it, other) - kBufs); i < it; ++i)
+      ptx::mbar_spin_drain(full(i), (i / kBufs) & 1, a.status, kStatusTimeout, 400000000ll);
   } else if (warp == 14) {
     // ------------------------------------------------------------ where the rows lie; scales of e4m3 rows
     // A batch's loads pass behind each other: positions of the next batch and pages of this one together, then the
@@ -792,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         const int bt = bi % kBatches;
         if (!FP4 && bi) scales((bt + kBatches - 1) % kBatches);
         ok = bi < kBatches || wait(&bars->bempty[bt], ((bi / kBatches) & 1) ^ 1);
+        if (kProbe && static_cast<uint32_t>(bi) == stop_at(kProbeRows)) ok = ok && run_out();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll
@@ -825,6 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
     int it = 0, n = 0, bn = 0;
     bool ok = true;
     for (; ok && pc.next(a); bn += batches(pc)) {
+      if (kProbe && w == 0 && static_cast<uint32_t>(n) == stop_at(kProbeQueries)) ok = __all_sync(0xffffffffu, run_out());
+      if (kProbe && !ok) break;
       const uint4* src[4];
       bool live[4];
       uint4 rp[4], r[4][4];
@@ -920,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         for (int i = 0; i < pc.k1 - pc.k0; ++i, ++it) {
           const int st = it % kStages, gs = it & 1, bt = (bn + i / kBatch) % kBatches;
           ok = wait(&bars->gfull[gs], (it >> 1) & 1) && (it < kStages || wait(&bars->tempty[st], ((it / kStages) & 1) ^ 1));
+          if (kProbe && w == 1 && static_cast<uint32_t>(it) == stop_at(kProbeDecode)) ok = ok && run_out();
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const bool there = rows[(bt * kBatch + i % kBatch) * kKeys + w * 16 + (lane & 15)] != a.past_row;  // of key 16 w + lane
@@ -999,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         float x[16];
         float mb = -INFINITY;
         uint32_t none = 0u;  // rows of zeros in the block
+        if (kProbe && ok && warp == 0 && static_cast<uint32_t>(b) == stop_at(kProbeSoftmax)) ok = __all_sync(0xffffffffu, run_out()) != 0;
         if (ok)
           ok = __all_sync(0xffffffffu, FP4 ? wait2(&bars->sfull[s2], (b >> 1) & 1, &bars->scfull[ss], (b / kStages) & 1)
                                        : (b - it) % kBatch ? wait(&bars->sfull[s2], (b >> 1) & 1)
@@ -1478,19 +1521,23 @@ Plan plan_of(const dsa_quant_mla_args* a) {
   return p;
 }
 
-template <bool FP4, bool ALL>
-cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s) {
+template <bool FP4, bool ALL, bool kProbe>
+cudaError_t launch_kernel(const CUtensorMap& map, const Args& k, cudaStream_t s) {
   static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory size
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto* kern = quant_mla_kernel<FP4, ALL>;
+  auto* kern = quant_mla_kernel<FP4, ALL, kProbe>;
   if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FP4>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   return launch_pdl_cluster(kern, dim3(k.parts), dim3(kThreads), Smem<FP4>::kBytes, ALL ? 1 : k.cluster, s, map, k);
+}
+template <bool FP4, bool ALL>
+cudaError_t launch_attend(const CUtensorMap& map, const Args& k, cudaStream_t s) {
+  return k.probe_site != 0 ? launch_kernel<FP4, ALL, true>(map, k, s) : launch_kernel<FP4, ALL, false>(map, k, s);
 }
 
 }  // namespace
@@ -1568,6 +1615,11 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   k.part_ml = reinterpret_cast<float*>(ws + p.off_ml);
   k.joins = reinterpret_cast<int2*>(ws + p.off_joins);
   k.status = status;
+  const Probe probe = armed_probe();
+  armed_probe() = Probe{0, 0, 0};
+  k.probe_site = probe.site;
+  k.probe_at = probe.at;
+  k.probe_cycles = 2 * static_cast<long long>(probe.limit_ns);  // some 2 cycles a nanosecond
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (!p.nb) {
@@ -1589,6 +1641,13 @@ dsa_status dsa_quant_mla(const dsa_quant_mla_args* a, dsa_stream_t stream) {
   const int blocks = all ? 2 * sm_count() : p.split > 1 && p.cluster == 1 ? std::min(2 * sm_count(), (p.rest * 64 + per - 1) / per) : 0;
   if (blocks) e = launch_pdl(all ? quant_join_kernel<true> : quant_join_kernel<false>, dim3(blocks), dim3(kJoinThreads), 0, s, k);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_test_arm_quant_mla_timeout(int site, unsigned at, unsigned long long limit_ns) {
+  const int role = site & ~kProbeOdd;
+  if (role < kProbeMma || role > kProbeSoftmax || site < 0 || limit_ns > 1000000000ull) return DSA_ERR_INVALID_ARGUMENT;
+  armed_probe() = limit_ns == 0 ? Probe{0, 0, 0} : Probe{site, at, limit_ns};
+  return DSA_OK;
 }
 
 }  // extern "C"

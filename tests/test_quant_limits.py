@@ -42,3 +42,11 @@ def test_tiles_are_not_cut_less_for_the_sake_of_a_cluster(dsa, kw):  # noqa: F81
                                 dict(total_q=30, H=32, topk_width=512)], ids=str)
 def test_pieces_of_a_cluster_take_no_workspace(dsa, kw):  # noqa: F811
     assert _size(dsa, **kw) == 0
+
+
+@pytest.mark.parametrize("site,limit,good", [(1, 1000, True), (7, 10 ** 9, True), (15, 1000, True), (0, 1000, False), (8, 1000, False),
+                                             (16, 1000, False), (-1, 1000, False), (1, 10 ** 9 + 1, False)])
+def test_arguments_of_the_failure_hook(dsa, site, limit, good):  # noqa: F811
+    want = dsa.DSA_OK if good else dsa.DSA_ERR_INVALID_ARGUMENT
+    assert dsa.lib().dsa_test_arm_quant_mla_timeout(site, 0, limit) == want
+    assert dsa.lib().dsa_test_arm_quant_mla_timeout(1, 0, 0) == dsa.DSA_OK  # disarmed again
