@@ -60,6 +60,7 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 }
 // hi + lo as one float whose last bit is set where it was cut: rounding this to fewer bits rounds the sum.
 __device__ __forceinline__ float to_odd(float hi, float lo) {
+  if (lo == 0.f) return hi;  // (-0 too)
   const float s = __fadd_rn(hi, lo), e = __fsub_rn(lo, __fsub_rn(s, hi));
   if (e == 0.f) return s;
   const uint32_t b = __float_as_uint(s);

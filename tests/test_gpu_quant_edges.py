@@ -28,3 +28,22 @@ def test_without_requests_all_rows_are_padding(row, k):
 def test_cuts_of_few_tiles(row, H, k, queries):
     """On both sides of the rule that takes a cluster or memory for the pieces of a tile."""
     Case(row, H, 64, [(queries, max(k, 2500))], k=k, seed=k + queries).check()
+
+
+@pytest.mark.parametrize("row", FORMATS)
+def test_the_sign_of_zeros(row):
+    """-0 is written as -0 by rows that are taken once and by those, one in some 100, that are taken again."""
+    n = 1200
+    g = torch.Generator().manual_seed(1)
+    c = torch.randn((n, 512), generator=g).to(torch.bfloat16)
+    c[:, ::3] = -0.0
+    c[:, 1::3] = 0.0
+    w = 1 + 0.1 * torch.randn(512, generator=g)
+    cache = torch.zeros((1, n, row), dtype=torch.uint8, device="cuda")
+    dsa.dsa_mla_quant_append(c.cuda(), torch.zeros((n, 64), dtype=torch.bfloat16, device="cuda"), torch.arange(n).cuda(), cache,
+                             norm_weight=w.cuda())
+    _ok()
+    got = cache[0].cpu().numpy()
+    lc, lr = qc.latent(c, torch.zeros((n, 64), dtype=torch.bfloat16), norm_weight=w)
+    want = [qc.encode_row(a, b, row) for a, b in zip(lc, lr)]
+    assert (got == want).all()
