@@ -60,9 +60,8 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 }
 // hi + lo as one float whose last bit is set where it was cut: rounding this to fewer bits rounds the sum.
 __device__ __forceinline__ float to_odd(float hi, float lo) {
-  if (lo == 0.f) return hi;  // (-0 too)
   const float s = __fadd_rn(hi, lo), e = __fsub_rn(lo, __fsub_rn(s, hi));
-  if (e == 0.f) return s;
+  if (e == 0.f) return __uint_as_float(__float_as_uint(s) | (__float_as_uint(hi) & 0x80000000u));  // (-0 + 0 is -0 here)
   const uint32_t b = __float_as_uint(s);
   return __uint_as_float(((e > 0.f) == (s > 0.f) ? b : b - 1u) | 1u);
 }
