@@ -558,7 +558,7 @@ dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* args, dsa_strea
  * cu_lens[b], row t = cu_lens[b] + i of c_kv and k_rope gets what position starts[b] + i of the request
  * (i itself when starts is NULL) stands for, exactly.  The rows may be views of one [total, 576] array
  * (c_stride, r_stride elements apart, 512 and 64 or more, multiples of 8; any when total = 1).  total is the outputs'
- * length: rows past cu_lens[B] are left as they were, rows past total are dropped.  A position whose
+ * length: rows before cu_lens[0] and from cu_lens[B] on are left as they were, rows past total are dropped.  A position whose
  * page is outside the cache, or that the table does not cover, leaves its row as it was and is
  * reported through dsa_check_device_status.  c_kv, k_rope and cache 16-byte aligned.
  * With pages of its own, the result is a bf16 cache that dsa_prefix_mla and dsa_sparse_mla take.

@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(kWarps * 32) quant_read_kernel(const dsa_mla_q
   ptx::grid_dep_launch();
   const int t = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= a.total || t >= __ldg(a.cu_lens + a.B)) return;
-  const int b = sequence_of(a.cu_lens, a.B, t);
-  const long long pos = static_cast<long long>(t) - __ldg(a.cu_lens + b) + (a.starts ? __ldg(a.starts + b) : 0);
+  const int b = sequence_of(a.cu_lens, a.B, t), first = __ldg(a.cu_lens + b);
+  if (t < first) return;
+  const long long pos = static_cast<long long>(t) - first + (a.starts ? __ldg(a.starts + b) : 0);
   const long long lp = pos / a.page_size;
   const int page = pos >= 0 && lp < a.max_pages_per_seq
                        ? __ldg(a.block_tables + static_cast<long long>(b) * a.max_pages_per_seq + lp) : -1;

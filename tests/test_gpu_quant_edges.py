@@ -47,3 +47,15 @@ def test_the_sign_of_zeros(row):
     lc, lr = qc.latent(c, torch.zeros((n, 64), dtype=torch.bfloat16), norm_weight=w)
     want = [qc.encode_row(a, b, row) for a, b in zip(lc, lr)]
     assert (got == want).all()
+
+
+@pytest.mark.parametrize("row", FORMATS)
+def test_read_leaves_rows_before_the_first_request(row):
+    """Offsets that begin behind other rows of the output: those are no request's, and starts do not move into them."""
+    case = Case(row, 1, 16, [(1, 40), (1, 25)], seed=2)
+    every = dsa.dsa_mla_quant_read(case.cache, case.bt, I32([0, 12, 17]), total=17, starts=I32([20, 3]))
+    c, r = torch.full((40, 512), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((40, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_mla_quant_read(case.cache, case.bt, I32([10, 22, 27]), total=40, starts=I32([20, 3]), c_kv=c, k_rope=r)
+    _ok()
+    assert (c[:10] == 9).all() and (r[:10] == 9).all() and (c[27:] == 9).all() and (r[27:] == 9).all()
+    assert torch.equal(c[10:27], every[0]) and torch.equal(r[10:27], every[1])
