@@ -149,9 +149,14 @@ __device__ __forceinline__ Codes encode(const float (&v)[16], bool* near) {
 }
 
 // The same row with every value in two floats, 2^-44 of it off: x the inputs, w the weights.  (fp64 itself took 8 us for
-// 64 rows, some of which always come here.)
+// 64 rows, some of which always come here.)  A row whose squares are too small for fp32 is taken 2^80 times as large, which
+// leaves c as it is.
 template <bool FP4>
-__device__ __noinline__ Codes encode_close(const float (&x)[16], const float (&w)[16], float eps) {
+__device__ __noinline__ Codes encode_close(const float (&in)[16], const float (&w)[16], float eps, bool tiny) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = in[i] * (tiny ? 0x1p80f : 1.f);
+  if (tiny) eps = eps * 0x1p80f * 0x1p80f;
   Two ss{0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = add(ss, Two{x[i] * x[i], 0.f});  // (a square of 8 bits is exact)
@@ -292,7 +297,8 @@ __global__ void __launch_bounds__(kWarps * 32) quant_append_kernel(const dsa_mla
       for (int i = 0; i < 16; ++i) v[i] = x[i] * (inv * w[i]);
       bool near;
       c = encode<FP4, true>(v, &near);
-      if (__any_sync(0xffffffffu, near)) c = encode_close<FP4>(x, w, a.norm_eps);
+      const bool tiny = mean < 0x1p-90f;  // squares this small lose bits, or all
+      if (__any_sync(0xffffffffu, near | tiny)) c = encode_close<FP4>(x, w, a.norm_eps, tiny);
     } else {
       c = encode<FP4, false>(x, nullptr);
     }

@@ -59,3 +59,23 @@ def test_read_leaves_rows_before_the_first_request(row):
     _ok()
     assert (c[:10] == 9).all() and (r[:10] == 9).all() and (c[27:] == 9).all() and (r[27:] == 9).all()
     assert torch.equal(c[10:27], every[0]) and torch.equal(r[10:27], every[1])
+
+
+@pytest.mark.parametrize("row", FORMATS)
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30])
+@pytest.mark.parametrize("power", [-45, -52, -66, -75, -100, -125])
+def test_norms_of_small_rows(row, eps, power):
+    """Rows whose squares fp32 cannot hold: the norm is that of the values all the same, or what the epsilon leaves of them."""
+    g = torch.Generator().manual_seed(-power)
+    c = torch.ldexp(torch.randn((7, 512), generator=g), torch.tensor(power)).to(torch.bfloat16)
+    c[3] = 0
+    r = torch.randn((7, 64), generator=g).to(torch.bfloat16)
+    w = 1 + 0.1 * torch.randn(512, generator=g)
+    cache = torch.zeros((1, 7, row), dtype=torch.uint8, device="cuda")
+    dsa.dsa_mla_quant_append(c.cuda(), r.cuda(), torch.arange(7).cuda(), cache, norm_weight=w.cuda(), norm_eps=eps)
+    _ok()
+    got = cache[0].cpu().numpy()
+    live = [0, 1, 2, 4, 5, 6]
+    lc, lr = qc.latent(c[live], r[live], norm_weight=w, norm_eps=eps)
+    assert (got[live] == [qc.encode_row(a, b, row) for a, b in zip(lc, lr)]).all()
+    assert not qc.decode_row(got[3])[0].any()
