@@ -401,10 +401,14 @@ dsa_status dsa_mla_quant_append(const dsa_mla_quant_append_args* a, dsa_stream_t
     return DSA_ERR_INVALID_ARGUMENT;
   unsigned* status = device_status_ptr();
   if (!status) return DSA_ERR_CUDA;
-  // Tokens a warp: more of them share the weights' loads, as long as the warps fill the SMs.  With the read-back of the
-  // same rows, 1, 2, 4 tokens a warp: 64 rows 11.0, 11.0, 12.3 us; 8195 20.1, 18.8, 20.4; 74967 in 4 bits 101.9, 90.9, 85.4.
+  // Tokens a warp: more of them share the weights' loads, as long as the warps fill the SMs.  1, 2, 4 tokens a warp, us by itself:
+  //   norm, 8 bits     64 rows 2.6, 3.1, 3.7    2048 5.2, 4.7, 5.2    8192 10.6, 9.8, 8.2    32768 29.7, 26.3, 22.6
+  //   norm, 4 bits     64 rows 4.7, 5.2, 6.7    2048 6.8, 6.3, 7.2    8192 12.4, 10.7, 10.2  32768 32.0, 26.1, 23.7
+  //   without, 8 bits  2048 2.6, 2.7, 3.1       4096 3.7, 3.1, 3.6    16384 7.2, 5.7, 5.7    32768 12.3, 9.8, 8.8
+  //   without, 4 bits  2048 3.6, 3.9, 5.1       4096 4.7, 4.7, 5.7    16384 10.3, 9.7, 9.3   32768 18.4, 16.0, 16.4
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->n >= 16384 ? launch_append<4>(*a, status, s) : a->n >= 4096 ? launch_append<2>(*a, status, s) : launch_append<1>(*a, status, s);
+  const int two = a->norm_weight ? 2048 : 4096, four = a->norm_weight ? 8192 : 16384;
+  const cudaError_t e = a->n >= four ? launch_append<4>(*a, status, s) : a->n >= two ? launch_append<2>(*a, status, s) : launch_append<1>(*a, status, s);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -79,3 +79,22 @@ def test_norms_of_small_rows(row, eps, power):
     lc, lr = qc.latent(c[live], r[live], norm_weight=w, norm_eps=eps)
     assert (got[live] == [qc.encode_row(a, b, row) for a, b in zip(lc, lr)]).all()
     assert not qc.decode_row(got[3])[0].any()
+
+
+@pytest.mark.parametrize("row", FORMATS)
+@pytest.mark.parametrize("norm,n", [(True, 2047), (True, 2048), (True, 2051), (True, 8191), (True, 8195), (False, 4095), (False, 4097),
+                                    (False, 16383), (False, 16387)])
+def test_the_number_of_tokens_a_warp_does_not_matter(row, norm, n):
+    """Both sides of the rule for one, two and four tokens a warp: the same bytes as from calls of a few rows."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    c = torch.randn((n, 512), generator=g, device="cuda").to(torch.bfloat16)
+    r = torch.randn((n, 64), generator=g, device="cuda").to(torch.bfloat16)
+    kw = dict(norm_weight=1 + 0.1 * torch.randn(512, generator=g, device="cuda")) if norm else {}
+    slots = torch.randperm(n + 9, generator=g, device="cuda")[:n]
+    slots[::11] = -1
+    one, many = (torch.full((-(-(n + 9) // 64), 64, row), 3, dtype=torch.uint8, device="cuda") for _ in range(2))
+    dsa.dsa_mla_quant_append(c, r, slots.contiguous(), one, **kw)
+    for i in range(0, n, 1000):
+        dsa.dsa_mla_quant_append(c[i: i + 1000], r[i: i + 1000], slots[i: i + 1000].contiguous(), many, **kw)
+    _ok()
+    assert torch.equal(one, many)
