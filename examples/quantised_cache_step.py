@@ -62,19 +62,16 @@ class Batch:
     def prompt(self, new_tokens):
         """Attention output and lse of prompts, over rows read back into pages of bf16."""
         cu, q = self._write(new_tokens)
-        held = [-(-n // PAGE) for n in self.lens.tolist()]
-        ends = torch.tensor([0] + held, device=self.device).cumsum(0)
-        rows = int(ends[-1]) * PAGE
-        starts = (ends * PAGE).to(torch.int32)       # request b's rows from its first page on, the last page not full
-        kv = torch.zeros((rows, KV_RANK), dtype=torch.bfloat16, device=self.device), torch.zeros((rows, ROPE_DIM), dtype=torch.bfloat16, device=self.device)
-        pages = torch.full((len(held), max(held)), -1, dtype=torch.int32, device=self.device)
-        for b, n in enumerate(held):                 # one request at a time: its rows are dense, its pages too
-            pages[b, :n] = torch.arange(n, device=self.device) + ends[b]
-            at = slice(int(starts[b]), int(starts[b]) + n * PAGE)
-            cu_b = torch.stack([torch.zeros_like(self.lens[b]), self.lens[b]])
-            dsa.dsa_mla_quant_read(self.cache, self.tables[b: b + 1], cu_b, total=n * PAGE, c_kv=kv[0][at], k_rope=kv[1][at])
-        return dsa.dsa_prefix_mla(q[..., :KV_RANK], q[..., KV_RANK:], kv[0].view(-1, PAGE, KV_RANK), kv[1].view(-1, PAGE, ROPE_DIM),
-                                  pages, cu, self.lens, prefix_len=0, scale=SCALE)
+        # every request's rows in whole pages, one request behind the other: what follows a sequence's end in its last page may be
+        # anything, no query sees it
+        held = (self.lens + PAGE - 1) // PAGE
+        ends = torch.nn.functional.pad(held.cumsum(0), (1, 0)).to(torch.int32)
+        total = int(ends[-1])
+        c, r = dsa.dsa_mla_quant_read(self.cache, self.tables, ends * PAGE, total=total * PAGE)
+        page = torch.arange(int(held.max()), dtype=torch.int32, device=self.device)[None]
+        pages = torch.where(page < held[:, None], ends[:-1, None] + page, -1)
+        return dsa.dsa_prefix_mla(q[..., :KV_RANK], q[..., KV_RANK:], c.view(-1, PAGE, KV_RANK), r.view(-1, PAGE, ROPE_DIM), pages, cu,
+                                  self.lens, prefix_len=0, scale=SCALE)
 
     def step(self, new_tokens, topk):
         """(out, lse) over every position and over topk selected keys a query."""
