@@ -525,7 +525,8 @@ dsa_status dsa_prefix_mla(const dsa_prefix_mla_args* args, dsa_stream_t stream);
  * held as bf16(r) / 2^E (exact for 2^-66 <= |r| < 2^67).  A mean over 512 normal values is off by
  * 2.7 % (e4m3) and 10 % (e2m1) of their size.
  * Rows are the library's own: dsa_mla_quant_append writes and dsa_mla_quant_read reads them.  A page
- * may be moved or copied as bytes.
+ * may be moved or copied as bytes.  Nothing in a row tells its format: a cache of another layout whose rows
+ * have as many bytes is taken for one of these, and read wrongly.
  */
 
 /* Bytes of a row of this format; 0 for one that there is not. */
@@ -536,7 +537,8 @@ int dsa_mla_quant_row_bytes(int format);
  * sqrt(mean(c_kv^2) + norm_eps) (c_kv itself without norm_weight) and r = RoPE(k_rope) (k_rope itself
  * without rope_cos), written to row slot of the cache in `format`.  Arguments, slots and reports are
  * those of dsa_mla_cache_append; cache is 16-byte aligned.  Inputs of rows that are written must be
- * finite, the sum of squares of a row too.  Two rows for one slot: one of them, or a mixture.
+ * finite, the sum of squares of a row too (codes hold no infinity, and 4-bit ones no NaN: the largest code of the
+ * block stands in its place, and nothing is reported).  Two rows for one slot: one of them, or a mixture.
  */
 typedef struct {
   int format, n, kv_rank, rope_dim, page_size, num_pages, rope_interleaved, rope_rows;
@@ -591,10 +593,11 @@ dsa_status dsa_mla_quant_read(const dsa_mla_quant_read_args* args, dsa_stream_t 
  *   8, any in a dimension of size 1; the last dimension dense); out [total_q, H, 512] bf16 dense;
  *   lse [total_q, H]; topk [total_q, topk_width].
  * kv_rank = 512, rope_dim = 64, 1 <= H <= 128, scale > 0; total_q * H and num_pages * page_size below
- * 2^31 - 128; topk_width at most 2^31 - 256.  Rows of the cache that no query attends to may hold anything; the others are finite, and
- * so are the queries of rows that are not padding (what is not finite makes its own query and head
- * NaN).  A page outside the cache is skipped and reported through dsa_check_device_status, as are
- * positions past the table (topk_width = 0).  Results do not depend on the run.  workspace:
+ * 2^31 - 128; topk_width at most 2^31 - 256.  Rows of the cache that no query attends to may hold
+ * anything; the others are finite, their 2^E within a factor of 2^100 for one query (rows of zeros count
+ * as 2^-60), and the queries of rows that are not padding are finite (what is not makes its own query
+ * and head NaN).  A page outside the cache is skipped and reported through dsa_check_device_status, as
+ * are positions past the table.  Results do not depend on the run.  workspace:
  * dsa_quant_mla_workspace_size bytes (0: none is taken), 16-byte aligned like the other pointers.
  * Weights enter out to 2^-7 each.  Small ones, of which many may count together, are rounded up for some keys and down for
  * others: a key whose weight times its row's 2^E is below 2^-11 of the largest such product is off by up to 2^-17 of that,

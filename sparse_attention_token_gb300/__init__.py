@@ -1004,7 +1004,8 @@ def dsa_mla_quant_row_bytes(format: int) -> int:
 
 
 def _quant_cache(cache: torch.Tensor, here: int):
-    """(format, pages, page size, device pointer) of a quantised latent cache."""
+    """(format, pages, page size, device pointer) of a quantised latent cache.  The row's size is all that tells the format:
+    rows of another layout that have as many bytes are not told apart."""
     shape = cache.shape
     if len(shape) != 3 or shape[2] not in _QUANT_FORMATS:
         raise ValueError("cache must have shape [num_pages, page_size, 656 (DSA_FP8_E4M3) or 416 (DSA_FP4_E2M1)], got "
@@ -1020,7 +1021,9 @@ def dsa_mla_quant_append(c_kv: torch.Tensor, k_rope: torch.Tensor, slot_mapping:
     """dsa_mla_cache_append into a quantised cache [num_pages, page_size, row] uint8, in place: c_kv [n, 512]
     (root-mean-square norm times norm_weight, when given) and k_rope [n, 64] (turned by row positions[t] of
     rope_cos / rope_sin, when given) as one row of 656 bytes (e4m3) or 416 (e2m1), by the cache's row size,
-    at the slots slot_mapping [n] (int64; negative = skip)."""
+    at the slots slot_mapping [n] (int64; negative = skip).  Rows are laid out as only this package does: a cache of
+    another origin whose rows have 656 bytes too is not recognised as foreign, neither here nor by dsa_mla_quant_read
+    and dsa_quant_mla.  Inputs are finite (4 bits hold no NaN)."""
     if not (c_kv.dim() == k_rope.dim() == 2 and (rope_cos is None or rope_cos.dim() == 2)):
         _expect([(c_kv, "c_kv", (None, None)), (k_rope, "k_rope", (None, None)), (rope_cos, "rope_cos", (None, None))])
     n, R = c_kv.shape
@@ -1095,8 +1098,8 @@ def dsa_quant_mla(q_nope, q_rope, cache, block_tables, cu_q_lens, seq_lens, topk
     """Latent attention over a quantised cache [num_pages, page_size, row] uint8: each query over its selected
     keys topk [total_q, k] int32 (any order, -1 skipped), or without topk over every position up to its own.
     Returns (out [total_q, H, 512] bf16, lse [total_q, H] fp32, the natural logarithm of the sum of
-    exponentials); a query without keys gets zeros and -inf.  q_nope [total_q, H, 512] and q_rope
-    [total_q, H, 64] bf16 may be views of one tensor.  out, lse and the workspace
+    exponentials); a query without keys gets zeros and -inf.  The cache's rows are those of dsa_mla_quant_append.
+    q_nope [total_q, H, 512] and q_rope [total_q, H, 64] bf16 may be views of one tensor.  out, lse and the workspace
     (dsa_quant_mla_workspace_size bytes, which may be none) are allocated when not given."""
     qs, rs, bs = q_nope.shape, q_rope.shape, block_tables.shape
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1

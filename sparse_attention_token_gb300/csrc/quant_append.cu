@@ -4,13 +4,14 @@
 //
 // A code is that of c in exact arithmetic.  In fp32, c is off by up to 13 * 2^-24 (12 roundings of the sum of squares
 // and eps count half through the root, which is 2 * 2^-24 off itself; then two products and the three of its scaling),
-// which moves a value next to a border between two codes over it: once in some 10^5 values, by a whole step of the code.  So each decision (the row's exponent, a
-// block's scale, every code) is taken for c (1 - 2^-20) and for c (1 + 2^-20); where the two differ, one row in some
-// 100, the warp takes the row again with two floats a value.  Without norm c is the input and fp32 is exact.
+// which moves a value next to a border between two codes over it: once in some 10^5 values, by a whole step of the code.
+// So each decision (the row's exponent, a block's scale, every code) is taken for c (1 - 2^-20) and for c (1 + 2^-20);
+// where the two differ, one row in some 100, the warp takes the row again with two floats a value.  Without norm c is the
+// input and fp32 is exact.
 //
 // One warp takes a token: lane i holds the values 16 i .. 16 i + 15, which are one block of the 4-bit format.
 // In a graph with the read-back of the same rows: 64 tokens 6.2 us (latency: launch, slot, row, reductions, store; rows
-// that are taken again 1 us of it), 8195 tokens in 8 bits 14.3 (4.7 at the copy bandwidth), 74967 in 4 bits 77 (38): there
+// that are taken again 1 us of it), 8193 tokens in 8 bits 12.4 (4.7 at the copy bandwidth), 74968 in 4 bits 78 (38): there
 // the arithmetic of the decisions, some 90 instructions a value pair, takes longer than the bytes.
 #include <cuda_runtime.h>
 

@@ -13,17 +13,18 @@
 //   x' = x + E - kExpRef,  m' its running maximum,  p = 2^(x' - m' + kPShift) in an e4m3 and an e5m2 term (two_terms):
 //       O = sum p c8,  L = sum p 2^(kExpRef - E) (fp32, of the unrounded p),  out = 2^kExpRef O / L
 // Two 8-bit planes cost the tensor cores what one bf16 plane does and half the shared memory traffic.  Taking E
-// into the maximum keeps p in range whatever the rows' scales are.  Against 64 bits the output's mean error is 0.0020 of
-// its size, 0.0017 of which is its own rounding to bf16; lse is within 6e-8.
+// into the maximum keeps p in range whatever the rows' scales are.  On random rows, against 64 bits, the output's root mean
+// square error is 0.0017 to 0.0021 of its size (the most with few keys), 0.00166 of which is its own rounding to bf16; lse is
+// off by 2e-6 at most, 3e-7 to 5e-7 on average.
 //
 // Work: a tile is a query and up to 64 heads, its keys are cut into blocks of 64; how tiles come to CTAs stands at Pieces.
 // A tile done in one piece is normalised and written; the pieces of the others, (O, m', L) in fp32, are joined by the CTAs of
 // a cluster that hold them, or else go through memory to a second kernel.  Roles of a CTA:
 //   warps 0..7    softmax, two groups that take 32 keys each of every block.  Rows of S alternate between 16 hi and
 //                 16 lo rows, so that a lane and the one 16 further hold a head's two planes; each adds the planes
-//                 for half of its group's keys.  (Alternate blocks to the groups: 312 us instead of 315 for the first
-//                 figure below, but 37.0 instead of 34.9 for 62 x 128 heads x 1001 keys in 4 bits, and 4 % more for
-//                 the other 4-bit cases: there the time from S to P is what counts);
+//                 for half of its group's keys.  (Alternate blocks to the groups took 1 % less for the first figure
+//                 below, but 6 % more for 62 x 128 heads x 1001 keys in 4 bits, and 4 % more for the other 4-bit
+//                 cases: there the time from S to P is what counts);
 //   warps 8..11   query rows: bf16 -> hi, lo in TMEM (A operand), 2^a q_rope in shared memory;
 //                 4-bit rows also: codes from the staged rows to e4m3 tiles;
 //   warps 12, 15  rows of the cache by gathering TMA: e4m3 tiles in 128-byte columns, 4-bit rows whole;
@@ -34,18 +35,18 @@
 // bytes meets 128 x 576 + 2 x 64 x 512 multiplications.
 //
 // What bounds it (GB300, 1.9 GHz, captured in a graph):
-//   block     the MMAs of a block take 1470 cycles.  e4m3: 2000 to 2100 a block, by the softmax (some 350 instructions a
-//             warp, each waiting for the one before, and a barrier) and the four tiles in flight: a tile is gathered (950 cycles from
-//             L2, 1430 with one issuing warp less), waits its turn, is multiplied twice and freed; 2800 a block when rows
-//             come from DRAM.  1127 queries x 64 heads x 2048 keys: 315 us, 166 at the tensor cores' rate.  4 bits: three
-//             tiles, and decoding stands in the round: 2700 a block.
+//   block     the MMAs of a block take the tensor pipe for 1150 cycles.  e4m3: 2070 a block, by the softmax (some 350
+//             instructions a warp, each waiting for the one before, and a barrier) and the four tiles in flight: a tile is gathered
+//             (950 cycles from L2, 1430 with one issuing warp less), waits its turn, is multiplied twice and freed; 2430 a
+//             block when rows come from DRAM.  1127 queries x 64 heads x 2048 keys: 316 us, the tensor pipe active for 46 % of
+//             them, 166 at the tensor cores' rate.  4 bits: three tiles, and decoding stands in the round: 2600 a block.
 //   piece     some 8000 to 10000 cycles before a CTA's first MMA (launch, queries, look-up, first rows), 10000 from a
 //             piece's last product to the next one's first (next queries 6000, then their first block's softmax; the
-//             output, 6000, beside them).  64 queries x 64 heads x 2048 keys: 45 us (e4m3) and 43 (4 bits), 14 and 9 at
+//             output, 6000, beside them).  64 queries x 64 heads x 2048 keys: 44.5 us (e4m3) and 43 (4 bits), 14 and 9 at
 //             the copy bandwidth.
 //   join      in a cluster 3 us; through memory 7 to 14, 2 of which its CTAs wait for room.
-// Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained
-// (bounded) and TMEM is freed.
+// Every wait is bounded; after one gives up, every role stops, the MMAs and copies in flight are drained (bounded; with any
+// role's wait made to run out, a call ends some 0.1 ms later), the CTAs of a cluster meet all the same and TMEM is freed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
