@@ -421,20 +421,42 @@ __device__ __forceinline__ void put_scale_of_zeros(float4* block, int key) {
   pair[0] = __uint_as_float(0x3F800001u);
   pair[2] = static_cast<float>(kZeroExp - kExpRef);
 }
-// Of the rows `rows[32 j]` (e4m3) whose bits j are set in `of`, those whose codes are all zeros.  (Only rows of E = 0 are
-// asked about; another row of that scale has a code of 224 or more, found in its first bytes as a rule.)
-__device__ __noinline__ unsigned rows_of_zeros(const uint8_t* cache, const int* rows, unsigned of) {
-#pragma unroll 1
-  for (int i = 0; i < kRank / 16 && of; ++i) {
-    uint4 v[8];
+// Of the rows `rows[32 j + lane]` (e4m3) whose bits j are set in a lane's `of`, those whose codes are all zeros.  Only rows of
+// E = 0 are asked about.  Another row of that scale is told by its first codes as a rule; the rest are looked at by the
+// whole warp, eight at a time.  (1100 x 64 heads x 2048 keys: 3 % more time where every row has E = 0, 4 % where one in a hundred
+// is zeros, three times as much where all are.)
+__device__ __noinline__ unsigned rows_of_zeros(const uint8_t* cache, const int* rows, unsigned of, int lane) {
+  uint4 first[2 * kBatch];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = of >> j & 1 ? __ldg(reinterpret_cast<const uint4*>(cache + static_cast<long long>(rows[32 * j]) * kRow8) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if ((v[j].x | v[j].y | v[j].z | v[j].w) & 0x7F7F7F7Fu) of &= ~(1u << j);
+  for (int j = 0; j < 2 * kBatch; ++j) {
+    first[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (of >> j & 1) first[j] = __ldg(reinterpret_cast<const uint4*>(cache + static_cast<long long>(rows[32 * j + lane]) * kRow8));
   }
-  return of;
+#pragma unroll
+  for (int j = 0; j < 2 * kBatch; ++j)
+    if ((first[j].x | first[j].y | first[j].z | first[j].w) & 0x7F7F7F7Fu) of &= ~(1u << j);
+  unsigned found = 0u;
+#pragma unroll 1
+  for (int j = 0; j < 2 * kBatch; ++j) {
+    unsigned left = __ballot_sync(0xffffffffu, of >> j & 1u);
+    while (left) {
+      uint4 v[8];
+      int at[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        at[i] = left ? __ffs(static_cast<int>(left)) - 1 : -1;
+        left &= left - 1;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at[i] >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(cache + static_cast<long long>(rows[32 * j + at[i]]) * kRow8) + lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool some = __any_sync(0xffffffffu, ((v[i].x | v[i].y | v[i].z | v[i].w) & 0x7F7F7F7Fu) != 0u);
+        if (at[i] == lane && !some) found |= 1u << j;
+      }
+    }
+  }
+  return found;
 }
 __device__ __forceinline__ float2 add2(float2 a, float b) {
   float2 d;
@@ -776,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_mla_kernel(const __grid_con
         z |= (u[j] == 1.f ? 1u : 0u) << j;
       }
       if (__builtin_expect(__any_sync(0xffffffffu, z != 0u), 0)) {
-        z = rows_of_zeros(a.cache, rows + bt * kBatch * kKeys + lane, z);
+        z = rows_of_zeros(a.cache, rows + bt * kBatch * kKeys, z, lane);
         __syncwarp();
         some = __reduce_or_sync(0xffffffffu, z);
         for (; z; z &= z - 1) {
