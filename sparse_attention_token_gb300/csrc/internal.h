@@ -107,26 +107,9 @@ struct PdlOffScope {
   ~PdlOffScope() { pdl_off() = prev; }
 };
 
-// Launch with programmatic stream serialisation: the kernel may be scheduled while the
-// previous kernel on the stream drains, runs its prologue, and waits (grid_dep_wait)
+// Launch with programmatic stream serialisation, in clusters of `cluster` CTAs (1: none): the kernel may be scheduled
+// while the previous kernel on the stream drains, runs its prologue, and waits (grid_dep_wait)
 // before it touches global memory that kernel may write.
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              Args&&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl_off() ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
-// The same in clusters of `cluster` CTAs (1: none).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
                                       Args&&... args) {
@@ -151,6 +134,11 @@ inline cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 bl
   cfg.attrs = at;
   cfg.numAttrs = static_cast<unsigned>(n);
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                              Args&&... args) {
+  return launch_pdl_cluster(kern, grid, block, smem, 1, st, std::forward<Args>(args)...);
 }
 
 // Failure-path test hook: the next score launch of the calling host thread gets this
